@@ -62,6 +62,7 @@ typedef enum {
 #define SE_DEVERR_PAGE_RANGE   0x1u  /* a block-table entry outside [0, num_pages) */
 #define SE_DEVERR_LENGTH       0x2u  /* a length or selected-page id outside its declared bound */
 #define SE_DEVERR_WAIT_TIMEOUT 0x4u  /* a bounded wait (an mbarrier, or another CTA's counter) gave up */
+#define SE_DEVERR_NO_PAGES     0x8u  /* se_block_tables_extend: the pool had too few free pages for a request */
 
 /*
  * Paged KV cache view. Physical page p of KV head h holds tokens in slots
@@ -337,6 +338,112 @@ SE_API se_status_t se_sparse_paged_decode(const se_paged_kv_t* kv, const void* q
                                    int32_t batch, const int32_t* sel_pages, const int32_t* sel_counts,
                                    int32_t sel_stride, float sm_scale, void* out, float* out_lse,
                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Page pool, block tables and slot maps, built on the GPU from request lengths.
+ *
+ * The caller keeps a pool's free pages as a stack in device memory:
+ *   free_pages: int32 [num_pages], the page ids free_pages[0 .. count - 1];
+ *   pool_state: int32 [4]: {count, 0, 0, 0} ([1] is the calls' arrival counter, zero between calls).
+ * A fresh pool is free_pages[i] = i, pool_state = {num_pages, 0, 0, 0}. Calls on one
+ * pool must not overlap on the GPU.
+ *
+ * se_block_tables_extend -- pages, table entries and slots for the new tokens of
+ * a batch: new_lens[b] tokens (0 allowed) behind the seq_lens[b] cached ones.
+ *   have_b = ceil(seq_lens[b] / 16), need_b = ceil((seq_lens[b] + new_lens[b]) / 16) - have_b;
+ *   page have_b + i of request b (i < need_b) is free_pages[count - 1 - (need_0 + .. + need_{b-1} + i)],
+ *   written to block_table[b][have_b + i]; count drops by the pages taken. Entries of
+ *   cached pages are read, all others left as they are.
+ *   token_start int32 [batch + 1]: the first of request b's tokens in the batch of new
+ *     tokens (an exclusive prefix sum of new_lens; token_start[batch] is their number),
+ *     clipped to max_new_tokens;
+ *   slot_map int32 [max_new_tokens]: 16 * page + offset in the page for every new token,
+ *     -1 behind the last one (padding, which se_paged_kv_store skips);
+ *   positions int32 [max_new_tokens] or NULL: the token's position in its request, 0 behind
+ *     the last one;
+ *   seq_lens_after int32 [batch] = seq_lens + new_lens; may be seq_lens itself.
+ * A request is not served when its lengths are negative or exceed bt_stride * 16, or its
+ * tokens end behind max_new_tokens (SE_DEVERR_LENGTH), or the pages left do not suffice
+ * (SE_DEVERR_NO_PAGES; in batch order, and then no later request that needs a page is
+ * served). Such a request takes no page, its slots are -1, its positions 0 and its
+ * length stays. A page id outside [0, num_pages) sets SE_DEVERR_PAGE_RANGE, and its tokens'
+ * slots are -1. batch <= 16384; max_new_tokens >= 0 is on the host, so that a recorded
+ * step serves any lengths up to it; bt_stride and num_pages < 2^27.
+ *
+ * se_block_tables_release -- the pages of the tokens behind keep_lens[b] (NULL: of
+ * every token) back to the pool: logical pages ceil(keep_lens[b] / 16) .. ceil(seq_lens[b] / 16) - 1
+ * of request b, the exact inverse of the extension from keep_lens to seq_lens: called
+ * straight after it, it restores free_pages. The table entries are left as they are;
+ * the caller's lengths become keep_lens. A page must be in one request only, and be
+ * returned once. Lengths out of order or beyond the table: SE_DEVERR_LENGTH, nothing of that
+ * request is returned. More pages than the pool lacks: SE_DEVERR_PAGE_RANGE, nothing is
+ * returned. A page id out of range: SE_DEVERR_PAGE_RANGE, and -1 in its place on the stack.
+ */
+SE_API se_status_t se_block_tables_extend(const int32_t* free_pages, int32_t* pool_state, int32_t num_pages,
+                                          int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
+                                          const int32_t* new_lens, int32_t batch, int32_t* seq_lens_after,
+                                          int32_t* token_start, int32_t* slot_map, int32_t* positions,
+                                          int32_t max_new_tokens, void* stream);
+SE_API se_status_t se_block_tables_release(int32_t* free_pages, int32_t* pool_state, int32_t num_pages,
+                                           const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
+                                           const int32_t* keep_lens, int32_t batch, void* stream);
+
+/*
+ * se_paged_kv_store -- the K and V rows of a ragged batch of new tokens (a prompt,
+ * chunks of prompts, one token per request) into their slots.
+ * Token t of num_tokens goes to row slot_map[t] % 16 of page slot_map[t] / 16, every KV
+ * head; tokens with a negative slot are padding and skipped.
+ *   k_new: bf16, the row of token t and KV head h at k_new + t * k_stride + h * head_dim
+ *     (elements), v_new alike with head_dim_v; NULL for a latent cache (kv->v == kv->k).
+ *     Strides are multiples of 8 and at least num_kv_heads * head_dim (head_dim_v), so that
+ *     the rows can be columns of a fused projection's output.
+ * With kv->summary, the page summaries are updated as se_quest_update_summaries does
+ * token by token: from the new keys alone for a page whose slot 0 is among them,
+ * otherwise together with the page's present summary. The new tokens of one page stand
+ * next to each other in the batch, as in the slot map of se_block_tables_extend, and a
+ * slot is named once. A slot named twice in neighbouring tokens keeps the later one
+ * (with kv->summary); elsewhere, and without kv->summary, it holds rows of either.
+ * head_dim and head_dim_v: multiples of 8 up to 576. A slot at or behind num_pages * 16 sets
+ * SE_DEVERR_PAGE_RANGE and is skipped.
+ */
+SE_API se_status_t se_paged_kv_store(const se_paged_kv_t* kv, const void* k_new, int64_t k_stride, const void* v_new,
+                                     int64_t v_stride, const int32_t* slot_map, int32_t num_tokens, void* stream);
+
+/*
+ * se_paged_decode -- attention of one new token per request over its cached
+ * tokens, without a selection: a cache that SnapKV has compacted, layers kept dense
+ * beside the sparse ones, or a sink and a recent window.
+ * SparseEngine, Table 7 (logit z, weight alpha; the history includes the current
+ * token) and Tables 9-12 (sink and recent tokens).
+ * For request b with L = seq_lens[b] and query head a (KV head h = a / (num_q_heads / num_kv_heads)),
+ * over the kept positions j: all j < L when recent_tokens is 0 (sink_tokens must be 0
+ * too), otherwise those with j < sink_tokens or j >= L - recent_tokens:
+ *     z_j = sm_scale * q[b][a] . k_j
+ *     out[b][a]  = sum_j softmax(z)_j v_j       (bf16, round to nearest even)
+ *     out_lse[b][a] = log sum_j exp(z_j)        (fp32, natural log; optional)
+ * A request without tokens (and a row whose logits are all -inf) writes out = 0 and
+ * lse = -inf. Cache rows that are not kept are never used, whatever they hold.
+ *   q: bf16, query head a of request b at q + b * q_stride + a * head_dim (elements;
+ *     q_stride >= num_q_heads * head_dim, a multiple of 8); out: bf16 [batch][num_q_heads][head_dim_v];
+ *   out_lse: fp32 [batch][num_q_heads] or NULL;
+ *   workspace: se_paged_decode_workspace_size bytes, whatever the lengths, zero-filled
+ *     before its first use (every call leaves its counters zero). Calls that share a
+ *     workspace must not overlap on the GPU.
+ * Lengths stay on the device: a recorded step serves any lengths. A length outside
+ * [0, 16 * bt_stride] sets SE_DEVERR_LENGTH and is clipped; a page id out of range sets
+ * SE_DEVERR_PAGE_RANGE and its page is skipped. The work is split over the cache's
+ * pages by the lengths alone and joined in a fixed order: equal inputs give equal bits.
+ * Shapes: head_dim = head_dim_v of 64, 128 or 256 with 1..64 query heads per KV head, or a latent
+ * cache (head_dim 576, head_dim_v 512, one KV head, kv->v == kv->k, 16..64 query heads in
+ * multiples of 16).
+ * se_paged_decode_workspace_size returns 0 for sizes that are not supported.
+ */
+SE_API size_t se_paged_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                             int32_t head_dim, int32_t head_dim_v);
+SE_API se_status_t se_paged_decode(const se_paged_kv_t* kv, const void* q, int64_t q_stride, int32_t num_q_heads,
+                                   const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
+                                   int32_t batch, int32_t sink_tokens, int32_t recent_tokens, float sm_scale,
+                                   void* out, float* out_lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * SnapKV eviction at the end of prefill (SparseEngine: Sparse-First Inference

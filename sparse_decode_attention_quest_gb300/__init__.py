@@ -28,13 +28,15 @@ __all__ = [
     "se_sparse_paged_decode_noalloc", "se_snapkv_workspace_size", "se_snapkv_window_scores", "se_snapkv_select",
     "se_snapkv_compact", "se_snapkv_score_and_compact", "se_snapkv_select_windowed",
     "se_snapkv_score_and_compact_windowed", "se_debug_snapkv_wait_probe", "SEGraph", "se_capture_begin",
-    "se_capture_end", "exported_symbols",
+    "se_capture_end", "se_block_tables_extend", "se_block_tables_release", "se_paged_kv_store",
+    "se_paged_decode_workspace_size", "se_paged_decode", "exported_symbols",
 ]
 
 SE_OK = 0
 DEVERR_PAGE_RANGE = 0x1
 DEVERR_LENGTH = 0x2
 DEVERR_WAIT_TIMEOUT = 0x4
+DEVERR_NO_PAGES = 0x8
 APPEND_OVERLAP_PREVIOUS = 0x1  # se_quest_update_summaries_ex: may run alongside the previous kernel
 
 
@@ -57,6 +59,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _F = ctypes.c_float
 _Z = ctypes.c_size_t
+_L = ctypes.c_int64
 _KV = ctypes.POINTER(SEPagedKV)
 
 _SIGNATURES = {
@@ -83,6 +86,11 @@ _SIGNATURES = {
                                              ctypes.POINTER(_I)]),
     "se_sparse_paged_decode": (ctypes.c_int, [_KV, _P, _I, _P, _I, _P, _I, _P, _P, _I, _F, _P, _P, _P, _Z, _P]),
     "se_sparse_paged_decode_noalloc": (ctypes.c_int, [_KV, _P, _I, _P, _I, _P, _I, _P, _P, _I, _F, _P, _P, _P]),
+    "se_block_tables_extend": (ctypes.c_int, [_P, _P, _I, _P, _I, _P, _P, _I, _P, _P, _P, _P, _I, _P]),
+    "se_block_tables_release": (ctypes.c_int, [_P, _P, _I, _P, _I, _P, _P, _I, _P]),
+    "se_paged_kv_store": (ctypes.c_int, [_KV, _P, _L, _P, _L, _P, _I, _P]),
+    "se_paged_decode_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
+    "se_paged_decode": (ctypes.c_int, [_KV, _P, _L, _I, _P, _I, _P, _I, _I, _I, _F, _P, _P, _P, _Z, _P]),
     "se_snapkv_workspace_size": (_Z, [_I, _I, _I, _I]),
     "se_snapkv_window_scores": (ctypes.c_int, [_KV, _P, _I, _I, _P, _I, _P, _I, _I, _F, _P, _I, _P, _P, _Z, _P]),
     "se_snapkv_select": (ctypes.c_int, [_P, _I, _P, _I, _I, _I, _I, _I, _I, _P, _I, _P, _P]),
@@ -392,6 +400,122 @@ def se_sparse_paged_decode_noalloc(kv: SEPagedKV, q, block_table, seq_lens, sel_
                                               _ptr(sel_counts, torch.int32, "sel_counts"), sel_pages.shape[-1],
                                               float(sm_scale), _ptr(out, torch.bfloat16, "out"),
                                               _ptr(out_lse, torch.float32, "out_lse"), _stream(stream)))
+
+
+# ------------------------------------------- page pool, row store, dense paged decode
+def _same_len(t, n: int, name: str):
+    if t.numel() != n:
+        raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
+
+
+def _on_current_device(*tensors):
+    """The library launches on the current device: tensors of another one are refused."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.get_device() != dev:
+            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+
+
+def _rows_ptr(t, heads: int, width: int, dtype, name: str):
+    """(pointer, row stride) of [N][heads][width] rows whose heads are dense; the N rows may be
+    any distance apart (columns of a fused projection's output, say)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != width:
+        raise ValueError(f"{name}: expected shape [N][{heads}][{width}], got {list(t.shape)}")
+    n, s = t.shape[0], t.stride()
+    if (width > 1 and s[2] != 1) or (heads > 1 and s[1] != width):
+        raise ValueError(f"{name}: the heads of a row must be dense")
+    return t.data_ptr(), s[0] if n > 1 else heads * width
+
+
+def se_block_tables_extend(free_pages, pool_state, block_table, seq_lens, new_lens, seq_lens_after, token_start,
+                           slot_map, positions=None, stream=None):
+    """Pages, table entries, slots and positions for new_lens[b] tokens behind the seq_lens[b] cached
+    ones; ``free_pages`` (int32, as long as the pool has pages) and ``pool_state`` (int32 [4]) are the
+    pool, ``slot_map.numel()`` is the most new tokens a call takes. ``seq_lens_after`` may be ``seq_lens``."""
+    lib = load_library()
+    batch = block_table.shape[0]
+    _on_current_device(free_pages, pool_state, block_table, seq_lens, new_lens, seq_lens_after, token_start, slot_map,
+                       positions)
+    _same_len(pool_state, 4, "pool_state")
+    _same_len(seq_lens, batch, "seq_lens")
+    _same_len(new_lens, batch, "new_lens")
+    _same_len(seq_lens_after, batch, "seq_lens_after")
+    _same_len(token_start, batch + 1, "token_start")
+    if positions is not None:
+        _same_len(positions, slot_map.numel(), "positions")
+    i32 = torch.int32
+    _check(lib.se_block_tables_extend(_ptr(free_pages, i32, "free_pages"), _ptr(pool_state, i32, "pool_state"),
+                                      free_pages.numel(), _ptr(block_table, i32, "block_table"), block_table.shape[1],
+                                      _ptr(seq_lens, i32, "seq_lens"), _ptr(new_lens, i32, "new_lens"), batch,
+                                      _ptr(seq_lens_after, i32, "seq_lens_after"),
+                                      _ptr(token_start, i32, "token_start"), _ptr(slot_map, i32, "slot_map"),
+                                      _ptr(positions, i32, "positions"), slot_map.numel(), _stream(stream)))
+
+
+def se_block_tables_release(free_pages, pool_state, block_table, seq_lens, keep_lens=None, stream=None):
+    """The pages of the tokens behind keep_lens[b] (None: of every token) back to the pool."""
+    lib = load_library()
+    batch = block_table.shape[0]
+    _on_current_device(free_pages, pool_state, block_table, seq_lens, keep_lens)
+    _same_len(pool_state, 4, "pool_state")
+    _same_len(seq_lens, batch, "seq_lens")
+    if keep_lens is not None:
+        _same_len(keep_lens, batch, "keep_lens")
+    i32 = torch.int32
+    _check(lib.se_block_tables_release(_ptr(free_pages, i32, "free_pages"), _ptr(pool_state, i32, "pool_state"),
+                                       free_pages.numel(), _ptr(block_table, i32, "block_table"),
+                                       block_table.shape[1], _ptr(seq_lens, i32, "seq_lens"),
+                                       _ptr(keep_lens, i32, "keep_lens"), batch, _stream(stream)))
+
+
+def se_paged_kv_store(kv: SEPagedKV, k_new, v_new, slot_map, stream=None):
+    """The rows k_new and v_new [T][Hkv][D] (tokens any stride apart; v_new None for a latent cache) of
+    slot_map.numel() new tokens into their slots; with a summary in ``kv``, its pages' bounds too."""
+    lib = load_library()
+    _on_current_device(k_new, v_new, slot_map)
+    tokens = slot_map.numel()
+    kp, ks = _rows_ptr(k_new, kv.num_kv_heads, kv.head_dim, torch.bfloat16, "k_new")
+    vp, vs = (None, 0) if v_new is None else _rows_ptr(v_new, kv.num_kv_heads, kv.head_dim_v, torch.bfloat16, "v_new")
+    if k_new.shape[0] != tokens or (v_new is not None and v_new.shape[0] != tokens):
+        raise ValueError("k_new, v_new and slot_map differ in tokens")
+    _check(lib.se_paged_kv_store(ctypes.byref(kv), kp, ks, vp, vs, _ptr(slot_map, torch.int32, "slot_map"), tokens,
+                                 _stream(stream)))
+
+
+def se_paged_decode_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                   head_dim_v: int) -> int:
+    """Bytes of se_paged_decode's workspace, whatever the lengths (0: shape not supported)."""
+    return int(load_library().se_paged_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, head_dim_v))
+
+
+def se_paged_decode(kv: SEPagedKV, q, block_table, seq_lens, sm_scale: float, out, out_lse, workspace,
+                    sink_tokens: int = 0, recent_tokens: int = 0, stream=None):
+    """Attention of one new token per request over its cached tokens (all of them, or with
+    ``recent_tokens`` the first ``sink_tokens`` and the last ``recent_tokens``): q [B][Hq][D] (requests any
+    stride apart) -> out [B][Hq][Dv], out_lse [B][Hq] or None. ``workspace``: uint8, zeroed once."""
+    lib = load_library()
+    _on_current_device(q, block_table, seq_lens, out, out_lse, workspace)
+    if q.dim() != 3:
+        raise ValueError("q: expected [batch][num_q_heads][head_dim]")
+    batch, hq = q.shape[0], q.shape[1]
+    qp, qs = _rows_ptr(q, hq, kv.head_dim, torch.bfloat16, "q")
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError("block_table: expected [batch][pages]")
+    _same_len(seq_lens, batch, "seq_lens")
+    _same_len(out, batch * hq * kv.head_dim_v, "out")
+    if out_lse is not None:
+        _same_len(out_lse, batch * hq, "out_lse")
+    _check(lib.se_paged_decode(ctypes.byref(kv), qp, qs, hq, _ptr(block_table, torch.int32, "block_table"),
+                               block_table.shape[1], _ptr(seq_lens, torch.int32, "seq_lens"), batch, int(sink_tokens),
+                               int(recent_tokens), float(sm_scale), _ptr(out, torch.bfloat16, "out"),
+                               _ptr(out_lse, torch.float32, "out_lse"), _ptr(workspace, torch.uint8, "workspace"),
+                               0 if workspace is None else workspace.numel(), _stream(stream)))
 
 
 # ---------------------------------------------------------------- SnapKV

@@ -128,8 +128,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 int pages_of(long long tokens) { return (int)((tokens + se::kPageSize - 1) / se::kPageSize); }
 
-// Common checks of a paged cache view.
-se_status_t check_kv(const char* fn, const se_paged_kv_t* kv, bool need_summary) {
+// Checks of a paged cache view's pointers, sizes and strides, whatever the head dims.
+se_status_t check_kv_layout(const char* fn, const se_paged_kv_t* kv, bool need_summary) {
   if (!kv) return fail(SE_ERR_INVALID_ARG, fn, "kv is NULL");
   if (!kv->k || !kv->v) return fail(SE_ERR_INVALID_ARG, fn, "kv->k / kv->v is NULL");
   if (need_summary && !kv->summary) return fail(SE_ERR_INVALID_ARG, fn, "kv->summary is NULL");
@@ -144,6 +144,13 @@ se_status_t check_kv(const char* fn, const se_paged_kv_t* kv, bool need_summary)
     return fail(SE_ERR_INVALID_ARG, fn, "row strides must cover the head dims and be multiples of 8");
   if ((long long)kv->num_pages * kv->num_kv_heads * se::kPageSize >= (1ll << 31))
     return fail(SE_ERR_UNSUPPORTED, fn, "cache holds 2^31 or more token rows");
+  return SE_OK;
+}
+
+// Common checks of the Quest and SnapKV calls' cache view.
+se_status_t check_kv(const char* fn, const se_paged_kv_t* kv, bool need_summary) {
+  const se_status_t st = check_kv_layout(fn, kv, need_summary);
+  if (st != SE_OK) return st;
   if (kv->head_dim != 128 && kv->head_dim != 576) return fail(SE_ERR_UNSUPPORTED, fn, "head_dim must be 128 or 576");
   return SE_OK;
 }
@@ -750,3 +757,133 @@ se_status_t check_decode_call(const char* fn, const se_paged_kv_t* kv, const voi
 }
 
 }  // namespace se
+
+// ------------------------------------------------ page pool, row store, dense paged decode
+extern "C" {
+
+se_status_t se_block_tables_extend(const int32_t* free_pages, int32_t* pool_state, int32_t num_pages,
+                                   int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
+                                   const int32_t* new_lens, int32_t batch, int32_t* seq_lens_after,
+                                   int32_t* token_start, int32_t* slot_map, int32_t* positions,
+                                   int32_t max_new_tokens, void* stream) {
+  static const char* fn = "se_block_tables_extend";
+  if (batch < 0 || max_new_tokens < 0 || num_pages < 0 || bt_stride < 1)
+    return fail(SE_ERR_INVALID_ARG, fn, "negative size or bt_stride < 1");
+  if (!pool_state || !token_start || (num_pages > 0 && !free_pages) || (max_new_tokens > 0 && !slot_map) ||
+      (batch > 0 && (!block_table || !seq_lens || !new_lens || !seq_lens_after)))
+    return fail(SE_ERR_INVALID_ARG, fn, "NULL pointer");
+  if (!aligned16(free_pages) || !aligned16(pool_state) || !aligned16(block_table) || !aligned16(seq_lens) ||
+      !aligned16(new_lens) || !aligned16(seq_lens_after) || !aligned16(token_start) || !aligned16(slot_map) ||
+      !aligned16(positions))
+    return fail(SE_ERR_INVALID_ARG, fn, "pointers must be 16-byte aligned");
+  if (batch > se::block_tables_max_batch()) return fail(SE_ERR_UNSUPPORTED, fn, "batch > 16384");
+  if (num_pages >= (1 << 27) || bt_stride >= (1 << 27))
+    return fail(SE_ERR_UNSUPPORTED, fn, "2^27 or more pages (slots are 32-bit)");
+  DeviceInfo* d = nullptr;
+  cudaError_t e = current_device(&d);
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  e = se::launch_block_tables_extend(free_pages, pool_state, num_pages, block_table, bt_stride, seq_lens, new_lens,
+                                     batch, seq_lens_after, token_start, slot_map, positions, max_new_tokens,
+                                     d->sm_count, d->err, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SE_OK : cuda_fail(fn, e);
+}
+
+se_status_t se_block_tables_release(int32_t* free_pages, int32_t* pool_state, int32_t num_pages,
+                                    const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
+                                    const int32_t* keep_lens, int32_t batch, void* stream) {
+  static const char* fn = "se_block_tables_release";
+  if (batch < 0 || num_pages < 0 || bt_stride < 1)
+    return fail(SE_ERR_INVALID_ARG, fn, "negative size or bt_stride < 1");
+  if (!pool_state || (num_pages > 0 && !free_pages) || (batch > 0 && (!block_table || !seq_lens)))
+    return fail(SE_ERR_INVALID_ARG, fn, "NULL pointer");
+  if (!aligned16(free_pages) || !aligned16(pool_state) || !aligned16(block_table) || !aligned16(seq_lens) ||
+      !aligned16(keep_lens))
+    return fail(SE_ERR_INVALID_ARG, fn, "pointers must be 16-byte aligned");
+  if (batch > se::block_tables_max_batch()) return fail(SE_ERR_UNSUPPORTED, fn, "batch > 16384");
+  if (num_pages >= (1 << 27) || bt_stride >= (1 << 27))
+    return fail(SE_ERR_UNSUPPORTED, fn, "2^27 or more pages (slots are 32-bit)");
+  if (batch == 0) return SE_OK;
+  DeviceInfo* d = nullptr;
+  cudaError_t e = current_device(&d);
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  e = se::launch_block_tables_release(free_pages, pool_state, num_pages, block_table, bt_stride, seq_lens, keep_lens,
+                                      batch, d->sm_count, d->err, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SE_OK : cuda_fail(fn, e);
+}
+
+se_status_t se_paged_kv_store(const se_paged_kv_t* kv, const void* k_new, int64_t k_stride, const void* v_new,
+                              int64_t v_stride, const int32_t* slot_map, int32_t num_tokens, void* stream) {
+  static const char* fn = "se_paged_kv_store";
+  se_status_t st = check_kv_layout(fn, kv, false);
+  if (st != SE_OK) return st;
+  if (kv->head_dim > 576 || kv->head_dim_v > 576) return fail(SE_ERR_UNSUPPORTED, fn, "head dims up to 576");
+  if (num_tokens < 0) return fail(SE_ERR_INVALID_ARG, fn, "num_tokens < 0");
+  const bool latent = kv->v == kv->k;
+  if (latent && v_new) return fail(SE_ERR_INVALID_ARG, fn, "v_new must be NULL when kv->v == kv->k");
+  if (num_tokens == 0) return SE_OK;
+  if (!k_new || !slot_map) return fail(SE_ERR_INVALID_ARG, fn, "k_new/slot_map NULL");
+  if (!latent && !v_new) return fail(SE_ERR_INVALID_ARG, fn, "v_new NULL for a separate value cache");
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(slot_map))
+    return fail(SE_ERR_INVALID_ARG, fn, "pointers must be 16-byte aligned");
+  if (k_stride < (int64_t)kv->num_kv_heads * kv->head_dim || (k_stride % 8) ||
+      (!latent && (v_stride < (int64_t)kv->num_kv_heads * kv->head_dim_v || (v_stride % 8))))
+    return fail(SE_ERR_INVALID_ARG, fn, "token strides must cover the heads' rows and be multiples of 8");
+  DeviceInfo* d = nullptr;
+  cudaError_t e = current_device(&d);
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  e = se::launch_kv_store(view_of(kv), static_cast<uint16_t*>(kv->k), static_cast<uint16_t*>(kv->v),
+                          static_cast<const uint16_t*>(k_new), k_stride, static_cast<const uint16_t*>(v_new), v_stride,
+                          slot_map, num_tokens, d->err, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SE_OK : cuda_fail(fn, e);
+}
+
+size_t se_paged_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                      int32_t head_dim_v) {
+  if (batch < 0 || num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads) return 0;
+  if (!se::paged_decode_supported(num_kv_heads, head_dim, head_dim_v, num_q_heads, head_dim != head_dim_v)) return 0;
+  return round16(se::paged_decode_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim_v));
+}
+
+se_status_t se_paged_decode(const se_paged_kv_t* kv, const void* q, int64_t q_stride, int32_t num_q_heads,
+                            const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens, int32_t batch,
+                            int32_t sink_tokens, int32_t recent_tokens, float sm_scale, void* out, float* out_lse,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  static const char* fn = "se_paged_decode";
+  se_status_t st = check_kv_layout(fn, kv, false);
+  if (st != SE_OK) return st;
+  if (batch < 0) return fail(SE_ERR_INVALID_ARG, fn, "batch < 0");
+  if (num_q_heads < 1 || num_q_heads % kv->num_kv_heads)
+    return fail(SE_ERR_INVALID_ARG, fn, "num_q_heads must be a positive multiple of num_kv_heads");
+  if (!se::paged_decode_supported(kv->num_kv_heads, kv->head_dim, kv->head_dim_v, num_q_heads, kv->v == kv->k))
+    return fail(SE_ERR_UNSUPPORTED, fn,
+                "head_dim = head_dim_v of 64, 128 or 256 with separate K and V and <= 64 query heads per KV head, or "
+                "a 576/512 latent cache with 16..64 query heads");
+  if (sink_tokens < 0 || recent_tokens < 0) return fail(SE_ERR_INVALID_ARG, fn, "negative window");
+  if (sink_tokens > 0 && recent_tokens == 0)
+    return fail(SE_ERR_INVALID_ARG, fn, "sink_tokens without recent_tokens (0 keeps every token)");
+  if (!std::isfinite(sm_scale)) return fail(SE_ERR_INVALID_ARG, fn, "sm_scale not finite");
+  if (q_stride < (int64_t)num_q_heads * kv->head_dim || (q_stride % 8))
+    return fail(SE_ERR_INVALID_ARG, fn, "q_stride must cover the heads and be a multiple of 8");
+  if (bt_stride < 1) return fail(SE_ERR_INVALID_ARG, fn, "bt_stride < 1");
+  if (bt_stride >= (1 << 27)) return fail(SE_ERR_UNSUPPORTED, fn, "2^27 or more pages per request");
+  if (batch > 16384) return fail(SE_ERR_UNSUPPORTED, fn, "batch > 16384");
+  if (batch == 0) return SE_OK;
+  if (!q || !block_table || !seq_lens || !out) return fail(SE_ERR_INVALID_ARG, fn, "NULL pointer");
+  if (!aligned16(q) || !aligned16(block_table) || !aligned16(seq_lens) || !aligned16(out) || !aligned16(out_lse) ||
+      !aligned16(workspace))
+    return fail(SE_ERR_INVALID_ARG, fn, "pointers must be 16-byte aligned");
+  if (workspace_bytes <
+      se::paged_decode_workspace_bytes(batch, num_q_heads, kv->num_kv_heads, kv->head_dim_v))
+    return fail(SE_ERR_WORKSPACE, fn, "workspace too small");
+  if (!workspace) return fail(SE_ERR_INVALID_ARG, fn, "workspace NULL");
+  DeviceInfo* d = nullptr;
+  cudaError_t e = current_device(&d);
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  e = se::launch_paged_decode(view_of(kv), static_cast<const uint16_t*>(q), q_stride, num_q_heads, block_table,
+                              bt_stride, seq_lens, batch, sink_tokens, recent_tokens, sm_scale,
+                              static_cast<uint16_t*>(out), out_lse, workspace, d->sm_count, d->err,
+                              static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SE_OK : cuda_fail(fn, e);
+}
+
+}  // extern "C"

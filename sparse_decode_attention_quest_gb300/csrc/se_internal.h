@@ -149,6 +149,31 @@ cudaError_t launch_snapkv_gather(const KvView& src, uint16_t* dk, uint16_t* dv, 
                                  int32_t dst_bt_stride, const int32_t* lens, int32_t batch, const int32_t* kept,
                                  int32_t kept_stride, const int32_t* kept_counts, unsigned* err, cudaStream_t stream);
 
+// ---- block_tables.cu: page pool, block tables and slot maps
+int block_tables_max_batch();
+cudaError_t launch_block_tables_extend(const int32_t* free_pages, int32_t* pool_state, int32_t num_pages,
+                                       int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
+                                       const int32_t* new_lens, int32_t batch, int32_t* seq_lens_after,
+                                       int32_t* token_start, int32_t* slot_map, int32_t* positions,
+                                       int32_t max_new_tokens, int sm_count, unsigned* err, cudaStream_t stream);
+cudaError_t launch_block_tables_release(int32_t* free_pages, int32_t* pool_state, int32_t num_pages,
+                                        const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
+                                        const int32_t* keep_lens, int32_t batch, int sm_count, unsigned* err,
+                                        cudaStream_t stream);
+
+// ---- kv_store.cu: rows of new tokens into their slots (+ summaries when kv.summary is set)
+cudaError_t launch_kv_store(const KvView& kv, uint16_t* k_mut, uint16_t* v_mut, const uint16_t* k_new,
+                            long long k_stride, const uint16_t* v_new, long long v_stride, const int32_t* slot_map,
+                            int32_t num_tokens, unsigned* err, cudaStream_t stream);
+
+// ---- paged_decode.cu: one new token over the whole cache, or over a sink and a recent window
+bool paged_decode_supported(int num_kv_heads, int head_dim, int head_dim_v, int num_q_heads, bool latent);
+size_t paged_decode_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim_v);
+cudaError_t launch_paged_decode(const KvView& kv, const uint16_t* q, long long q_stride, int32_t num_q_heads,
+                                const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens, int32_t batch,
+                                int32_t sink_tokens, int32_t recent_tokens, float sm_scale, uint16_t* out,
+                                float* out_lse, void* workspace, int sm_count, unsigned* err, cudaStream_t stream);
+
 // ---- api.cu: per-device context and helpers shared with other entry points
 cudaError_t device_context(int* sm_count, unsigned** err);
 void set_error_detail(const char* fn, const char* what);
