@@ -3,6 +3,7 @@
 // tensor-map encoding for the TMA copies, and dispatch to the kernels.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -840,8 +841,10 @@ se_status_t se_paged_kv_store(const se_paged_kv_t* kv, const void* k_new, int64_
 size_t se_paged_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                       int32_t head_dim_v) {
   if (batch < 0 || num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads) return 0;
-  if (!se::paged_decode_supported(num_kv_heads, head_dim, head_dim_v, num_q_heads, head_dim != head_dim_v)) return 0;
-  return round16(se::paged_decode_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim_v));
+  if (se::paged_latent_supported(num_kv_heads, head_dim, head_dim_v, num_q_heads))
+    return round16(se::paged_latent_workspace_bytes(batch, num_q_heads));
+  if (!se::paged_decode_supported(num_kv_heads, head_dim, head_dim_v, num_q_heads)) return 0;
+  return round16(se::paged_decode_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim));
 }
 
 se_status_t se_paged_decode(const se_paged_kv_t* kv, const void* q, int64_t q_stride, int32_t num_q_heads,
@@ -854,7 +857,9 @@ se_status_t se_paged_decode(const se_paged_kv_t* kv, const void* q, int64_t q_st
   if (batch < 0) return fail(SE_ERR_INVALID_ARG, fn, "batch < 0");
   if (num_q_heads < 1 || num_q_heads % kv->num_kv_heads)
     return fail(SE_ERR_INVALID_ARG, fn, "num_q_heads must be a positive multiple of num_kv_heads");
-  if (!se::paged_decode_supported(kv->num_kv_heads, kv->head_dim, kv->head_dim_v, num_q_heads, kv->v == kv->k))
+  const bool latent = kv->v == kv->k;
+  if (latent ? !se::paged_latent_supported(kv->num_kv_heads, kv->head_dim, kv->head_dim_v, num_q_heads)
+             : !se::paged_decode_supported(kv->num_kv_heads, kv->head_dim, kv->head_dim_v, num_q_heads))
     return fail(SE_ERR_UNSUPPORTED, fn,
                 "head_dim = head_dim_v of 64, 128 or 256 with separate K and V and <= 64 query heads per KV head, or "
                 "a 576/512 latent cache with 16..64 query heads");
@@ -866,21 +871,34 @@ se_status_t se_paged_decode(const se_paged_kv_t* kv, const void* q, int64_t q_st
     return fail(SE_ERR_INVALID_ARG, fn, "q_stride must cover the heads and be a multiple of 8");
   if (bt_stride < 1) return fail(SE_ERR_INVALID_ARG, fn, "bt_stride < 1");
   if (bt_stride >= (1 << 27)) return fail(SE_ERR_UNSUPPORTED, fn, "2^27 or more pages per request");
-  if (batch > 16384) return fail(SE_ERR_UNSUPPORTED, fn, "batch > 16384");
+  if (batch > se::paged_decode_max_batch()) return fail(SE_ERR_UNSUPPORTED, fn, "batch > 4096");
   if (batch == 0) return SE_OK;
   if (!q || !block_table || !seq_lens || !out) return fail(SE_ERR_INVALID_ARG, fn, "NULL pointer");
   if (!aligned16(q) || !aligned16(block_table) || !aligned16(seq_lens) || !aligned16(out) || !aligned16(out_lse) ||
       !aligned16(workspace))
     return fail(SE_ERR_INVALID_ARG, fn, "pointers must be 16-byte aligned");
-  if (workspace_bytes <
-      se::paged_decode_workspace_bytes(batch, num_q_heads, kv->num_kv_heads, kv->head_dim_v))
+  if (workspace_bytes < (latent ? se::paged_latent_workspace_bytes(batch, num_q_heads)
+                                : se::paged_decode_workspace_bytes(batch, num_q_heads, kv->num_kv_heads, kv->head_dim)))
     return fail(SE_ERR_WORKSPACE, fn, "workspace too small");
   if (!workspace) return fail(SE_ERR_INVALID_ARG, fn, "workspace NULL");
   DeviceInfo* d = nullptr;
   cudaError_t e = current_device(&d);
   if (e != cudaSuccess) return cuda_fail(fn, e);
-  e = se::launch_paged_decode(view_of(kv), static_cast<const uint16_t*>(q), q_stride, num_q_heads, block_table,
-                              bt_stride, seq_lens, batch, sink_tokens, recent_tokens, sm_scale,
+  const long long rows = std::max(1ll, (long long)kv->num_pages * kv->num_kv_heads * se::kPageSize);
+  if (latent) {
+    e = se::launch_paged_latent(view_of(kv), static_cast<const uint16_t*>(q), q_stride, num_q_heads, block_table,
+                                bt_stride, seq_lens, batch, sink_tokens, recent_tokens, sm_scale,
+                                static_cast<uint16_t*>(out), out_lse, workspace, d->sm_count, d->err,
+                                static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SE_OK : cuda_fail(fn, e);
+  }
+  const int box = se::kPageSize * se::paged_decode_box_heads(kv->num_kv_heads, num_q_heads, kv->head_dim);
+  CUtensorMap kmap, vmap;
+  if (!encode_row_chunks_map(&kmap, kv->k, rows, kv->row_stride_k, kv->head_dim / 64, box) ||
+      !encode_row_chunks_map(&vmap, kv->v, rows, kv->row_stride_v, kv->head_dim / 64, box))
+    return fail(SE_ERR_CUDA, fn, "cuTensorMapEncodeTiled failed");
+  e = se::launch_paged_decode(kmap, vmap, view_of(kv), static_cast<const uint16_t*>(q), q_stride, num_q_heads,
+                              block_table, bt_stride, seq_lens, batch, sink_tokens, recent_tokens, sm_scale,
                               static_cast<uint16_t*>(out), out_lse, workspace, d->sm_count, d->err,
                               static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SE_OK : cuda_fail(fn, e);

@@ -1,24 +1,72 @@
 // Attention of one new token per request over its whole paged cache, or over
 // its first sink and last recent tokens (SparseEngine: Sparse-First Inference
 // Engine, Table 7: logit z and weight alpha over the history, the current token
-// included; Tables 9-12: sink and recent tokens).
+// included; Tables 9-12: sink and recent tokens), for head dims 64, 128 and 256.
 //
 //     z_j = sm_scale q . k_j over the kept positions j < L,
 //     out = sum_j exp(z_j - m) v_j / l,  l = sum_j exp(z_j - m),  lse = m + log l,
-// in one pass with a running maximum m and sum l. One CTA per (request, query head).
+// in one pass over K and V with a running maximum m and sum l. Every kept K and V
+// row is read once and serves all query heads of its KV head, a few flops per
+// byte: the floor is the time of those bytes from HBM, and the design is about
+// keeping copies in flight.
+//
+//  * Work: the kept pages of (request, KV head group) items, one after another,
+//    form one range, which the CTAs (one per SM) share equally: ragged lengths
+//    balance, and a single long request spreads over every SM. An item that
+//    spans CTAs leaves a partial (output, log-sum-exp) per CTA; a CTA has at
+//    most two, for the item it starts inside and the item it ends inside, so
+//    the workspace does not grow with the lengths. The CTA that publishes an
+//    item's last partial merges them in the order of the pages.
+//  * Copies: a page's rows of one KV head are 16 x D bf16, and the heads of a
+//    group of Hc lie next to each other, so that one TMA box of 64 dims x
+//    16 Hc rows x D / 64 brings a whole page of the group (16 to 32 KB for 4 to 8
+//    heads). One warp issues them into a ring of five 32 KB slots, K and V of a
+//    step in turn, 128-byte swizzled.
+//  * Products: a consumer warp holds one (KV head, 16 query rows) state; R warps
+//    share the pages of a step when the heads do not fill the warps. S = Q K^T
+//    and O += P V are m16n8k16 bf16 MMAs with fp32 accumulators; a group of
+//    G <= 16 query heads wastes rows of the tile, which does not matter at a few
+//    flops per byte.
+//  * Rows that are not kept: their logits become -inf, and their value rows are
+//    zeroed in shared memory first, since 0 * NaN is not 0.
 #include "se_ptx.cuh"
 
 namespace se {
 namespace {
 
-constexpr int kThreads = 128;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kSlots = 5;
+constexpr int kSlotBytes = 32 * 1024;
+constexpr int kMetaRing = 4;     // steps whose page masks are held (at most three are in flight)
+constexpr int kMaxPages = 16;    // pages of a step
+constexpr int kMaxCtas = 192;    // partial slots: two per CTA
+constexpr int kMaxBatch = 4096;  // requests whose prefix fits beside the ring
+
+template <int kD>
+struct Cfg {
+  static constexpr int kWarps = kD == 256 ? 4 : 8;  // consumers
+  static constexpr int kConsumers = kWarps * 32;
+  static constexpr int kThreads = kConsumers + 32;
+  static constexpr int kChunks = kD / 64;
+  static constexpr int kBlocks = kSlotBytes / (kPageSize * kD * 2);  // (page, head) blocks of a slot
+  static constexpr int kStageFloats = kWarps * 8 * kD;               // eight rows of every warp's state
+  static constexpr int kFixed = 1024 + kSlots * kSlotBytes + kStageFloats * 4 + kWarps * 32 * 4 +
+                                kMetaRing * kMaxPages * 4 + 2 * kSlots * 8 + 64;
+};
 
 struct PagedArgs {
-  KvView kv;
   const uint16_t* q;
   long long q_stride;
   int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t group;        // query heads per KV head
+  int32_t heads;        // KV heads of an item (Hc)
+  int32_t head_groups;  // items per request
+  int32_t mtiles;       // 16-row query tiles per KV head
+  int32_t replicas;     // warps that share a (head, tile)
+  int32_t step_pages;   // pages of a step
+  int32_t num_pages;
+  int32_t batch;
   const int32_t* block_table;
   int32_t bt_stride;
   const int32_t* seq_lens;
@@ -26,87 +74,596 @@ struct PagedArgs {
   float scale_log2;
   uint16_t* out;
   float* out_lse;
+  float* o_part;        // [2 * CTAs][heads * group][D]
+  float* lse_part;      // [2 * CTAs][heads * group], log2 domain
+  uint32_t* arrivals;   // [batch * head_groups], zero between calls
   unsigned* err;
 };
 
-__global__ void __launch_bounds__(kThreads) paged_decode_kernel(const PagedArgs a) {
-  pdl_enter();
-  __shared__ float qs[576], sc[kPageSize];
-  const int b = blockIdx.x / a.num_q_heads, hq = blockIdx.x % a.num_q_heads;
-  const int H = a.kv.num_kv_heads, h = hq / (a.num_q_heads / H), D = a.kv.head_dim, Dv = a.kv.head_dim_v;
+// The kept pages of a request: logical pages 0 .. sink_pages - 1, then recent_page .. (all pages: sink_pages = n).
+struct Kept {
+  int len;          // tokens (clipped)
+  int from;         // kept: j < sink or j >= from
+  int n;            // kept pages
+  int sink_pages;
+  int recent_page;
+  __device__ __forceinline__ int logical(int i) const { return i < sink_pages ? i : i - sink_pages + recent_page; }
+};
+
+__device__ __forceinline__ Kept kept_of(int L, int bt_stride, int sink, int recent, unsigned* err) {
+  Kept k;
+  if (L < 0 || L > (long long)bt_stride * kPageSize) {
+    raise_error(err, SE_DEVERR_LENGTH);
+    L = L < 0 ? 0 : bt_stride * kPageSize;
+  }
+  k.len = L;
+  const int pages = L / kPageSize + (L % kPageSize != 0);
+  k.from = recent > 0 && L > recent ? L - recent : 0;
+  const int sp = sink / kPageSize + (sink % kPageSize != 0), rp = k.from / kPageSize;
+  if (k.from <= sink || sp > rp) {  // no page is left out
+    k.n = k.sink_pages = pages;
+    k.recent_page = pages;
+    if (k.from <= sink) k.from = 0;
+  } else {
+    k.sink_pages = sp;
+    k.recent_page = rp;
+    k.n = sp + pages - rp;
+  }
+  return k;
+}
+
+// Segments of a CTA's slice: the pages [lo, hi) of item (b, hg).
+struct Segment {
+  const int* prefix;
+  int groups, end, x;  // x: the slice position after the segment
+  int b, hg, lo, hi, n, item_start;
+  __device__ __forceinline__ void init(const int* pf, int batch, int hgs, int start, int stop) {
+    prefix = pf;
+    groups = hgs;
+    end = stop;
+    x = start;
+    int l = 0, h = batch;
+    while (h - l > 1) {
+      const int mid = (l + h) >> 1;
+      if (prefix[mid] * groups <= start) l = mid; else h = mid;
+    }
+    b = l;
+  }
+  __device__ __forceinline__ bool next() {
+    if (x >= end) return false;
+    while (prefix[b + 1] * groups <= x) ++b;
+    n = prefix[b + 1] - prefix[b];
+    const int rel = x - prefix[b] * groups;
+    hg = rel / n;
+    lo = rel - hg * n;
+    hi = min(n, lo + end - x);
+    item_start = x - lo;
+    x += hi - lo;
+    return true;
+  }
+};
+
+// Which of a page's 16 tokens are kept: t < hi and (t < a or t >= z), packed as hi | a << 8 | z << 16.
+__device__ __forceinline__ uint32_t page_mask(const Kept& k, int sink, int page) {
+  const int j0 = page * kPageSize;
+  const int hi = min(kPageSize, k.len - j0);
+  const int a = k.from == 0 ? kPageSize : max(0, min(kPageSize, sink - j0));
+  const int z = max(0, min(kPageSize, k.from - j0));
+  return (uint32_t)hi | (uint32_t)a << 8 | (uint32_t)z << 16;
+}
+__device__ __forceinline__ bool in_mask(uint32_t m, int t) {
+  return t < (int)(m & 0xff) && (t < (int)(m >> 8 & 0xff) || t >= (int)(m >> 16));
+}
+__device__ __forceinline__ bool mask_is_full(uint32_t m) {
+  return (m & 0xff) == kPageSize && ((m >> 8 & 0xff) == kPageSize || (m >> 16) == 0);
+}
+
+// Kept pages per request and their exclusive prefix (prefix[batch]: the total), by the whole CTA.
+template <int kThreads>
+__device__ __forceinline__ void kept_prefix(const PagedArgs& a, int* prefix, long long* sums) {
+  constexpr int kWarps = kThreads / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int c = threadIdx.x; c < D; c += kThreads)
-    qs[c] = __uint_as_float((uint32_t)a.q[(size_t)b * a.q_stride + (size_t)hq * D + c] << 16);
-  int L = a.seq_lens[b];
-  if (L < 0 || L > (long long)a.bt_stride * kPageSize) {
-    if (threadIdx.x == 0) raise_error(a.err, SE_DEVERR_LENGTH);
-    L = L < 0 ? 0 : a.bt_stride * kPageSize;
+  // Positions are 32-bit: requests beyond that many pages are reported and cut short.
+  const long long most = 0x7fffffff / a.head_groups;
+  long long at = 0;
+  for (int base = 0; base < a.batch; base += kThreads) {
+    const int b = base + threadIdx.x;
+    int n = b < a.batch ? kept_of(a.seq_lens[b], a.bt_stride, a.sink, a.recent, a.err).n : 0;
+    long long incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    long long before = at, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sums[w];
+      all += sums[w];
+    }
+    __syncthreads();
+    incl += before;
+    if (b < a.batch) {
+      if (incl > most) raise_error(a.err, SE_DEVERR_LENGTH);
+      prefix[b + 1] = (int)(incl < most ? incl : most);
+    }
+    at += all;
   }
-  const int lo = a.recent > 0 ? max(0, L - a.recent) : 0;  // kept: j < sink or j >= lo
+  if (threadIdx.x == 0) prefix[0] = 0;
   __syncthreads();
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int p = 0; p * kPageSize < L; ++p) {
-    if (p * kPageSize >= a.sink && (p + 1) * kPageSize <= lo) continue;
-    const int phys = a.block_table[(size_t)b * a.bt_stride + p];
-    if (phys < 0 || phys >= a.kv.num_pages) {
-      if (threadIdx.x == 0) raise_error(a.err, SE_DEVERR_PAGE_RANGE);
-      continue;
-    }
-    const size_t row0 = ((size_t)phys * H + h) * kPageSize;
-    for (int i = warp; i < kPageSize; i += kThreads / 32) {
-      const int j = p * kPageSize + i;
-      const bool kept = j < L && (j < a.sink || j >= lo);
-      float s = 0.f;
-      if (kept)
-        for (int c = lane; c < D; c += 32)
-          s += qs[c] * __uint_as_float((uint32_t)a.kv.k[(row0 + i) * a.kv.row_stride_k + c] << 16);
-      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      if (lane == 0) sc[i] = kept ? s * a.scale_log2 : -INFINITY;
-    }
-    __syncthreads();
-    float n = m;
-    for (int i = 0; i < kPageSize; ++i) n = fmaxf(n, sc[i]);
-    const float base = n == -INFINITY ? 0.f : n, f = exp2f(m - base);
-    m = n;
-    l *= f;
-    for (int k = 0; k < 4; ++k) o[k] *= f;
-    for (int i = 0; i < kPageSize; ++i) {
-      const int j = p * kPageSize + i;
-      if (!(j < L && (j < a.sink || j >= lo))) continue;
-      const float w = exp2f(sc[i] - base);
-      l += w;
-      for (int k = 0, d = threadIdx.x; d < Dv; ++k, d += kThreads)
-        o[k] += w * __uint_as_float((uint32_t)a.kv.v[(row0 + i) * a.kv.row_stride_v + d] << 16);
-    }
-    __syncthreads();
+}
+
+template <int kD>
+__global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
+                                                                           const __grid_constant__ CUtensorMap vmap,
+                                                                           const PagedArgs a) {
+  using C = Cfg<kD>;
+  pdl_enter();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* stage = reinterpret_cast<float*>(ring + kSlots * kSlotBytes);  // [warps][8][D]
+  float* ml = stage + C::kStageFloats;                                  // [warps][(m, l)][16]
+  uint32_t* meta = reinterpret_cast<uint32_t*>(ml + C::kWarps * 32);    // [kMetaRing][kMaxPages]
+  uint64_t* full = reinterpret_cast<uint64_t*>(meta + kMetaRing * kMaxPages);
+  uint64_t* empty = full + kSlots;
+  int* flags = reinterpret_cast<int*>(empty + kSlots);  // [4]
+  int* prefix = flags + 4;                              // [batch + 1]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int heads = a.heads, G = a.group, rows = heads * G, HG = a.head_groups, Pg = a.step_pages;
+  const int combos = heads * a.mtiles, active = combos * a.replicas;
+
+  kept_prefix<C::kThreads>(a, prefix, reinterpret_cast<long long*>(stage));
+  // Requests without a kept token: the empty sum.
+  for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+    if (prefix[b + 1] != prefix[b]) continue;
+    const size_t r0 = (size_t)b * a.num_q_heads;
+    uint4* o = reinterpret_cast<uint4*>(a.out + r0 * kD);
+    for (int i = threadIdx.x; i < a.num_q_heads * kD / 8; i += C::kThreads) o[i] = make_uint4(0, 0, 0, 0);
+    if (a.out_lse)
+      for (int i = threadIdx.x; i < a.num_q_heads; i += C::kThreads) a.out_lse[r0 + i] = -INFINITY;
   }
-  const size_t row = (size_t)b * a.num_q_heads + hq;
-  const bool empty = l == 0.f;
-  for (int k = 0, d = threadIdx.x; d < Dv; ++k, d += kThreads)
-    a.out[row * Dv + d] = (uint16_t)(pack_bf16x2(empty ? 0.f : o[k] / l, 0.f) & 0xffffu);
-  if (a.out_lse && threadIdx.x == 0) a.out_lse[row] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
+  const int total = prefix[a.batch] * HG;
+  // Equal slices in whole steps, two steps at least.
+  int per_cta = (int)(((long long)total + gridDim.x - 1) / gridDim.x);
+  per_cta = max(2 * Pg, (per_cta + Pg - 1) / Pg * Pg);
+  const long long start64 = (long long)blockIdx.x * per_cta;
+  if (start64 >= total) return;
+  const int start = (int)start64, end = min((long long)total, start64 + per_cta);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], active);
+    }
+    mbar_fence_init();
+  }
+  __syncthreads();
+  Segment seg;
+  seg.init(prefix, a.batch, HG, start, end);
+  bool dead = false;  // a bounded wait gave up: no further waits or products, but every barrier
+
+  if (warp == C::kWarps) {
+    // ------------------------------------------------------------ TMA producer
+    const uint64_t policy = l2_evict_first_policy();
+    const uint32_t page_bytes = (uint32_t)heads * kPageSize * kD * 2;
+    int j = 0, step = 0;
+    while (!dead && seg.next()) {
+      const Kept k = kept_of(a.seq_lens[seg.b], a.bt_stride, a.sink, a.recent, nullptr);
+      const int32_t* bt = a.block_table + (size_t)seg.b * a.bt_stride;
+      auto entry = [&](int i) { return i < seg.hi ? bt[k.logical(i)] : -1; };
+      // Two windows of 32 table entries, one per lane: the second is loaded while the first is copied.
+      int base = seg.lo, cur = entry(base + lane), nxt = entry(base + 32 + lane);
+      for (int i0 = seg.lo; i0 < seg.hi && !dead; i0 += Pg, ++step) {
+        if (i0 >= base + 32) {
+          base += 32;
+          cur = nxt;
+          nxt = entry(base + 32 + lane);
+        }
+        const int i = i0 + lane;
+        const int pc = __shfl_sync(0xffffffffu, cur, (i - base) & 31), pn = __shfl_sync(0xffffffffu, nxt, (i - base) & 31);
+        const int phys = i < base + 32 ? pc : pn;
+        const bool mine = lane < Pg && i < seg.hi;
+        const bool ok = mine && phys >= 0 && phys < a.num_pages;
+        if (mine && !ok) raise_error(a.err, SE_DEVERR_PAGE_RANGE);
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ok)) * page_bytes;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++j) {
+          const int s = j % kSlots;
+          if (lane == 0 && j >= kSlots && !mbar_wait(&empty[s], (j / kSlots - 1) & 1)) dead = true;
+          dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
+          if (dead) break;
+          if (kv == 0 && lane < Pg) meta[(step % kMetaRing) * kMaxPages + lane] = ok ? page_mask(k, a.sink, k.logical(i)) : 0u;
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
+          __syncwarp();
+          if (ok)
+            tma_load_3d(ring + s * kSlotBytes + lane * page_bytes, kv ? &vmap : &kmap, 0,
+                        (phys * a.num_kv_heads + seg.hg * heads) * kPageSize, 0, &full[s], policy);
+        }
+      }
+    }
+    // Every copy has landed before the CTA leaves.
+    if (lane == 0) {
+      for (int u = max(0, j - kSlots); u < j; ++u)
+        if (!mbar_wait(&full[u % kSlots], (u / kSlots) & 1)) dead = true;
+      if (dead) raise_error(a.err, SE_DEVERR_WAIT_TIMEOUT);
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const bool works = warp < active;
+  const int combo = warp % combos, replica = warp / combos;
+  const int hc = combo / a.mtiles, mt = combo % a.mtiles;
+  const int g = lane >> 2, t = lane & 3;
+  const int row_a = mt * 16 + g, row_b = row_a + 8;  // query heads of the KV head's group
+  const bool has_a = works && row_a < G, has_b = works && row_b < G;
+  const uint32_t ring0 = smem_addr(ring);
+  const uint32_t plane = (uint32_t)heads * kPageSize * 128;  // 64 dims of a page's rows
+  const uint32_t page_bytes = plane * C::kChunks;
+  int j = 0, step = 0;
+  int split_items = 0;  // bit 0: the first segment left a partial in slot 0; bit 1: the last in slot 1
+  int split_b[2], split_hg[2], split_start[2], split_n[2];
+
+  while (seg.next()) {
+    uint32_t qa[kD / 16][4];
+    {
+      const uint16_t* q0 = a.q + (size_t)seg.b * a.q_stride + (size_t)((seg.hg * heads + hc) * G) * kD;
+      const uint16_t *qr0 = q0 + (size_t)row_a * kD, *qr1 = q0 + (size_t)row_b * kD;
+#pragma unroll
+      for (int ks = 0; ks < kD / 16; ++ks) {
+        const int c = ks * 16 + 2 * t;
+        qa[ks][0] = has_a ? *reinterpret_cast<const uint32_t*>(qr0 + c) : 0u;
+        qa[ks][2] = has_a ? *reinterpret_cast<const uint32_t*>(qr0 + c + 8) : 0u;
+        qa[ks][1] = has_b ? *reinterpret_cast<const uint32_t*>(qr1 + c) : 0u;
+        qa[ks][3] = has_b ? *reinterpret_cast<const uint32_t*>(qr1 + c + 8) : 0u;
+      }
+    }
+    float o[kD / 8][4];
+#pragma unroll
+    for (int n = 0; n < kD / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+    for (int i0 = seg.lo; i0 < seg.hi; i0 += Pg, ++step, j += 2) {
+      if (!works) continue;
+      const int sk = j % kSlots, sv = (j + 1) % kSlots;
+      if (!dead && !mbar_wait(&full[sk], (j / kSlots) & 1)) dead = true;
+      bool v_here = false, zeroed = false;
+      for (int pg = replica; pg < Pg; pg += a.replicas) {
+        const uint32_t mask = dead || i0 + pg >= seg.hi ? 0u : meta[(step % kMetaRing) * kMaxPages + pg];
+        const bool last = pg + a.replicas >= Pg;
+        const uint32_t blk = pg * page_bytes + (uint32_t)hc * kPageSize * 128;
+        uint32_t pa0 = 0, pa1 = 0, pa2 = 0, pa3 = 0;
+        if (mask) {
+          const uint32_t kt = ring0 + sk * kSlotBytes + blk;
+          // Two n-tiles of 8 tokens, each in two accumulators: shorter chains of dependent products.
+          float s4[4][4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s4[x][0] = s4[x][1] = s4[x][2] = s4[x][3] = 0.f;
+          const int krow = (lane & 7) + ((lane >> 4) << 3), ksub = (lane >> 3) & 1;
+#pragma unroll
+          for (int ks = 0; ks < kD / 16; ++ks) {
+            uint32_t r0, r1, r2, r3;
+            ldmatrix_x4(r0, r1, r2, r3, kt + (ks >> 2) * plane + swz128(krow, ((ks & 3) << 1) + ksub));
+            mma_bf16_16816(s4[2 * (ks & 1)], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], r0, r1);
+            mma_bf16_16816(s4[2 * (ks & 1) + 1], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], r2, r3);
+          }
+          float sc[2][4];
+          const bool whole = mask_is_full(mask);
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float z = (s4[nt][e] + s4[nt + 2][e]) * a.scale_log2;
+              sc[nt][e] = whole || in_mask(mask, nt * 8 + 2 * t + (e & 1)) ? z : -INFINITY;
+            }
+          float x0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+          float x1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+          x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+          x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+          x0 = fmaxf(x0, m0);
+          x1 = fmaxf(x1, m1);
+          // A row that has seen nothing but -inf keeps m = -inf and takes 0 as its base.
+          const float b0 = x0 == -INFINITY ? 0.f : x0, b1 = x1 == -INFINITY ? 0.f : x1;
+          const float c0 = fast_exp2(m0 - b0), c1 = fast_exp2(m1 - b1);
+          m0 = x0;
+          m1 = x1;
+          float p[2][4];
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            p[nt][0] = fast_exp2(sc[nt][0] - b0);
+            p[nt][1] = fast_exp2(sc[nt][1] - b0);
+            p[nt][2] = fast_exp2(sc[nt][2] - b1);
+            p[nt][3] = fast_exp2(sc[nt][3] - b1);
+          }
+          l0 = l0 * c0 + ((p[0][0] + p[0][1]) + (p[1][0] + p[1][1]));
+          l1 = l1 * c1 + ((p[0][2] + p[0][3]) + (p[1][2] + p[1][3]));
+#pragma unroll
+          for (int n = 0; n < kD / 8; ++n) {
+            o[n][0] *= c0;
+            o[n][1] *= c0;
+            o[n][2] *= c1;
+            o[n][3] *= c1;
+          }
+          // P meets V as bf16 (half a step, 2^-8 of each weight), as the MMA wants; l sums it unrounded.
+          pa0 = pack_bf16x2(p[0][0], p[0][1]);
+          pa1 = pack_bf16x2(p[0][2], p[0][3]);
+          pa2 = pack_bf16x2(p[1][0], p[1][1]);
+          pa3 = pack_bf16x2(p[1][2], p[1][3]);
+        }
+        if (last) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[sk]);
+        }
+        if (!v_here) {
+          if (!dead && !mbar_wait(&full[sv], ((j + 1) / kSlots) & 1)) dead = true;
+          v_here = true;
+        }
+        if (mask && !dead) {
+          const uint32_t vt = ring0 + sv * kSlotBytes + blk;
+          if (!mask_is_full(mask)) {
+            // Stale rows may hold NaN: zero them (two lanes per row).
+            const int r = lane >> 1;
+            if (!in_mask(mask, r))
+              for (int c = lane & 1; c < kD / 8; c += 2)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + (c >> 3) * plane + swz128(r, c & 7)),
+                             "r"(0u)
+                             : "memory");
+            zeroed = true;
+            __syncwarp();
+          }
+          const int vtok = lane & 15, vsub = lane >> 4;
+#pragma unroll
+          for (int n = 0; n < kD / 16; ++n) {
+            const int chunk = 2 * n + vsub;
+            uint32_t r0, r1, r2, r3;
+            ldmatrix_x4_trans(r0, r1, r2, r3, vt + (chunk >> 3) * plane + swz128(vtok, chunk & 7));
+            mma_bf16_16816(o[2 * n], pa0, pa1, pa2, pa3, r0, r1);
+            mma_bf16_16816(o[2 * n + 1], pa0, pa1, pa2, pa3, r2, r3);
+          }
+        }
+      }
+      if (zeroed) fence_proxy_async_smem();  // before the next copy into the slot
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[sv]);
+    }
+
+    // ---- the end of a segment: this CTA's share of item (b, hg) is done
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    const int first_cta = seg.item_start / per_cta;
+    const bool split = seg.lo > 0 || seg.hi < seg.n;
+    const int slot = seg.lo > 0 ? 0 : 1;
+    if (split) {
+      split_items |= 1 << slot;
+      split_b[slot] = seg.b;
+      split_hg[slot] = seg.hg;
+      split_start[slot] = first_cta;
+      split_n[slot] = (seg.item_start + seg.n - 1) / per_cta - first_cta + 1;
+    }
+    const size_t out_row0 = (size_t)seg.b * a.num_q_heads + (size_t)seg.hg * rows;
+    const size_t part_row0 = (size_t)(2 * blockIdx.x + slot) * rows;
+    if (a.replicas == 1) {
+      if (works) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (!(half ? has_b : has_a)) continue;
+          const float l = half ? l1 : l0, m = half ? m1 : m0;
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+          const int r = hc * G + (half ? row_b : row_a);
+#pragma unroll
+          for (int n = 0; n < kD / 8; ++n) {
+            const float x = o[n][2 * half] * inv, y = o[n][2 * half + 1] * inv;
+            if (split)
+              *reinterpret_cast<float2*>(a.o_part + (part_row0 + r) * kD + n * 8 + 2 * t) = make_float2(x, y);
+            else
+              *reinterpret_cast<uint32_t*>(a.out + (out_row0 + r) * kD + n * 8 + 2 * t) = pack_bf16x2(x, y);
+          }
+          if (t == 0) {
+            if (split)
+              a.lse_part[part_row0 + r] = lse2;
+            else if (a.out_lse)
+              a.out_lse[out_row0 + r] = lse2 * kLn2;
+          }
+        }
+      }
+    } else {
+      // R warps hold parts of the same rows: merged through shared memory, eight rows of each tile at a time.
+      named_bar_sync(1, C::kConsumers);  // the previous segment's merge is over
+      if (works && t == 0) {
+        ml[warp * 32 + g] = m0;
+        ml[warp * 32 + 16 + g] = l0;
+        ml[warp * 32 + 8 + g] = m1;
+        ml[warp * 32 + 24 + g] = l1;
+      }
+      for (int half = 0; half < (G > 8 ? 2 : 1); ++half) {
+        if (half) named_bar_sync(1, C::kConsumers);
+        if (works) {
+          float* dst = stage + (warp * 8 + g) * kD + 2 * t;
+#pragma unroll
+          for (int n = 0; n < kD / 8; ++n)
+            *reinterpret_cast<float2*>(dst + n * 8) = half ? make_float2(o[n][2], o[n][3]) : make_float2(o[n][0], o[n][1]);
+        }
+        named_bar_sync(1, C::kConsumers);
+        for (int e = threadIdx.x; e < combos * 8 * (kD / 4); e += C::kConsumers) {
+          const int d = e % (kD / 4) * 4, gr = e / (kD / 4) % 8, c = e / (kD / 4) / 8;
+          const int qr = (c % a.mtiles) * 16 + half * 8 + gr;
+          if (qr >= G) continue;
+          float M = -INFINITY;
+          for (int w = c; w < active; w += combos) M = fmaxf(M, ml[w * 32 + half * 8 + gr]);
+          const float base = M == -INFINITY ? 0.f : M;
+          float l = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int w = c; w < active; w += combos) {
+            const float f = fast_exp2(ml[w * 32 + half * 8 + gr] - base);
+            l += f * ml[w * 32 + 16 + half * 8 + gr];
+            const float4 v = *reinterpret_cast<const float4*>(stage + (w * 8 + gr) * kD + d);
+            acc.x += f * v.x;
+            acc.y += f * v.y;
+            acc.z += f * v.z;
+            acc.w += f * v.w;
+          }
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const float lse2 = l == 0.f ? -INFINITY : M + log2f(l);
+          const int r = (c / a.mtiles) * G + qr;
+          acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+          if (split)
+            *reinterpret_cast<float4*>(a.o_part + (part_row0 + r) * kD + d) = acc;
+          else
+            *reinterpret_cast<uint2*>(a.out + (out_row0 + r) * kD + d) =
+                make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+          if (d == 0) {
+            if (split)
+              a.lse_part[part_row0 + r] = lse2;
+            else if (a.out_lse)
+              a.out_lse[out_row0 + r] = lse2 * kLn2;
+          }
+        }
+      }
+    }
+  }
+  if (dead && lane == 0) raise_error(a.err, SE_DEVERR_WAIT_TIMEOUT);
+
+  // ---- Publish: count this CTA in on the (at most two) items it shares with others; whoever completes an
+  // item's count merges its partials (written by other CTAs: read past L1) and resets the counter.
+  if (split_items == 0) return;  // the same for all consumers
+  __threadfence();
+  named_bar_sync(1, C::kConsumers);
+  if (threadIdx.x < 2) {
+    const int s = threadIdx.x;
+    int last = 0;
+    if (split_items >> s & 1) {
+      uint32_t* cnt = a.arrivals + (size_t)split_b[s] * HG + split_hg[s];
+      last = atomic_add_acq_rel_gpu(cnt, 1u) == (uint32_t)split_n[s] - 1;
+      if (last) *cnt = 0;
+    }
+    flags[s] = last;
+  }
+  named_bar_sync(1, C::kConsumers);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    if (!(split_items >> s & 1) || !flags[s]) continue;
+    const int c0 = split_start[s], ns = split_n[s];
+    const size_t out_row0 = (size_t)split_b[s] * a.num_q_heads + (size_t)split_hg[s] * rows;
+    for (int e = threadIdx.x; e < rows * (kD / 4); e += C::kConsumers) {
+      const int r = e / (kD / 4), d = e % (kD / 4) * 4;
+      float M = -INFINITY, wsum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i0 = 0; i0 < ns; i0 += 8) {
+        float ls[8];
+        float4 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int i = min(i0 + u, ns - 1);
+          // The item's first CTA holds it in slot 1 (the item starts there), the others in slot 0.
+          const size_t row = (size_t)(2 * (c0 + i) + (i == 0)) * rows + r;
+          ls[u] = i0 + u < ns ? __ldcg(a.lse_part + row) : -INFINITY;
+          v[u] = __ldcg(reinterpret_cast<const float4*>(a.o_part + row * kD + d));
+        }
+        float mn = M;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) mn = fmaxf(mn, ls[u]);
+        const float base = mn == -INFINITY ? 0.f : mn;
+        const float f = fast_exp2(M - base);
+        M = mn;
+        wsum *= f;
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          if (i0 + u >= ns) continue;
+          const float w = fast_exp2(ls[u] - base);
+          wsum += w;
+          acc.x += w * v[u].x;
+          acc.y += w * v[u].y;
+          acc.z += w * v[u].z;
+          acc.w += w * v[u].w;
+        }
+      }
+      const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+      *reinterpret_cast<uint2*>(a.out + (out_row0 + r) * kD + d) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (a.out_lse && d == 0) a.out_lse[out_row0 + r] = wsum == 0.f ? -INFINITY : (M + log2f(wsum)) * kLn2;
+    }
+  }
+}
+
+// How the heads of a call are laid over the consumer warps.
+struct HeadPlan {
+  int heads, head_groups, mtiles, replicas, step_pages;
+};
+HeadPlan head_plan(int num_kv_heads, int group, int head_dim) {
+  const int warps = head_dim == 256 ? Cfg<256>::kWarps : Cfg<128>::kWarps;
+  const int blocks = kSlotBytes / (kPageSize * head_dim * 2);
+  HeadPlan p;
+  p.mtiles = (group + 15) / 16;
+  p.heads = 1;
+  for (int c = 2; c * p.mtiles <= warps; ++c)
+    if (num_kv_heads % c == 0) p.heads = c;
+  p.head_groups = num_kv_heads / p.heads;
+  p.replicas = warps / (p.heads * p.mtiles);
+  p.step_pages = blocks / p.heads / p.replicas * p.replicas;
+  return p;
+}
+
+template <int kD>
+cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const PagedArgs& a, int grid,
+                   cudaStream_t stream) {
+  const size_t smem = Cfg<kD>::kFixed + (size_t)(a.batch + 1) * 4;
+  static_assert(Cfg<kD>::kFixed + (kMaxBatch + 1) * 4 <= 227 * 1024, "the largest batch fits");
+  cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<kD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Cfg<kD>::kFixed + (kMaxBatch + 1) * 4);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(paged_decode_kernel<kD>, dim3(grid), dim3(Cfg<kD>::kThreads), smem, stream, kmap, vmap, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-bool paged_decode_supported(int num_kv_heads, int head_dim, int head_dim_v, int num_q_heads, bool latent) {
-  if (latent) return num_kv_heads == 1 && head_dim == 576 && head_dim_v == 512 && num_q_heads % 16 == 0 && num_q_heads >= 16 && num_q_heads <= 64;
-  return head_dim == head_dim_v && (head_dim == 64 || head_dim == 128 || head_dim == 256) && num_q_heads / num_kv_heads <= 64;
+int paged_decode_max_batch() { return kMaxBatch; }
+
+bool paged_decode_supported(int num_kv_heads, int head_dim, int head_dim_v, int num_q_heads) {
+  return head_dim == head_dim_v && (head_dim == 64 || head_dim == 128 || head_dim == 256) &&
+         num_q_heads / num_kv_heads <= 64;
 }
 
-size_t paged_decode_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim_v) {
-  return 16;
+int paged_decode_box_heads(int num_kv_heads, int num_q_heads, int head_dim) {
+  return head_plan(num_kv_heads, num_q_heads / num_kv_heads, head_dim).heads;
 }
 
-cudaError_t launch_paged_decode(const KvView& kv, const uint16_t* q, long long q_stride, int32_t num_q_heads,
-                                const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens, int32_t batch,
-                                int32_t sink_tokens, int32_t recent_tokens, float sm_scale, uint16_t* out,
-                                float* out_lse, void* workspace, int sm_count, unsigned* err, cudaStream_t stream) {
+// Partials of every CTA (outputs, then log-sum-exps), then the arrival counters.
+size_t paged_decode_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
+  const HeadPlan p = head_plan(num_kv_heads, num_q_heads / num_kv_heads, head_dim);
+  const size_t rows = (size_t)p.heads * (num_q_heads / num_kv_heads);
+  return (2 * kMaxCtas * rows * (head_dim + 1) + (size_t)batch * p.head_groups) * sizeof(float);
+}
+
+cudaError_t launch_paged_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, const KvView& kv, const uint16_t* q,
+                                long long q_stride, int32_t num_q_heads, const int32_t* block_table,
+                                int32_t bt_stride, const int32_t* seq_lens, int32_t batch, int32_t sink_tokens,
+                                int32_t recent_tokens, float sm_scale, uint16_t* out, float* out_lse, void* workspace,
+                                int sm_count, unsigned* err, cudaStream_t stream) {
+  const int group = num_q_heads / kv.num_kv_heads;
+  const HeadPlan p = head_plan(kv.num_kv_heads, group, kv.head_dim);
   PagedArgs a;
-  a.kv = kv;
   a.q = q;
   a.q_stride = q_stride;
   a.num_q_heads = num_q_heads;
+  a.num_kv_heads = kv.num_kv_heads;
+  a.group = group;
+  a.heads = p.heads;
+  a.head_groups = p.head_groups;
+  a.mtiles = p.mtiles;
+  a.replicas = p.replicas;
+  a.step_pages = p.step_pages;
+  a.num_pages = kv.num_pages;
+  a.batch = batch;
   a.block_table = block_table;
   a.bt_stride = bt_stride;
   a.seq_lens = seq_lens;
@@ -115,9 +672,17 @@ cudaError_t launch_paged_decode(const KvView& kv, const uint16_t* q, long long q
   a.scale_log2 = sm_scale * 1.4426950408889634f;
   a.out = out;
   a.out_lse = out_lse;
+  const size_t rows = (size_t)p.heads * group;
+  a.o_part = static_cast<float*>(workspace);
+  a.lse_part = a.o_part + 2 * kMaxCtas * rows * kv.head_dim;
+  a.arrivals = reinterpret_cast<uint32_t*>(a.lse_part + 2 * kMaxCtas * rows);
   a.err = err;
-  const cudaError_t e = launch_pdl(paged_decode_kernel, dim3((unsigned)(batch * num_q_heads)), dim3(kThreads), 0, stream, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  const int grid = sm_count < kMaxCtas ? sm_count : kMaxCtas;
+  switch (kv.head_dim) {
+    case 64: return launch<64>(kmap, vmap, a, grid, stream);
+    case 128: return launch<128>(kmap, vmap, a, grid, stream);
+    default: return launch<256>(kmap, vmap, a, grid, stream);
+  }
 }
 
 }  // namespace se

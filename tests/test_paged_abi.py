@@ -89,7 +89,7 @@ LATENT = dict(v=FAKE, num_kv_heads=1, head_dim=576, head_dim_v=512, row_stride_k
     (_kv(), {"sink": -1}, INVALID), (_kv(), {"recent": -1}, INVALID), (_kv(), {"sink": 4}, INVALID),
     (_kv(), {"scale": float("inf")}, INVALID), (_kv(), {"q_stride": 4088}, INVALID), (_kv(), {"q_stride": 4100}, INVALID),
     (_kv(), {"bt_stride": 0}, INVALID), (_kv(), {"bt_stride": 1 << 27}, UNSUPPORTED),
-    (_kv(), {"batch": 16385}, UNSUPPORTED), (_kv(), {"q": None}, INVALID), (_kv(), {"out": None}, INVALID),
+    (_kv(), {"batch": 4097}, UNSUPPORTED), (_kv(), {"q": None}, INVALID), (_kv(), {"out": None}, INVALID),
     (_kv(), {"bt": None}, INVALID), (_kv(), {"lens": None}, INVALID), (_kv(), {"q": FAKE + 8}, INVALID),
     (_kv(), {"out": FAKE + 4}, INVALID), (_kv(), {"lse": FAKE + 4}, INVALID), (_kv(), {"ws": FAKE + 8}, INVALID),
     (_kv(), {"ws": None}, INVALID), (_kv(), {"ws_bytes": 15}, WORKSPACE), (_kv(), {"batch": 0, "q": None}, 0),
