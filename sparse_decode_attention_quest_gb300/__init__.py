@@ -153,8 +153,8 @@ def _ptr(t: Optional[torch.Tensor], dtype=None, name="tensor"):
 
 
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the handle alone: building a Stream object costs more than most of a call's checks
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -403,34 +403,53 @@ def se_sparse_paged_decode_noalloc(kv: SEPagedKV, q, block_table, seq_lens, sel_
 
 
 # ------------------------------------------- page pool, row store, dense paged decode
-def _same_len(t, n: int, name: str):
-    if t.numel() != n:
-        raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
-
-
-def _on_current_device(*tensors):
-    """The library launches on the current device: tensors of another one are refused."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.is_cuda and t.get_device() != dev:
-            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-
-
-def _rows_ptr(t, heads: int, width: int, dtype, name: str):
-    """(pointer, row stride) of [N][heads][width] rows whose heads are dense; the N rows may be
-    any distance apart (columns of a fused projection's output, say)."""
+def _refuse(t, dtype, name: str, dev: int):
+    """The error of a tensor that _arg does not take."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.get_device() != dev:  # the library launches on the current device
+        raise ValueError(f"{name}: is on cuda:{t.get_device()}, the current device is cuda:{dev}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    raise ValueError(f"{name}: must be contiguous")
+
+
+def _arg(t, dtype, name: str, dev: int):
+    """Pointer of a contiguous tensor on the current device."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or not t.is_contiguous():
+        _refuse(t, dtype, name, dev)
+    return t.data_ptr()
+
+
+def _vec(t, n: int, dtype, name: str, dev: int):
+    """_arg of a tensor of n elements."""
+    p = _arg(t, dtype, name, dev)
+    if t.numel() != n:
+        raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
+    return p
+
+
+def _table(t, name: str, dev: int):
+    """(pointer, requests, width) of a block table."""
+    p = _arg(t, torch.int32, name, dev)
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected [batch][pages]")
+    return p, t.shape[0], t.shape[1]
+
+
+def _rows_ptr(t, heads: int, width: int, dtype, name: str, dev: int):
+    """(pointer, row stride) of [N][heads][width] rows whose heads are dense; the N rows may be
+    any distance apart (columns of a fused projection's output, say)."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype:
+        _refuse(t, dtype, name, dev)
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != width:
         raise ValueError(f"{name}: expected shape [N][{heads}][{width}], got {list(t.shape)}")
-    n, s = t.shape[0], t.stride()
-    if (width > 1 and s[2] != 1) or (heads > 1 and s[1] != width):
+    row, head, one = t.stride()
+    if (width > 1 and one != 1) or (heads > 1 and head != width):
         raise ValueError(f"{name}: the heads of a row must be dense")
-    return t.data_ptr(), s[0] if n > 1 else heads * width
+    return t.data_ptr(), row if t.shape[0] > 1 else heads * width
 
 
 def se_block_tables_extend(free_pages, pool_state, block_table, seq_lens, new_lens, seq_lens_after, token_start,
@@ -438,53 +457,39 @@ def se_block_tables_extend(free_pages, pool_state, block_table, seq_lens, new_le
     """Pages, table entries, slots and positions for new_lens[b] tokens behind the seq_lens[b] cached
     ones; ``free_pages`` (int32, as long as the pool has pages) and ``pool_state`` (int32 [4]) are the
     pool, ``slot_map.numel()`` is the most new tokens a call takes. ``seq_lens_after`` may be ``seq_lens``."""
-    lib = load_library()
-    batch = block_table.shape[0]
-    _on_current_device(free_pages, pool_state, block_table, seq_lens, new_lens, seq_lens_after, token_start, slot_map,
-                       positions)
-    _same_len(pool_state, 4, "pool_state")
-    _same_len(seq_lens, batch, "seq_lens")
-    _same_len(new_lens, batch, "new_lens")
-    _same_len(seq_lens_after, batch, "seq_lens_after")
-    _same_len(token_start, batch + 1, "token_start")
-    if positions is not None:
-        _same_len(positions, slot_map.numel(), "positions")
-    i32 = torch.int32
-    _check(lib.se_block_tables_extend(_ptr(free_pages, i32, "free_pages"), _ptr(pool_state, i32, "pool_state"),
-                                      free_pages.numel(), _ptr(block_table, i32, "block_table"), block_table.shape[1],
-                                      _ptr(seq_lens, i32, "seq_lens"), _ptr(new_lens, i32, "new_lens"), batch,
-                                      _ptr(seq_lens_after, i32, "seq_lens_after"),
-                                      _ptr(token_start, i32, "token_start"), _ptr(slot_map, i32, "slot_map"),
-                                      _ptr(positions, i32, "positions"), slot_map.numel(), _stream(stream)))
+    lib, dev, i32 = load_library(), torch.cuda.current_device(), torch.int32
+    table, batch, width = _table(block_table, "block_table", dev)
+    slots = slot_map.numel()
+    _check(lib.se_block_tables_extend(
+        _arg(free_pages, i32, "free_pages", dev), _vec(pool_state, 4, i32, "pool_state", dev), free_pages.numel(),
+        table, width, _vec(seq_lens, batch, i32, "seq_lens", dev), _vec(new_lens, batch, i32, "new_lens", dev), batch,
+        _vec(seq_lens_after, batch, i32, "seq_lens_after", dev),
+        _vec(token_start, batch + 1, i32, "token_start", dev), _arg(slot_map, i32, "slot_map", dev),
+        None if positions is None else _vec(positions, slots, i32, "positions", dev), slots, _stream(stream)))
 
 
 def se_block_tables_release(free_pages, pool_state, block_table, seq_lens, keep_lens=None, stream=None):
     """The pages of the tokens behind keep_lens[b] (None: of every token) back to the pool."""
-    lib = load_library()
-    batch = block_table.shape[0]
-    _on_current_device(free_pages, pool_state, block_table, seq_lens, keep_lens)
-    _same_len(pool_state, 4, "pool_state")
-    _same_len(seq_lens, batch, "seq_lens")
-    if keep_lens is not None:
-        _same_len(keep_lens, batch, "keep_lens")
-    i32 = torch.int32
-    _check(lib.se_block_tables_release(_ptr(free_pages, i32, "free_pages"), _ptr(pool_state, i32, "pool_state"),
-                                       free_pages.numel(), _ptr(block_table, i32, "block_table"),
-                                       block_table.shape[1], _ptr(seq_lens, i32, "seq_lens"),
-                                       _ptr(keep_lens, i32, "keep_lens"), batch, _stream(stream)))
+    lib, dev, i32 = load_library(), torch.cuda.current_device(), torch.int32
+    table, batch, width = _table(block_table, "block_table", dev)
+    _check(lib.se_block_tables_release(
+        _arg(free_pages, i32, "free_pages", dev), _vec(pool_state, 4, i32, "pool_state", dev), free_pages.numel(),
+        table, width, _vec(seq_lens, batch, i32, "seq_lens", dev),
+        None if keep_lens is None else _vec(keep_lens, batch, i32, "keep_lens", dev), batch, _stream(stream)))
 
 
 def se_paged_kv_store(kv: SEPagedKV, k_new, v_new, slot_map, stream=None):
     """The rows k_new and v_new [T][Hkv][D] (tokens any stride apart; v_new None for a latent cache) of
     slot_map.numel() new tokens into their slots; with a summary in ``kv``, its pages' bounds too."""
-    lib = load_library()
-    _on_current_device(k_new, v_new, slot_map)
+    lib, dev = load_library(), torch.cuda.current_device()
     tokens = slot_map.numel()
-    kp, ks = _rows_ptr(k_new, kv.num_kv_heads, kv.head_dim, torch.bfloat16, "k_new")
-    vp, vs = (None, 0) if v_new is None else _rows_ptr(v_new, kv.num_kv_heads, kv.head_dim_v, torch.bfloat16, "v_new")
+    kp, ks = _rows_ptr(k_new, kv.num_kv_heads, kv.head_dim, torch.bfloat16, "k_new", dev)
+    vp, vs = None, 0
+    if v_new is not None:
+        vp, vs = _rows_ptr(v_new, kv.num_kv_heads, kv.head_dim_v, torch.bfloat16, "v_new", dev)
     if k_new.shape[0] != tokens or (v_new is not None and v_new.shape[0] != tokens):
         raise ValueError("k_new, v_new and slot_map differ in tokens")
-    _check(lib.se_paged_kv_store(ctypes.byref(kv), kp, ks, vp, vs, _ptr(slot_map, torch.int32, "slot_map"), tokens,
+    _check(lib.se_paged_kv_store(ctypes.byref(kv), kp, ks, vp, vs, _arg(slot_map, torch.int32, "slot_map", dev), tokens,
                                  _stream(stream)))
 
 
@@ -499,23 +504,20 @@ def se_paged_decode(kv: SEPagedKV, q, block_table, seq_lens, sm_scale: float, ou
     """Attention of one new token per request over its cached tokens (all of them, or with
     ``recent_tokens`` the first ``sink_tokens`` and the last ``recent_tokens``): q [B][Hq][D] (requests any
     stride apart) -> out [B][Hq][Dv], out_lse [B][Hq] or None. ``workspace``: uint8, zeroed once."""
-    lib = load_library()
-    _on_current_device(q, block_table, seq_lens, out, out_lse, workspace)
-    if q.dim() != 3:
+    lib, dev = load_library(), torch.cuda.current_device()
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q: expected [batch][num_q_heads][head_dim]")
     batch, hq = q.shape[0], q.shape[1]
-    qp, qs = _rows_ptr(q, hq, kv.head_dim, torch.bfloat16, "q")
-    if block_table.dim() != 2 or block_table.shape[0] != batch:
-        raise ValueError("block_table: expected [batch][pages]")
-    _same_len(seq_lens, batch, "seq_lens")
-    _same_len(out, batch * hq * kv.head_dim_v, "out")
-    if out_lse is not None:
-        _same_len(out_lse, batch * hq, "out_lse")
-    _check(lib.se_paged_decode(ctypes.byref(kv), qp, qs, hq, _ptr(block_table, torch.int32, "block_table"),
-                               block_table.shape[1], _ptr(seq_lens, torch.int32, "seq_lens"), batch, int(sink_tokens),
-                               int(recent_tokens), float(sm_scale), _ptr(out, torch.bfloat16, "out"),
-                               _ptr(out_lse, torch.float32, "out_lse"), _ptr(workspace, torch.uint8, "workspace"),
-                               0 if workspace is None else workspace.numel(), _stream(stream)))
+    qp, qs = _rows_ptr(q, hq, kv.head_dim, torch.bfloat16, "q", dev)
+    table, rows, width = _table(block_table, "block_table", dev)
+    if rows != batch:
+        raise ValueError(f"block_table: expected {batch} rows, got {rows}")
+    _check(lib.se_paged_decode(
+        ctypes.byref(kv), qp, qs, hq, table, width, _vec(seq_lens, batch, torch.int32, "seq_lens", dev), batch,
+        sink_tokens, recent_tokens, sm_scale, _vec(out, batch * hq * kv.head_dim_v, torch.bfloat16, "out", dev),
+        None if out_lse is None else _vec(out_lse, batch * hq, torch.float32, "out_lse", dev),
+        None if workspace is None else _arg(workspace, torch.uint8, "workspace", dev),
+        0 if workspace is None else workspace.numel(), _stream(stream)))
 
 
 # ---------------------------------------------------------------- SnapKV

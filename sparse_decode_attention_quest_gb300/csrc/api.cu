@@ -125,6 +125,21 @@ bool encode_window_map(CUtensorMap* map, const void* base, int batch, int window
   return r == CUDA_SUCCESS;
 }
 
+// 3-D view of decode queries bf16 [batch][num_q_heads][width], requests `q_stride` elements apart: boxes of
+// 64 dims x all heads x 1 request (128-byte swizzle).
+bool encode_query_map(CUtensorMap* map, const void* base, int batch, int num_q_heads, int width, long long q_stride) {
+  auto fn = encode_tiled();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)num_q_heads, (cuuint64_t)batch};
+  cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)q_stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)num_q_heads, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int pages_of(long long tokens) { return (int)((tokens + se::kPageSize - 1) / se::kPageSize); }
@@ -842,9 +857,9 @@ size_t se_paged_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_
                                       int32_t head_dim_v) {
   if (batch < 0 || num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads) return 0;
   if (se::paged_latent_supported(num_kv_heads, head_dim, head_dim_v, num_q_heads))
-    return round16(se::paged_latent_workspace_bytes(batch, num_q_heads));
+    return round16(se::paged_latent_workspace_bytes(num_q_heads));
   if (!se::paged_decode_supported(num_kv_heads, head_dim, head_dim_v, num_q_heads)) return 0;
-  return round16(se::paged_decode_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim));
+  return round16(se::paged_decode_workspace_bytes(num_q_heads, num_kv_heads, head_dim));
 }
 
 se_status_t se_paged_decode(const se_paged_kv_t* kv, const void* q, int64_t q_stride, int32_t num_q_heads,
@@ -871,14 +886,15 @@ se_status_t se_paged_decode(const se_paged_kv_t* kv, const void* q, int64_t q_st
     return fail(SE_ERR_INVALID_ARG, fn, "q_stride must cover the heads and be a multiple of 8");
   if (bt_stride < 1) return fail(SE_ERR_INVALID_ARG, fn, "bt_stride < 1");
   if (bt_stride >= (1 << 27)) return fail(SE_ERR_UNSUPPORTED, fn, "2^27 or more pages per request");
-  if (batch > se::paged_decode_max_batch()) return fail(SE_ERR_UNSUPPORTED, fn, "batch > 4096");
+  if (batch > (latent ? se::paged_latent_max_batch() : se::paged_decode_max_batch()))
+    return fail(SE_ERR_UNSUPPORTED, fn, "batch > 4096 (latent cache: 1024)");
   if (batch == 0) return SE_OK;
   if (!q || !block_table || !seq_lens || !out) return fail(SE_ERR_INVALID_ARG, fn, "NULL pointer");
   if (!aligned16(q) || !aligned16(block_table) || !aligned16(seq_lens) || !aligned16(out) || !aligned16(out_lse) ||
       !aligned16(workspace))
     return fail(SE_ERR_INVALID_ARG, fn, "pointers must be 16-byte aligned");
-  if (workspace_bytes < (latent ? se::paged_latent_workspace_bytes(batch, num_q_heads)
-                                : se::paged_decode_workspace_bytes(batch, num_q_heads, kv->num_kv_heads, kv->head_dim)))
+  if (workspace_bytes < (latent ? se::paged_latent_workspace_bytes(num_q_heads)
+                                : se::paged_decode_workspace_bytes(num_q_heads, kv->num_kv_heads, kv->head_dim)))
     return fail(SE_ERR_WORKSPACE, fn, "workspace too small");
   if (!workspace) return fail(SE_ERR_INVALID_ARG, fn, "workspace NULL");
   DeviceInfo* d = nullptr;
@@ -886,10 +902,13 @@ se_status_t se_paged_decode(const se_paged_kv_t* kv, const void* q, int64_t q_st
   if (e != cudaSuccess) return cuda_fail(fn, e);
   const long long rows = std::max(1ll, (long long)kv->num_pages * kv->num_kv_heads * se::kPageSize);
   if (latent) {
-    e = se::launch_paged_latent(view_of(kv), static_cast<const uint16_t*>(q), q_stride, num_q_heads, block_table,
-                                bt_stride, seq_lens, batch, sink_tokens, recent_tokens, sm_scale,
-                                static_cast<uint16_t*>(out), out_lse, workspace, d->sm_count, d->err,
-                                static_cast<cudaStream_t>(stream));
+    CUtensorMap kvmap, qmap;
+    if (!encode_row_chunks_map(&kvmap, kv->k, rows, kv->row_stride_k, kv->head_dim / 64, se::kPageSize / 2) ||
+        !encode_query_map(&qmap, q, batch, num_q_heads, kv->head_dim, q_stride))
+      return fail(SE_ERR_CUDA, fn, "cuTensorMapEncodeTiled failed");
+    e = se::launch_paged_latent(kvmap, qmap, view_of(kv), num_q_heads, block_table, bt_stride, seq_lens, batch,
+                                sink_tokens, recent_tokens, sm_scale, static_cast<uint16_t*>(out), out_lse, workspace,
+                                d->sm_count, d->err, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SE_OK : cuda_fail(fn, e);
   }
   const int box = se::kPageSize * se::paged_decode_box_heads(kv->num_kv_heads, num_q_heads, kv->head_dim);

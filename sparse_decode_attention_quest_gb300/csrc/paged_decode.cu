@@ -15,8 +15,13 @@
 //    balance, and a single long request spreads over every SM. An item that
 //    spans CTAs leaves a partial (output, log-sum-exp) per CTA; a CTA has at
 //    most two, for the item it starts inside and the item it ends inside, so
-//    the workspace does not grow with the lengths. The CTA that publishes an
-//    item's last partial merges them in the order of the pages.
+//    the workspace does not grow with the lengths.
+//  * Join: the CTA that publishes an item's last partial merges them in the order
+//    of the pages, while they are few enough for one SM (kInlineBytes); the
+//    partials of an item over more CTAs go to a second kernel, a CTA per row,
+//    which is launched when the table's width allows such items. One CTA reads
+//    partials from L2 at about 60 bytes a clock: merging 32 of 16 KB took it 25 of
+//    46 us (4 requests of 2.5K tokens, 32 query heads).
 //  * Copies: a page's rows of one KV head are 16 x D bf16, and the heads of a
 //    group of Hc lie next to each other, so that one TMA box of 64 dims x
 //    16 Hc rows x D / 64 brings a whole page of the group (16 to 32 KB for 4 to 8
@@ -29,7 +34,9 @@
 //    flops per byte.
 //  * Rows that are not kept: their logits become -inf, and their value rows are
 //    zeroed in shared memory first, since 0 * NaN is not 0.
-#include "se_ptx.cuh"
+#include <algorithm>
+
+#include "se_paged.cuh"
 
 namespace se {
 namespace {
@@ -41,6 +48,8 @@ constexpr int kMetaRing = 4;     // steps whose page masks are held (at most thr
 constexpr int kMaxPages = 16;    // pages of a step
 constexpr int kMaxCtas = 192;    // partial slots: two per CTA
 constexpr int kMaxBatch = 4096;  // requests whose prefix fits beside the ring
+constexpr int kInlineBytes = 128 * 1024;  // partials of an item that one CTA merges
+constexpr int kJoinWarps = 8;
 
 template <int kD>
 struct Cfg {
@@ -76,41 +85,13 @@ struct PagedArgs {
   float* out_lse;
   float* o_part;        // [2 * CTAs][heads * group][D]
   float* lse_part;      // [2 * CTAs][heads * group], log2 domain
-  uint32_t* arrivals;   // [batch * head_groups], zero between calls
+  // An item that spans CTAs is the only one to go on behind its first CTA, so that CTA's index names it.
+  uint32_t* arrivals;   // [kMaxCtas] by first CTA, zero between calls
+  int2* joins;          // [CTAs] by first CTA: item and partials for the join kernel (0 partials: nothing to do)
+  int32_t inline_splits;  // most partials that a CTA of this kernel merges
+  bool deferred;        // the join kernel follows
   unsigned* err;
 };
-
-// The kept pages of a request: logical pages 0 .. sink_pages - 1, then recent_page .. (all pages: sink_pages = n).
-struct Kept {
-  int len;          // tokens (clipped)
-  int from;         // kept: j < sink or j >= from
-  int n;            // kept pages
-  int sink_pages;
-  int recent_page;
-  __device__ __forceinline__ int logical(int i) const { return i < sink_pages ? i : i - sink_pages + recent_page; }
-};
-
-__device__ __forceinline__ Kept kept_of(int L, int bt_stride, int sink, int recent, unsigned* err) {
-  Kept k;
-  if (L < 0 || L > (long long)bt_stride * kPageSize) {
-    raise_error(err, SE_DEVERR_LENGTH);
-    L = L < 0 ? 0 : bt_stride * kPageSize;
-  }
-  k.len = L;
-  const int pages = L / kPageSize + (L % kPageSize != 0);
-  k.from = recent > 0 && L > recent ? L - recent : 0;
-  const int sp = sink / kPageSize + (sink % kPageSize != 0), rp = k.from / kPageSize;
-  if (k.from <= sink || sp > rp) {  // no page is left out
-    k.n = k.sink_pages = pages;
-    k.recent_page = pages;
-    if (k.from <= sink) k.from = 0;
-  } else {
-    k.sink_pages = sp;
-    k.recent_page = rp;
-    k.n = sp + pages - rp;
-  }
-  return k;
-}
 
 // Segments of a CTA's slice: the pages [lo, hi) of item (b, hg).
 struct Segment {
@@ -143,58 +124,6 @@ struct Segment {
   }
 };
 
-// Which of a page's 16 tokens are kept: t < hi and (t < a or t >= z), packed as hi | a << 8 | z << 16.
-__device__ __forceinline__ uint32_t page_mask(const Kept& k, int sink, int page) {
-  const int j0 = page * kPageSize;
-  const int hi = min(kPageSize, k.len - j0);
-  const int a = k.from == 0 ? kPageSize : max(0, min(kPageSize, sink - j0));
-  const int z = max(0, min(kPageSize, k.from - j0));
-  return (uint32_t)hi | (uint32_t)a << 8 | (uint32_t)z << 16;
-}
-__device__ __forceinline__ bool in_mask(uint32_t m, int t) {
-  return t < (int)(m & 0xff) && (t < (int)(m >> 8 & 0xff) || t >= (int)(m >> 16));
-}
-__device__ __forceinline__ bool mask_is_full(uint32_t m) {
-  return (m & 0xff) == kPageSize && ((m >> 8 & 0xff) == kPageSize || (m >> 16) == 0);
-}
-
-// Kept pages per request and their exclusive prefix (prefix[batch]: the total), by the whole CTA.
-template <int kThreads>
-__device__ __forceinline__ void kept_prefix(const PagedArgs& a, int* prefix, long long* sums) {
-  constexpr int kWarps = kThreads / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // Positions are 32-bit: requests beyond that many pages are reported and cut short.
-  const long long most = 0x7fffffff / a.head_groups;
-  long long at = 0;
-  for (int base = 0; base < a.batch; base += kThreads) {
-    const int b = base + threadIdx.x;
-    int n = b < a.batch ? kept_of(a.seq_lens[b], a.bt_stride, a.sink, a.recent, a.err).n : 0;
-    long long incl = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
-    }
-    if (lane == 31) sums[warp] = incl;
-    __syncthreads();
-    long long before = at, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += sums[w];
-      all += sums[w];
-    }
-    __syncthreads();
-    incl += before;
-    if (b < a.batch) {
-      if (incl > most) raise_error(a.err, SE_DEVERR_LENGTH);
-      prefix[b + 1] = (int)(incl < most ? incl : most);
-    }
-    at += all;
-  }
-  if (threadIdx.x == 0) prefix[0] = 0;
-  __syncthreads();
-}
-
 template <int kD>
 __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                                                                            const __grid_constant__ CUtensorMap vmap,
@@ -214,7 +143,8 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
   const int heads = a.heads, G = a.group, rows = heads * G, HG = a.head_groups, Pg = a.step_pages;
   const int combos = heads * a.mtiles, active = combos * a.replicas;
 
-  kept_prefix<C::kThreads>(a, prefix, reinterpret_cast<long long*>(stage));
+  kept_prefix<C::kThreads>(a.seq_lens, a.batch, a.bt_stride, a.sink, a.recent, 0x7fffffff / HG, prefix,
+                           reinterpret_cast<long long*>(stage), a.err);
   // Requests without a kept token: the empty sum.
   for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
     if (prefix[b + 1] != prefix[b]) continue;
@@ -229,7 +159,10 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
   int per_cta = (int)(((long long)total + gridDim.x - 1) / gridDim.x);
   per_cta = max(2 * Pg, (per_cta + Pg - 1) / Pg * Pg);
   const long long start64 = (long long)blockIdx.x * per_cta;
-  if (start64 >= total) return;
+  if (start64 >= total) {
+    if (a.deferred && threadIdx.x == 0) a.joins[blockIdx.x] = make_int2(0, 0);
+    return;
+  }
   const int start = (int)start64, end = min((long long)total, start64 + per_cta);
 
   if (threadIdx.x == 0) {
@@ -304,8 +237,11 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
   const uint32_t plane = (uint32_t)heads * kPageSize * 128;  // 64 dims of a page's rows
   const uint32_t page_bytes = plane * C::kChunks;
   int j = 0, step = 0;
-  int split_items = 0;  // bit 0: the first segment left a partial in slot 0; bit 1: the last in slot 1
-  int split_b[2], split_hg[2], split_start[2], split_n[2];
+  // The items shared with other CTAs whose partials are merged here: 0 the one that began before the slice
+  // (partial slot 0), 1 the one that goes on behind it (slot 1).
+  bool shared0 = false, shared1 = false;
+  int item0 = 0, item1 = 0, first0 = 0, parts0 = 0, parts1 = 0;
+  int2 join = make_int2(0, 0);  // the item that goes on behind the slice, when the join kernel merges it
 
   while (seg.next()) {
     uint32_t qa[kD / 16][4];
@@ -440,12 +376,20 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
     const int first_cta = seg.item_start / per_cta;
     const bool split = seg.lo > 0 || seg.hi < seg.n;
     const int slot = seg.lo > 0 ? 0 : 1;
-    if (split) {
-      split_items |= 1 << slot;
-      split_b[slot] = seg.b;
-      split_hg[slot] = seg.hg;
-      split_start[slot] = first_cta;
-      split_n[slot] = (seg.item_start + seg.n - 1) / per_cta - first_cta + 1;
+    const int parts = split ? (seg.item_start + seg.n - 1) / per_cta - first_cta + 1 : 0;
+    const bool here = split && parts <= a.inline_splits;
+    const int item = seg.b * HG + seg.hg;
+    if (here && slot == 0) {
+      shared0 = true;
+      item0 = item;
+      first0 = first_cta;
+      parts0 = parts;
+    } else if (here) {
+      shared1 = true;
+      item1 = item;
+      parts1 = parts;
+    } else if (split && slot == 1) {
+      join = make_int2(item, parts);
     }
     const size_t out_row0 = (size_t)seg.b * a.num_q_heads + (size_t)seg.hg * rows;
     const size_t part_row0 = (size_t)(2 * blockIdx.x + slot) * rows;
@@ -530,28 +474,28 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
     }
   }
   if (dead && lane == 0) raise_error(a.err, SE_DEVERR_WAIT_TIMEOUT);
+  if (a.deferred && threadIdx.x == 0) a.joins[blockIdx.x] = join;
 
-  // ---- Publish: count this CTA in on the (at most two) items it shares with others; whoever completes an
-  // item's count merges its partials (written by other CTAs: read past L1) and resets the counter.
-  if (split_items == 0) return;  // the same for all consumers
+  // ---- Publish: count this CTA in on the (at most two) items it shares with few others; whoever completes
+  // an item's count merges its partials (written by other CTAs: read past L1) and resets the counter.
+  if (!shared0 && !shared1) return;  // the same for all consumers
   __threadfence();
   named_bar_sync(1, C::kConsumers);
   if (threadIdx.x < 2) {
-    const int s = threadIdx.x;
     int last = 0;
-    if (split_items >> s & 1) {
-      uint32_t* cnt = a.arrivals + (size_t)split_b[s] * HG + split_hg[s];
-      last = atomic_add_acq_rel_gpu(cnt, 1u) == (uint32_t)split_n[s] - 1;
+    if (threadIdx.x ? shared1 : shared0) {
+      uint32_t* cnt = a.arrivals + (threadIdx.x ? (int)blockIdx.x : first0);
+      last = atomic_add_acq_rel_gpu(cnt, 1u) == (uint32_t)(threadIdx.x ? parts1 : parts0) - 1;
       if (last) *cnt = 0;
     }
-    flags[s] = last;
+    flags[threadIdx.x] = last;
   }
   named_bar_sync(1, C::kConsumers);
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    if (!(split_items >> s & 1) || !flags[s]) continue;
-    const int c0 = split_start[s], ns = split_n[s];
-    const size_t out_row0 = (size_t)split_b[s] * a.num_q_heads + (size_t)split_hg[s] * rows;
+    if (!flags[s]) continue;
+    const int c0 = s ? (int)blockIdx.x : first0, ns = s ? parts1 : parts0;
+    const size_t out_row0 = (size_t)(s ? item1 : item0) * rows;  // items and their rows follow one another
     for (int e = threadIdx.x; e < rows * (kD / 4); e += C::kConsumers) {
       const int r = e / (kD / 4), d = e % (kD / 4) * 4;
       float M = -INFINITY, wsum = 0.f;
@@ -594,6 +538,90 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
   }
 }
 
+// Merges the partials of the items that span many CTAs: a CTA per (item, row), a share of the
+// partials per warp, joined in warp order. With M the largest log-sum-exp,
+//     out = sum_i exp2(lse_i - M) o_i / sum_i exp2(lse_i - M).
+template <int kD>
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const float* __restrict__ o_part,
+                                                                    const float* __restrict__ lse_part,
+                                                                    const int2* __restrict__ joins, int32_t ctas,
+                                                                    int32_t rows, uint16_t* __restrict__ out,
+                                                                    float* __restrict__ out_lse) {
+  pdl_enter();
+  constexpr int kV = kD / 32;  // values per lane
+  static_assert(kMaxCtas <= kJoinWarps * 32, "a lane per partial of the warp, a thread per item");
+  __shared__ int3 todo[kMaxCtas];
+  __shared__ int counts[kJoinWarps];
+  __shared__ float acc_s[kJoinWarps][kD];
+  __shared__ float m_s[kJoinWarps], l_s[kJoinWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ntodo = list_joins(joins, ctas, todo, counts);
+  for (int u = blockIdx.x; u < ntodo * rows; u += gridDim.x) {
+    const int3 jn = todo[u / rows];
+    const int r = u % rows;
+    const size_t out_row = (size_t)jn.y * rows + r;
+    // Partial i is in slot 1 of the item's first CTA (i = 0), in slot 0 of the others.
+    auto part = [&](int i) { return (size_t)(2 * (jn.x + i) + (i == 0)) * rows + r; };
+    const int mine = warp + kJoinWarps * lane;
+    const float ls = mine < jn.z ? lse_part[part(mine)] : -INFINITY;
+    float M = ls;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float w = fast_exp2(ls - (M == -INFINITY ? 0.f : M));
+    float l = w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    float acc[kV];
+#pragma unroll
+    for (int x = 0; x < kV; ++x) acc[x] = 0.f;
+    const int n = (jn.z - warp + kJoinWarps - 1) / kJoinWarps;
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float f = __shfl_sync(0xffffffffu, w, k);
+      const float* p = o_part + part(warp + kJoinWarps * k) * kD + lane * kV;
+      if constexpr (kV == 2) {
+        const float2 v = *reinterpret_cast<const float2*>(p);
+        acc[0] += f * v.x;
+        acc[1] += f * v.y;
+      } else {
+#pragma unroll
+        for (int x = 0; x < kV; x += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(p + x);
+          acc[x] += f * v.x;
+          acc[x + 1] += f * v.y;
+          acc[x + 2] += f * v.z;
+          acc[x + 3] += f * v.w;
+        }
+      }
+    }
+    __syncthreads();  // the previous unit's sums are read
+#pragma unroll
+    for (int x = 0; x < kV; ++x) acc_s[warp][lane * kV + x] = acc[x];
+    if (lane == 0) {
+      m_s[warp] = M;
+      l_s[warp] = l;
+    }
+    __syncthreads();
+    if (threadIdx.x < kD / 2) {
+      float top = m_s[0];
+#pragma unroll
+      for (int k = 1; k < kJoinWarps; ++k) top = fmaxf(top, m_s[k]);
+      const float base = top == -INFINITY ? 0.f : top;
+      float sum = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+      for (int k = 0; k < kJoinWarps; ++k) {
+        const float f = fast_exp2(m_s[k] - base);
+        sum += f * l_s[k];
+        x += f * acc_s[k][2 * threadIdx.x];
+        y += f * acc_s[k][2 * threadIdx.x + 1];
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      *reinterpret_cast<uint32_t*>(out + out_row * kD + 2 * threadIdx.x) = pack_bf16x2(x * inv, y * inv);
+      if (out_lse && threadIdx.x == 0) out_lse[out_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
+  }
+}
+
 // How the heads of a call are laid over the consumer warps.
 struct HeadPlan {
   int heads, head_groups, mtiles, replicas, step_pages;
@@ -621,7 +649,10 @@ cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const Paged
                                        Cfg<kD>::kFixed + (kMaxBatch + 1) * 4);
   if (e != cudaSuccess) return e;
   e = launch_pdl(paged_decode_kernel<kD>, dim3(grid), dim3(Cfg<kD>::kThreads), smem, stream, kmap, vmap, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  if (e != cudaSuccess || !a.deferred) return e;
+  const int rows = a.heads * a.group;
+  return launch_pdl(paged_join_kernel<kD>, dim3(std::min(grid * rows, 8 * grid)), dim3(kJoinWarps * 32), 0, stream,
+                    a.o_part, a.lse_part, a.joins, grid, rows, a.out, a.out_lse);
 }
 
 }  // namespace
@@ -637,11 +668,15 @@ int paged_decode_box_heads(int num_kv_heads, int num_q_heads, int head_dim) {
   return head_plan(num_kv_heads, num_q_heads / num_kv_heads, head_dim).heads;
 }
 
-// Partials of every CTA (outputs, then log-sum-exps), then the arrival counters.
-size_t paged_decode_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
+// Arrival counters and joins (the same place for every shape, so that a workspace serves calls of all shapes
+// that it is large enough for), then the CTAs' partials.
+constexpr size_t kCounterBytes = kMaxCtas * (sizeof(uint32_t) + sizeof(int2));
+static_assert(kCounterBytes % 16 == 0, "the partials are 16-byte aligned");
+
+size_t paged_decode_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
   const HeadPlan p = head_plan(num_kv_heads, num_q_heads / num_kv_heads, head_dim);
   const size_t rows = (size_t)p.heads * (num_q_heads / num_kv_heads);
-  return (2 * kMaxCtas * rows * (head_dim + 1) + (size_t)batch * p.head_groups) * sizeof(float);
+  return kCounterBytes + 2 * kMaxCtas * rows * (head_dim + 1) * sizeof(float);
 }
 
 cudaError_t launch_paged_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, const KvView& kv, const uint16_t* q,
@@ -673,11 +708,20 @@ cudaError_t launch_paged_decode(const CUtensorMap& kmap, const CUtensorMap& vmap
   a.out = out;
   a.out_lse = out_lse;
   const size_t rows = (size_t)p.heads * group;
-  a.o_part = static_cast<float*>(workspace);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.arrivals = reinterpret_cast<uint32_t*>(ws);
+  a.joins = reinterpret_cast<int2*>(ws + kMaxCtas * sizeof(uint32_t));
+  a.o_part = reinterpret_cast<float*>(ws + kCounterBytes);
   a.lse_part = a.o_part + 2 * kMaxCtas * rows * kv.head_dim;
-  a.arrivals = reinterpret_cast<uint32_t*>(a.lse_part + 2 * kMaxCtas * rows);
   a.err = err;
   const int grid = sm_count < kMaxCtas ? sm_count : kMaxCtas;
+  // The most partials an item can leave, from the width of the table (or of the windows) alone.
+  long long pages = bt_stride;
+  if (recent_tokens > 0)
+    pages = std::min(pages, ((long long)sink_tokens + kPageSize - 1) / kPageSize + recent_tokens / kPageSize + 2);
+  const long long most = std::min<long long>(grid, pages / (2 * p.step_pages) + 2);
+  a.inline_splits = std::max<int>(2, kInlineBytes / (int)(rows * kv.head_dim * 4));
+  a.deferred = most > a.inline_splits;
   switch (kv.head_dim) {
     case 64: return launch<64>(kmap, vmap, a, grid, stream);
     case 128: return launch<128>(kmap, vmap, a, grid, stream);

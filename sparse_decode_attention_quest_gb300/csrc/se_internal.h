@@ -170,7 +170,7 @@ cudaError_t launch_kv_store(const KvView& kv, uint16_t* k_mut, uint16_t* v_mut, 
 int paged_decode_max_batch();
 bool paged_decode_supported(int num_kv_heads, int head_dim, int head_dim_v, int num_q_heads);
 int paged_decode_box_heads(int num_kv_heads, int num_q_heads, int head_dim);
-size_t paged_decode_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim);
+size_t paged_decode_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim);
 // kmap, vmap: the caches as (64 dims, row, 64-dim chunk), boxes of 64 x 16 paged_decode_box_heads x all
 // chunks, 128-byte swizzle.
 cudaError_t launch_paged_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, const KvView& kv, const uint16_t* q,
@@ -181,11 +181,15 @@ cudaError_t launch_paged_decode(const CUtensorMap& kmap, const CUtensorMap& vmap
 
 // ---- latent_decode.cu: the same over a latent cache (576-dim rows, value = first 512 dims)
 bool paged_latent_supported(int num_kv_heads, int head_dim, int head_dim_v, int num_q_heads);
-size_t paged_latent_workspace_bytes(int32_t batch, int32_t num_q_heads);
-cudaError_t launch_paged_latent(const KvView& kv, const uint16_t* q, long long q_stride, int32_t num_q_heads,
-                                const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens, int32_t batch,
-                                int32_t sink_tokens, int32_t recent_tokens, float sm_scale, uint16_t* out,
-                                float* out_lse, void* workspace, int sm_count, unsigned* err, cudaStream_t stream);
+int paged_latent_max_batch();
+size_t paged_latent_workspace_bytes(int32_t num_q_heads);
+// kvmap: the cache as (64 dims, row, 64-dim chunk), boxes of 64 x 8 x 9; qmap: the queries as
+// [batch][num_q_heads][576], boxes of 64 x num_q_heads x 1 (both 128-byte swizzle).
+cudaError_t launch_paged_latent(const CUtensorMap& kvmap, const CUtensorMap& qmap, const KvView& kv,
+                                int32_t num_q_heads, const int32_t* block_table, int32_t bt_stride,
+                                const int32_t* seq_lens, int32_t batch, int32_t sink_tokens, int32_t recent_tokens,
+                                float sm_scale, uint16_t* out, float* out_lse, void* workspace, int sm_count,
+                                unsigned* err, cudaStream_t stream);
 
 // ---- api.cu: per-device context and helpers shared with other entry points
 cudaError_t device_context(int* sm_count, unsigned** err);

@@ -112,31 +112,37 @@ def test_decode_workspace_size(se_lib):
         assert f(*bad) == 0
 
 
-def test_binding_refuses_what_the_pointers_cannot_tell():
-    kv = _kv()
-    rows = torch.zeros(3, 4, 128, dtype=torch.bfloat16)
-    slots = torch.zeros(3, dtype=torch.int32)
-    with pytest.raises(ValueError, match="CUDA tensor"):
-        se._rows_ptr(rows, 4, 128, torch.bfloat16, "k_new")
-    for t, kind in [(rows.float(), TypeError), (rows[:, :2], ValueError), (rows[0], ValueError)]:
-        fake = _Fake(t)
-        with pytest.raises(kind):
-            se._rows_ptr(fake, 4, 128, torch.bfloat16, "k_new")
-    with pytest.raises(ValueError, match="dense"):
-        se._rows_ptr(_Fake(torch.zeros(3, 128, 4, dtype=torch.bfloat16).transpose(1, 2)), 4, 128, torch.bfloat16, "k")
-    # Rows a fused projection's width apart, and a single row of any stride, are fine.
-    fused = torch.zeros(5, 12, 128, dtype=torch.bfloat16)
-    assert se._rows_ptr(_Fake(fused[:, 4:8]), 4, 128, torch.bfloat16, "k")[1] == 12 * 128
-    assert se._rows_ptr(_Fake(fused[:1, 4:8]), 4, 128, torch.bfloat16, "k")[1] == 4 * 128
-    with pytest.raises(ValueError, match="elements"):
-        se._same_len(slots, 4, "slots")
-    assert kv.num_kv_heads == 4
-
-
-class _Fake(torch.Tensor):
-    """A CPU tensor that says it is on the GPU (its pointer is not used)."""
+class _OnGpu(torch.Tensor):
+    """A CPU tensor that says it is on cuda:0 (its pointer is not used)."""
     @staticmethod
     def __new__(cls, t):
         return torch.Tensor._make_subclass(cls, t)
 
     is_cuda = True
+
+    def get_device(self):
+        return 0
+
+
+def test_binding_refuses_what_the_pointers_cannot_tell():
+    bf16 = torch.bfloat16
+    rows = torch.zeros(3, 4, 128, dtype=bf16)
+    for t, dev, kind, text in [(rows, 0, ValueError, "CUDA tensor"), (_OnGpu(rows), 1, ValueError, "current device"),
+                               (_OnGpu(rows.float()), 0, TypeError, "expected"), (3, 0, TypeError, "torch.Tensor"),
+                               (_OnGpu(rows[:, :2]), 0, ValueError, "shape"), (_OnGpu(rows[0]), 0, ValueError, "shape"),
+                               (_OnGpu(torch.zeros(3, 128, 4, dtype=bf16).transpose(1, 2)), 0, ValueError, "dense")]:
+        with pytest.raises(kind, match=text):
+            se._rows_ptr(t, 4, 128, bf16, "k_new", dev)
+    # Rows a fused projection's width apart, and a single row of any stride, are fine.
+    fused = torch.zeros(5, 12, 128, dtype=bf16)
+    assert se._rows_ptr(_OnGpu(fused[:, 4:8]), 4, 128, bf16, "k", 0)[1] == 12 * 128
+    assert se._rows_ptr(_OnGpu(fused[:1, 4:8]), 4, 128, bf16, "k", 0)[1] == 4 * 128
+    slots = torch.zeros(4, 6, dtype=torch.int32)
+    for t, n, kind, text in [(slots, 24, ValueError, "CUDA tensor"), (_OnGpu(slots), 23, ValueError, "elements"),
+                             (_OnGpu(slots.long()), 24, TypeError, "expected"),
+                             (_OnGpu(slots.t()), 24, ValueError, "contiguous")]:
+        with pytest.raises(kind, match=text):
+            se._vec(t, n, torch.int32, "slots", 0)
+    with pytest.raises(ValueError, match="pages"):
+        se._table(_OnGpu(slots[0]), "block_table", 0)
+    assert se._table(_OnGpu(slots), "block_table", 0)[1:] == (4, 6)
