@@ -51,13 +51,14 @@ constexpr int kChunkBytes = kGroupRows * 128;
 constexpr int kGroupBytes = kChunks * kChunkBytes;      // 9 KB: one TMA box
 constexpr int kStageBytes = (kTileTok / kGroupRows) * kGroupBytes;  // 72 KB
 constexpr int kStages = 2;
-constexpr int kPrefetch = 4;                            // tiles ahead in L2
+constexpr int kPrefetch = 2;                            // tiles ahead in L2
 constexpr int kQRows = 64;
 constexpr int kQBytes = kChunks * kQRows * 128;
 constexpr int kPOff = 8 * kChunkBytes;                  // P of a group: over its RoPE chunk
 constexpr int kQOff = kStages * kStageBytes;
 constexpr int kMiscOff = kQOff + kQBytes;
 constexpr int kSoftThreads = 256;                       // warps 0-7: softmax + epilogue
+constexpr int kSoftWarps = kSoftThreads / 32;
 constexpr int kSWarp = 8;                               // issues S^T, owns TMEM
 constexpr int kPvWarp = 9;                              // issues PV
 constexpr int kLoadWarp = 10;                           // copies
@@ -197,13 +198,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
   uint64_t* s_full = bars + 4;   // [2] S^T of a tile is in TMEM
   uint64_t* s_free = bars + 6;   // [2] S^T read by the softmax threads
   uint64_t* p_full = bars + 8;   // [2] P written, rows not kept zeroed, O^T rescaled
-  uint64_t* o_done = bars + 10;  // the PV products of a tile are done
   uint64_t* o_free = bars + 11;  // O^T read by the epilogue
   uint64_t* q_full = bars + 12;  // the request's queries landed
   uint64_t* q_empty = bars + 13; // the last S^T product of a segment is done
   uint64_t* fin = bars + 14;     // every product of the CTA is done (both issuers)
   // The PV products of a segment's last tile are done, one phase per segment: the epilogue cannot wait on
-  // o_done, which may be a phase behind (a parity wait names the current or the preceding phase only).
+  // empty, which may be a phase behind (a parity wait names the current or the preceding phase only).
   uint64_t* o_last = bars + 15;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + kTmemSlotOff);
   uint32_t* masks = reinterpret_cast<uint32_t*>(misc + kMaskOff);
@@ -240,11 +240,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
       mbar_init(&s_full[s], 1);
-      mbar_init(&s_free[s], kSoftThreads);
-      mbar_init(&p_full[s], kSoftThreads);
+      mbar_init(&s_free[s], kSoftWarps);
+      mbar_init(&p_full[s], kSoftWarps);
     }
-    mbar_init(o_done, 1);
-    mbar_init(o_free, kSoftThreads);
+    mbar_init(o_free, kSoftWarps);
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(fin, 2);
@@ -380,7 +379,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         for (int mt = 0; mt < 4; ++mt)
           mma_elected(tmem + kOCol + mt * 64, dv + mt * kMt + ks * kStep, dp + ks * kStep, idesc, ks > 0 ? 1u : acc0);
       commit_elected(&empty[s]);
-      commit_elected(o_done);
       if (c.last()) commit_elected(o_last);
     }
     commit_elected(fin);
@@ -410,7 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         for (int i = 0; i < 16; ++i) r[i] = 0u;
       }
       tc05_fence_before();
-      mbar_arrive(&s_free[s]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_free[s]);
       const bool ok_f = mbar_wait(&full[s], (j >> 1) & 1);  // the masks of the tile
       dead = dead || !ok_s || !ok_f;
       const bool tok_ok = in_mask(masks[s * kTilePages + q4], tok);
@@ -466,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         }
         if (__any_sync(0xffffffffu, moved)) {
           // The O^T columns of this warp's head half (its lane quarter) to the new maxima.
-          const bool ok_o = __all_sync(0xffffffffu, mbar_wait(o_done, (j - 1) & 1));
+          const bool ok_o = __all_sync(0xffffffffu, mbar_wait(&empty[s ^ 1], ((j - 1) >> 1) & 1));
           if (ok_o) {
             float fc[32];  // factor of column cc of the half: lanes 0-15 hold heads 0-15, lanes 16-31 heads 16-31
 #pragma unroll
@@ -505,7 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
       st_shared_v4(prow + swz128(row % kGroupRows, (hh >> 3) + 1), pk[4], pk[5], pk[6], pk[7]);
       fence_proxy_async_smem();
       tc05_fence_before();
-      mbar_arrive(&p_full[s]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[s]);
 
       if (c.last()) {
         // ---- epilogue of the segment: O = O^T / l per head, or a partial
@@ -569,7 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
             a.out_lse[(size_t)b * Hq + threadIdx.x] = lse_s[threadIdx.x] * kLn2;
         }
         tc05_fence_before();
-        mbar_arrive(o_free);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_free);
       }
     }
     if (threadIdx.x == 0) a.joins[blockIdx.x] = join;
@@ -583,9 +584,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
   if (warp == kSWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the partials of the items that span CTAs: a CTA per (item, four heads, 32 dims), a share of the partials
-// per warp, joined in warp order. With M_h the largest log-sum-exp of head h,
+// Joins the partials of the items that span CTAs. With M_h the largest log-sum-exp of head h,
 //     out_h = sum_i exp2(lse_hi - M_h) o_hi / sum_i exp2(lse_hi - M_h).
+// A warp takes four heads and 32 dims of an item; share_of(partials) warps share the partials of an item that
+// has many, and are joined in their order.
 __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const float* __restrict__ o_part,
                                                                      const float* __restrict__ lse_part,
                                                                      const int2* __restrict__ joins, int32_t ctas,
@@ -598,13 +600,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const floa
   __shared__ float4 acc_s[kJoinWarps][32], m_s[kJoinWarps], l_s[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ntodo = list_joins(joins, ctas, todo, counts);
-  const int per_item = (Hq / 4) * (kDv / 32);
-  for (int u = blockIdx.x; u < ntodo * per_item; u += gridDim.x) {
-    const int3 jn = todo[u / per_item];
-    const int blk = u % per_item / (kDv / 32), d = u % (kDv / 32) * 32 + lane;
+  const int tasks = (Hq / 4) * (kDv / 32);
+  for (int u = blockIdx.x; u < ntodo * tasks; u += gridDim.x) {
+    const int3 jn = todo[u / tasks];
+    const int share = share_of(jn.z), k0 = u % tasks * (kJoinWarps / share);
+    if (k0 >= tasks) continue;  // fewer CTAs serve an item whose warps do not share
+    const int task = k0 + warp / share, sub = warp % share;  // tasks is a multiple of the warps
+    const int blk = task / (kDv / 32), d = task % (kDv / 32) * 32 + lane;
     // Partial i is in slot 1 of the item's first CTA (i = 0), in slot 0 of the others.
     auto part = [&](int i) { return (size_t)(2 * (jn.x + i) + (i == 0)) * (Hq / 4) + blk; };
-    const int mine = warp + kJoinWarps * lane;
+    const int mine = sub + share * lane;
     float4 w = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     if (mine < jn.z) w = *reinterpret_cast<const float4*>(lse_part + part(mine) * 4);
     float4 M = w;
@@ -615,15 +620,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const floa
       M.z = fmaxf(M.z, __shfl_xor_sync(0xffffffffu, M.z, o));
       M.w = fmaxf(M.w, __shfl_xor_sync(0xffffffffu, M.w, o));
     }
-    w = make_float4(fast_exp2(w.x - (M.x == -INFINITY ? 0.f : M.x)), fast_exp2(w.y - (M.y == -INFINITY ? 0.f : M.y)),
-                    fast_exp2(w.z - (M.z == -INFINITY ? 0.f : M.z)), fast_exp2(w.w - (M.w == -INFINITY ? 0.f : M.w)));
+    w = make_float4(fast_exp2(w.x - finite_base(M.x)), fast_exp2(w.y - finite_base(M.y)),
+                    fast_exp2(w.z - finite_base(M.z)), fast_exp2(w.w - finite_base(M.w)));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), l = acc;
-    const int n = (jn.z - warp + kJoinWarps - 1) / kJoinWarps;
+    const int n = (jn.z - sub + share - 1) / share;
 #pragma unroll 4
     for (int k = 0; k < n; ++k) {
       const float4 f = make_float4(__shfl_sync(0xffffffffu, w.x, k), __shfl_sync(0xffffffffu, w.y, k),
                                    __shfl_sync(0xffffffffu, w.z, k), __shfl_sync(0xffffffffu, w.w, k));
-      const float4 v = *reinterpret_cast<const float4*>(o_part + (part(warp + kJoinWarps * k) * kDv + d) * 4);
+      const float4 v = *reinterpret_cast<const float4*>(o_part + (part(sub + share * k) * kDv + d) * 4);
       acc = make_float4(acc.x + f.x * v.x, acc.y + f.y * v.y, acc.z + f.z * v.z, acc.w + f.w * v.w);
       l = make_float4(l.x + f.x, l.y + f.y, l.z + f.z, l.w + f.w);
     }
@@ -634,23 +639,24 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const floa
       l_s[warp] = l;
     }
     __syncthreads();
-    if (warp < 4) {  // warp h: head 4 blk + h
-      auto at = [&](const float4& v) { return warp == 0 ? v.x : warp == 1 ? v.y : warp == 2 ? v.z : v.w; };
+    // The output (head, 32 dims) pairs of the CTA's tasks, a warp each.
+    for (int x = warp; x < 4 * kJoinWarps / share; x += kJoinWarps) {
+      const int w0 = x / 4 * share, h = x % 4, tk = k0 + x / 4;
+      auto at = [&](const float4& v) { return h == 0 ? v.x : h == 1 ? v.y : h == 2 ? v.z : v.w; };
       float top = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, at(m_s[k]));
-      const float base = top == -INFINITY ? 0.f : top;
+      for (int k = 0; k < share; ++k) top = fmaxf(top, at(m_s[w0 + k]));
+      const float base = finite_base(top);
       float sum = 0.f, o = 0.f;
-#pragma unroll
-      for (int k = 0; k < kJoinWarps; ++k) {
-        const float f = fast_exp2(at(m_s[k]) - base);
-        sum += f * at(l_s[k]);
-        o += f * at(acc_s[k][lane]);
+      for (int k = 0; k < share; ++k) {
+        const float f = fast_exp2(at(m_s[w0 + k]) - base);
+        sum += f * at(l_s[w0 + k]);
+        o += f * at(acc_s[w0 + k][lane]);
       }
-      const size_t orow = (size_t)jn.y * Hq + blk * 4 + warp;
+      const size_t orow = (size_t)jn.y * Hq + tk / (kDv / 32) * 4 + h;
+      const int od = tk % (kDv / 32) * 32 + lane;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      out[orow * kDv + d] = (uint16_t)(pack_bf16x2(o * inv, 0.f) & 0xffffu);
-      if (out_lse && d == 0) out_lse[orow] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+      out[orow * kDv + od] = (uint16_t)(pack_bf16x2(o * inv, 0.f) & 0xffffu);
+      if (out_lse && od == 0) out_lse[orow] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
   }
 }

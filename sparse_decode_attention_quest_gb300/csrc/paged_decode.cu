@@ -16,12 +16,11 @@
 //    spans CTAs leaves a partial (output, log-sum-exp) per CTA; a CTA has at
 //    most two, for the item it starts inside and the item it ends inside, so
 //    the workspace does not grow with the lengths.
-//  * Join: the CTA that publishes an item's last partial merges them in the order
-//    of the pages, while they are few enough for one SM (kInlineBytes); the
-//    partials of an item over more CTAs go to a second kernel, a CTA per row,
-//    which is launched when the table's width allows such items. One CTA reads
-//    partials from L2 at about 60 bytes a clock: merging 32 of 16 KB took it 25 of
-//    46 us (4 requests of 2.5K tokens, 32 query heads).
+//  * Join: where the table's width bounds an item's partials to kInlineBytes, the
+//    CTA that publishes an item's last partial merges them in the order of the
+//    pages. Otherwise a second kernel does, a warp per row: one CTA reads
+//    partials from L2 at some 60 bytes a clock, and merging 32 of 16 KB took it
+//    25 of 46 us (4 requests of 2.5K tokens, 32 query heads).
 //  * Copies: a page's rows of one KV head are 16 x D bf16, and the heads of a
 //    group of Hc lie next to each other, so that one TMA box of 64 dims x
 //    16 Hc rows x D / 64 brings a whole page of the group (16 to 32 KB for 4 to 8
@@ -48,7 +47,7 @@ constexpr int kMetaRing = 4;     // steps whose page masks are held (at most thr
 constexpr int kMaxPages = 16;    // pages of a step
 constexpr int kMaxCtas = 192;    // partial slots: two per CTA
 constexpr int kMaxBatch = 4096;  // requests whose prefix fits beside the ring
-constexpr int kInlineBytes = 128 * 1024;  // partials of an item that one CTA merges
+constexpr int kInlineBytes = 48 * 1024;  // partials of an item, at most, where one CTA merges them
 constexpr int kJoinWarps = 8;
 
 template <int kD>
@@ -88,7 +87,6 @@ struct PagedArgs {
   // An item that spans CTAs is the only one to go on behind its first CTA, so that CTA's index names it.
   uint32_t* arrivals;   // [kMaxCtas] by first CTA, zero between calls
   int2* joins;          // [CTAs] by first CTA: item and partials for the join kernel (0 partials: nothing to do)
-  int32_t inline_splits;  // most partials that a CTA of this kernel merges
   bool deferred;        // the join kernel follows
   unsigned* err;
 };
@@ -377,7 +375,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
     const bool split = seg.lo > 0 || seg.hi < seg.n;
     const int slot = seg.lo > 0 ? 0 : 1;
     const int parts = split ? (seg.item_start + seg.n - 1) / per_cta - first_cta + 1 : 0;
-    const bool here = split && parts <= a.inline_splits;
+    const bool here = split && !a.deferred;
     const int item = seg.b * HG + seg.hg;
     if (here && slot == 0) {
       shared0 = true;
@@ -538,9 +536,10 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
   }
 }
 
-// Merges the partials of the items that span many CTAs: a CTA per (item, row), a share of the
-// partials per warp, joined in warp order. With M the largest log-sum-exp,
+// Joins the partials of the items that span many CTAs. With M the largest log-sum-exp of a row,
 //     out = sum_i exp2(lse_i - M) o_i / sum_i exp2(lse_i - M).
+// A warp takes a row; share_of(partials) warps share the partials of an item that has many, and are joined in
+// their order.
 template <int kD>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const float* __restrict__ o_part,
                                                                     const float* __restrict__ lse_part,
@@ -558,27 +557,28 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const float
   const int ntodo = list_joins(joins, ctas, todo, counts);
   for (int u = blockIdx.x; u < ntodo * rows; u += gridDim.x) {
     const int3 jn = todo[u / rows];
-    const int r = u % rows;
-    const size_t out_row = (size_t)jn.y * rows + r;
+    const int share = share_of(jn.z), r0 = u % rows * (kJoinWarps / share);
+    if (r0 >= rows) continue;  // fewer CTAs serve an item whose warps do not share
+    const int r = min(r0 + warp / share, rows - 1), sub = warp % share;
     // Partial i is in slot 1 of the item's first CTA (i = 0), in slot 0 of the others.
     auto part = [&](int i) { return (size_t)(2 * (jn.x + i) + (i == 0)) * rows + r; };
-    const int mine = warp + kJoinWarps * lane;
+    const int mine = sub + share * lane;
     const float ls = mine < jn.z ? lse_part[part(mine)] : -INFINITY;
     float M = ls;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float w = fast_exp2(ls - (M == -INFINITY ? 0.f : M));
+    const float w = fast_exp2(ls - finite_base(M));
     float l = w;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     float acc[kV];
 #pragma unroll
     for (int x = 0; x < kV; ++x) acc[x] = 0.f;
-    const int n = (jn.z - warp + kJoinWarps - 1) / kJoinWarps;
+    const int n = (jn.z - sub + share - 1) / share;
 #pragma unroll 4
     for (int k = 0; k < n; ++k) {
       const float f = __shfl_sync(0xffffffffu, w, k);
-      const float* p = o_part + part(warp + kJoinWarps * k) * kD + lane * kV;
+      const float* p = o_part + part(sub + share * k) * kD + lane * kV;
       if constexpr (kV == 2) {
         const float2 v = *reinterpret_cast<const float2*>(p);
         acc[0] += f * v.x;
@@ -602,22 +602,24 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const float
       l_s[warp] = l;
     }
     __syncthreads();
-    if (threadIdx.x < kD / 2) {
-      float top = m_s[0];
-#pragma unroll
-      for (int k = 1; k < kJoinWarps; ++k) top = fmaxf(top, m_s[k]);
-      const float base = top == -INFINITY ? 0.f : top;
+    // The CTA's rows, in pairs of values.
+    for (int e = threadIdx.x; e < kJoinWarps / share * (kD / 2); e += kJoinWarps * 32) {
+      const int w0 = e / (kD / 2) * share, d = e % (kD / 2) * 2, row = r0 + e / (kD / 2);
+      if (row >= rows) continue;
+      float top = -INFINITY;
+      for (int k = 0; k < share; ++k) top = fmaxf(top, m_s[w0 + k]);
+      const float base = finite_base(top);
       float sum = 0.f, x = 0.f, y = 0.f;
-#pragma unroll
-      for (int k = 0; k < kJoinWarps; ++k) {
-        const float f = fast_exp2(m_s[k] - base);
-        sum += f * l_s[k];
-        x += f * acc_s[k][2 * threadIdx.x];
-        y += f * acc_s[k][2 * threadIdx.x + 1];
+      for (int k = 0; k < share; ++k) {
+        const float f = fast_exp2(m_s[w0 + k] - base);
+        sum += f * l_s[w0 + k];
+        x += f * acc_s[w0 + k][d];
+        y += f * acc_s[w0 + k][d + 1];
       }
+      const size_t orow = (size_t)jn.y * rows + row;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      *reinterpret_cast<uint32_t*>(out + out_row * kD + 2 * threadIdx.x) = pack_bf16x2(x * inv, y * inv);
-      if (out_lse && threadIdx.x == 0) out_lse[out_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+      *reinterpret_cast<uint32_t*>(out + orow * kD + d) = pack_bf16x2(x * inv, y * inv);
+      if (out_lse && d == 0) out_lse[orow] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
   }
 }
@@ -720,8 +722,7 @@ cudaError_t launch_paged_decode(const CUtensorMap& kmap, const CUtensorMap& vmap
   if (recent_tokens > 0)
     pages = std::min(pages, ((long long)sink_tokens + kPageSize - 1) / kPageSize + recent_tokens / kPageSize + 2);
   const long long most = std::min<long long>(grid, pages / (2 * p.step_pages) + 2);
-  a.inline_splits = std::max<int>(2, kInlineBytes / (int)(rows * kv.head_dim * 4));
-  a.deferred = most > a.inline_splits;
+  a.deferred = most * (long long)(rows * kv.head_dim * sizeof(float)) > kInlineBytes;
   switch (kv.head_dim) {
     case 64: return launch<64>(kmap, vmap, a, grid, stream);
     case 128: return launch<128>(kmap, vmap, a, grid, stream);

@@ -109,4 +109,10 @@ __device__ __forceinline__ int list_joins(const int2* joins, int ctas, int3* tod
   return all;
 }
 
+// Warps that share the partials of an item: each takes eight or fewer, until all eight warps of a CTA share.
+__device__ __forceinline__ int share_of(int partials) { return partials <= 8 ? 1 : partials <= 16 ? 2 : partials <= 32 ? 4 : 8; }
+
+// The base of exponentials whose largest argument is m: 0 where nothing but -inf has been seen.
+__device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
+
 }  // namespace se
