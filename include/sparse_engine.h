@@ -401,8 +401,8 @@ SE_API se_status_t se_block_tables_release(int32_t* free_pages, int32_t* pool_st
  * token by token: from the new keys alone for a page whose slot 0 is among them,
  * otherwise together with the page's present summary. The new tokens of one page stand
  * next to each other in the batch, as in the slot map of se_block_tables_extend, and a
- * slot is named once. A slot named twice in neighbouring tokens keeps the later one
- * (with kv->summary); elsewhere, and without kv->summary, it holds rows of either.
+ * slot is named once. A slot named twice in neighbouring tokens of one page keeps the
+ * later row; elsewhere it holds pieces of either.
  * head_dim and head_dim_v: multiples of 8 up to 576. A slot at or behind num_pages * 16 sets
  * SE_DEVERR_PAGE_RANGE and is skipped.
  */

@@ -849,7 +849,7 @@ se_status_t se_paged_kv_store(const se_paged_kv_t* kv, const void* k_new, int64_
   if (e != cudaSuccess) return cuda_fail(fn, e);
   e = se::launch_kv_store(view_of(kv), static_cast<uint16_t*>(kv->k), static_cast<uint16_t*>(kv->v),
                           static_cast<const uint16_t*>(k_new), k_stride, static_cast<const uint16_t*>(v_new), v_stride,
-                          slot_map, num_tokens, d->err, static_cast<cudaStream_t>(stream));
+                          slot_map, num_tokens, d->sm_count, d->err, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SE_OK : cuda_fail(fn, e);
 }
 

@@ -164,7 +164,7 @@ cudaError_t launch_block_tables_release(int32_t* free_pages, int32_t* pool_state
 // ---- kv_store.cu: rows of new tokens into their slots (+ summaries when kv.summary is set)
 cudaError_t launch_kv_store(const KvView& kv, uint16_t* k_mut, uint16_t* v_mut, const uint16_t* k_new,
                             long long k_stride, const uint16_t* v_new, long long v_stride, const int32_t* slot_map,
-                            int32_t num_tokens, unsigned* err, cudaStream_t stream);
+                            int32_t num_tokens, int sm_count, unsigned* err, cudaStream_t stream);
 
 // ---- paged_decode.cu: one new token over the whole cache, or over a sink and a recent window
 int paged_decode_max_batch();
