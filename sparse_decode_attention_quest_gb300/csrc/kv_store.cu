@@ -16,10 +16,10 @@
 // nothing is exchanged between threads. What counts is bytes in flight: 80
 // registers a thread (24 warps on an SM) without a spill carry 4 x 32K tokens of 8
 // heads at 6.58 TB/s (168 us; 97% of the measured copy rate), 64 registers with
-// 24 bytes spilled 183 us, and per-token row lookups in the loop 238 us. The window is 16 tokens, about a run of a
-// prompt, for long batches, and shorter where there are fewer windows than
-// warps, down to one token for a decode step, whose tokens lie in pages of
-// their own.
+// 24 bytes spilled 183 us, and per-token row lookups in the loop 238 us.
+// The window is 16 tokens, about a run of a prompt, for long batches, and shorter
+// where there are fewer windows than warps, down to one token for a decode step,
+// whose tokens lie in pages of their own.
 #include "se_ptx.cuh"
 
 namespace se {
@@ -97,13 +97,16 @@ __global__ void __launch_bounds__(kWarps * 32, 3) store_kernel(const StoreArgs a
     uint4 mn = make_uint4(0x7f807f80u, 0x7f807f80u, 0x7f807f80u, 0x7f807f80u);  // +inf
     uint4 mx = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);  // -inf
     bool opened = false;
-    // The run's length as far as the lanes see it.
+    // The run's length: as far as the lanes see it, and from memory behind them.
     const uint32_t same = __ballot_sync(0xffffffffu, pg == page) >> i0;
     const int seen = same == (0xffffffffu >> i0) ? 32 - i0 : __ffs(~same) - 1;
     const int first = t0 - 1 + i0, s0 = __shfl_sync(0xffffffffu, sl, i0);
     const uint32_t inrow = __ballot_sync(0xffffffffu, sl - s0 == lane - i0) >> i0;
     const uint16_t* from = src + (size_t)first * src_stride;
-    const bool ordered = i0 + seen < 32 && (inrow & ((1u << seen) - 1)) == (1u << seen) - 1;
+    int n = seen;
+    if (i0 + seen == 32)
+      while (first + n < T && a.slot_map[first + n] >= 0 && a.slot_map[first + n] / kPageSize == page) ++n;
+    const bool ordered = n == seen && (inrow & ((1u << seen) - 1)) == (1u << seen) - 1;
     if (ordered) {
       // Rows one after another in the page, as a slot map built from lengths has them.
       const int r0 = s0 % kPageSize;
@@ -139,10 +142,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) store_kernel(const StoreArgs a
         }
       }
     } else {
-      // Rows in any order, and a run of more tokens than the lanes see (slots named twice).
-      int n = seen;
-      if (i0 + seen == 32)
-        while (first + n < T && a.slot_map[first + n] >= 0 && a.slot_map[first + n] / kPageSize == page) ++n;
+      // Rows in any order, and a run of more tokens than a page has (slots named twice).
       for (int k = 0; k < n; ++k) {
         const int row = a.slot_map[first + k] % kPageSize;
         opened = opened || row == 0;

@@ -102,6 +102,20 @@ def test_latent_rows(cuda_device, summary):
     _check(cuda_device, slots, pages, 1, 576, Dv=512, latent=True, summary=summary)
 
 
+@pytest.mark.parametrize("before", range(16))
+def test_long_prompts_at_every_offset(cuda_device, before):
+    """Long batches are cut into windows of 16 tokens: runs that begin at each place of a window."""
+    slots, pages = _slots([(before, 5200 - before), (0, 30 + before), (before, 5200)], torch.Generator().manual_seed(9))
+    _check(cuda_device, slots, pages, 8, 128, seed=before)
+
+
+def test_a_slot_named_twice_behind_a_full_page(cuda_device):
+    """A page's 16 tokens at a window's end, and one of its slots once more behind it."""
+    slots, pages = _slots([(0, 5000)], torch.Generator().manual_seed(10))
+    slots = slots[:1] + slots[:2031] + [slots[2030]] + slots[2031:]
+    _check(cuda_device, slots, pages, 8, 128)
+
+
 @pytest.mark.parametrize("summary", [True, False])
 def test_padding_is_skipped(cuda_device, summary):
     slots, pages = _slots(RUNS["ragged"], torch.Generator().manual_seed(5))
