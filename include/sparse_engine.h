@@ -435,9 +435,9 @@ SE_API se_status_t se_paged_kv_store(const se_paged_kv_t* kv, const void* k_new,
  * pages by the lengths alone and joined in a fixed order: equal inputs give equal bits.
  * Shapes: head_dim = head_dim_v of 64, 128 or 256 with 1..64 query heads per KV head, or a latent
  * cache (head_dim 576, head_dim_v 512, one KV head, kv->v == kv->k, 16..64 query heads in
- * multiples of 16); batch <= 4096 (latent cache: 1024). The kept pages of a batch, summed over its requests and
- * times num_kv_heads, stay below 2^31 (beyond: SE_DEVERR_LENGTH, and the last requests are
- * cut short).
+ * multiples of 16); batch <= 4096 (latent cache: 512). The kept pages of a batch and 16 more per request, times
+ * num_kv_heads, stay below 2^31 (beyond: SE_DEVERR_LENGTH, and the last requests count as
+ * empty).
  * se_paged_decode_workspace_size returns 0 for sizes that are not supported.
  */
 SE_API size_t se_paged_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,

@@ -887,7 +887,7 @@ se_status_t se_paged_decode(const se_paged_kv_t* kv, const void* q, int64_t q_st
   if (bt_stride < 1) return fail(SE_ERR_INVALID_ARG, fn, "bt_stride < 1");
   if (bt_stride >= (1 << 27)) return fail(SE_ERR_UNSUPPORTED, fn, "2^27 or more pages per request");
   if (batch > (latent ? se::paged_latent_max_batch() : se::paged_decode_max_batch()))
-    return fail(SE_ERR_UNSUPPORTED, fn, "batch > 4096 (latent cache: 1024)");
+    return fail(SE_ERR_UNSUPPORTED, fn, "batch > 4096 (latent cache: 512)");
   if (batch == 0) return SE_OK;
   if (!q || !block_table || !seq_lens || !out) return fail(SE_ERR_INVALID_ARG, fn, "NULL pointer");
   if (!aligned16(q) || !aligned16(block_table) || !aligned16(seq_lens) || !aligned16(out) || !aligned16(out_lse) ||

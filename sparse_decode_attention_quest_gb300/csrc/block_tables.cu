@@ -249,8 +249,8 @@ cudaError_t launch_block_tables_extend(const int32_t* free_pages, int32_t* pool_
                                        int32_t* token_start, int32_t* slot_map, int32_t* positions,
                                        int32_t max_new_tokens, int sm_count, unsigned* err, cudaStream_t stream) {
   const size_t smem = (3 * (size_t)batch + 1) * sizeof(int);
-  cudaError_t e = cudaFuncSetAttribute(extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (3 * block_tables_max_batch() + 1) * (int)sizeof(int));
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(extend_kernel, (3 * block_tables_max_batch() + 1) * (int)sizeof(int), allowed);
   if (e != cudaSuccess) return e;
   e = launch_pdl(extend_kernel, dim3(grid_for(max_new_tokens, sm_count)), dim3(kThreads), smem, stream, free_pages,
                  pool_state, num_pages, block_table, bt_stride, seq_lens, new_lens, batch, seq_lens_after,
@@ -263,8 +263,8 @@ cudaError_t launch_block_tables_release(int32_t* free_pages, int32_t* pool_state
                                         const int32_t* keep_lens, int32_t batch, int sm_count, unsigned* err,
                                         cudaStream_t stream) {
   const size_t smem = (2 * (size_t)batch + 1) * sizeof(int);
-  cudaError_t e = cudaFuncSetAttribute(release_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (2 * block_tables_max_batch() + 1) * (int)sizeof(int));
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(release_kernel, (2 * block_tables_max_batch() + 1) * (int)sizeof(int), allowed);
   if (e != cudaSuccess) return e;
   const long long most = (long long)batch * bt_stride < num_pages ? (long long)batch * bt_stride : num_pages;
   e = launch_pdl(release_kernel, dim3(grid_for(most, sm_count)), dim3(kThreads), smem, stream, free_pages, pool_state,

@@ -12,10 +12,10 @@
 // 64-token tile takes 1290 clocks for S^T and 870 for PV measured alone, of the
 // 3100 that its 72 KB take at an SM's share of HBM. So both must overlap the copies.
 //
-//  * Work: the kept pages of all requests form one range that the CTAs share
-//    equally, in tiles of 64 tokens (4 pages). An item that spans CTAs leaves a
-//    partial per CTA (at most two per CTA, whatever the lengths), and a second
-//    kernel joins them.
+//  * Work: the requests follow one another on a line, each as long as its kept
+//    pages and an overhead, which the CTAs share equally in tiles of 64 tokens (4
+//    pages). An item that spans CTAs leaves a partial per CTA (at most two per
+//    CTA, whatever the lengths), and a second kernel joins them.
 //  * A tile is eight groups of 8 rows, each group nine 64-dim chunks of 8 rows x
 //    128 bytes, 128-byte swizzled: one 3-D TMA box per group. The queries (72 KB)
 //    leave room for two tiles, 144 KB, which must cover the copies' latency as
@@ -68,8 +68,9 @@ constexpr int kSCol = 0;                                // S^T of tile parity s:
 constexpr int kOCol = 256;                              // O^T M-tile mt: columns 256 + 64 mt
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kSoftBar = 1;
+constexpr int kItemPages = 8;                           // what starting and finishing a request costs, in pages
 constexpr int kMaxCtas = 192;
-constexpr int kMaxBatch = 1024;
+constexpr int kMaxBatch = 512;
 constexpr int kJoinWarps = 8;
 
 // Shared memory behind the queries.
@@ -83,7 +84,7 @@ constexpr int kLinvOff = 3584;    // [64]
 constexpr int kLseOff = 3840;     // [64]
 constexpr int kSumsOff = 4096;    // [12] 64-bit
 constexpr int kPrefixOff = 4224;  // [batch + 1]
-constexpr int kSmemMax = 1024 + kMiscOff + kPrefixOff + (kMaxBatch + 1) * 4;
+constexpr int kSmemMax = 1024 + kMiscOff + kPrefixOff + (2 * kMaxBatch + 1) * 4;
 static_assert(kSmemMax <= 227 * 1024, "the largest batch fits");
 
 struct LatentArgs {
@@ -144,35 +145,20 @@ __device__ __forceinline__ int reduced_index(int lane) {
   return 8 * (lane & 1) + 4 * ((lane >> 1) & 1) + 2 * ((lane >> 2) & 1) + ((lane >> 3) & 1);
 }
 
-// The tiles of a CTA's slice in order: segments (the pages [lo, hi) of a request), cut into tiles of 4 pages.
+// The tiles of a CTA's slice in order: its segments, cut into tiles of 4 pages.
 struct TileCursor {
-  const int* prefix;
-  int end, x;
-  int item, lo, hi, n, item_start, ntiles, t, seg, j;
+  Segments sg;
+  int ntiles, t, seg, j;
   bool valid;
   __device__ void open() {
-    valid = x < end;
+    valid = sg.next();
     if (!valid) return;
-    while (prefix[item + 1] <= x) ++item;
-    item_start = prefix[item];
-    n = prefix[item + 1] - item_start;
-    lo = x - item_start;
-    hi = min(n, end - item_start);
-    x = item_start + hi;
-    ntiles = (hi - lo + kTilePages - 1) / kTilePages;
+    ntiles = (sg.hi - sg.lo + kTilePages - 1) / kTilePages;
     t = 0;
   }
-  __device__ void init(const int* pf, int batch, int start, int stop) {
-    prefix = pf;
-    end = stop;
-    x = start;
+  __device__ void init(const Slices& slices, int start, int stop) {
+    sg.init(slices, start, stop);
     seg = j = 0;
-    int l = 0, h = batch;
-    while (h - l > 1) {
-      const int mid = (l + h) >> 1;
-      if (prefix[mid] <= start) l = mid; else h = mid;
-    }
-    item = l;
     open();
   }
   __device__ bool last() const { return t == ntiles - 1; }
@@ -213,10 +199,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
   float* linv = reinterpret_cast<float*>(misc + kLinvOff);
   float* lse_s = reinterpret_cast<float*>(misc + kLseOff);
   int* prefix = reinterpret_cast<int*>(misc + kPrefixOff);
+  int* lens = prefix + a.batch + 1;  // [batch]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hq = a.Hq;
 
-  kept_prefix<kThreads>(a.seq_lens, a.batch, a.bt_stride, a.sink, a.recent, 0x7fffffff, prefix,
+  kept_prefix<kThreads>(a.seq_lens, a.batch, a.bt_stride, a.sink, a.recent, kItemPages, 0x7fffffff, prefix, lens,
                         reinterpret_cast<long long*>(misc + kSumsOff), a.err);
   for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
     if (prefix[b + 1] != prefix[b]) continue;  // no kept token: the empty sum
@@ -225,15 +212,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
     if (a.out_lse)
       for (int i = threadIdx.x; i < Hq; i += kThreads) a.out_lse[(size_t)b * Hq + i] = -INFINITY;
   }
-  const int total = prefix[a.batch];
-  int per_cta = (int)(((long long)total + gridDim.x - 1) / gridDim.x);
-  per_cta = max(2 * kTilePages, (per_cta + kTilePages - 1) / kTilePages * kTilePages);
-  const long long start64 = (long long)blockIdx.x * per_cta;
-  if (start64 >= total) {
+  Slices slices;
+  slices.init(prefix, a.batch, 1, kItemPages, kTilePages, gridDim.x);
+  const int2 slice = slice_of(slices, blockIdx.x);
+  if (slice.x >= slice.y) {
     if (threadIdx.x == 0) a.joins[blockIdx.x] = make_int2(0, 0);
     return;
   }
-  const int start = (int)start64, end = (int)min((long long)total, start64 + per_cta);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -258,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
   const uint32_t smem0 = smem_addr(smem);
   bool dead = false;  // a bounded wait gave up: leave the loops, no further waits
   TileCursor c;
-  c.init(prefix, a.batch, start, end);
+  c.init(slices, slice.x, slice.y);
 
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------ copies
@@ -267,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
     int base = 0, cur = 0, nxt = 0;
     const int32_t* bt = nullptr;
     auto entry = [&](int i) {  // physical page of the segment's page i, -1: none
-      if (i >= c.hi) return -1;
+      if (i >= c.sg.hi) return -1;
       const int ph = bt[k.logical(i)];
       if (ph >= 0 && ph < a.num_pages) return ph;
       raise_error(a.err, SE_DEVERR_PAGE_RANGE);
@@ -280,10 +265,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
       return i < base + 32 ? pc : pn;
     };
     for (; c.valid; c.next()) {
-      const int s = c.j & 1, i0 = c.lo + c.t * kTilePages;
+      const int s = c.j & 1, i0 = c.sg.lo + c.t * kTilePages;
       if (c.t == 0) {
-        k = kept_of(a.seq_lens[c.item], a.bt_stride, a.sink, a.recent, nullptr);
-        bt = a.block_table + (size_t)c.item * a.bt_stride;
+        k = kept_of(lens[c.sg.b], a.bt_stride, a.sink, a.recent, nullptr);
+        bt = a.block_table + (size_t)c.sg.b * a.bt_stride;
         base = i0;
         cur = entry(base + lane);
         nxt = entry(base + 32 + lane);
@@ -319,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         }
         if (lane == 0) mbar_arrive_expect_tx(q_full, (uint32_t)Hq * kD * 2);
         __syncwarp();
-        if (lane < kChunks) tma_load_3d(smem + kQOff + lane * kQRows * 128, &qmap, lane * 64, 0, c.item, q_full, policy);
+        if (lane < kChunks) tma_load_3d(smem + kQOff + lane * kQRows * 128, &qmap, lane * 64, 0, c.sg.b, q_full, policy);
       }
     }
     // Every copy has landed before the CTA leaves.
@@ -391,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
     const int hr = hh + reduced_index(lane);  // head of this thread's reduction results
     const int row = q4 * kPageSize + tok;     // token row of the tile
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
+    const int parts1 = neighbours_of(slices, blockIdx.x, slice).parts1;
     int2 join = make_int2(0, 0);              // the item that goes on behind the slice
     float m_h[16], l_h[16];
 #pragma unroll
@@ -509,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
 
       if (c.last()) {
         // ---- epilogue of the segment: O = O^T / l per head, or a partial
-        const int b = c.item;
+        const int b = c.sg.b;
         const bool ok_e = __all_sync(0xffffffffu, mbar_wait(o_last, c.seg & 1));
         dead = dead || !ok_e;
         float w[16];
@@ -528,9 +514,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
           lse_s[h] = l == 0.f ? -INFINITY : mrow[h] + log2f(l);
         }
         named_bar_sync(kSoftBar, kSoftThreads);
-        const bool split = c.lo > 0 || c.hi < c.n;
-        const int slot = 2 * blockIdx.x + (c.lo > 0 ? 0 : 1);
-        if (c.lo == 0 && split) join = make_int2(b, (c.item_start + c.n - 1) / per_cta - (int)blockIdx.x + 1);
+        const bool split = c.sg.split();
+        const int slot = 2 * blockIdx.x + (c.sg.lo > 0 ? 0 : 1);
+        if (c.sg.lo == 0 && split) join = make_int2(b, parts1);
         if (ok_e) {
           tc05_fence_after();
 #pragma unroll 1
@@ -698,8 +684,9 @@ cudaError_t launch_paged_latent(const CUtensorMap& kvmap, const CUtensorMap& qma
   a.lse_part = a.o_part + 2 * kMaxCtas * (size_t)num_q_heads * kDv;
   a.err = err;
   const int grid = std::min(sm_count, kMaxCtas);
-  const size_t smem = 1024 + kMiscOff + kPrefixOff + (size_t)(batch + 1) * 4;
-  cudaError_t e = cudaFuncSetAttribute(latent_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+  const size_t smem = 1024 + kMiscOff + kPrefixOff + (size_t)(2 * batch + 1) * 4;
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(latent_decode_kernel, kSmemMax, allowed);
   if (e != cudaSuccess) return e;
   e = launch_pdl(latent_decode_kernel, dim3(grid), dim3(kThreads), smem, stream, kvmap, qmap, a);
   if (e != cudaSuccess) return e;

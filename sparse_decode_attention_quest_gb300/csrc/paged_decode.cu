@@ -10,12 +10,12 @@
 // byte: the floor is the time of those bytes from HBM, and the design is about
 // keeping copies in flight.
 //
-//  * Work: the kept pages of (request, KV head group) items, one after another,
-//    form one range, which the CTAs (one per SM) share equally: ragged lengths
-//    balance, and a single long request spreads over every SM. An item that
-//    spans CTAs leaves a partial (output, log-sum-exp) per CTA; a CTA has at
-//    most two, for the item it starts inside and the item it ends inside, so
-//    the workspace does not grow with the lengths.
+//  * Work: (request, KV head group) items follow one another on a line, each as
+//    long as its kept pages and a step's worth of overhead; the CTAs (one per SM)
+//    take equal slices: ragged lengths balance, and a single long request spreads
+//    over every SM. An item that spans CTAs leaves a partial (output,
+//    log-sum-exp) per CTA; a CTA has at most two, for the item it starts inside
+//    and the item it ends inside, so the workspace does not grow with the lengths.
 //  * Join: where the table's width bounds an item's partials to kInlineBytes, the
 //    CTA that publishes an item's last partial merges them in the order of the
 //    pages. Otherwise a second kernel does, a warp per row: one CTA reads
@@ -57,9 +57,10 @@ struct Cfg {
   static constexpr int kThreads = kConsumers + 32;
   static constexpr int kChunks = kD / 64;
   static constexpr int kBlocks = kSlotBytes / (kPageSize * kD * 2);  // (page, head) blocks of a slot
-  static constexpr int kStageFloats = kWarps * 8 * kD;               // eight rows of every warp's state
+  static constexpr int kStageFloats = kWarps * 8 * kD;               // states handed over at a segment's end
   static constexpr int kFixed = 1024 + kSlots * kSlotBytes + kStageFloats * 4 + kWarps * 32 * 4 +
                                 kMetaRing * kMaxPages * 4 + 2 * kSlots * 8 + 64;
+  static constexpr int kMaxSmem = kFixed + (2 * kMaxBatch + 1) * 4;
 };
 
 struct PagedArgs {
@@ -72,6 +73,7 @@ struct PagedArgs {
   int32_t head_groups;  // items per request
   int32_t mtiles;       // 16-row query tiles per KV head
   int32_t replicas;     // warps that share a (head, tile)
+  int32_t handover;     // rows of a state handed over at a time: 16, or 8 where 16 do not fit
   int32_t step_pages;   // pages of a step
   int32_t num_pages;
   int32_t batch;
@@ -91,36 +93,97 @@ struct PagedArgs {
   unsigned* err;
 };
 
-// Segments of a CTA's slice: the pages [lo, hi) of item (b, hg).
-struct Segment {
-  const int* prefix;
-  int groups, end, x;  // x: the slice position after the segment
-  int b, hg, lo, hi, n, item_start;
-  __device__ __forceinline__ void init(const int* pf, int batch, int hgs, int start, int stop) {
-    prefix = pf;
-    groups = hgs;
-    end = stop;
-    x = start;
-    int l = 0, h = batch;
-    while (h - l > 1) {
-      const int mid = (l + h) >> 1;
-      if (prefix[mid] * groups <= start) l = mid; else h = mid;
-    }
-    b = l;
-  }
-  __device__ __forceinline__ bool next() {
-    if (x >= end) return false;
-    while (prefix[b + 1] * groups <= x) ++b;
-    n = prefix[b + 1] - prefix[b];
-    const int rel = x - prefix[b] * groups;
-    hg = rel / n;
-    lo = rel - hg * n;
-    hi = min(n, lo + end - x);
-    item_start = x - lo;
-    x += hi - lo;
-    return true;
-  }
+// Joins the partials of `parts` CTAs (first .. first + parts - 1) for the rows r0 .. of an item, by kW warps: a
+// warp per row, or `share` of them when a row has many partials, joined in their order. With M the largest
+// log-sum-exp of a row,
+//     out = sum_i exp2(lse_i - M) o_i / sum_i exp2(lse_i - M).
+template <int kD, int kW>
+struct JoinSmem {
+  float acc[kW][kD];
+  float m[kW], l[kW];
 };
+template <int kD, int kW, typename Sync>
+__device__ __forceinline__ void join_rows(const float* o_part, const float* lse_part, int first, int parts, int item,
+                                          int rows, int r0, int share, JoinSmem<kD, kW>& sm, uint16_t* out,
+                                          float* out_lse, Sync sync) {
+  constexpr int kV = kD / 32;  // values per lane
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = min(r0 + warp / share, rows - 1), sub = warp % share;
+  // Partial i is in slot 1 of the item's first CTA (i = 0), in slot 0 of the others. Other CTAs wrote it: past L1.
+  auto part = [&](int i) { return (size_t)(2 * (first + i) + (i == 0)) * rows + r; };
+  const int n = (parts - sub + share - 1) / share;
+  float M = -INFINITY, l = 0.f, acc[kV];
+#pragma unroll
+  for (int x = 0; x < kV; ++x) acc[x] = 0.f;
+  // Batches of eight partials, their loads in flight beside those of their log-sum-exps.
+  for (int k0 = 0; k0 < n; k0 += 8) {
+    float v[8][kV];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float* p = o_part + part(min(sub + share * (k0 + k), parts - 1)) * kD + lane * kV;
+      if constexpr (kV == 2) {
+        const float2 t = __ldcg(reinterpret_cast<const float2*>(p));
+        v[k][0] = t.x;
+        v[k][1] = t.y;
+      } else {
+#pragma unroll
+        for (int x = 0; x < kV; x += 4) {
+          const float4 t = __ldcg(reinterpret_cast<const float4*>(p + x));
+          v[k][x] = t.x;
+          v[k][x + 1] = t.y;
+          v[k][x + 2] = t.z;
+          v[k][x + 3] = t.w;
+        }
+      }
+    }
+    const int mine = sub + share * (k0 + lane);
+    const float ls = lane < 8 && mine < parts ? __ldcg(lse_part + part(mine)) : -INFINITY;
+    float top = ls;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = fmaxf(M, __shfl_sync(0xffffffffu, top, 0));
+    const float base = finite_base(top), f0 = fast_exp2(M - base), w = fast_exp2(ls - base);
+    M = top;
+    l *= f0;
+#pragma unroll
+    for (int x = 0; x < kV; ++x) acc[x] *= f0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (k0 + k >= n) continue;
+      const float f = __shfl_sync(0xffffffffu, w, k);
+      l += f;
+#pragma unroll
+      for (int x = 0; x < kV; ++x) acc[x] += f * v[k][x];
+    }
+  }
+  sync();  // the previous rows' sums are read
+#pragma unroll
+  for (int x = 0; x < kV; ++x) sm.acc[warp][lane * kV + x] = acc[x];
+  if (lane == 0) {
+    sm.m[warp] = M;
+    sm.l[warp] = l;
+  }
+  sync();
+  // The rows' values, in pairs.
+  for (int e = threadIdx.x; e < kW / share * (kD / 2); e += kW * 32) {
+    const int w0 = e / (kD / 2) * share, d = e % (kD / 2) * 2, row = r0 + e / (kD / 2);
+    if (row >= rows) continue;
+    float top = -INFINITY;
+    for (int k = 0; k < share; ++k) top = fmaxf(top, sm.m[w0 + k]);
+    const float base = finite_base(top);
+    float sum = 0.f, x = 0.f, y = 0.f;
+    for (int k = 0; k < share; ++k) {
+      const float f = fast_exp2(sm.m[w0 + k] - base);
+      sum += f * sm.l[w0 + k];
+      x += f * sm.acc[w0 + k][d];
+      y += f * sm.acc[w0 + k][d + 1];
+    }
+    const size_t orow = (size_t)item * rows + row;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint32_t*>(out + orow * kD + d) = pack_bf16x2(x * inv, y * inv);
+    if (out_lse && d == 0) out_lse[orow] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  }
+}
 
 template <int kD>
 __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -137,11 +200,12 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
   uint64_t* empty = full + kSlots;
   int* flags = reinterpret_cast<int*>(empty + kSlots);  // [4]
   int* prefix = flags + 4;                              // [batch + 1]
+  int* lens = prefix + a.batch + 1;                     // [batch]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int heads = a.heads, G = a.group, rows = heads * G, HG = a.head_groups, Pg = a.step_pages;
   const int combos = heads * a.mtiles, active = combos * a.replicas;
 
-  kept_prefix<C::kThreads>(a.seq_lens, a.batch, a.bt_stride, a.sink, a.recent, 0x7fffffff / HG, prefix,
+  kept_prefix<C::kThreads>(a.seq_lens, a.batch, a.bt_stride, a.sink, a.recent, Pg, 0x7fffffff / HG, prefix, lens,
                            reinterpret_cast<long long*>(stage), a.err);
   // Requests without a kept token: the empty sum.
   for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
@@ -152,16 +216,13 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
     if (a.out_lse)
       for (int i = threadIdx.x; i < a.num_q_heads; i += C::kThreads) a.out_lse[r0 + i] = -INFINITY;
   }
-  const int total = prefix[a.batch] * HG;
-  // Equal slices in whole steps, two steps at least.
-  int per_cta = (int)(((long long)total + gridDim.x - 1) / gridDim.x);
-  per_cta = max(2 * Pg, (per_cta + Pg - 1) / Pg * Pg);
-  const long long start64 = (long long)blockIdx.x * per_cta;
-  if (start64 >= total) {
+  Slices slices;
+  slices.init(prefix, a.batch, HG, Pg, Pg, gridDim.x);
+  const int2 slice = slice_of(slices, blockIdx.x);
+  if (slice.x >= slice.y) {
     if (a.deferred && threadIdx.x == 0) a.joins[blockIdx.x] = make_int2(0, 0);
     return;
   }
-  const int start = (int)start64, end = min((long long)total, start64 + per_cta);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSlots; ++s) {
@@ -171,8 +232,8 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
     mbar_fence_init();
   }
   __syncthreads();
-  Segment seg;
-  seg.init(prefix, a.batch, HG, start, end);
+  Segments seg;
+  seg.init(slices, slice.x, slice.y);
   bool dead = false;  // a bounded wait gave up: no further waits or products, but every barrier
 
   if (warp == C::kWarps) {
@@ -181,7 +242,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
     const uint32_t page_bytes = (uint32_t)heads * kPageSize * kD * 2;
     int j = 0, step = 0;
     while (!dead && seg.next()) {
-      const Kept k = kept_of(a.seq_lens[seg.b], a.bt_stride, a.sink, a.recent, nullptr);
+      const Kept k = kept_of(lens[seg.b], a.bt_stride, a.sink, a.recent, nullptr);
       const int32_t* bt = a.block_table + (size_t)seg.b * a.bt_stride;
       auto entry = [&](int i) { return i < seg.hi ? bt[k.logical(i)] : -1; };
       // Two windows of 32 table entries, one per lane: the second is loaded while the first is copied.
@@ -211,7 +272,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
           __syncwarp();
           if (ok)
             tma_load_3d(ring + s * kSlotBytes + lane * page_bytes, kv ? &vmap : &kmap, 0,
-                        (phys * a.num_kv_heads + seg.hg * heads) * kPageSize, 0, &full[s], policy);
+                        (phys * a.num_kv_heads + seg.group * heads) * kPageSize, 0, &full[s], policy);
         }
       }
     }
@@ -235,16 +296,14 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
   const uint32_t plane = (uint32_t)heads * kPageSize * 128;  // 64 dims of a page's rows
   const uint32_t page_bytes = plane * C::kChunks;
   int j = 0, step = 0;
-  // The items shared with other CTAs whose partials are merged here: 0 the one that began before the slice
-  // (partial slot 0), 1 the one that goes on behind it (slot 1).
-  bool shared0 = false, shared1 = false;
-  int item0 = 0, item1 = 0, first0 = 0, parts0 = 0, parts1 = 0;
-  int2 join = make_int2(0, 0);  // the item that goes on behind the slice, when the join kernel merges it
+  const Neighbours share = neighbours_of(slices, blockIdx.x, slice);  // while the first copies are on their way
+  int item0 = 0, item1 = 0;  // the items of the partials in slots 0 and 1
+  bool handed = false;
 
   while (seg.next()) {
     uint32_t qa[kD / 16][4];
     {
-      const uint16_t* q0 = a.q + (size_t)seg.b * a.q_stride + (size_t)((seg.hg * heads + hc) * G) * kD;
+      const uint16_t* q0 = a.q + (size_t)seg.b * a.q_stride + (size_t)((seg.group * heads + hc) * G) * kD;
       const uint16_t *qr0 = q0 + (size_t)row_a * kD, *qr1 = q0 + (size_t)row_b * kD;
 #pragma unroll
       for (int ks = 0; ks < kD / 16; ++ks) {
@@ -302,7 +361,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
           x0 = fmaxf(x0, m0);
           x1 = fmaxf(x1, m1);
           // A row that has seen nothing but -inf keeps m = -inf and takes 0 as its base.
-          const float b0 = x0 == -INFINITY ? 0.f : x0, b1 = x1 == -INFINITY ? 0.f : x1;
+          const float b0 = finite_base(x0), b1 = finite_base(x1);
           const float c0 = fast_exp2(m0 - b0), c1 = fast_exp2(m1 - b1);
           m0 = x0;
           m1 = x1;
@@ -371,90 +430,99 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    const int first_cta = seg.item_start / per_cta;
-    const bool split = seg.lo > 0 || seg.hi < seg.n;
-    const int slot = seg.lo > 0 ? 0 : 1;
-    const int parts = split ? (seg.item_start + seg.n - 1) / per_cta - first_cta + 1 : 0;
-    const bool here = split && !a.deferred;
-    const int item = seg.b * HG + seg.hg;
-    if (here && slot == 0) {
-      shared0 = true;
-      item0 = item;
-      first0 = first_cta;
-      parts0 = parts;
-    } else if (here) {
-      shared1 = true;
-      item1 = item;
-      parts1 = parts;
-    } else if (split && slot == 1) {
-      join = make_int2(item, parts);
-    }
-    const size_t out_row0 = (size_t)seg.b * a.num_q_heads + (size_t)seg.hg * rows;
+    const bool split = seg.split();
+    const int slot = seg.lo > 0 ? 0 : 1, item = seg.b * HG + seg.group;
+    if (split && slot == 0) item0 = item;
+    if (split && slot == 1) item1 = item;
+    const size_t out_row0 = (size_t)seg.b * a.num_q_heads + (size_t)seg.group * rows;
     const size_t part_row0 = (size_t)(2 * blockIdx.x + slot) * rows;
-    if (a.replicas == 1) {
-      if (works) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!(half ? has_b : has_a)) continue;
-          const float l = half ? l1 : l0, m = half ? m1 : m0;
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
-          const int r = hc * G + (half ? row_b : row_a);
+    // R warps hold parts of the same rows. Up to three: the others hand their states over through shared memory,
+    // 16 or 8 rows at a time, and stream on; warp 0 of the R folds them into its own in order. Named barriers of
+    // the R warps: 2 + 2 combo, states are there; 3 + 2 combo, the slots are free again.
+    const bool shares_out = a.replicas > 3;
+    if (works && a.replicas > 1 && !shares_out) {
+      const uint32_t threads = a.replicas * 32;
+      for (int half = 0; half < (G > 8 ? 2 : 1); half += a.handover / 8) {
+        const bool both = a.handover == 16 && G > 8;
+        if (replica > 0) {
+          if (handed) named_bar_sync(3 + 2 * combo, threads);
+          handed = true;
+          // Slots by (replica - 1, combo).
+          const int sl = (replica - 1) * combos + combo;
+          float* dst = stage + (sl * a.handover + g) * kD + 2 * t;
 #pragma unroll
           for (int n = 0; n < kD / 8; ++n) {
-            const float x = o[n][2 * half] * inv, y = o[n][2 * half + 1] * inv;
-            if (split)
-              *reinterpret_cast<float2*>(a.o_part + (part_row0 + r) * kD + n * 8 + 2 * t) = make_float2(x, y);
-            else
-              *reinterpret_cast<uint32_t*>(a.out + (out_row0 + r) * kD + n * 8 + 2 * t) = pack_bf16x2(x, y);
+            *reinterpret_cast<float2*>(dst + n * 8) = half ? make_float2(o[n][2], o[n][3]) : make_float2(o[n][0], o[n][1]);
+            if (both) *reinterpret_cast<float2*>(dst + 8 * kD + n * 8) = make_float2(o[n][2], o[n][3]);
           }
           if (t == 0) {
-            if (split)
-              a.lse_part[part_row0 + r] = lse2;
-            else if (a.out_lse)
-              a.out_lse[out_row0 + r] = lse2 * kLn2;
+            ml[sl * 32 + g] = half ? m1 : m0;
+            ml[sl * 32 + 16 + g] = half ? l1 : l0;
+            if (both) {
+              ml[sl * 32 + 8 + g] = m1;
+              ml[sl * 32 + 24 + g] = l1;
+            }
           }
-        }
-      }
-    } else {
-      // R warps hold parts of the same rows: merged through shared memory, eight rows of each tile at a time.
-      named_bar_sync(1, C::kConsumers);  // the previous segment's merge is over
-      if (works && t == 0) {
-        ml[warp * 32 + g] = m0;
-        ml[warp * 32 + 16 + g] = l0;
-        ml[warp * 32 + 8 + g] = m1;
-        ml[warp * 32 + 24 + g] = l1;
-      }
-      for (int half = 0; half < (G > 8 ? 2 : 1); ++half) {
-        if (half) named_bar_sync(1, C::kConsumers);
-        if (works) {
-          float* dst = stage + (warp * 8 + g) * kD + 2 * t;
+          named_bar_arrive(2 + 2 * combo, threads);
+        } else {
+          named_bar_sync(2 + 2 * combo, threads);
+          for (int r = 0; r < a.replicas - 1; ++r) {
+            const int sl = r * combos + combo;
+            auto fold = [&](int e, int row, float& m, float& l) {
+              const float ms = ml[sl * 32 + row], ls = ml[sl * 32 + 16 + row];
+              const float M = fmaxf(m, ms), base = finite_base(M);
+              const float fo = fast_exp2(m - base), fs = fast_exp2(ms - base);
+              const float* src = stage + (sl * a.handover + row) * kD + 2 * t;
 #pragma unroll
-          for (int n = 0; n < kD / 8; ++n)
-            *reinterpret_cast<float2*>(dst + n * 8) = half ? make_float2(o[n][2], o[n][3]) : make_float2(o[n][0], o[n][1]);
+              for (int n = 0; n < kD / 8; ++n) {
+                const float2 v = *reinterpret_cast<const float2*>(src + n * 8);
+                o[n][e] = fo * o[n][e] + fs * v.x;
+                o[n][e + 1] = fo * o[n][e + 1] + fs * v.y;
+              }
+              l = fo * l + fs * ls;
+              m = M;
+            };
+            if (half == 0) fold(0, g, m0, l0);
+            if (half == 1) fold(2, g, m1, l1);
+            if (both) fold(2, 8 + g, m1, l1);
+          }
+          const bool more = seg.more() || (half == 0 && G > 8 && !both);
+          if (more) named_bar_arrive(3 + 2 * combo, threads);
         }
-        named_bar_sync(1, C::kConsumers);
-        for (int e = threadIdx.x; e < combos * 8 * (kD / 4); e += C::kConsumers) {
-          const int d = e % (kD / 4) * 4, gr = e / (kD / 4) % 8, c = e / (kD / 4) / 8;
-          const int qr = (c % a.mtiles) * 16 + half * 8 + gr;
+      }
+    }
+    if (works && shares_out) {
+      // More: all R stage their states, eight rows at a time, and share the sums (one warp folding seven states
+      // took 1.3 us longer at the end of a slice).
+      const uint32_t threads = a.replicas * 32;
+      for (int half = 0; half < (G > 8 ? 2 : 1); ++half) {
+        if (handed) named_bar_sync(3 + 2 * combo, threads);
+        handed = true;
+        float* dst = stage + (warp * 8 + g) * kD + 2 * t;
+#pragma unroll
+        for (int n = 0; n < kD / 8; ++n)
+          *reinterpret_cast<float2*>(dst + n * 8) = half ? make_float2(o[n][2], o[n][3]) : make_float2(o[n][0], o[n][1]);
+        if (t == 0) {
+          ml[warp * 32 + g] = half ? m1 : m0;
+          ml[warp * 32 + 16 + g] = half ? l1 : l0;
+        }
+        named_bar_sync(2 + 2 * combo, threads);
+        for (int e = replica * 32 + lane; e < 8 * (kD / 4); e += threads) {
+          const int d = e % (kD / 4) * 4, gr = e / (kD / 4), qr = mt * 16 + half * 8 + gr;
           if (qr >= G) continue;
           float M = -INFINITY;
-          for (int w = c; w < active; w += combos) M = fmaxf(M, ml[w * 32 + half * 8 + gr]);
-          const float base = M == -INFINITY ? 0.f : M;
+          for (int w = combo; w < active; w += combos) M = fmaxf(M, ml[w * 32 + gr]);
+          const float base = finite_base(M);
           float l = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int w = c; w < active; w += combos) {
-            const float f = fast_exp2(ml[w * 32 + half * 8 + gr] - base);
-            l += f * ml[w * 32 + 16 + half * 8 + gr];
+          for (int w = combo; w < active; w += combos) {
+            const float f = fast_exp2(ml[w * 32 + gr] - base);
+            l += f * ml[w * 32 + 16 + gr];
             const float4 v = *reinterpret_cast<const float4*>(stage + (w * 8 + gr) * kD + d);
-            acc.x += f * v.x;
-            acc.y += f * v.y;
-            acc.z += f * v.z;
-            acc.w += f * v.w;
+            acc = make_float4(acc.x + f * v.x, acc.y + f * v.y, acc.z + f * v.z, acc.w + f * v.w);
           }
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          const float lse2 = l == 0.f ? -INFINITY : M + log2f(l);
-          const int r = (c / a.mtiles) * G + qr;
+          const float inv = l == 0.f ? 0.f : 1.f / l, lse2 = l == 0.f ? -INFINITY : M + log2f(l);
+          const int r = hc * G + qr;
           acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
           if (split)
             *reinterpret_cast<float4*>(a.o_part + (part_row0 + r) * kD + d) = acc;
@@ -470,76 +538,64 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
         }
       }
     }
+    if (works && replica == 0 && !shares_out) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (!(half ? has_b : has_a)) continue;
+        const float l = half ? l1 : l0, m = half ? m1 : m0;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+        const int r = hc * G + (half ? row_b : row_a);
+#pragma unroll
+        for (int n = 0; n < kD / 8; ++n) {
+          const float x = o[n][2 * half] * inv, y = o[n][2 * half + 1] * inv;
+          if (split)
+            *reinterpret_cast<float2*>(a.o_part + (part_row0 + r) * kD + n * 8 + 2 * t) = make_float2(x, y);
+          else
+            *reinterpret_cast<uint32_t*>(a.out + (out_row0 + r) * kD + n * 8 + 2 * t) = pack_bf16x2(x, y);
+        }
+        if (t == 0) {
+          if (split)
+            a.lse_part[part_row0 + r] = lse2;
+          else if (a.out_lse)
+            a.out_lse[out_row0 + r] = lse2 * kLn2;
+        }
+      }
+    }
   }
   if (dead && lane == 0) raise_error(a.err, SE_DEVERR_WAIT_TIMEOUT);
-  if (a.deferred && threadIdx.x == 0) a.joins[blockIdx.x] = join;
+  if (a.deferred && threadIdx.x == 0) a.joins[blockIdx.x] = make_int2(item1, share.parts1);
 
   // ---- Publish: count this CTA in on the (at most two) items it shares with few others; whoever completes
   // an item's count merges its partials (written by other CTAs: read past L1) and resets the counter.
-  if (!shared0 && !shared1) return;  // the same for all consumers
+  if (a.deferred || (share.parts0 == 0 && share.parts1 == 0)) return;  // the same for all consumers
   __threadfence();
   named_bar_sync(1, C::kConsumers);
   if (threadIdx.x < 2) {
+    const int parts = threadIdx.x ? share.parts1 : share.parts0;
     int last = 0;
-    if (threadIdx.x ? shared1 : shared0) {
-      uint32_t* cnt = a.arrivals + (threadIdx.x ? (int)blockIdx.x : first0);
-      last = atomic_add_acq_rel_gpu(cnt, 1u) == (uint32_t)(threadIdx.x ? parts1 : parts0) - 1;
+    if (parts > 0) {
+      uint32_t* cnt = a.arrivals + (threadIdx.x ? (int)blockIdx.x : share.first0);
+      last = atomic_add_acq_rel_gpu(cnt, 1u) == (uint32_t)parts - 1;
       if (last) *cnt = 0;
     }
     flags[threadIdx.x] = last;
   }
   named_bar_sync(1, C::kConsumers);
-#pragma unroll
+  auto* join_smem = reinterpret_cast<JoinSmem<kD, C::kWarps>*>(stage);  // the states staged there are read
+  static_assert(sizeof(JoinSmem<kD, C::kWarps>) <= (C::kStageFloats + C::kWarps * 32) * 4, "the join's sums fit");
+#pragma unroll 1
   for (int s = 0; s < 2; ++s) {
     if (!flags[s]) continue;
-    const int c0 = s ? (int)blockIdx.x : first0, ns = s ? parts1 : parts0;
-    const size_t out_row0 = (size_t)(s ? item1 : item0) * rows;  // items and their rows follow one another
-    for (int e = threadIdx.x; e < rows * (kD / 4); e += C::kConsumers) {
-      const int r = e / (kD / 4), d = e % (kD / 4) * 4;
-      float M = -INFINITY, wsum = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i0 = 0; i0 < ns; i0 += 8) {
-        float ls[8];
-        float4 v[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int i = min(i0 + u, ns - 1);
-          // The item's first CTA holds it in slot 1 (the item starts there), the others in slot 0.
-          const size_t row = (size_t)(2 * (c0 + i) + (i == 0)) * rows + r;
-          ls[u] = i0 + u < ns ? __ldcg(a.lse_part + row) : -INFINITY;
-          v[u] = __ldcg(reinterpret_cast<const float4*>(a.o_part + row * kD + d));
-        }
-        float mn = M;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) mn = fmaxf(mn, ls[u]);
-        const float base = mn == -INFINITY ? 0.f : mn;
-        const float f = fast_exp2(M - base);
-        M = mn;
-        wsum *= f;
-        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          if (i0 + u >= ns) continue;
-          const float w = fast_exp2(ls[u] - base);
-          wsum += w;
-          acc.x += w * v[u].x;
-          acc.y += w * v[u].y;
-          acc.z += w * v[u].z;
-          acc.w += w * v[u].w;
-        }
-      }
-      const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
-      *reinterpret_cast<uint2*>(a.out + (out_row0 + r) * kD + d) =
-          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-      if (a.out_lse && d == 0) a.out_lse[out_row0 + r] = wsum == 0.f ? -INFINITY : (M + log2f(wsum)) * kLn2;
-    }
+    const int first = s ? (int)blockIdx.x : share.first0, parts = s ? share.parts1 : share.parts0;
+    const int warps = min(C::kWarps, share_of(parts));
+    for (int r0 = 0; r0 < rows; r0 += C::kWarps / warps)
+      join_rows<kD, C::kWarps>(a.o_part, a.lse_part, first, parts, s ? item1 : item0, rows, r0, warps, *join_smem, a.out,
+                               a.out_lse, [] { named_bar_sync(1, C::kConsumers); });
   }
 }
 
-// Joins the partials of the items that span many CTAs. With M the largest log-sum-exp of a row,
-//     out = sum_i exp2(lse_i - M) o_i / sum_i exp2(lse_i - M).
-// A warp takes a row; share_of(partials) warps share the partials of an item that has many, and are joined in
-// their order.
+// The join of the items that span many CTAs, a CTA per few rows of an item.
 template <int kD>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const float* __restrict__ o_part,
                                                                     const float* __restrict__ lse_part,
@@ -547,80 +603,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const float
                                                                     int32_t rows, uint16_t* __restrict__ out,
                                                                     float* __restrict__ out_lse) {
   pdl_enter();
-  constexpr int kV = kD / 32;  // values per lane
-  static_assert(kMaxCtas <= kJoinWarps * 32, "a lane per partial of the warp, a thread per item");
+  static_assert(kMaxCtas <= kJoinWarps * 32, "a thread per item");
   __shared__ int3 todo[kMaxCtas];
   __shared__ int counts[kJoinWarps];
-  __shared__ float acc_s[kJoinWarps][kD];
-  __shared__ float m_s[kJoinWarps], l_s[kJoinWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ JoinSmem<kD, kJoinWarps> sm;
   const int ntodo = list_joins(joins, ctas, todo, counts);
   for (int u = blockIdx.x; u < ntodo * rows; u += gridDim.x) {
     const int3 jn = todo[u / rows];
     const int share = share_of(jn.z), r0 = u % rows * (kJoinWarps / share);
     if (r0 >= rows) continue;  // fewer CTAs serve an item whose warps do not share
-    const int r = min(r0 + warp / share, rows - 1), sub = warp % share;
-    // Partial i is in slot 1 of the item's first CTA (i = 0), in slot 0 of the others.
-    auto part = [&](int i) { return (size_t)(2 * (jn.x + i) + (i == 0)) * rows + r; };
-    const int mine = sub + share * lane;
-    const float ls = mine < jn.z ? lse_part[part(mine)] : -INFINITY;
-    float M = ls;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float w = fast_exp2(ls - finite_base(M));
-    float l = w;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    float acc[kV];
-#pragma unroll
-    for (int x = 0; x < kV; ++x) acc[x] = 0.f;
-    const int n = (jn.z - sub + share - 1) / share;
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float f = __shfl_sync(0xffffffffu, w, k);
-      const float* p = o_part + part(sub + share * k) * kD + lane * kV;
-      if constexpr (kV == 2) {
-        const float2 v = *reinterpret_cast<const float2*>(p);
-        acc[0] += f * v.x;
-        acc[1] += f * v.y;
-      } else {
-#pragma unroll
-        for (int x = 0; x < kV; x += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(p + x);
-          acc[x] += f * v.x;
-          acc[x + 1] += f * v.y;
-          acc[x + 2] += f * v.z;
-          acc[x + 3] += f * v.w;
-        }
-      }
-    }
-    __syncthreads();  // the previous unit's sums are read
-#pragma unroll
-    for (int x = 0; x < kV; ++x) acc_s[warp][lane * kV + x] = acc[x];
-    if (lane == 0) {
-      m_s[warp] = M;
-      l_s[warp] = l;
-    }
-    __syncthreads();
-    // The CTA's rows, in pairs of values.
-    for (int e = threadIdx.x; e < kJoinWarps / share * (kD / 2); e += kJoinWarps * 32) {
-      const int w0 = e / (kD / 2) * share, d = e % (kD / 2) * 2, row = r0 + e / (kD / 2);
-      if (row >= rows) continue;
-      float top = -INFINITY;
-      for (int k = 0; k < share; ++k) top = fmaxf(top, m_s[w0 + k]);
-      const float base = finite_base(top);
-      float sum = 0.f, x = 0.f, y = 0.f;
-      for (int k = 0; k < share; ++k) {
-        const float f = fast_exp2(m_s[w0 + k] - base);
-        sum += f * l_s[w0 + k];
-        x += f * acc_s[w0 + k][d];
-        y += f * acc_s[w0 + k][d + 1];
-      }
-      const size_t orow = (size_t)jn.y * rows + row;
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      *reinterpret_cast<uint32_t*>(out + orow * kD + d) = pack_bf16x2(x * inv, y * inv);
-      if (out_lse && d == 0) out_lse[orow] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-    }
+    join_rows<kD, kJoinWarps>(o_part, lse_part, jn.x, jn.z, jn.y, rows, r0, share, sm, out, out_lse,
+                              [] { __syncthreads(); });
   }
 }
 
@@ -642,13 +635,17 @@ HeadPlan head_plan(int num_kv_heads, int group, int head_dim) {
   return p;
 }
 
+int stage_floats(int head_dim) {
+  return head_dim == 64 ? Cfg<64>::kStageFloats : head_dim == 128 ? Cfg<128>::kStageFloats : Cfg<256>::kStageFloats;
+}
+
 template <int kD>
 cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const PagedArgs& a, int grid,
                    cudaStream_t stream) {
-  const size_t smem = Cfg<kD>::kFixed + (size_t)(a.batch + 1) * 4;
-  static_assert(Cfg<kD>::kFixed + (kMaxBatch + 1) * 4 <= 227 * 1024, "the largest batch fits");
-  cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<kD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Cfg<kD>::kFixed + (kMaxBatch + 1) * 4);
+  const size_t smem = Cfg<kD>::kFixed + (size_t)(2 * a.batch + 1) * 4;
+  static_assert(Cfg<kD>::kMaxSmem <= 227 * 1024, "the largest batch fits");
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(paged_decode_kernel<kD>, Cfg<kD>::kMaxSmem, allowed);
   if (e != cudaSuccess) return e;
   e = launch_pdl(paged_decode_kernel<kD>, dim3(grid), dim3(Cfg<kD>::kThreads), smem, stream, kmap, vmap, a);
   if (e != cudaSuccess || !a.deferred) return e;
@@ -699,6 +696,9 @@ cudaError_t launch_paged_decode(const CUtensorMap& kmap, const CUtensorMap& vmap
   a.mtiles = p.mtiles;
   a.replicas = p.replicas;
   a.step_pages = p.step_pages;
+  // The R - 1 states of every (head, tile) fit the staging area whole, or eight rows at a time.
+  const int staged = (p.replicas - 1) * p.heads * p.mtiles * (group > 8 ? 16 : 8) * kv.head_dim;
+  a.handover = group > 8 && staged <= stage_floats(kv.head_dim) ? 16 : 8;
   a.num_pages = kv.num_pages;
   a.batch = batch;
   a.block_table = block_table;
@@ -721,7 +721,7 @@ cudaError_t launch_paged_decode(const CUtensorMap& kmap, const CUtensorMap& vmap
   long long pages = bt_stride;
   if (recent_tokens > 0)
     pages = std::min(pages, ((long long)sink_tokens + kPageSize - 1) / kPageSize + recent_tokens / kPageSize + 2);
-  const long long most = std::min<long long>(grid, pages / (2 * p.step_pages) + 2);
+  const long long most = std::min<long long>(grid, (pages + p.step_pages) / (2 * p.step_pages + 1) + 2);
   a.deferred = most * (long long)(rows * kv.head_dim * sizeof(float)) > kInlineBytes;
   switch (kv.head_dim) {
     case 64: return launch<64>(kmap, vmap, a, grid, stream);

@@ -1,6 +1,6 @@
 // What the dense paged decodes share: which pages and tokens of a request are
-// kept, the prefix of the kept pages over a batch, and the list of items whose
-// partials are joined.
+// kept, how the kept pages of a batch are shared among the CTAs, and the list of
+// items whose partials are joined.
 #pragma once
 
 #include "se_ptx.cuh"
@@ -54,17 +54,125 @@ __device__ __forceinline__ bool mask_is_full(uint32_t m) {
   return (m & 0xff) == kPageSize && ((m >> 8 & 0xff) == kPageSize || (m >> 16) == 0);
 }
 
-// Kept pages per request as an exclusive prefix (prefix[batch]: the total), by the whole CTA. Positions are
-// 32-bit: requests that end behind page `most` are reported and cut short. sums: kThreads / 32 values.
+// The share-out of a batch among the CTAs. An item is a request (or one of its `groups` groups of KV heads); it
+// weighs its kept pages plus `over`, the pages' worth of time that starting and finishing an item costs a CTA, so
+// that many short requests spread over the CTAs. The items' weights follow one another on a line of length
+// `total`, cut every `span`. A cut within `over` of an item's end is moved there (a split costs a join), any
+// other to a multiple of `unit` pages of its item. span > 2 over, so that the cuts keep their order and every CTA
+// between an item's first and last holds pages of it.
+struct Slices {
+  const int* prefix;  // [batch + 1] weights of the requests before each (one group)
+  int batch, groups, over, unit, span, total;
+
+  __device__ __forceinline__ void init(const int* pf, int n, int g, int overhead, int page_unit, int ctas) {
+    prefix = pf;
+    batch = n;
+    groups = g;
+    over = overhead;
+    unit = page_unit;
+    total = pf[n] * g;
+    span = max(2 * over + 1, (int)(((unsigned)total + (unsigned)ctas - 1) / (unsigned)ctas));
+  }
+  // The request whose weight covers place p < total.
+  __device__ __forceinline__ int request_at(int p) const {
+    int l = 0, h = batch;
+    while (h - l > 1) {
+      const int mid = (l + h) >> 1;
+      if (prefix[mid] * groups <= p) l = mid; else h = mid;
+    }
+    return l;
+  }
+  // Where CTA k's slice begins (CTA k - 1's ends).
+  __device__ __forceinline__ int cut(int k) const {
+    if (k > (total - 1) / span) return total;
+    const int p = k * span, b = request_at(p), base = prefix[b] * groups, w = prefix[b + 1] - prefix[b];
+    const int s = groups == 1 ? base : p - (p - base) % w;  // the item's begin
+    if (p - s <= over) return s;
+    if (s + w - p <= over) return s + w;
+    return s + over + (p - s - over + unit - 1) / unit * unit;
+  }
+};
+
+// The slice [x, y) of a CTA. By a converged warp: a lane per cut.
+__device__ __forceinline__ int2 slice_of(const Slices& sl, int cta) {
+  const int mine = sl.cut(cta + (threadIdx.x & 1));
+  return make_int2(__shfl_sync(0xffffffffu, mine, 0), __shfl_sync(0xffffffffu, mine, 1));
+}
+
+// Who else holds the items that reach beyond a CTA's slice [x, y): the item that began before it (partial slot 0;
+// first0 the CTA where it begins, parts0 CTAs in all, 0: none) and the item that begins in it and goes on behind it
+// (slot 1; parts1 CTAs from this one on, 0: none).
+struct Neighbours {
+  int first0, parts0, parts1;
+};
+
+// By a converged warp: the cuts are the long part, so the lanes take one each.
+__device__ __forceinline__ Neighbours neighbours_of(const Slices& sl, int cta, int2 slice) {
+  Neighbours h;
+  const int lane = threadIdx.x & 31;
+  // The item over the slice's first place (even lanes) and over its last (odd lanes).
+  const int at = lane & 1 ? slice.y - 1 : slice.x;
+  const int b = sl.request_at(at), base = sl.prefix[b] * sl.groups, w = sl.prefix[b + 1] - sl.prefix[b];
+  const int s = sl.groups == 1 ? base : at - (at - base) % w;
+  const int s0 = __shfl_sync(0xffffffffu, s, 0), e0 = __shfl_sync(0xffffffffu, s + w, 0);
+  const int s1 = __shfl_sync(0xffffffffu, s, 1), e1 = __shfl_sync(0xffffffffu, s + w, 1);
+  // Lane i: a place's span and the cuts beside it. Places: the first and the last page of the item that began
+  // before, the last of the one that goes on behind.
+  const int place = lane < 8 ? s0 + sl.over : lane < 16 ? e0 - 1 : e1 - 1;
+  const int k = place / sl.span, c = sl.cut(k + (lane & 1));
+  const int lo = __shfl_sync(0xffffffffu, c, lane & ~1), hi = __shfl_sync(0xffffffffu, c, lane | 1);
+  const int owner = lo > place ? k - 1 : hi <= place ? k + 1 : k;
+  const int f0 = __shfl_sync(0xffffffffu, owner, 0), l0 = __shfl_sync(0xffffffffu, owner, 8);
+  const int l1 = __shfl_sync(0xffffffffu, owner, 16);
+  h.first0 = f0;
+  h.parts0 = s0 < slice.x ? l0 - f0 + 1 : 0;
+  h.parts1 = e1 > slice.y && s1 >= slice.x ? l1 - cta + 1 : 0;
+  return h;
+}
+
+// A CTA's slice, item by item: the pages [lo, hi) of the n of item (b, group).
+struct Segments {
+  Slices sl;
+  int x, end;
+  int b, group, lo, hi, n, item_start;
+  __device__ __forceinline__ void init(const Slices& slices, int start, int stop) {
+    sl = slices;
+    x = start;
+    end = stop;
+    b = start < stop ? sl.request_at(start) : 0;
+  }
+  __device__ __forceinline__ bool more() const { return x < end; }
+  __device__ __forceinline__ bool next() {
+    if (x >= end) return false;
+    while (sl.prefix[b + 1] * sl.groups <= x) ++b;
+    const int base = sl.prefix[b] * sl.groups, w = sl.prefix[b + 1] - sl.prefix[b];
+    group = sl.groups == 1 ? 0 : (x - base) / w;
+    item_start = base + group * w;
+    n = w - sl.over;
+    lo = max(0, x - item_start - sl.over);
+    x = min(item_start + w, end);
+    hi = x - item_start - sl.over;
+    return true;
+  }
+  __device__ __forceinline__ bool split() const { return lo > 0 || hi < n; }
+};
+
+// The requests' weights as an exclusive prefix (prefix[batch]: their sum), by the whole CTA. Places are 32-bit:
+// requests that end behind place `most` are reported and left empty from there on. lens: the lengths as read;
+// sums: kThreads / 32 values.
 template <int kThreads>
 __device__ __forceinline__ void kept_prefix(const int32_t* seq_lens, int batch, int bt_stride, int sink, int recent,
-                                            int most, int* prefix, long long* sums, unsigned* err) {
+                                            int over, int most, int* prefix, int* lens, long long* sums,
+                                            unsigned* err) {
   constexpr int kWarps = kThreads / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long at = 0;
   for (int base = 0; base < batch; base += kThreads) {
     const int b = base + threadIdx.x;
-    long long incl = b < batch ? kept_of(seq_lens[b], bt_stride, sink, recent, err).n : 0;
+    const int L = b < batch ? seq_lens[b] : 0;
+    if (b < batch) lens[b] = L;
+    const int n = kept_of(L, bt_stride, sink, recent, err).n;
+    long long incl = n > 0 ? n + over : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long t = __shfl_up_sync(0xffffffffu, incl, o);
@@ -80,14 +188,20 @@ __device__ __forceinline__ void kept_prefix(const int32_t* seq_lens, int batch, 
     }
     __syncthreads();
     incl += before;
-    if (b < batch) {
-      if (incl > most) raise_error(err, SE_DEVERR_LENGTH);
-      prefix[b + 1] = (int)(incl < most ? incl : most);
-    }
+    if (b < batch) prefix[b + 1] = (int)(incl < most ? incl : -1);
     at += all;
   }
   if (threadIdx.x == 0) prefix[0] = 0;
   __syncthreads();
+  if (at >= most) {
+    // Too long a line: the requests from the first that does not fit on are left out.
+    if (threadIdx.x == 0) {
+      raise_error(err, SE_DEVERR_LENGTH);
+      for (int b = 1; b <= batch; ++b)
+        if (prefix[b] < 0) prefix[b] = prefix[b - 1];
+    }
+    __syncthreads();
+  }
 }
 
 // The items to join, as (first CTA, item, partials), from joins[c] = (item, partials) of every CTA c (0 partials:

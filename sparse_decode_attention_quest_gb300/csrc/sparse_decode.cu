@@ -118,10 +118,6 @@ struct DecodeSmem {
   static_assert(kWarps * kRows * kHeadDim * 4 + 3 * kWarps * 16 * 4 <= kRing, "end-of-stream staging fits the ring");
 };
 
-__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t count) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-
 template <bool kHiRows>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_decode_kernel(const DecodeArgs a) {
   using Cfg = DecodeSmem<kHiRows>;

@@ -143,14 +143,16 @@ def test_windows(cuda_device, sink, recent, shape):
            recent=recent, seed=3).check()
 
 
-@pytest.mark.parametrize("batch,lo,hi", [(1, 4096, 4096), (1, 20011, 20011), (3, 1, 9000), (70, 0, 400), (300, 0, 64)])
-@pytest.mark.parametrize("shape", [(8, 2, 128), (64, 1, 576)])
+@pytest.mark.parametrize("batch,lo,hi", [(1, 4096, 4096), (1, 20011, 20011), (3, 1, 9000), (70, 0, 400), (300, 0, 64),
+                                         (51, 208, 208), (160, 330, 350), (200, 1, 17), (33, 1500, 1600), (2, 1, 30000)])
+@pytest.mark.parametrize("shape", [(8, 2, 128), (4, 1, 64), (16, 8, 64), (2, 1, 256), (64, 1, 576)])
 def test_splits(cuda_device, batch, lo, hi, shape):
     """Few long requests over many CTAs, many short ones in one, and ragged mixes."""
     Hq, H, D = shape
     g = np.random.default_rng(batch)
-    if D == 576 and batch == 300:
-        batch = 120
+    if D == 576:
+        batch, hi = min(batch, 120), min(hi, 20011)
+        lo = min(lo, hi)
     Inputs(cuda_device, g.integers(lo, hi + 1, batch).tolist(), Hq, H, D, latent=D == 576, seed=4).check()
 
 
