@@ -572,77 +572,97 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
 
 // Joins the partials of the items that span CTAs. With M_h the largest log-sum-exp of head h,
 //     out_h = sum_i exp2(lse_hi - M_h) o_hi / sum_i exp2(lse_hi - M_h).
-// A warp takes four heads and 32 dims of an item; share_of(partials) warps share the partials of an item that
-// has many, and are joined in their order.
+// A warp takes four heads and 128 dims of an item, four consecutive dims per lane; share_of(partials) warps share
+// the partials of an item that has many, and are joined in their order.
 __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const float* __restrict__ o_part,
                                                                      const float* __restrict__ lse_part,
                                                                      const int2* __restrict__ joins, int32_t ctas,
                                                                      int32_t Hq, uint16_t* __restrict__ out,
                                                                      float* __restrict__ out_lse) {
   pdl_enter();
-  static_assert(kMaxCtas <= kJoinWarps * 32, "a lane per partial of the warp, a thread per item");
-  __shared__ int3 todo[kMaxCtas];
-  __shared__ int counts[kJoinWarps];
-  __shared__ float4 acc_s[kJoinWarps][32], m_s[kJoinWarps], l_s[kJoinWarps];
+  static_assert(kMaxCtas <= kJoinWarps * 32, "a thread per item");
+  constexpr int kTaskDims = 128;
+  __shared__ int4 todo[kMaxCtas];
+  __shared__ int2 counts[kJoinWarps];
+  __shared__ float4 acc_s[kJoinWarps][4][32], m_s[kJoinWarps], l_s[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ntodo = list_joins(joins, ctas, todo, counts);
-  const int tasks = (Hq / 4) * (kDv / 32);
-  for (int u = blockIdx.x; u < ntodo * tasks; u += gridDim.x) {
-    const int3 jn = todo[u / tasks];
-    const int share = share_of(jn.z), k0 = u % tasks * (kJoinWarps / share);
-    if (k0 >= tasks) continue;  // fewer CTAs serve an item whose warps do not share
-    const int task = k0 + warp / share, sub = warp % share;  // tasks is a multiple of the warps
-    const int blk = task / (kDv / 32), d = task % (kDv / 32) * 32 + lane;
+  const int tasks = (Hq / 4) * (kDv / kTaskDims);  // a multiple of the warps
+  const int2 todos = list_joins(joins, ctas, tasks, todo, counts);
+  auto scale4 = [](const float4& a, const float4& f) { return make_float4(a.x * f.x, a.y * f.y, a.z * f.z, a.w * f.w); };
+  auto fma4 = [](const float4& f, const float4& v, const float4& a) {
+    return make_float4(a.x + f.x * v.x, a.y + f.y * v.y, a.z + f.z * v.z, a.w + f.w * v.w);
+  };
+  auto max4 = [](const float4& a, const float4& b) {
+    return make_float4(fmaxf(a.x, b.x), fmaxf(a.y, b.y), fmaxf(a.z, b.z), fmaxf(a.w, b.w));
+  };
+  // exp2(a - m), 0 where nothing but -inf has been seen.
+  auto weight4 = [](const float4& a, const float4& m) {
+    return make_float4(fast_exp2(a.x - finite_base(m.x)), fast_exp2(a.y - finite_base(m.y)),
+                       fast_exp2(a.z - finite_base(m.z)), fast_exp2(a.w - finite_base(m.w)));
+  };
+  for (int u = blockIdx.x; u < todos.y; u += gridDim.x) {
+    const int4 jn = join_of(todo, todos.x, u);
+    const int share = share_of(jn.z), task = (u - jn.w) * (kJoinWarps / share) + warp / share, sub = warp % share;
+    const int blk = task / (kDv / kTaskDims), d = task % (kDv / kTaskDims) * kTaskDims + 4 * lane;
     // Partial i is in slot 1 of the item's first CTA (i = 0), in slot 0 of the others.
     auto part = [&](int i) { return (size_t)(2 * (jn.x + i) + (i == 0)) * (Hq / 4) + blk; };
-    const int mine = sub + share * lane;
-    float4 w = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    if (mine < jn.z) w = *reinterpret_cast<const float4*>(lse_part + part(mine) * 4);
-    float4 M = w;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      M.x = fmaxf(M.x, __shfl_xor_sync(0xffffffffu, M.x, o));
-      M.y = fmaxf(M.y, __shfl_xor_sync(0xffffffffu, M.y, o));
-      M.z = fmaxf(M.z, __shfl_xor_sync(0xffffffffu, M.z, o));
-      M.w = fmaxf(M.w, __shfl_xor_sync(0xffffffffu, M.w, o));
-    }
-    w = make_float4(fast_exp2(w.x - finite_base(M.x)), fast_exp2(w.y - finite_base(M.y)),
-                    fast_exp2(w.z - finite_base(M.z)), fast_exp2(w.w - finite_base(M.w)));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), l = acc;
     const int n = (jn.z - sub + share - 1) / share;
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float4 f = make_float4(__shfl_sync(0xffffffffu, w.x, k), __shfl_sync(0xffffffffu, w.y, k),
-                                   __shfl_sync(0xffffffffu, w.z, k), __shfl_sync(0xffffffffu, w.w, k));
-      const float4 v = *reinterpret_cast<const float4*>(o_part + (part(sub + share * k) * kDv + d) * 4);
-      acc = make_float4(acc.x + f.x * v.x, acc.y + f.y * v.y, acc.z + f.z * v.z, acc.w + f.w * v.w);
-      l = make_float4(l.x + f.x, l.y + f.y, l.z + f.z, l.w + f.w);
-    }
-    __syncthreads();  // the previous unit's sums are read
-    acc_s[warp][lane] = acc;
-    if (lane == 0) {
-      m_s[warp] = M;
-      l_s[warp] = l;
-    }
-    __syncthreads();
-    // The output (head, 32 dims) pairs of the CTA's tasks, a warp each.
-    for (int x = warp; x < 4 * kJoinWarps / share; x += kJoinWarps) {
-      const int w0 = x / 4 * share, h = x % 4, tk = k0 + x / 4;
-      auto at = [&](const float4& v) { return h == 0 ? v.x : h == 1 ? v.y : h == 2 ? v.z : v.w; };
-      float top = -INFINITY;
-      for (int k = 0; k < share; ++k) top = fmaxf(top, at(m_s[w0 + k]));
-      const float base = finite_base(top);
-      float sum = 0.f, o = 0.f;
-      for (int k = 0; k < share; ++k) {
-        const float f = fast_exp2(at(m_s[w0 + k]) - base);
-        sum += f * at(l_s[w0 + k]);
-        o += f * at(acc_s[w0 + k][lane]);
+    float4 M = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY), l = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 acc[4] = {l, l, l, l};  // dims d .. d + 3 of the four heads
+    // Batches of four partials, their loads in flight beside those of their log-sum-exps.
+    for (int k0 = 0; k0 < n; k0 += 4) {
+      float4 v[4][4], ls[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        ls[k] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (k0 + k >= n) continue;
+        const size_t p = part(sub + share * (k0 + k));
+        ls[k] = *reinterpret_cast<const float4*>(lse_part + p * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[k][e] = *reinterpret_cast<const float4*>(o_part + (p * kDv + d + e) * 4);
       }
-      const size_t orow = (size_t)jn.y * Hq + tk / (kDv / 32) * 4 + h;
-      const int od = tk % (kDv / 32) * 32 + lane;
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      out[orow * kDv + od] = (uint16_t)(pack_bf16x2(o * inv, 0.f) & 0xffffu);
-      if (out_lse && od == 0) out_lse[orow] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+      const float4 top = max4(M, max4(max4(ls[0], ls[1]), max4(ls[2], ls[3])));
+      const float4 f0 = weight4(M, top);
+      M = top;
+      l = scale4(l, f0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = scale4(acc[e], f0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k0 + k >= n) continue;
+        const float4 w = weight4(ls[k], M);
+        l = make_float4(l.x + w.x, l.y + w.y, l.z + w.z, l.w + w.w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = fma4(w, v[k][e], acc[e]);
+      }
+    }
+    if (share > 1) {
+      __syncthreads();  // the previous unit's sums are read
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc_s[warp][e][lane] = acc[e];
+      if (lane == 0) {
+        m_s[warp] = M;
+        l_s[warp] = l;
+      }
+      __syncthreads();
+      if (sub > 0) continue;  // the first of the warps that share adds the others
+      for (int k = 1; k < share; ++k) {
+        const float4 mk = m_s[warp + k], top = max4(M, mk), f0 = weight4(M, top), fk = weight4(mk, top);
+        M = top;
+        l = fma4(fk, l_s[warp + k], scale4(l, f0));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = fma4(fk, acc_s[warp + k][e][lane], scale4(acc[e], f0));
+      }
+    }
+    const size_t row = (size_t)jn.y * Hq + blk * 4;
+    const float ll[4] = {l.x, l.y, l.z, l.w}, mm[4] = {M.x, M.y, M.z, M.w};
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      auto at = [&](const float4& v) { return h == 0 ? v.x : h == 1 ? v.y : h == 2 ? v.z : v.w; };
+      const float inv = ll[h] == 0.f ? 0.f : 1.f / ll[h];
+      *reinterpret_cast<uint2*>(out + (row + h) * kDv + d) = make_uint2(
+          pack_bf16x2(at(acc[0]) * inv, at(acc[1]) * inv), pack_bf16x2(at(acc[2]) * inv, at(acc[3]) * inv));
+      if (out_lse && d == 0) out_lse[row + h] = ll[h] == 0.f ? -INFINITY : (mm[h] + log2f(ll[h])) * kLn2;
     }
   }
 }

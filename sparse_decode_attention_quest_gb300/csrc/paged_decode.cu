@@ -120,7 +120,8 @@ __device__ __forceinline__ void join_rows(const float* o_part, const float* lse_
     float v[8][kV];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float* p = o_part + part(min(sub + share * (k0 + k), parts - 1)) * kD + lane * kV;
+      if (k0 + k >= n) continue;
+      const float* p = o_part + part(sub + share * (k0 + k)) * kD + lane * kV;
       if constexpr (kV == 2) {
         const float2 t = __ldcg(reinterpret_cast<const float2*>(p));
         v[k][0] = t.x;
@@ -155,6 +156,16 @@ __device__ __forceinline__ void join_rows(const float* o_part, const float* lse_
 #pragma unroll
       for (int x = 0; x < kV; ++x) acc[x] += f * v[k][x];
     }
+  }
+  if (share == 1) {
+    if (r0 + warp >= rows) return;
+    const size_t orow = (size_t)item * rows + r;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int x = 0; x < kV; x += 2)
+      *reinterpret_cast<uint32_t*>(out + orow * kD + lane * kV + x) = pack_bf16x2(acc[x] * inv, acc[x + 1] * inv);
+    if (out_lse && lane == 0) out_lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+    return;
   }
   sync();  // the previous rows' sums are read
 #pragma unroll
@@ -604,16 +615,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const float
                                                                     float* __restrict__ out_lse) {
   pdl_enter();
   static_assert(kMaxCtas <= kJoinWarps * 32, "a thread per item");
-  __shared__ int3 todo[kMaxCtas];
-  __shared__ int counts[kJoinWarps];
+  __shared__ int4 todo[kMaxCtas];
+  __shared__ int2 counts[kJoinWarps];
   __shared__ JoinSmem<kD, kJoinWarps> sm;
-  const int ntodo = list_joins(joins, ctas, todo, counts);
-  for (int u = blockIdx.x; u < ntodo * rows; u += gridDim.x) {
-    const int3 jn = todo[u / rows];
-    const int share = share_of(jn.z), r0 = u % rows * (kJoinWarps / share);
-    if (r0 >= rows) continue;  // fewer CTAs serve an item whose warps do not share
-    join_rows<kD, kJoinWarps>(o_part, lse_part, jn.x, jn.z, jn.y, rows, r0, share, sm, out, out_lse,
-                              [] { __syncthreads(); });
+  const int2 n = list_joins(joins, ctas, rows, todo, counts);
+  for (int u = blockIdx.x; u < n.y; u += gridDim.x) {
+    const int4 j = join_of(todo, n.x, u);
+    const int share = share_of(j.z);
+    join_rows<kD, kJoinWarps>(o_part, lse_part, j.x, j.z, j.y, rows, (u - j.w) * (kJoinWarps / share), share, sm, out,
+                              out_lse, [] { __syncthreads(); });
   }
 }
 

@@ -204,27 +204,48 @@ __device__ __forceinline__ void kept_prefix(const int32_t* seq_lens, int batch, 
   }
 }
 
-// The items to join, as (first CTA, item, partials), from joins[c] = (item, partials) of every CTA c (0 partials:
-// none), in the order of their CTAs: every CTA of the join kernel makes the same list. By the whole CTA, which has
-// a thread per entry; returns the number of items. counts: one value per warp.
-__device__ __forceinline__ int list_joins(const int2* joins, int ctas, int3* todo, int* counts) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int2 j = threadIdx.x < ctas ? joins[threadIdx.x] : make_int2(0, 0);
-  const uint32_t some = __ballot_sync(0xffffffffu, j.y > 0);
-  if (lane == 0) counts[warp] = __popc(some);
-  __syncthreads();
-  int at = __popc(some & ((1u << lane) - 1)), all = 0;
-  for (int w = 0; w < (int)blockDim.x / 32; ++w) {
-    at += w < warp ? counts[w] : 0;
-    all += counts[w];
-  }
-  if (j.y > 0) todo[at] = make_int3(threadIdx.x, j.x, j.y);
-  __syncthreads();
-  return all;
-}
-
 // Warps that share the partials of an item: each takes eight or fewer, until all eight warps of a CTA share.
 __device__ __forceinline__ int share_of(int partials) { return partials <= 8 ? 1 : partials <= 16 ? 2 : partials <= 32 ? 4 : 8; }
+
+// The items to join, as (first CTA, item, partials, first unit), from joins[c] = (item, partials) of every CTA c (0
+// partials: none), in the order of their CTAs: every CTA of a join kernel makes the same list. An item has
+// ceil(tasks * share_of(partials) / warps) units, a CTA's work each: a task per warp, or per share_of warps. By the
+// whole CTA (a thread per entry). counts: two values per warp. Returns (items, units).
+__device__ __forceinline__ int2 list_joins(const int2* joins, int ctas, int tasks, int4* todo, int2* counts) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int2 j = threadIdx.x < ctas ? joins[threadIdx.x] : make_int2(0, 0);
+  const uint32_t some = __ballot_sync(0xffffffffu, j.y > 0);
+  const int units = j.y > 0 ? (tasks * share_of(j.y) + warps - 1) / warps : 0;
+  int incl = units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  if (lane == 31) counts[warp] = make_int2(__popc(some), incl);
+  __syncthreads();
+  int at = __popc(some & ((1u << lane) - 1)), first = incl - units, items = 0, all = 0;
+  for (int w = 0; w < warps; ++w) {
+    const int2 c = counts[w];
+    at += w < warp ? c.x : 0;
+    first += w < warp ? c.y : 0;
+    items += c.x;
+    all += c.y;
+  }
+  if (j.y > 0) todo[at] = make_int4(threadIdx.x, j.x, j.y, first);
+  __syncthreads();
+  return make_int2(items, all);
+}
+
+// The item of unit u.
+__device__ __forceinline__ int4 join_of(const int4* todo, int items, int u) {
+  int l = 0, h = items;
+  while (h - l > 1) {
+    const int mid = (l + h) >> 1;
+    if (todo[mid].w <= u) l = mid; else h = mid;
+  }
+  return todo[l];
+}
 
 // The base of exponentials whose largest argument is m: 0 where nothing but -inf has been seen.
 __device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
