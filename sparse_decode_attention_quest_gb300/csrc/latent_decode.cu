@@ -69,7 +69,6 @@ constexpr int kOCol = 256;                              // O^T M-tile mt: column
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kSoftBar = 1;
 constexpr int kItemPages = 8;                           // what starting and finishing a request costs, in pages
-constexpr int kMaxCtas = 192;
 constexpr int kMaxBatch = 512;
 constexpr int kJoinWarps = 8;
 
@@ -667,8 +666,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const floa
   }
 }
 
-constexpr size_t kJoinsBytes = kMaxCtas * sizeof(int2);
-
 }  // namespace
 
 int paged_latent_max_batch() { return kMaxBatch; }
@@ -679,7 +676,7 @@ bool paged_latent_supported(int num_kv_heads, int head_dim, int head_dim_v, int 
 }
 
 size_t paged_latent_workspace_bytes(int32_t num_q_heads) {
-  return kJoinsBytes + 2 * kMaxCtas * (size_t)num_q_heads * (kDv + 1) * sizeof(float);
+  return kCounterBytes + 2 * kMaxCtas * (size_t)num_q_heads * (kDv + 1) * sizeof(float);
 }
 
 cudaError_t launch_paged_latent(const CUtensorMap& kvmap, const CUtensorMap& qmap, const KvView& kv,
@@ -699,8 +696,9 @@ cudaError_t launch_paged_latent(const CUtensorMap& kvmap, const CUtensorMap& qma
   a.scale_log2 = sm_scale * 1.4426950408889634f;
   a.out = out;
   a.out_lse = out_lse;
-  a.joins = static_cast<int2*>(workspace);
-  a.o_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kJoinsBytes);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.joins = reinterpret_cast<int2*>(ws + kArrivalBytes);  // the arrival counters before them are not used here
+  a.o_part = reinterpret_cast<float*>(ws + kCounterBytes);
   a.lse_part = a.o_part + 2 * kMaxCtas * (size_t)num_q_heads * kDv;
   a.err = err;
   const int grid = std::min(sm_count, kMaxCtas);

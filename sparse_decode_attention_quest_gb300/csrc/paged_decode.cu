@@ -45,7 +45,6 @@ constexpr int kSlots = 5;
 constexpr int kSlotBytes = 32 * 1024;
 constexpr int kMetaRing = 4;     // steps whose page masks are held (at most three are in flight)
 constexpr int kMaxPages = 16;    // pages of a step
-constexpr int kMaxCtas = 192;    // partial slots: two per CTA
 constexpr int kMaxBatch = 4096;  // requests whose prefix fits beside the ring
 constexpr int kInlineBytes = 48 * 1024;  // partials of an item, at most, where one CTA merges them
 constexpr int kJoinWarps = 8;
@@ -677,11 +676,6 @@ int paged_decode_box_heads(int num_kv_heads, int num_q_heads, int head_dim) {
   return head_plan(num_kv_heads, num_q_heads / num_kv_heads, head_dim).heads;
 }
 
-// Arrival counters and joins (the same place for every shape, so that a workspace serves calls of all shapes
-// that it is large enough for), then the CTAs' partials.
-constexpr size_t kCounterBytes = kMaxCtas * (sizeof(uint32_t) + sizeof(int2));
-static_assert(kCounterBytes % 16 == 0, "the partials are 16-byte aligned");
-
 size_t paged_decode_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
   const HeadPlan p = head_plan(num_kv_heads, num_q_heads / num_kv_heads, head_dim);
   const size_t rows = (size_t)p.heads * (num_q_heads / num_kv_heads);
@@ -722,7 +716,7 @@ cudaError_t launch_paged_decode(const CUtensorMap& kmap, const CUtensorMap& vmap
   const size_t rows = (size_t)p.heads * group;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.arrivals = reinterpret_cast<uint32_t*>(ws);
-  a.joins = reinterpret_cast<int2*>(ws + kMaxCtas * sizeof(uint32_t));
+  a.joins = reinterpret_cast<int2*>(ws + kArrivalBytes);
   a.o_part = reinterpret_cast<float*>(ws + kCounterBytes);
   a.lse_part = a.o_part + 2 * kMaxCtas * rows * kv.head_dim;
   a.err = err;

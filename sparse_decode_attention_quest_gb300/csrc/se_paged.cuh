@@ -7,6 +7,15 @@
 
 namespace se {
 
+// The workspace of a dense paged decode: arrival counters of the items by their first CTA (zero between calls),
+// the joins of every CTA, then the partials, two slots per CTA. The counters lie in the same place for every
+// shape, and nothing else is written there, so that a workspace serves calls of all shapes that it is large
+// enough for.
+constexpr int kMaxCtas = 192;
+constexpr size_t kArrivalBytes = kMaxCtas * sizeof(uint32_t);
+constexpr size_t kCounterBytes = kArrivalBytes + kMaxCtas * sizeof(int2);
+static_assert(kArrivalBytes % 16 == 0 && kCounterBytes % 16 == 0, "aligned for vector accesses");
+
 // The kept pages of a request: logical pages 0 .. sink_pages - 1, then recent_page .. (all pages: sink_pages = n).
 struct Kept {
   int len;   // tokens (clipped to the table)

@@ -8,6 +8,10 @@ library's kernels:
     se_quest_topk_pages_windowed (top-k pages + the sink/recent windows + the last page, ascending)
     se_sparse_paged_decode      (split-K flash-decode over the selected pages, partials merged in the same launch)
 or all four in one launch (se_quest_fused_step, run_fused).
+
+PagedCache is the cache's life around that step: pages from a pool, the rows of new tokens
+into their slots, dense attention over the cache, and the pages back
+(se_block_tables_extend, se_paged_kv_store, se_paged_decode, se_block_tables_release).
 """
 from __future__ import annotations
 
@@ -16,8 +20,9 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import (APPEND_OVERLAP_PREVIOUS, paged_kv, se_quest_build_summaries, se_quest_fused_step, se_quest_kept_pages_max,
-               se_quest_score_pages, se_quest_score_pages_ws, se_quest_score_workspace_size,
+from . import (APPEND_OVERLAP_PREVIOUS, paged_kv, se_block_tables_extend, se_block_tables_release, se_copy_async,
+               se_paged_decode, se_paged_decode_workspace_size, se_paged_kv_store, se_quest_build_summaries, se_quest_fused_step,
+               se_quest_kept_pages_max, se_quest_score_pages, se_quest_score_pages_ws, se_quest_score_workspace_size,
                se_quest_topk_pages_windowed, se_quest_update_summaries,
                se_quest_update_summaries_ex, se_snapkv_score_and_compact_windowed,
                se_snapkv_workspace_size, se_sparse_decode_plan, se_sparse_decode_workspace_size,
@@ -30,6 +35,71 @@ def new_summary(k_cache: torch.Tensor) -> torch.Tensor:
     """Summary storage beside a cache [P][Hkv][16][D]: bf16 [P][Hkv][2][D]."""
     P, H, _, D = k_cache.shape
     return torch.empty(P, H, 2, D, dtype=torch.bfloat16, device=k_cache.device)
+
+
+class DenseAttention:
+    """se_paged_decode's buffers for a cache view: output, log-sum-exp and workspace of ``batch`` requests."""
+
+    def __init__(self, kv, batch: int, num_q_heads: int, device, sm_scale: Optional[float] = None):
+        self.kv = kv
+        self.sm_scale = sm_scale if sm_scale is not None else 1.0 / math.sqrt(kv.head_dim)
+        self.out = torch.empty(batch, num_q_heads, kv.head_dim_v, dtype=torch.bfloat16, device=device)
+        self.lse = torch.empty(batch, num_q_heads, dtype=torch.float32, device=device)
+        ws = se_paged_decode_workspace_size(batch, num_q_heads, kv.num_kv_heads, kv.head_dim, kv.head_dim_v)
+        # zero-filled once: the counters of the join start at zero and every call leaves them so
+        self.workspace = torch.zeros(max(ws, 16), dtype=torch.uint8, device=device)
+
+    def run(self, q, block_table, seq_lens, sink_tokens: int = 0, recent_tokens: int = 0, stream=None, kv=None):
+        se_paged_decode(self.kv if kv is None else kv, q, block_table, seq_lens, self.sm_scale, self.out, self.lse,
+                        self.workspace, sink_tokens, recent_tokens, stream)
+        return self.out
+
+
+class PagedCache:
+    """A paged cache with its page pool, for up to ``batch`` requests of up to ``max_len`` tokens.
+
+    A step is extend (pages, slots and positions for the new tokens), store (their K and V rows, and the
+    page summaries when the cache keeps them) and attend (one query per request over all its tokens, or over
+    a sink and a recent window). Lengths live on the device and nothing depends on them on the host, so the
+    calls of a step can be recorded once (se_capture_begin ... se_capture_end) and replayed. release returns
+    pages to the pool. ``head_dim_v`` (with ``latent``): the value is the first dims of the key row.
+    """
+
+    def __init__(self, num_pages: int, batch: int, max_len: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                 max_new_tokens: int, device, latent: bool = False, head_dim_v: Optional[int] = None,
+                 summary: bool = False, sm_scale: Optional[float] = None):
+        i32 = dict(dtype=torch.int32, device=device)
+        self.k = torch.zeros(num_pages, num_kv_heads, PAGE, head_dim, dtype=torch.bfloat16, device=device)
+        self.v = None if latent else torch.zeros_like(self.k)
+        self.summary = new_summary(self.k) if summary else None
+        self.kv = paged_kv(self.k, self.v, self.summary, head_dim_v if latent else None)
+        self.free_pages = torch.arange(num_pages, **i32)
+        self.pool_state = torch.tensor([num_pages, 0, 0, 0], **i32)
+        self.block_table = torch.zeros(batch, max(1, (max_len + PAGE - 1) // PAGE), **i32)
+        self.lens = torch.zeros(batch, **i32)
+        self.no_tokens = torch.zeros(batch, **i32)
+        self.token_start = torch.zeros(batch + 1, **i32)
+        self.slot_map = torch.full((max_new_tokens,), -1, **i32)
+        self.positions = torch.zeros(max_new_tokens, **i32)
+        self.attention = DenseAttention(self.kv, batch, num_q_heads, device, sm_scale)
+
+    def extend(self, new_lens, stream=None):
+        """Pages and slots for new_lens[b] tokens of every request; the lengths grow."""
+        se_block_tables_extend(self.free_pages, self.pool_state, self.block_table, self.lens, new_lens, self.lens,
+                               self.token_start, self.slot_map, self.positions, stream)
+
+    def store(self, k_new, v_new=None, stream=None):
+        """The rows [T][Hkv][D] of the tokens that extend placed, in batch order (T up to max_new_tokens)."""
+        se_paged_kv_store(self.kv, k_new, v_new, self.slot_map[:k_new.shape[0]], stream)
+
+    def attend(self, q, sink_tokens: int = 0, recent_tokens: int = 0, stream=None):
+        return self.attention.run(q, self.block_table, self.lens, sink_tokens, recent_tokens, stream)
+
+    def release(self, keep_lens=None, stream=None):
+        """The pages behind keep_lens[b] tokens (None: all of them) back to the pool; the lengths shrink. A page
+        that keep_lens ends in keeps its summary, which bounds the dropped keys too."""
+        se_block_tables_release(self.free_pages, self.pool_state, self.block_table, self.lens, keep_lens, stream)
+        se_copy_async(self.lens, self.no_tokens if keep_lens is None else keep_lens, stream)
 
 
 class QuestDecodeStep:
@@ -64,6 +134,7 @@ class QuestDecodeStep:
         ws = se_sparse_decode_workspace_size(self.B, self.Hq, self.H, self.Dv, self.sel_stride)
         # zero-filled once: the decode's split-merge counters start at zero and every call leaves them so
         self.workspace = torch.zeros(max(ws, 16), dtype=torch.uint8, device=dev)
+        self.dense: Optional[DenseAttention] = None
         self.score_ws = None
         if score_workspace:
             sws = se_quest_score_workspace_size(self.B, self.H, self.D)
@@ -97,6 +168,13 @@ class QuestDecodeStep:
         se_sparse_paged_decode(self.kv, q, self.block_table, seq_lens, self.sel if sel is None else sel,
                                self.counts if counts is None else counts, self.sm_scale, self.out, self.lse,
                                self.workspace, stream)
+
+    def attend_dense(self, q, seq_lens, stream=None):
+        """Attention over every page of the cache instead of the selected ones: a layer that stays dense.
+        The output is a buffer of its own (``self.dense.out``)."""
+        if self.dense is None:
+            self.dense = DenseAttention(self.kv, self.B, self.Hq, self.k_cache.device, self.sm_scale)
+        return self.dense.run(q, self.block_table, seq_lens, stream=stream)
 
     def run_fused(self, q, seq_lens, k_new=None, v_new=None, stream=None):
         """The whole step in one launch (se_quest_fused_step): ``seq_lens`` are the lengths
@@ -171,6 +249,7 @@ class SnapKVDecodeCache:
         self.live = 0
         self.lens = torch.zeros(batch, dtype=torch.int32, device=device)
         self.q_window = torch.zeros(batch, window, num_q_heads, head_dim, dtype=torch.bfloat16, device=device)
+        self.attention: Optional[DenseAttention] = None
         self.kept = torch.empty(batch, num_kv_heads, self.kept_max, dtype=torch.int32, device=device)
         self.counts = torch.empty(batch, num_kv_heads, dtype=torch.int32, device=device)
         self.steps = 0
@@ -205,3 +284,10 @@ class SnapKVDecodeCache:
         self.steps += 1
         if self.steps == self.period:
             self.evict_from(self.kv(), self.block_table, self.lens, self.q_window, self.max_len, stream)
+
+    def attend(self, q, stream=None):
+        """Attention of one query per request q [B][Hq][D] over its tokens in the live pool: the decode of a
+        compacted cache."""
+        if self.attention is None:
+            self.attention = DenseAttention(self.kv(), self.B, self.Hq, self.lens.device, self.sm_scale)
+        return self.attention.run(q, self.block_table, self.lens, stream=stream, kv=self.kv())

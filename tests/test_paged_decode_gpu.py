@@ -79,6 +79,7 @@ class Inputs:
                            self.ws if ws is None else ws, self.sink, self.recent, stream)
         torch.cuda.synchronize()
         assert bool((out[B] == GUARD).all()) and bool((ls[B:] == GUARD).all())  # rows behind the batch
+        assert not bool((self.ws if ws is None else ws)[:768].any())            # the counters are back at zero
         return out[:B], ls[:B] if lse else None
 
     def oracle(self):
