@@ -9,8 +9,10 @@
 // A kept row (1152 bytes) is read once. With 64 heads it takes 139 kflop, 121
 // flops a byte: at the copy rate a third of the tensor cores' time at full rate,
 // but the products are small (64 heads) and bound by shared-memory reads: a
-// 64-token tile takes 1290 clocks for S^T and 870 for PV measured alone, of the
-// 3100 that its 72 KB take at an SM's share of HBM. So both must overlap the copies.
+// 64-token tile takes 1200 clocks for S^T and 870 for PV measured alone, of the
+// 3150 that its 72 KB take at the rate at which the 128-dim caches are read (7.1
+// TB/s over 152 SMs at 2.07 GHz). So both must overlap the copies, and a tile's
+// softmax must be short.
 //
 //  * Work: the requests follow one another on a line, each as long as its kept
 //    pages and an overhead, which the CTAs share equally in tiles of 64 tokens (4
@@ -21,12 +23,16 @@
 //    leave room for two tiles, 144 KB, which must cover the copies' latency as
 //    well as the two products and the softmax: so the boxes of the tiles to come
 //    are prefetched into L2 kPrefetch tiles ahead.
-//  * S^T = K Q^T: M = 64 tokens, N = heads, 36 K steps; the tile is the K-major A
-//    operand, the queries are B. O^T += V^T P^T: four M = 128 products per 16
-//    tokens, A = the tile's first 512 dims read MN-major, B = P read MN-major. One
-//    warp issues each, all lanes converged with an elected issuer: a lone lane's
-//    code moves every descriptor to the uniform registers first and issues an
-//    S^T product every 49 clocks instead of 35.
+//  * S^T = K Q^T: M = 64 tokens, N = heads, 36 K steps in two accumulators; the
+//    tile is the K-major A operand, the queries are B. O^T += V^T P^T: four M = 128
+//    products per 16 tokens, A = the tile's first 512 dims read MN-major, B = P read
+//    MN-major. Two warps issue S^T and one PV, all lanes converged with an elected
+//    issuer: a lone lane's code moves every descriptor to the uniform registers
+//    first and issues an S^T product every 49 clocks instead of 35. (One warp for
+//    all products, PV first, was slower: 436 against 416 us for 64 x 32K tokens;
+//    so was releasing a tile page by page, whose commits cost more than the earlier
+//    copies gained.) The second S^T warp gained 16 us, logits scaled and shifted
+//    in one FMA 20 us: 392 us.
 //  * Eight softmax warps read S^T from TMEM (a thread one token x 16 heads), keep
 //    a running maximum per head that moves only when a tile exceeds it by 2^8
 //    (then the heads' output columns are rescaled in TMEM), and write P as bf16
@@ -59,12 +65,13 @@ constexpr int kQOff = kStages * kStageBytes;
 constexpr int kMiscOff = kQOff + kQBytes;
 constexpr int kSoftThreads = 256;                       // warps 0-7: softmax + epilogue
 constexpr int kSoftWarps = kSoftThreads / 32;
-constexpr int kSWarp = 8;                               // issues S^T, owns TMEM
+constexpr int kSWarp = 8;                               // issues S^T of chunks 0-4, owns TMEM
 constexpr int kPvWarp = 9;                              // issues PV
 constexpr int kLoadWarp = 10;                           // copies
-constexpr int kThreads = 352;
+constexpr int kSWarp2 = 11;                             // issues S^T of chunks 5-8
+constexpr int kThreads = 384;
 constexpr int kTmemCols = 512;
-constexpr int kSCol = 0;                                // S^T of tile parity s: columns 64 s
+constexpr int kSCol = 0;                                // S^T of tile parity s: columns 128 s and 128 s + 64, to be added
 constexpr int kOCol = 256;                              // O^T M-tile mt: columns 256 + 64 mt
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kSoftBar = 1;
@@ -186,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
   uint64_t* o_free = bars + 11;  // O^T read by the epilogue
   uint64_t* q_full = bars + 12;  // the request's queries landed
   uint64_t* q_empty = bars + 13; // the last S^T product of a segment is done
-  uint64_t* fin = bars + 14;     // every product of the CTA is done (both issuers)
+  uint64_t* fin = bars + 14;     // every product of the CTA is done (all three issuers)
   // The PV products of a segment's last tile are done, one phase per segment: the epilogue cannot wait on
   // empty, which may be a phase behind (a parity wait names the current or the preceding phase only).
   uint64_t* o_last = bars + 15;
@@ -223,14 +230,14 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&s_full[s], 1);
+      mbar_init(&s_full[s], 2);
       mbar_init(&s_free[s], kSoftWarps);
       mbar_init(&p_full[s], kSoftWarps);
     }
     mbar_init(o_free, kSoftWarps);
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
-    mbar_init(fin, 2);
+    mbar_init(q_empty, 2);
+    mbar_init(fin, 3);
     mbar_init(o_last, 1);
     mbar_fence_init();
   }
@@ -278,11 +285,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
       }
       const int i = i0 + pg;
       const int phys = page_of(i);
-      // L2 prefetch: the tile kPrefetch ahead (lanes 0-7), and at a segment's start those before it.
-      for (int d = c.t == 0 ? 1 : kPrefetch; d <= kPrefetch; ++d) {
-        const int ahead = page_of(i + d * kTilePages);
-        if (lane < 8 && ahead >= 0) tma_prefetch_3d(&kvmap, 0, ahead * kPageSize + hf * kGroupRows, 0);
-      }
       if (lane == 0 && c.j >= 2 && !mbar_wait(&empty[s], ((c.j >> 1) - 1) & 1)) dead = true;
       dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
       if (dead) break;
@@ -305,6 +307,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         __syncwarp();
         if (lane < kChunks) tma_load_3d(smem + kQOff + lane * kQRows * 128, &qmap, lane * 64, 0, c.sg.b, q_full, policy);
       }
+      // L2 prefetch: the tile kPrefetch ahead (lanes 0-7), and at a segment's start those before it.
+      for (int d = c.t == 0 ? 1 : kPrefetch; d <= kPrefetch; ++d) {
+        const int ahead = page_of(i + d * kTilePages);
+        if (lane < 8 && ahead >= 0) tma_prefetch_3d(&kvmap, 0, ahead * kPageSize + hf * kGroupRows, 0);
+      }
     }
     // Every copy has landed before the CTA leaves.
     if (lane == 0) {
@@ -313,7 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
       if (dead) raise_error(a.err, SE_DEVERR_WAIT_TIMEOUT);
     }
     __syncwarp();
-  } else if (warp == kSWarp) {
+  } else if (warp == kSWarp || warp == kSWarp2) {
+    const int hf = warp == kSWarp2;  // the half of the K steps
     // ------------------------------------------------------------ S^T
     const uint32_t idesc = umma_idesc_bf16(64, Hq);
     const uint64_t dk0 = umma_desc_sw128_groups(smem0, kGroupBytes), dq = umma_desc_sw128(smem0 + kQOff);
@@ -326,15 +334,18 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         break;
       }
       tc05_fence_after();
-      const uint32_t d = tmem + kSCol + s * 64;
+      const uint32_t d = tmem + kSCol + s * 128 + hf * 64;
       const uint64_t dk = dk0 + (s ? (uint64_t)(kStageBytes >> 4) : 0);
       // 16 dims are 32 bytes of a 128-byte row; the next 64 dims are a chunk further.
 #pragma unroll
-      for (int ch = 0; ch < kChunks; ++ch)
+      for (int ch = 0; ch < 5; ++ch) {
+        if (ch == 4 && hf) break;  // 5 and 4 chunks
+        const int cc = ch + 5 * hf;
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-          mma_elected(d, dk + ch * (kChunkBytes >> 4) + 2 * x, dq + ch * (kQRows * 128 >> 4) + 2 * x, idesc,
+          mma_elected(d, dk + cc * (kChunkBytes >> 4) + 2 * x, dq + cc * (kQRows * 128 >> 4) + 2 * x, idesc,
                       ch + x > 0 ? 1u : 0u);
+      }
       commit_elected(&s_full[s]);
       if (c.last()) commit_elected(q_empty);
     }
@@ -377,17 +388,21 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
     const int parts1 = neighbours_of(slices, blockIdx.x, slice).parts1;
     int2 join = make_int2(0, 0);              // the item that goes on behind the slice
-    float m_h[16], l_h[16];
+    float m_h[16], b_h[16], l_h[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m_h[i] = l_h[i] = 0.f;
+    for (int i = 0; i < 16; ++i) m_h[i] = b_h[i] = l_h[i] = 0.f;
     for (; c.valid; c.next()) {
       const int j = c.j, t = c.t, s = j & 1;
       const bool ok_s = __all_sync(0xffffffffu, mbar_wait(&s_full[s], (j >> 1) & 1));
       uint32_t r[16];
       if (ok_s) {
         tc05_fence_after();
-        tmem_ld16x2_16(tmem + lane_base + kSCol + s * 64 + 32 * (warp >> 2), r);
+        uint32_t r2[16];
+        tmem_ld16x2_16(tmem + lane_base + kSCol + s * 128 + 32 * (warp >> 2), r);
+        tmem_ld16x2_16(tmem + lane_base + kSCol + s * 128 + 64 + 32 * (warp >> 2), r2);
         tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(r2[i]));
       } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i) r[i] = 0u;
@@ -398,11 +413,14 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
       const bool ok_f = mbar_wait(&full[s], (j >> 1) & 1);  // the masks of the tile
       dead = dead || !ok_s || !ok_f;
       const bool tok_ok = in_mask(masks[s * kTilePages + q4], tok);
-      float x[16], v[16];
+      // Logits against the running maxima (0 for a head that has none yet).
+      float x[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        x[i] = (tok_ok && hh + i < Hq) ? __uint_as_float(r[i]) * a.scale_log2 : -INFINITY;
-        v[i] = x[i];
+      for (int i = 0; i < 16; ++i) x[i] = fmaf(__uint_as_float(r[i]), a.scale_log2, -b_h[i]);
+      if (!tok_ok || hh + 16 > Hq) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (!tok_ok || hh + i >= Hq) x[i] = -INFINITY;
       }
       if (!tok_ok && (warp >> 2) == 0) {
         // Rows that are not kept (or not copied) may hold NaN: zero their value dims, as 0 * NaN is not 0.
@@ -416,8 +434,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
       // nothing but P and l. Otherwise the tile maxima are exchanged and the running maxima recomputed.
       bool need = t == 0 || dead;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) need = need || x[i] > m_h[i] + kRescaleLog2;
+      for (int i = 0; i < 16; ++i) need = need || x[i] > kRescaleLog2;
       if (bar_red_or(kSoftBar, kSoftThreads, need)) {
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = tok_ok && hh + i < Hq ? __uint_as_float(r[i]) * a.scale_log2 : -INFINITY;
         half_warp_reduce16<true>(v, lane);
         // Two buffers by tile parity: the barriers keep every thread within one tile of the others.
         float* xm = xmax + s * 256;
@@ -446,6 +467,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
             moved = moved || mv;
             m_h[i] = mn;
             l_h[i] = t == 0 ? 0.f : l_h[i] * f[i];
+            b_h[i] = finite_base(mn);
+            x[i] = tok_ok && hh + i < Hq ? fmaf(__uint_as_float(r[i]), a.scale_log2, -b_h[i]) : -INFINITY;
           }
         }
         if (__any_sync(0xffffffffu, moved)) {
@@ -477,9 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
       uint32_t pk[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float ma = m_h[2 * i] == -INFINITY ? 0.f : m_h[2 * i];
-        const float mb = m_h[2 * i + 1] == -INFINITY ? 0.f : m_h[2 * i + 1];
-        const float pa = fast_exp2(x[2 * i] - ma), pb = fast_exp2(x[2 * i + 1] - mb);
+        const float pa = fast_exp2(x[2 * i]), pb = fast_exp2(x[2 * i + 1]);
         l_h[2 * i] += pa;
         l_h[2 * i + 1] += pb;
         pk[i] = pack_bf16x2(pa, pb);

@@ -26,11 +26,15 @@
 //    16 Hc rows x D / 64 brings a whole page of the group (16 to 32 KB for 4 to 8
 //    heads). One warp issues them into a ring of five 32 KB slots, K and V of a
 //    step in turn, 128-byte swizzled.
-//  * Products: a consumer warp holds one (KV head, 16 query rows) state; R warps
-//    share the pages of a step when the heads do not fill the warps. S = Q K^T
-//    and O += P V are m16n8k16 bf16 MMAs with fp32 accumulators; a group of
-//    G <= 16 query heads wastes rows of the tile, which does not matter at a few
-//    flops per byte.
+//  * Products: a consumer warp holds one (KV head, tile of query heads) state; R
+//    warps share the pages of a step when the heads do not fill the warps. S^T =
+//    K Q^T and O^T += V^T P^T are m16n8k16 bf16 MMAs with fp32 accumulators: the
+//    page's 16 tokens, or 16 dims, are the rows, and up to 8 query heads the
+//    columns (two column tiles for 9 to 16), so that a group of up to eight heads
+//    wastes no rows: the other way round, with heads as rows, half of the MMAs
+//    and of the exponentials were for rows that do not exist, and a block took
+//    a warp 450 instructions (8 x 16K tokens, 4 KV heads: 50.7 us). P^T goes from
+//    accumulator to operand layout by two 8 x 8 transposes in registers.
 //  * Rows that are not kept: their logits become -inf, and their value rows are
 //    zeroed in shared memory first, since 0 * NaN is not 0.
 #include <algorithm>
@@ -48,6 +52,13 @@ constexpr int kMaxPages = 16;    // pages of a step
 constexpr int kMaxBatch = 4096;  // requests whose prefix fits beside the ring
 constexpr int kInlineBytes = 48 * 1024;  // partials of an item, at most, where one CTA merges them
 constexpr int kJoinWarps = 8;
+
+// Where a state staged in shared memory keeps (head, dim): the dims of a row of D, turned by eight per pair of
+// heads, so that the accumulators' lanes (four head pairs, eight dims) write to 32 banks.
+template <int kD>
+__device__ __forceinline__ int stage_at(int head, int dim) {
+  return head * kD + (dim ^ (((head >> 1) & 3) << 3));
+}
 
 template <int kD>
 struct Cfg {
@@ -70,9 +81,8 @@ struct PagedArgs {
   int32_t group;        // query heads per KV head
   int32_t heads;        // KV heads of an item (Hc)
   int32_t head_groups;  // items per request
-  int32_t mtiles;       // 16-row query tiles per KV head
+  int32_t mtiles;       // tiles of 8 or 16 query heads per KV head
   int32_t replicas;     // warps that share a (head, tile)
-  int32_t handover;     // rows of a state handed over at a time: 16, or 8 where 16 do not fit
   int32_t step_pages;   // pages of a step
   int32_t num_pages;
   int32_t batch;
@@ -195,7 +205,7 @@ __device__ __forceinline__ void join_rows(const float* o_part, const float* lse_
   }
 }
 
-template <int kD>
+template <int kD, int kNt>
 __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                                                                            const __grid_constant__ CUtensorMap vmap,
                                                                            const PagedArgs a) {
@@ -300,8 +310,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
   const int combo = warp % combos, replica = warp / combos;
   const int hc = combo / a.mtiles, mt = combo % a.mtiles;
   const int g = lane >> 2, t = lane & 3;
-  const int row_a = mt * 16 + g, row_b = row_a + 8;  // query heads of the KV head's group
-  const bool has_a = works && row_a < G, has_b = works && row_b < G;
+  const int tile_head = mt * 8 * kNt;  // first query head of the tile, in its KV head's group
   const uint32_t ring0 = smem_addr(ring);
   const uint32_t plane = (uint32_t)heads * kPageSize * 128;  // 64 dims of a page's rows
   const uint32_t page_bytes = plane * C::kChunks;
@@ -311,23 +320,29 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
   bool handed = false;
 
   while (seg.next()) {
-    uint32_t qa[kD / 16][4];
-    {
-      const uint16_t* q0 = a.q + (size_t)seg.b * a.q_stride + (size_t)((seg.group * heads + hc) * G) * kD;
-      const uint16_t *qr0 = q0 + (size_t)row_a * kD, *qr1 = q0 + (size_t)row_b * kD;
+    // Q^T as the B operand: head g of each column tile, dims 2 t, 2 t + 1 and 8 more.
+    uint32_t qb[kD / 16][kNt][2];
+#pragma unroll
+    for (int nt = 0; nt < kNt; ++nt) {
+      const int hd = tile_head + nt * 8 + g;
+      const bool real = works && hd < G;
+      const uint16_t* qr = a.q + (size_t)seg.b * a.q_stride + (size_t)((seg.group * heads + hc) * G + (real ? hd : 0)) * kD;
 #pragma unroll
       for (int ks = 0; ks < kD / 16; ++ks) {
-        const int c = ks * 16 + 2 * t;
-        qa[ks][0] = has_a ? *reinterpret_cast<const uint32_t*>(qr0 + c) : 0u;
-        qa[ks][2] = has_a ? *reinterpret_cast<const uint32_t*>(qr0 + c + 8) : 0u;
-        qa[ks][1] = has_b ? *reinterpret_cast<const uint32_t*>(qr1 + c) : 0u;
-        qa[ks][3] = has_b ? *reinterpret_cast<const uint32_t*>(qr1 + c + 8) : 0u;
+        qb[ks][nt][0] = real ? *reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * t) : 0u;
+        qb[ks][nt][1] = real ? *reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * t + 8) : 0u;
       }
     }
-    float o[kD / 8][4];
+    // O^T: dims 16 i + g (0, 1) and 8 more (2, 3), heads 2 t and 2 t + 1 of each column tile; m and l of those heads
+    // (l: the thread's tokens only).
+    float o[kD / 16][kNt][4], m[kNt][2], l[kNt][2];
 #pragma unroll
-    for (int n = 0; n < kD / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    for (int nt = 0; nt < kNt; ++nt) {
+#pragma unroll
+      for (int i = 0; i < kD / 16; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
 
     for (int i0 = seg.lo; i0 < seg.hi; i0 += Pg, ++step, j += 2) {
       if (!works) continue;
@@ -338,65 +353,78 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
         const uint32_t mask = dead || i0 + pg >= seg.hi ? 0u : meta[(step % kMetaRing) * kMaxPages + pg];
         const bool last = pg + a.replicas >= Pg;
         const uint32_t blk = pg * page_bytes + (uint32_t)hc * kPageSize * 128;
-        uint32_t pa0 = 0, pa1 = 0, pa2 = 0, pa3 = 0;
+        uint32_t pb[kNt][2];
         if (mask) {
           const uint32_t kt = ring0 + sk * kSlotBytes + blk;
-          // Two n-tiles of 8 tokens, each in two accumulators: shorter chains of dependent products.
-          float s4[4][4];
+          // S^T in two accumulators: shorter chains of dependent products.
+          float s2[kNt][2][4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) s4[x][0] = s4[x][1] = s4[x][2] = s4[x][3] = 0.f;
-          const int krow = (lane & 7) + ((lane >> 4) << 3), ksub = (lane >> 3) & 1;
+          for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s2[nt][0][e] = s2[nt][1][e] = 0.f;
 #pragma unroll
           for (int ks = 0; ks < kD / 16; ++ks) {
             uint32_t r0, r1, r2, r3;
-            ldmatrix_x4(r0, r1, r2, r3, kt + (ks >> 2) * plane + swz128(krow, ((ks & 3) << 1) + ksub));
-            mma_bf16_16816(s4[2 * (ks & 1)], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], r0, r1);
-            mma_bf16_16816(s4[2 * (ks & 1) + 1], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], r2, r3);
+            ldmatrix_x4(r0, r1, r2, r3, kt + (ks >> 2) * plane + swz128(lane & 15, ((ks & 3) << 1) + (lane >> 4)));
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt)
+              mma_bf16_16816(s2[nt][ks & 1], r0, r1, r2, r3, qb[ks][nt][0], qb[ks][nt][1]);
           }
-          float sc[2][4];
-          const bool whole = mask_is_full(mask);
+          // Tokens g (0, 1) and g + 8 (2, 3), heads 2 t and 2 t + 1.
+          float z[kNt][4];
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
+          for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float z = (s4[nt][e] + s4[nt + 2][e]) * a.scale_log2;
-              sc[nt][e] = whole || in_mask(mask, nt * 8 + 2 * t + (e & 1)) ? z : -INFINITY;
+            for (int e = 0; e < 4; ++e) z[nt][e] = (s2[nt][0][e] + s2[nt][1][e]) * a.scale_log2;
+          if (!mask_is_full(mask)) {
+            const bool k0 = in_mask(mask, g), k1 = in_mask(mask, g + 8);
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt) {
+              z[nt][0] = k0 ? z[nt][0] : -INFINITY;
+              z[nt][1] = k0 ? z[nt][1] : -INFINITY;
+              z[nt][2] = k1 ? z[nt][2] : -INFINITY;
+              z[nt][3] = k1 ? z[nt][3] : -INFINITY;
             }
-          float x0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-          float x1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
-          x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-          x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-          x0 = fmaxf(x0, m0);
-          x1 = fmaxf(x1, m1);
-          // A row that has seen nothing but -inf keeps m = -inf and takes 0 as its base.
-          const float b0 = finite_base(x0), b1 = finite_base(x1);
-          const float c0 = fast_exp2(m0 - b0), c1 = fast_exp2(m1 - b1);
-          m0 = x0;
-          m1 = x1;
-          float p[2][4];
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            p[nt][0] = fast_exp2(sc[nt][0] - b0);
-            p[nt][1] = fast_exp2(sc[nt][1] - b0);
-            p[nt][2] = fast_exp2(sc[nt][2] - b1);
-            p[nt][3] = fast_exp2(sc[nt][3] - b1);
           }
-          l0 = l0 * c0 + ((p[0][0] + p[0][1]) + (p[1][0] + p[1][1]));
-          l1 = l1 * c1 + ((p[0][2] + p[0][3]) + (p[1][2] + p[1][3]));
+          float top[kNt][2];
+          bool moved = false;
 #pragma unroll
-          for (int n = 0; n < kD / 8; ++n) {
-            o[n][0] *= c0;
-            o[n][1] *= c0;
-            o[n][2] *= c1;
-            o[n][3] *= c1;
+          for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              top[nt][e] = fmaxf(z[nt][e], z[nt][2 + e]);
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xffffffffu, top[nt][e], x));
+              moved = moved || top[nt][e] > m[nt][e];
+            }
+          if (__any_sync(0xffffffffu, moved)) {
+            // Some head's maximum moves: its sums follow.
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float mn = fmaxf(m[nt][e], top[nt][e]), f = fast_exp2(m[nt][e] - finite_base(mn));
+                m[nt][e] = mn;
+                l[nt][e] *= f;
+#pragma unroll
+                for (int i = 0; i < kD / 16; ++i) {
+                  o[i][nt][e] *= f;
+                  o[i][nt][2 + e] *= f;
+                }
+              }
           }
-          // P meets V as bf16 (half a step, 2^-8 of each weight), as the MMA wants; l sums it unrounded.
-          pa0 = pack_bf16x2(p[0][0], p[0][1]);
-          pa1 = pack_bf16x2(p[0][2], p[0][3]);
-          pa2 = pack_bf16x2(p[1][0], p[1][1]);
-          pa3 = pack_bf16x2(p[1][2], p[1][3]);
+#pragma unroll
+          for (int nt = 0; nt < kNt; ++nt) {
+            // A head that has seen nothing but -inf keeps m = -inf and takes 0 as its base.
+            const float b0 = finite_base(m[nt][0]), b1 = finite_base(m[nt][1]);
+            const float p0 = fast_exp2(z[nt][0] - b0), p1 = fast_exp2(z[nt][1] - b1);
+            const float p2 = fast_exp2(z[nt][2] - b0), p3 = fast_exp2(z[nt][3] - b1);
+            l[nt][0] += p0 + p2;
+            l[nt][1] += p1 + p3;
+            // P meets V as bf16 (half a step, 2^-8 of each weight), as the MMA wants; l sums it unrounded.
+            pb[nt][0] = transpose_8x8_b16(pack_bf16x2(p0, p1));
+            pb[nt][1] = transpose_8x8_b16(pack_bf16x2(p2, p3));
+          }
         }
         if (last) {
           __syncwarp();
@@ -419,14 +447,14 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
             zeroed = true;
             __syncwarp();
           }
-          const int vtok = lane & 15, vsub = lane >> 4;
 #pragma unroll
-          for (int n = 0; n < kD / 16; ++n) {
-            const int chunk = 2 * n + vsub;
+          for (int i = 0; i < kD / 16; ++i) {
+            const int chunk = 2 * i + ((lane >> 3) & 1);
             uint32_t r0, r1, r2, r3;
-            ldmatrix_x4_trans(r0, r1, r2, r3, vt + (chunk >> 3) * plane + swz128(vtok, chunk & 7));
-            mma_bf16_16816(o[2 * n], pa0, pa1, pa2, pa3, r0, r1);
-            mma_bf16_16816(o[2 * n + 1], pa0, pa1, pa2, pa3, r2, r3);
+            ldmatrix_x4_trans(r0, r1, r2, r3,
+                              vt + (chunk >> 3) * plane + swz128((lane & 7) + ((lane >> 4) << 3), chunk & 7));
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt) mma_bf16_16816(o[i][nt], r0, r1, r2, r3, pb[nt][0], pb[nt][1]);
           }
         }
       }
@@ -436,135 +464,62 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
     }
 
     // ---- the end of a segment: this CTA's share of item (b, hg) is done
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
     const bool split = seg.split();
     const int slot = seg.lo > 0 ? 0 : 1, item = seg.b * HG + seg.group;
     if (split && slot == 0) item0 = item;
     if (split && slot == 1) item1 = item;
     const size_t out_row0 = (size_t)seg.b * a.num_q_heads + (size_t)seg.group * rows;
     const size_t part_row0 = (size_t)(2 * blockIdx.x + slot) * rows;
-    // R warps hold parts of the same rows. Up to three: the others hand their states over through shared memory,
-    // 16 or 8 rows at a time, and stream on; warp 0 of the R folds them into its own in order. Named barriers of
-    // the R warps: 2 + 2 combo, states are there; 3 + 2 combo, the slots are free again.
-    const bool shares_out = a.replicas > 3;
-    if (works && a.replicas > 1 && !shares_out) {
-      const uint32_t threads = a.replicas * 32;
-      for (int half = 0; half < (G > 8 ? 2 : 1); half += a.handover / 8) {
-        const bool both = a.handover == 16 && G > 8;
-        if (replica > 0) {
-          if (handed) named_bar_sync(3 + 2 * combo, threads);
-          handed = true;
-          // Slots by (replica - 1, combo).
-          const int sl = (replica - 1) * combos + combo;
-          float* dst = stage + (sl * a.handover + g) * kD + 2 * t;
+    // The R warps of a (head, tile) stage their states, eight query heads at a time, and share the sums and the
+    // output. Named barriers of the R warps: 2 + 2 combo, the states are there; 3 + 2 combo, they are read.
+    if (!works) continue;
+    const uint32_t threads = a.replicas * 32;
 #pragma unroll
-          for (int n = 0; n < kD / 8; ++n) {
-            *reinterpret_cast<float2*>(dst + n * 8) = half ? make_float2(o[n][2], o[n][3]) : make_float2(o[n][0], o[n][1]);
-            if (both) *reinterpret_cast<float2*>(dst + 8 * kD + n * 8) = make_float2(o[n][2], o[n][3]);
-          }
-          if (t == 0) {
-            ml[sl * 32 + g] = half ? m1 : m0;
-            ml[sl * 32 + 16 + g] = half ? l1 : l0;
-            if (both) {
-              ml[sl * 32 + 8 + g] = m1;
-              ml[sl * 32 + 24 + g] = l1;
-            }
-          }
-          named_bar_arrive(2 + 2 * combo, threads);
-        } else {
-          named_bar_sync(2 + 2 * combo, threads);
-          for (int r = 0; r < a.replicas - 1; ++r) {
-            const int sl = r * combos + combo;
-            auto fold = [&](int e, int row, float& m, float& l) {
-              const float ms = ml[sl * 32 + row], ls = ml[sl * 32 + 16 + row];
-              const float M = fmaxf(m, ms), base = finite_base(M);
-              const float fo = fast_exp2(m - base), fs = fast_exp2(ms - base);
-              const float* src = stage + (sl * a.handover + row) * kD + 2 * t;
+    for (int nt = 0; nt < kNt; ++nt) {
+      if (tile_head + nt * 8 >= G) continue;
+      if (a.replicas > 1 && handed) named_bar_sync(3 + 2 * combo, threads);
+      __syncwarp();
+      handed = true;
+      float* dst = stage + warp * 8 * kD;
 #pragma unroll
-              for (int n = 0; n < kD / 8; ++n) {
-                const float2 v = *reinterpret_cast<const float2*>(src + n * 8);
-                o[n][e] = fo * o[n][e] + fs * v.x;
-                o[n][e + 1] = fo * o[n][e + 1] + fs * v.y;
-              }
-              l = fo * l + fs * ls;
-              m = M;
-            };
-            if (half == 0) fold(0, g, m0, l0);
-            if (half == 1) fold(2, g, m1, l1);
-            if (both) fold(2, 8 + g, m1, l1);
-          }
-          const bool more = seg.more() || (half == 0 && G > 8 && !both);
-          if (more) named_bar_arrive(3 + 2 * combo, threads);
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
+        const int hd = 2 * t + e;
+#pragma unroll
+        for (int i = 0; i < kD / 16; ++i) {
+          dst[stage_at<kD>(hd, 16 * i + g)] = o[i][nt][e];
+          dst[stage_at<kD>(hd, 16 * i + g + 8)] = o[i][nt][2 + e];
+        }
+        if (g == 0) {
+          ml[warp * 16 + hd] = m[nt][e];
+          ml[warp * 16 + 8 + hd] = l[nt][e];
         }
       }
-    }
-    if (works && shares_out) {
-      // More: all R stage their states, eight rows at a time, and share the sums (one warp folding seven states
-      // took 1.3 us longer at the end of a slice).
-      const uint32_t threads = a.replicas * 32;
-      for (int half = 0; half < (G > 8 ? 2 : 1); ++half) {
-        if (handed) named_bar_sync(3 + 2 * combo, threads);
-        handed = true;
-        float* dst = stage + (warp * 8 + g) * kD + 2 * t;
-#pragma unroll
-        for (int n = 0; n < kD / 8; ++n)
-          *reinterpret_cast<float2*>(dst + n * 8) = half ? make_float2(o[n][2], o[n][3]) : make_float2(o[n][0], o[n][1]);
-        if (t == 0) {
-          ml[warp * 32 + g] = half ? m1 : m0;
-          ml[warp * 32 + 16 + g] = half ? l1 : l0;
+      if (a.replicas > 1) named_bar_sync(2 + 2 * combo, threads); else __syncwarp();
+#pragma unroll 4
+      for (int e = replica * 32 + lane; e < min(8, G - tile_head - nt * 8) * (kD / 4); e += threads) {
+        const int d = e % (kD / 4) * 4, hd = e / (kD / 4), qr = tile_head + nt * 8 + hd;
+        float M = -INFINITY;
+        for (int w = combo; w < active; w += combos) M = fmaxf(M, ml[w * 16 + hd]);
+        const float base = finite_base(M);
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = combo; w < active; w += combos) {
+          const float f = fast_exp2(ml[w * 16 + hd] - base);
+          sum += f * ml[w * 16 + 8 + hd];
+          const float4 v = *reinterpret_cast<const float4*>(stage + w * 8 * kD + stage_at<kD>(hd, d));
+          acc = make_float4(acc.x + f * v.x, acc.y + f * v.y, acc.z + f * v.z, acc.w + f * v.w);
         }
-        named_bar_sync(2 + 2 * combo, threads);
-        for (int e = replica * 32 + lane; e < 8 * (kD / 4); e += threads) {
-          const int d = e % (kD / 4) * 4, gr = e / (kD / 4), qr = mt * 16 + half * 8 + gr;
-          if (qr >= G) continue;
-          float M = -INFINITY;
-          for (int w = combo; w < active; w += combos) M = fmaxf(M, ml[w * 32 + gr]);
-          const float base = finite_base(M);
-          float l = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int w = combo; w < active; w += combos) {
-            const float f = fast_exp2(ml[w * 32 + gr] - base);
-            l += f * ml[w * 32 + 16 + gr];
-            const float4 v = *reinterpret_cast<const float4*>(stage + (w * 8 + gr) * kD + d);
-            acc = make_float4(acc.x + f * v.x, acc.y + f * v.y, acc.z + f * v.z, acc.w + f * v.w);
-          }
-          const float inv = l == 0.f ? 0.f : 1.f / l, lse2 = l == 0.f ? -INFINITY : M + log2f(l);
-          const int r = hc * G + qr;
-          acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-          if (split)
-            *reinterpret_cast<float4*>(a.o_part + (part_row0 + r) * kD + d) = acc;
-          else
-            *reinterpret_cast<uint2*>(a.out + (out_row0 + r) * kD + d) =
-                make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-          if (d == 0) {
-            if (split)
-              a.lse_part[part_row0 + r] = lse2;
-            else if (a.out_lse)
-              a.out_lse[out_row0 + r] = lse2 * kLn2;
-          }
-        }
-      }
-    }
-    if (works && replica == 0 && !shares_out) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (!(half ? has_b : has_a)) continue;
-        const float l = half ? l1 : l0, m = half ? m1 : m0;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
-        const int r = hc * G + (half ? row_b : row_a);
-#pragma unroll
-        for (int n = 0; n < kD / 8; ++n) {
-          const float x = o[n][2 * half] * inv, y = o[n][2 * half + 1] * inv;
-          if (split)
-            *reinterpret_cast<float2*>(a.o_part + (part_row0 + r) * kD + n * 8 + 2 * t) = make_float2(x, y);
-          else
-            *reinterpret_cast<uint32_t*>(a.out + (out_row0 + r) * kD + n * 8 + 2 * t) = pack_bf16x2(x, y);
-        }
-        if (t == 0) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum, lse2 = sum == 0.f ? -INFINITY : M + log2f(sum);
+        const int r = hc * G + qr;
+        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (split)
+          *reinterpret_cast<float4*>(a.o_part + (part_row0 + r) * kD + d) = acc;
+        else
+          *reinterpret_cast<uint2*>(a.out + (out_row0 + r) * kD + d) =
+              make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+        if (d == 0) {
           if (split)
             a.lse_part[part_row0 + r] = lse2;
           else if (a.out_lse)
@@ -634,29 +589,30 @@ HeadPlan head_plan(int num_kv_heads, int group, int head_dim) {
   const int warps = head_dim == 256 ? Cfg<256>::kWarps : Cfg<128>::kWarps;
   const int blocks = kSlotBytes / (kPageSize * head_dim * 2);
   HeadPlan p;
-  p.mtiles = (group + 15) / 16;
-  p.heads = 1;
-  for (int c = 2; c * p.mtiles <= warps; ++c)
-    if (num_kv_heads % c == 0) p.heads = c;
+  p.mtiles = group <= 8 ? 1 : (group + 15) / 16;
+  // As many heads per box as leave at most an eighth of a slot empty (ten heads: boxes of two, not of five; 4 KB
+  // boxes of one head read at 91% of the measured copy rate, slots five eighths full at 73%).
+  for (int c = 1; c * p.mtiles <= warps; ++c) {
+    if (num_kv_heads % c) continue;
+    const int r = warps / (c * p.mtiles), pages = blocks / c / r * r;
+    if (c > 1 && pages * c * 8 < blocks * 7) continue;
+    p.heads = c;
+    p.replicas = r;
+    p.step_pages = pages;
+  }
   p.head_groups = num_kv_heads / p.heads;
-  p.replicas = warps / (p.heads * p.mtiles);
-  p.step_pages = blocks / p.heads / p.replicas * p.replicas;
   return p;
 }
 
-int stage_floats(int head_dim) {
-  return head_dim == 64 ? Cfg<64>::kStageFloats : head_dim == 128 ? Cfg<128>::kStageFloats : Cfg<256>::kStageFloats;
-}
-
-template <int kD>
+template <int kD, int kNt>
 cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const PagedArgs& a, int grid,
                    cudaStream_t stream) {
   const size_t smem = Cfg<kD>::kFixed + (size_t)(2 * a.batch + 1) * 4;
   static_assert(Cfg<kD>::kMaxSmem <= 227 * 1024, "the largest batch fits");
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem(paged_decode_kernel<kD>, Cfg<kD>::kMaxSmem, allowed);
+  cudaError_t e = allow_smem(paged_decode_kernel<kD, kNt>, Cfg<kD>::kMaxSmem, allowed);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(paged_decode_kernel<kD>, dim3(grid), dim3(Cfg<kD>::kThreads), smem, stream, kmap, vmap, a);
+  e = launch_pdl(paged_decode_kernel<kD, kNt>, dim3(grid), dim3(Cfg<kD>::kThreads), smem, stream, kmap, vmap, a);
   if (e != cudaSuccess || !a.deferred) return e;
   const int rows = a.heads * a.group;
   return launch_pdl(paged_join_kernel<kD>, dim3(std::min(grid * rows, 8 * grid)), dim3(kJoinWarps * 32), 0, stream,
@@ -700,9 +656,6 @@ cudaError_t launch_paged_decode(const CUtensorMap& kmap, const CUtensorMap& vmap
   a.mtiles = p.mtiles;
   a.replicas = p.replicas;
   a.step_pages = p.step_pages;
-  // The R - 1 states of every (head, tile) fit the staging area whole, or eight rows at a time.
-  const int staged = (p.replicas - 1) * p.heads * p.mtiles * (group > 8 ? 16 : 8) * kv.head_dim;
-  a.handover = group > 8 && staged <= stage_floats(kv.head_dim) ? 16 : 8;
   a.num_pages = kv.num_pages;
   a.batch = batch;
   a.block_table = block_table;
@@ -728,9 +681,9 @@ cudaError_t launch_paged_decode(const CUtensorMap& kmap, const CUtensorMap& vmap
   const long long most = std::min<long long>(grid, (pages + p.step_pages) / (2 * p.step_pages + 1) + 2);
   a.deferred = most * (long long)(rows * kv.head_dim * sizeof(float)) > kInlineBytes;
   switch (kv.head_dim) {
-    case 64: return launch<64>(kmap, vmap, a, grid, stream);
-    case 128: return launch<128>(kmap, vmap, a, grid, stream);
-    default: return launch<256>(kmap, vmap, a, grid, stream);
+    case 64: return group <= 8 ? launch<64, 1>(kmap, vmap, a, grid, stream) : launch<64, 2>(kmap, vmap, a, grid, stream);
+    case 128: return group <= 8 ? launch<128, 1>(kmap, vmap, a, grid, stream) : launch<128, 2>(kmap, vmap, a, grid, stream);
+    default: return group <= 8 ? launch<256, 1>(kmap, vmap, a, grid, stream) : launch<256, 2>(kmap, vmap, a, grid, stream);
   }
 }
 
