@@ -205,7 +205,9 @@ __device__ __forceinline__ void join_rows(const float* o_part, const float* lse_
   }
 }
 
-template <int kD, int kNt>
+// kNt: column tiles of eight query heads; kSolo: no two warps share a (head, tile) (code of its own: as a branch
+// beside the other it cost that one 0.8 us of 9.9).
+template <int kD, int kNt, bool kSolo>
 __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                                                                            const __grid_constant__ CUtensorMap vmap,
                                                                            const PagedArgs a) {
@@ -477,7 +479,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
 #pragma unroll
     for (int nt = 0; nt < kNt; ++nt) {
       if (tile_head + nt * 8 >= G) continue;
-      if (a.replicas > 1 && handed) named_bar_sync(3 + 2 * combo, threads);
+      if (!kSolo && handed) named_bar_sync(3 + 2 * combo, threads);
       __syncwarp();
       handed = true;
       float* dst = stage + warp * 8 * kD;
@@ -486,6 +488,23 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
         const int hd = 2 * t + e;
+        if constexpr (kSolo) {
+          // No other states: the row is final.
+          const float inv = l[nt][e] == 0.f ? 0.f : 1.f / l[nt][e];
+          const float lse2 = l[nt][e] == 0.f ? -INFINITY : m[nt][e] + log2f(l[nt][e]);
+          const int qr = tile_head + nt * 8 + hd, r = hc * G + qr;
+#pragma unroll
+          for (int i = 0; i < kD / 16; ++i) {
+            o[i][nt][e] *= inv;
+            o[i][nt][2 + e] *= inv;
+          }
+          if (g == 0 && qr < G) {
+            if (split)
+              a.lse_part[part_row0 + r] = lse2;
+            else if (a.out_lse)
+              a.out_lse[out_row0 + r] = lse2 * kLn2;
+          }
+        }
 #pragma unroll
         for (int i = 0; i < kD / 16; ++i) {
           dst[stage_at<kD>(hd, 16 * i + g)] = o[i][nt][e];
@@ -496,10 +515,26 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
           ml[warp * 16 + 8 + hd] = l[nt][e];
         }
       }
-      if (a.replicas > 1) named_bar_sync(2 + 2 * combo, threads); else __syncwarp();
+      const int hds = min(8, G - tile_head - nt * 8);
+      const size_t r0 = hc * G + tile_head + nt * 8;
+      if constexpr (kSolo) {
+        __syncwarp();
 #pragma unroll 4
-      for (int e = replica * 32 + lane; e < min(8, G - tile_head - nt * 8) * (kD / 4); e += threads) {
-        const int d = e % (kD / 4) * 4, hd = e / (kD / 4), qr = tile_head + nt * 8 + hd;
+        for (int e = lane; e < hds * (kD / 4); e += 32) {
+          const int d = e % (kD / 4) * 4, hd = e / (kD / 4);
+          const float4 v = *reinterpret_cast<const float4*>(dst + stage_at<kD>(hd, d));
+          if (split)
+            *reinterpret_cast<float4*>(a.o_part + (part_row0 + r0 + hd) * kD + d) = v;
+          else
+            *reinterpret_cast<uint2*>(a.out + (out_row0 + r0 + hd) * kD + d) =
+                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        }
+        continue;
+      }
+      named_bar_sync(2 + 2 * combo, threads);
+#pragma unroll 4
+      for (int e = replica * 32 + lane; e < hds * (kD / 4); e += threads) {
+        const int d = e % (kD / 4) * 4, hd = e / (kD / 4);
         float M = -INFINITY;
         for (int w = combo; w < active; w += combos) M = fmaxf(M, ml[w * 16 + hd]);
         const float base = finite_base(M);
@@ -512,7 +547,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
           acc = make_float4(acc.x + f * v.x, acc.y + f * v.y, acc.z + f * v.z, acc.w + f * v.w);
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum, lse2 = sum == 0.f ? -INFINITY : M + log2f(sum);
-        const int r = hc * G + qr;
+        const size_t r = r0 + hd;
         acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         if (split)
           *reinterpret_cast<float4*>(a.o_part + (part_row0 + r) * kD + d) = acc;
@@ -604,19 +639,28 @@ HeadPlan head_plan(int num_kv_heads, int group, int head_dim) {
   return p;
 }
 
-template <int kD, int kNt>
-cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const PagedArgs& a, int grid,
+template <int kD, int kNt, bool kSolo>
+cudaError_t launch_as(const CUtensorMap& kmap, const CUtensorMap& vmap, const PagedArgs& a, int grid,
                    cudaStream_t stream) {
   const size_t smem = Cfg<kD>::kFixed + (size_t)(2 * a.batch + 1) * 4;
   static_assert(Cfg<kD>::kMaxSmem <= 227 * 1024, "the largest batch fits");
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem(paged_decode_kernel<kD, kNt>, Cfg<kD>::kMaxSmem, allowed);
+  cudaError_t e = allow_smem(paged_decode_kernel<kD, kNt, kSolo>, Cfg<kD>::kMaxSmem, allowed);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(paged_decode_kernel<kD, kNt>, dim3(grid), dim3(Cfg<kD>::kThreads), smem, stream, kmap, vmap, a);
+  e = launch_pdl(paged_decode_kernel<kD, kNt, kSolo>, dim3(grid), dim3(Cfg<kD>::kThreads), smem, stream, kmap, vmap, a);
   if (e != cudaSuccess || !a.deferred) return e;
   const int rows = a.heads * a.group;
   return launch_pdl(paged_join_kernel<kD>, dim3(std::min(grid * rows, 8 * grid)), dim3(kJoinWarps * 32), 0, stream,
                     a.o_part, a.lse_part, a.joins, grid, rows, a.out, a.out_lse);
+}
+
+template <int kD>
+cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const PagedArgs& a, int grid,
+                   cudaStream_t stream) {
+  const bool solo = a.replicas == 1;
+  if (a.group <= 8)
+    return solo ? launch_as<kD, 1, true>(kmap, vmap, a, grid, stream) : launch_as<kD, 1, false>(kmap, vmap, a, grid, stream);
+  return solo ? launch_as<kD, 2, true>(kmap, vmap, a, grid, stream) : launch_as<kD, 2, false>(kmap, vmap, a, grid, stream);
 }
 
 }  // namespace
@@ -681,9 +725,9 @@ cudaError_t launch_paged_decode(const CUtensorMap& kmap, const CUtensorMap& vmap
   const long long most = std::min<long long>(grid, (pages + p.step_pages) / (2 * p.step_pages + 1) + 2);
   a.deferred = most * (long long)(rows * kv.head_dim * sizeof(float)) > kInlineBytes;
   switch (kv.head_dim) {
-    case 64: return group <= 8 ? launch<64, 1>(kmap, vmap, a, grid, stream) : launch<64, 2>(kmap, vmap, a, grid, stream);
-    case 128: return group <= 8 ? launch<128, 1>(kmap, vmap, a, grid, stream) : launch<128, 2>(kmap, vmap, a, grid, stream);
-    default: return group <= 8 ? launch<256, 1>(kmap, vmap, a, grid, stream) : launch<256, 2>(kmap, vmap, a, grid, stream);
+    case 64: return launch<64>(kmap, vmap, a, grid, stream);
+    case 128: return launch<128>(kmap, vmap, a, grid, stream);
+    default: return launch<256>(kmap, vmap, a, grid, stream);
   }
 }
 
