@@ -152,9 +152,9 @@ def _ptr(t: Optional[torch.Tensor], dtype=None, name="tensor"):
     return t.data_ptr()
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
     if stream is None:  # the handle alone: building a Stream object costs more than most of a call's checks
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -418,17 +418,18 @@ def _refuse(t, dtype, name: str, dev: int):
 
 def _arg(t, dtype, name: str, dev: int):
     """Pointer of a contiguous tensor on the current device."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous():
         _refuse(t, dtype, name, dev)
     return t.data_ptr()
 
 
 def _vec(t, n: int, dtype, name: str, dev: int):
-    """_arg of a tensor of n elements."""
-    p = _arg(t, dtype, name, dev)
+    """Pointer of a contiguous tensor of n elements on the current device."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous():
+        _refuse(t, dtype, name, dev)
     if t.numel() != n:
         raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
-    return p
+    return t.data_ptr()
 
 
 def _table(t, name: str, dev: int):
@@ -465,7 +466,7 @@ def se_block_tables_extend(free_pages, pool_state, block_table, seq_lens, new_le
         table, width, _vec(seq_lens, batch, i32, "seq_lens", dev), _vec(new_lens, batch, i32, "new_lens", dev), batch,
         _vec(seq_lens_after, batch, i32, "seq_lens_after", dev),
         _vec(token_start, batch + 1, i32, "token_start", dev), _arg(slot_map, i32, "slot_map", dev),
-        None if positions is None else _vec(positions, slots, i32, "positions", dev), slots, _stream(stream)))
+        None if positions is None else _vec(positions, slots, i32, "positions", dev), slots, _stream(stream, dev)))
 
 
 def se_block_tables_release(free_pages, pool_state, block_table, seq_lens, keep_lens=None, stream=None):
@@ -475,7 +476,7 @@ def se_block_tables_release(free_pages, pool_state, block_table, seq_lens, keep_
     _check(lib.se_block_tables_release(
         _arg(free_pages, i32, "free_pages", dev), _vec(pool_state, 4, i32, "pool_state", dev), free_pages.numel(),
         table, width, _vec(seq_lens, batch, i32, "seq_lens", dev),
-        None if keep_lens is None else _vec(keep_lens, batch, i32, "keep_lens", dev), batch, _stream(stream)))
+        None if keep_lens is None else _vec(keep_lens, batch, i32, "keep_lens", dev), batch, _stream(stream, dev)))
 
 
 def se_paged_kv_store(kv: SEPagedKV, k_new, v_new, slot_map, stream=None):
@@ -490,7 +491,7 @@ def se_paged_kv_store(kv: SEPagedKV, k_new, v_new, slot_map, stream=None):
     if k_new.shape[0] != tokens or (v_new is not None and v_new.shape[0] != tokens):
         raise ValueError("k_new, v_new and slot_map differ in tokens")
     _check(lib.se_paged_kv_store(ctypes.byref(kv), kp, ks, vp, vs, _arg(slot_map, torch.int32, "slot_map", dev), tokens,
-                                 _stream(stream)))
+                                 _stream(stream, dev)))
 
 
 def se_paged_decode_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -517,7 +518,7 @@ def se_paged_decode(kv: SEPagedKV, q, block_table, seq_lens, sm_scale: float, ou
         sink_tokens, recent_tokens, sm_scale, _vec(out, batch * hq * kv.head_dim_v, torch.bfloat16, "out", dev),
         None if out_lse is None else _vec(out_lse, batch * hq, torch.float32, "out_lse", dev),
         None if workspace is None else _arg(workspace, torch.uint8, "workspace", dev),
-        0 if workspace is None else workspace.numel(), _stream(stream)))
+        0 if workspace is None else workspace.numel(), _stream(stream, dev)))
 
 
 # ---------------------------------------------------------------- SnapKV
