@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hq = a.Hq;
 
-  kept_prefix<kThreads>(a.seq_lens, a.batch, a.bt_stride, a.sink, a.recent, kItemPages, 0x7fffffff, prefix, lens,
+  kept_prefix<kThreads>(a.seq_lens, a.batch, a.bt_stride, a.sink, a.recent, kItemPages, kMaxPlaces, prefix, lens,
                         reinterpret_cast<long long*>(misc + kSumsOff), a.err);
   for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
     if (prefix[b + 1] != prefix[b]) continue;  // no kept token: the empty sum
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
       tc05_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_free[s]);
-      const bool ok_f = mbar_wait(&full[s], (j >> 1) & 1);  // the masks of the tile
+      const bool ok_f = __all_sync(0xffffffffu, mbar_wait(&full[s], (j >> 1) & 1));  // the masks of the tile
       dead = dead || !ok_s || !ok_f;
       const bool tok_ok = in_mask(masks[s * kTilePages + q4], tok);
       // Logits against the running maxima (0 for a head that has none yet).

@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* stage = reinterpret_cast<float*>(ring + kSlots * kSlotBytes);  // [warps][8][D]
-  float* ml = stage + C::kStageFloats;                                  // [warps][(m, l)][16]
+  float* ml = stage + C::kStageFloats;                                  // [warps][(m, l)][8]
   uint32_t* meta = reinterpret_cast<uint32_t*>(ml + C::kWarps * 32);    // [kMetaRing][kMaxPages]
   uint64_t* full = reinterpret_cast<uint64_t*>(meta + kMetaRing * kMaxPages);
   uint64_t* empty = full + kSlots;
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
   const int heads = a.heads, G = a.group, rows = heads * G, HG = a.head_groups, Pg = a.step_pages;
   const int combos = heads * a.mtiles, active = combos * a.replicas;
 
-  kept_prefix<C::kThreads>(a.seq_lens, a.batch, a.bt_stride, a.sink, a.recent, Pg, 0x7fffffff / HG, prefix, lens,
+  kept_prefix<C::kThreads>(a.seq_lens, a.batch, a.bt_stride, a.sink, a.recent, Pg, kMaxPlaces / HG, prefix, lens,
                            reinterpret_cast<long long*>(stage), a.err);
   // Requests without a kept token: the empty sum.
   for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
     for (int i0 = seg.lo; i0 < seg.hi; i0 += Pg, ++step, j += 2) {
       if (!works) continue;
       const int sk = j % kSlots, sv = (j + 1) % kSlots;
-      if (!dead && !mbar_wait(&full[sk], (j / kSlots) & 1)) dead = true;
+      if (!dead && !__all_sync(0xffffffffu, mbar_wait(&full[sk], (j / kSlots) & 1))) dead = true;
       bool v_here = false, zeroed = false;
       for (int pg = replica; pg < Pg; pg += a.replicas) {
         const uint32_t mask = dead || i0 + pg >= seg.hi ? 0u : meta[(step % kMetaRing) * kMaxPages + pg];
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
           if (lane == 0) mbar_arrive(&empty[sk]);
         }
         if (!v_here) {
-          if (!dead && !mbar_wait(&full[sv], ((j + 1) / kSlots) & 1)) dead = true;
+          if (!dead && !__all_sync(0xffffffffu, mbar_wait(&full[sv], ((j + 1) / kSlots) & 1))) dead = true;
           v_here = true;
         }
         if (mask && !dead) {

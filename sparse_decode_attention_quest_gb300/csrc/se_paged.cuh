@@ -63,6 +63,9 @@ __device__ __forceinline__ bool mask_is_full(uint32_t m) {
   return (m & 0xff) == kPageSize && ((m >> 8 & 0xff) == kPageSize || (m >> 16) == 0);
 }
 
+// The longest line of items: places and the cuts beside them stay within 32 bits.
+constexpr int kMaxPlaces = 0x7fffffff - 64;
+
 // The share-out of a batch among the CTAs. An item is a request (or one of its `groups` groups of KV heads); it
 // weighs its kept pages plus `over`, the pages' worth of time that starting and finishing an item costs a CTA, so
 // that many short requests spread over the CTAs. The items' weights follow one another on a line of length

@@ -93,6 +93,17 @@ def test_batches(cuda_device, batch):
     c.release()
 
 
+def test_largest_batch(cuda_device):
+    c = Case(cuda_device, 20000, 2, 16384, seed=6)
+    g = np.random.default_rng(6)
+    new = g.integers(0, 18, 16384).tolist()
+    c.extend(new, sum(new))
+    c.release([n // 2 for n in c.lens])
+    with pytest.raises(se.SparseEngineError, match="16384"):
+        z = lambda n: torch.zeros(n, dtype=torch.int32, device=cuda_device)
+        se.se_block_tables_extend(c.free, c.state, z((16385, 2)), z(16385), z(16385), z(16385), z(16386), z(8))
+
+
 @pytest.mark.parametrize("total", [2047, 2048, 2049, 70001])
 def test_long_maps(cuda_device, total):
     """Maps that several CTAs fill, with a padded end."""

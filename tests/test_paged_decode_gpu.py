@@ -308,6 +308,66 @@ def test_agrees_with_the_sparse_decode_over_every_page(cuda_device):
     assert (np.abs((mine.double() - out.double()).cpu().numpy()) <= 2.0 ** -6 * (mag + np.abs(ref))).all()
 
 
+@pytest.mark.parametrize("batch,shape", [(4096, (2, 1, 64)), (512, (16, 1, 576))])
+def test_largest_batches(cuda_device, batch, shape):
+    Hq, H, D = shape
+    g = np.random.default_rng(1)
+    Inputs(cuda_device, g.integers(0, 24, batch).tolist(), Hq, H, D, latent=D == 576, seed=16).check()
+    with pytest.raises(se.SparseEngineError, match="batch >"):
+        z = lambda *n: torch.zeros(*n, dtype=torch.int32, device=cuda_device)
+        bf = lambda *n: torch.zeros(*n, dtype=torch.bfloat16, device=cuda_device)
+        k = bf(1, H, 16, D)
+        dv = 512 if D == 576 else D
+        se.se_paged_decode(se.paged_kv(k, None if D == 576 else k.clone(), None, dv), bf(batch + 1, Hq, D),
+                           z(batch + 1, 1), z(batch + 1), 0.1, bf(batch + 1, Hq, dv), None,
+                           torch.zeros(64 << 20, dtype=torch.uint8, device=cuda_device))
+
+
+@pytest.mark.parametrize("H,D,pages", [(8, 128, 140000), (1, 576, 240000)])
+def test_a_cache_of_more_than_two_to_the_31_elements(cuda_device, H, D, pages):
+    """Rows written to and read from the pages at both ends of a 4.5 GB cache."""
+    dev = cuda_device
+    latent = D == 576
+    Hq, dv = (16, 512) if latent else (8, 128)
+    assert pages * H * 16 * D > 2 ** 31
+    g = torch.Generator().manual_seed(17)
+    k = torch.empty(pages, H, 16, D, dtype=torch.bfloat16, device=dev)
+    v = None if latent else torch.empty_like(k)
+    n = [300, 77]
+    ids = [[pages - 1 - i for i in range(19)], [0, pages - 20, 1, pages // 2, pages - 21]]
+    table = torch.zeros(2, 19, dtype=torch.int32)
+    for b in range(2):
+        table[b, :len(ids[b])] = torch.tensor(ids[b], dtype=torch.int32)
+    slots = torch.tensor([ids[b][j // 16] * 16 + j % 16 for b in range(2) for j in range(n[b])], dtype=torch.int32)
+    kn = torch.randn(sum(n), H, D, generator=g).to(torch.bfloat16)
+    vn = None if latent else torch.randn(sum(n), H, D, generator=g).to(torch.bfloat16)
+    kv = se.paged_kv(k, v, None, dv)
+    se.se_paged_kv_store(kv, kn.to(dev), None if latent else vn.to(dev), slots.to(dev))
+    q = torch.randn(2, Hq, D, generator=g).to(torch.bfloat16)
+    out = torch.empty(2, Hq, dv, dtype=torch.bfloat16, device=dev)
+    lse = torch.empty(2, Hq, device=dev)
+    ws = torch.zeros(se.se_paged_decode_workspace_size(2, Hq, H, D, dv), dtype=torch.uint8, device=dev)
+    scale = 1.0 / math.sqrt(D)
+    se.se_paged_decode(kv, q.to(dev), table.to(dev), torch.tensor(n, dtype=torch.int32, device=dev), scale, out, lse, ws)
+    # The same rows in a small cache, for the oracle.
+    m = -(-sum(n) // 16) + 2
+    small_k, small_v = np.zeros((m, H, 16, D)), None if latent else np.zeros((m, H, 16, D))
+    st = np.zeros((2, 19), dtype=np.int64)
+    at = 0
+    for b in range(2):
+        st[b, :len(ids[b])] = np.arange(len(ids[b])) + at
+        for j in range(n[b]):
+            row = sum(n[:b]) + j
+            small_k[st[b, j // 16], :, j % 16] = kn[row].float().numpy()
+            if not latent:
+                small_v[st[b, j // 16], :, j % 16] = vn[row].float().numpy()
+        at += len(ids[b])
+    ref, rlse, mag, _ = op.decode(small_k, small_v, st, n, q.float().numpy(), scale, dv)
+    tol = (2.0 ** -8 + 1e-4) * mag + 2.0 ** -8 * np.abs(ref) * (1 + 2.0 ** -7)
+    assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
+    assert np.abs(lse.cpu().numpy() - rlse).max() < 1e-4
+
+
 def test_binding_checks(cuda_device):
     x = Inputs(cuda_device, [5, 6], 8, 2, 128, seed=15)
     out = torch.empty(2, 8, 128, dtype=torch.bfloat16, device=cuda_device)
