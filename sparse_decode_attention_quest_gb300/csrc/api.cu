@@ -911,7 +911,8 @@ se_status_t se_paged_decode(const se_paged_kv_t* kv, const void* q, int64_t q_st
                                 d->sm_count, d->err, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SE_OK : cuda_fail(fn, e);
   }
-  const int box = se::kPageSize * se::paged_decode_box_heads(kv->num_kv_heads, num_q_heads, kv->head_dim);
+  const int box = se::kPageSize * se::paged_decode_box_heads(kv->num_kv_heads, num_q_heads, kv->head_dim, bt_stride,
+                                                             sink_tokens, recent_tokens, d->sm_count);
   CUtensorMap kmap, vmap;
   if (!encode_row_chunks_map(&kmap, kv->k, rows, kv->row_stride_k, kv->head_dim / 64, box) ||
       !encode_row_chunks_map(&vmap, kv->v, rows, kv->row_stride_v, kv->head_dim / 64, box))

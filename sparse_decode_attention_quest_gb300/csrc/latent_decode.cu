@@ -71,13 +71,14 @@ constexpr int kLoadWarp = 10;                           // copies
 constexpr int kSWarp2 = 11;                             // issues S^T of chunks 5-8
 constexpr int kThreads = 384;
 constexpr int kTmemCols = 512;
-constexpr int kSCol = 0;                                // S^T of tile parity s: columns 128 s and 128 s + 64, to be added
+constexpr int kSCol = 0;                                // S^T of tile parity s: columns 128 s + those 64 further
 constexpr int kOCol = 256;                              // O^T M-tile mt: columns 256 + 64 mt
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kSoftBar = 1;
 constexpr int kItemPages = 8;                           // what starting and finishing a request costs, in pages
 constexpr int kMaxBatch = 512;
 constexpr int kJoinWarps = 8;
+constexpr int kTaskDims = 128;                          // dims of a join task
 
 // Shared memory behind the queries.
 constexpr int kBarOff = 0;        // mbarriers
@@ -267,7 +268,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
     // Lane l of a tile's first eight: half l % 2 of its page l / 2.
     const int pg = (lane >> 1) & 3, hf = lane & 1;
     auto page_of = [&](int i) {
-      const int pc = __shfl_sync(0xffffffffu, cur, (i - base) & 31), pn = __shfl_sync(0xffffffffu, nxt, (i - base) & 31);
+      const int pc = __shfl_sync(0xffffffffu, cur, (i - base) & 31);
+      const int pn = __shfl_sync(0xffffffffu, nxt, (i - base) & 31);
       return i < base + 32 ? pc : pn;
     };
     for (; c.valid; c.next()) {
@@ -305,7 +307,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         }
         if (lane == 0) mbar_arrive_expect_tx(q_full, (uint32_t)Hq * kD * 2);
         __syncwarp();
-        if (lane < kChunks) tma_load_3d(smem + kQOff + lane * kQRows * 128, &qmap, lane * 64, 0, c.sg.b, q_full, policy);
+        if (lane < kChunks)
+          tma_load_3d(smem + kQOff + lane * kQRows * 128, &qmap, lane * 64, 0, c.sg.b, q_full, policy);
       }
       // L2 prefetch: the tile kPrefetch ahead (lanes 0-7), and at a segment's start those before it.
       for (int d = c.t == 0 ? 1 : kPrefetch; d <= kPrefetch; ++d) {
@@ -601,14 +604,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const floa
                                                                      float* __restrict__ out_lse) {
   pdl_enter();
   static_assert(kMaxCtas <= kJoinWarps * 32, "a thread per item");
-  constexpr int kTaskDims = 128;
   __shared__ int4 todo[kMaxCtas];
   __shared__ int2 counts[kJoinWarps];
   __shared__ float4 acc_s[kJoinWarps][4][32], m_s[kJoinWarps], l_s[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tasks = (Hq / 4) * (kDv / kTaskDims);  // a multiple of the warps
   const int2 todos = list_joins(joins, ctas, tasks, todo, counts);
-  auto scale4 = [](const float4& a, const float4& f) { return make_float4(a.x * f.x, a.y * f.y, a.z * f.z, a.w * f.w); };
+  auto scale4 = [](const float4& a, const float4& f) {
+    return make_float4(a.x * f.x, a.y * f.y, a.z * f.z, a.w * f.w);
+  };
   auto fma4 = [](const float4& f, const float4& v, const float4& a) {
     return make_float4(a.x + f.x * v.x, a.y + f.y * v.y, a.z + f.z * v.z, a.w + f.w * v.w);
   };
@@ -729,8 +733,10 @@ cudaError_t launch_paged_latent(const CUtensorMap& kvmap, const CUtensorMap& qma
   if (e != cudaSuccess) return e;
   e = launch_pdl(latent_decode_kernel, dim3(grid), dim3(kThreads), smem, stream, kvmap, qmap, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(latent_join_kernel, dim3(8 * grid), dim3(kJoinWarps * 32), 0, stream, a.o_part, a.lse_part,
-                    a.joins, grid, num_q_heads, out, out_lse);
+  // An item has at most as many units as tasks, and no more items than CTAs reach beyond a slice.
+  const int units = std::min(grid, batch) * (num_q_heads / 4) * (kDv / kTaskDims);
+  return launch_pdl(latent_join_kernel, dim3(std::min(units, 8 * grid)), dim3(kJoinWarps * 32), 0, stream, a.o_part,
+                    a.lse_part, a.joins, grid, num_q_heads, out, out_lse);
 }
 
 }  // namespace se

@@ -16,11 +16,14 @@
 //    over every SM. An item that spans CTAs leaves a partial (output,
 //    log-sum-exp) per CTA; a CTA has at most two, for the item it starts inside
 //    and the item it ends inside, so the workspace does not grow with the lengths.
-//  * Join: where the table's width bounds an item's partials to kInlineBytes, the
-//    CTA that publishes an item's last partial merges them in the order of the
-//    pages. Otherwise a second kernel does, a warp per row: one CTA reads
-//    partials from L2 at some 60 bytes a clock, and merging 32 of 16 KB took it
-//    25 of 46 us (4 requests of 2.5K tokens, 32 query heads).
+//  * Join: where the table's (or the windows') width bounds an item's partials to
+//    kInlineBytes, if need be with fewer KV heads per item, the CTA that publishes
+//    an item's last partial merges them in the order of the pages. Otherwise a
+//    second kernel does, a warp per row: one CTA reads partials from L2 at some 60
+//    bytes a clock, and merging 32 of 16 KB took it 25 of 46 us (4 requests of 2.5K
+//    tokens, 32 query heads). 48 windows of 1,064 tokens: 27.5 us, against 29.0 with
+//    the second kernel and 29.5 with a bound of 100 KB; one request of 4K tokens:
+//    10.0 us, against 10.8 with the second kernel.
 //  * Copies: a page's rows of one KV head are 16 x D bf16, and the heads of a
 //    group of Hc lie next to each other, so that one TMA box of 64 dims x
 //    16 Hc rows x D / 64 brings a whole page of the group (16 to 32 KB for 4 to 8
@@ -51,6 +54,7 @@ constexpr int kMetaRing = 4;     // steps whose page masks are held (at most thr
 constexpr int kMaxPages = 16;    // pages of a step
 constexpr int kMaxBatch = 4096;  // requests whose prefix fits beside the ring
 constexpr int kInlineBytes = 48 * 1024;  // partials of an item, at most, where one CTA merges them
+constexpr int kInlineWidth = 32;          // pages of an item from which smaller boxes are taken for that
 constexpr int kJoinWarps = 8;
 
 // Where a state staged in shared memory keeps (head, dim): the dims of a row of D, turned by eight per pair of
@@ -276,7 +280,8 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
           nxt = entry(base + 32 + lane);
         }
         const int i = i0 + lane;
-        const int pc = __shfl_sync(0xffffffffu, cur, (i - base) & 31), pn = __shfl_sync(0xffffffffu, nxt, (i - base) & 31);
+        const int pc = __shfl_sync(0xffffffffu, cur, (i - base) & 31);
+        const int pn = __shfl_sync(0xffffffffu, nxt, (i - base) & 31);
         const int phys = i < base + 32 ? pc : pn;
         const bool mine = lane < Pg && i < seg.hi;
         const bool ok = mine && phys >= 0 && phys < a.num_pages;
@@ -288,7 +293,8 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
           if (lane == 0 && j >= kSlots && !mbar_wait(&empty[s], (j / kSlots - 1) & 1)) dead = true;
           dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
           if (dead) break;
-          if (kv == 0 && lane < Pg) meta[(step % kMetaRing) * kMaxPages + lane] = ok ? page_mask(k, a.sink, k.logical(i)) : 0u;
+          if (kv == 0 && lane < Pg)
+            meta[(step % kMetaRing) * kMaxPages + lane] = ok ? page_mask(k, a.sink, k.logical(i)) : 0u;
           __syncwarp();
           if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
           __syncwarp();
@@ -328,7 +334,8 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
     for (int nt = 0; nt < kNt; ++nt) {
       const int hd = tile_head + nt * 8 + g;
       const bool real = works && hd < G;
-      const uint16_t* qr = a.q + (size_t)seg.b * a.q_stride + (size_t)((seg.group * heads + hc) * G + (real ? hd : 0)) * kD;
+      const int row = (seg.group * heads + hc) * G + (real ? hd : 0);
+      const uint16_t* qr = a.q + (size_t)seg.b * a.q_stride + (size_t)row * kD;
 #pragma unroll
       for (int ks = 0; ks < kD / 16; ++ks) {
         qb[ks][nt][0] = real ? *reinterpret_cast<const uint32_t*>(qr + ks * 16 + 2 * t) : 0u;
@@ -396,7 +403,8 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
             for (int e = 0; e < 2; ++e) {
               top[nt][e] = fmaxf(z[nt][e], z[nt][2 + e]);
 #pragma unroll
-              for (int x = 4; x < 32; x <<= 1) top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xffffffffu, top[nt][e], x));
+              for (int x = 4; x < 32; x <<= 1)
+                top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xffffffffu, top[nt][e], x));
               moved = moved || top[nt][e] > m[nt][e];
             }
           if (__any_sync(0xffffffffu, moved)) {
@@ -590,8 +598,8 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
     const int first = s ? (int)blockIdx.x : share.first0, parts = s ? share.parts1 : share.parts0;
     const int warps = min(C::kWarps, share_of(parts));
     for (int r0 = 0; r0 < rows; r0 += C::kWarps / warps)
-      join_rows<kD, C::kWarps>(a.o_part, a.lse_part, first, parts, s ? item1 : item0, rows, r0, warps, *join_smem, a.out,
-                               a.out_lse, [] { named_bar_sync(1, C::kConsumers); });
+      join_rows<kD, C::kWarps>(a.o_part, a.lse_part, first, parts, s ? item1 : item0, rows, r0, warps, *join_smem,
+                               a.out, a.out_lse, [] { named_bar_sync(1, C::kConsumers); });
   }
 }
 
@@ -616,18 +624,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const float
   }
 }
 
-// How the heads of a call are laid over the consumer warps.
+// How the heads of a call are laid over the consumer warps, and where its joins run.
 struct HeadPlan {
   int heads, head_groups, mtiles, replicas, step_pages;
+  bool deferred;
 };
-HeadPlan head_plan(int num_kv_heads, int group, int head_dim) {
+
+// As many heads per box as leave at most an eighth of a slot empty (ten heads: boxes of two, not of five; 4 KB boxes
+// of one head read at 91% of the measured copy rate, slots five eighths full at 73%), and no more than `most_heads`.
+HeadPlan head_plan(int num_kv_heads, int group, int head_dim, int most_heads) {
   const int warps = head_dim == 256 ? Cfg<256>::kWarps : Cfg<128>::kWarps;
   const int blocks = kSlotBytes / (kPageSize * head_dim * 2);
   HeadPlan p;
   p.mtiles = group <= 8 ? 1 : (group + 15) / 16;
-  // As many heads per box as leave at most an eighth of a slot empty (ten heads: boxes of two, not of five; 4 KB
-  // boxes of one head read at 91% of the measured copy rate, slots five eighths full at 73%).
-  for (int c = 1; c * p.mtiles <= warps; ++c) {
+  for (int c = 1; c <= most_heads && c * p.mtiles <= warps; ++c) {
     if (num_kv_heads % c) continue;
     const int r = warps / (c * p.mtiles), pages = blocks / c / r * r;
     if (c > 1 && pages * c * 8 < blocks * 7) continue;
@@ -636,8 +646,32 @@ HeadPlan head_plan(int num_kv_heads, int group, int head_dim) {
     p.step_pages = pages;
   }
   p.head_groups = num_kv_heads / p.heads;
+  p.deferred = true;
   return p;
 }
+
+// The largest boxes, unless the table's (or the windows') width bounds an item's partials so far that smaller ones
+// let the decode kernel join them: fewer heads per item are fewer rows to join and more CTAs that join. Not
+// for short items, which are seldom split: more of them cost more than the join (64 requests of up to 19 pages, 8 KV
+// heads of 64 dims: 16.8 us, 21.9 in boxes of four; up to 157 pages, 4 heads of 128 dims: 31.6, and 30.0 in boxes of
+// one).
+HeadPlan call_plan(int num_kv_heads, int group, int head_dim, int32_t bt_stride, int32_t sink_tokens,
+                   int32_t recent_tokens, int ctas) {
+  long long width = bt_stride;
+  if (recent_tokens > 0)
+    width = std::min(width, ((long long)sink_tokens + kPageSize - 1) / kPageSize + recent_tokens / kPageSize + 2);
+  for (int c = 8; c > 0;) {
+    HeadPlan p = head_plan(num_kv_heads, group, head_dim, c);
+    if (c < 8 && width < kInlineWidth) break;
+    const long long parts = std::min<long long>(ctas, (width + p.step_pages) / (2 * p.step_pages + 1) + 2);
+    p.deferred = parts * p.heads * group * head_dim * (long long)sizeof(float) > kInlineBytes;
+    if (!p.deferred) return p;
+    c = p.heads - 1;
+  }
+  return head_plan(num_kv_heads, group, head_dim, 8);
+}
+
+int ctas_of(int sm_count) { return sm_count < kMaxCtas ? sm_count : kMaxCtas; }
 
 template <int kD, int kNt, bool kSolo>
 cudaError_t launch_as(const CUtensorMap& kmap, const CUtensorMap& vmap, const PagedArgs& a, int grid,
@@ -650,7 +684,9 @@ cudaError_t launch_as(const CUtensorMap& kmap, const CUtensorMap& vmap, const Pa
   e = launch_pdl(paged_decode_kernel<kD, kNt, kSolo>, dim3(grid), dim3(Cfg<kD>::kThreads), smem, stream, kmap, vmap, a);
   if (e != cudaSuccess || !a.deferred) return e;
   const int rows = a.heads * a.group;
-  return launch_pdl(paged_join_kernel<kD>, dim3(std::min(grid * rows, 8 * grid)), dim3(kJoinWarps * 32), 0, stream,
+  // An item has at most `rows` units, and no more items than CTAs reach beyond a slice.
+  const int units = std::min(grid, a.batch * a.head_groups) * rows;
+  return launch_pdl(paged_join_kernel<kD>, dim3(std::min(units, 8 * grid)), dim3(kJoinWarps * 32), 0, stream,
                     a.o_part, a.lse_part, a.joins, grid, rows, a.out, a.out_lse);
 }
 
@@ -659,8 +695,10 @@ cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const Paged
                    cudaStream_t stream) {
   const bool solo = a.replicas == 1;
   if (a.group <= 8)
-    return solo ? launch_as<kD, 1, true>(kmap, vmap, a, grid, stream) : launch_as<kD, 1, false>(kmap, vmap, a, grid, stream);
-  return solo ? launch_as<kD, 2, true>(kmap, vmap, a, grid, stream) : launch_as<kD, 2, false>(kmap, vmap, a, grid, stream);
+    return solo ? launch_as<kD, 1, true>(kmap, vmap, a, grid, stream)
+                : launch_as<kD, 1, false>(kmap, vmap, a, grid, stream);
+  return solo ? launch_as<kD, 2, true>(kmap, vmap, a, grid, stream)
+              : launch_as<kD, 2, false>(kmap, vmap, a, grid, stream);
 }
 
 }  // namespace
@@ -672,12 +710,14 @@ bool paged_decode_supported(int num_kv_heads, int head_dim, int head_dim_v, int 
          num_q_heads / num_kv_heads <= 64;
 }
 
-int paged_decode_box_heads(int num_kv_heads, int num_q_heads, int head_dim) {
-  return head_plan(num_kv_heads, num_q_heads / num_kv_heads, head_dim).heads;
+int paged_decode_box_heads(int num_kv_heads, int num_q_heads, int head_dim, int32_t bt_stride, int32_t sink_tokens,
+                           int32_t recent_tokens, int sm_count) {
+  return call_plan(num_kv_heads, num_q_heads / num_kv_heads, head_dim, bt_stride, sink_tokens, recent_tokens,
+                   ctas_of(sm_count)).heads;
 }
 
 size_t paged_decode_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
-  const HeadPlan p = head_plan(num_kv_heads, num_q_heads / num_kv_heads, head_dim);
+  const HeadPlan p = head_plan(num_kv_heads, num_q_heads / num_kv_heads, head_dim, 8);  // the most rows of an item
   const size_t rows = (size_t)p.heads * (num_q_heads / num_kv_heads);
   return kCounterBytes + 2 * kMaxCtas * rows * (head_dim + 1) * sizeof(float);
 }
@@ -688,7 +728,8 @@ cudaError_t launch_paged_decode(const CUtensorMap& kmap, const CUtensorMap& vmap
                                 int32_t recent_tokens, float sm_scale, uint16_t* out, float* out_lse, void* workspace,
                                 int sm_count, unsigned* err, cudaStream_t stream) {
   const int group = num_q_heads / kv.num_kv_heads;
-  const HeadPlan p = head_plan(kv.num_kv_heads, group, kv.head_dim);
+  const int grid = ctas_of(sm_count);
+  const HeadPlan p = call_plan(kv.num_kv_heads, group, kv.head_dim, bt_stride, sink_tokens, recent_tokens, grid);
   PagedArgs a;
   a.q = q;
   a.q_stride = q_stride;
@@ -717,13 +758,7 @@ cudaError_t launch_paged_decode(const CUtensorMap& kmap, const CUtensorMap& vmap
   a.o_part = reinterpret_cast<float*>(ws + kCounterBytes);
   a.lse_part = a.o_part + 2 * kMaxCtas * rows * kv.head_dim;
   a.err = err;
-  const int grid = sm_count < kMaxCtas ? sm_count : kMaxCtas;
-  // The most partials an item can leave, from the width of the table (or of the windows) alone.
-  long long pages = bt_stride;
-  if (recent_tokens > 0)
-    pages = std::min(pages, ((long long)sink_tokens + kPageSize - 1) / kPageSize + recent_tokens / kPageSize + 2);
-  const long long most = std::min<long long>(grid, (pages + p.step_pages) / (2 * p.step_pages + 1) + 2);
-  a.deferred = most * (long long)(rows * kv.head_dim * sizeof(float)) > kInlineBytes;
+  a.deferred = p.deferred;
   switch (kv.head_dim) {
     case 64: return launch<64>(kmap, vmap, a, grid, stream);
     case 128: return launch<128>(kmap, vmap, a, grid, stream);

@@ -182,7 +182,9 @@ cudaError_t launch_kv_store(const KvView& kv, uint16_t* k_mut, uint16_t* v_mut, 
 // ---- paged_decode.cu: one new token over the whole cache, or over a sink and a recent window
 int paged_decode_max_batch();
 bool paged_decode_supported(int num_kv_heads, int head_dim, int head_dim_v, int num_q_heads);
-int paged_decode_box_heads(int num_kv_heads, int num_q_heads, int head_dim);
+// KV heads per TMA box of a call.
+int paged_decode_box_heads(int num_kv_heads, int num_q_heads, int head_dim, int32_t bt_stride, int32_t sink_tokens,
+                           int32_t recent_tokens, int sm_count);
 size_t paged_decode_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim);
 // kmap, vmap: the caches as (64 dims, row, 64-dim chunk), boxes of 64 x 16 paged_decode_box_heads x all
 // chunks, 128-byte swizzle.

@@ -217,7 +217,9 @@ __device__ __forceinline__ void kept_prefix(const int32_t* seq_lens, int batch, 
 }
 
 // Warps that share the partials of an item: each takes eight or fewer, until all eight warps of a CTA share.
-__device__ __forceinline__ int share_of(int partials) { return partials <= 8 ? 1 : partials <= 16 ? 2 : partials <= 32 ? 4 : 8; }
+__device__ __forceinline__ int share_of(int partials) {
+  return partials <= 8 ? 1 : partials <= 16 ? 2 : partials <= 32 ? 4 : 8;
+}
 
 // The items to join, as (first CTA, item, partials, first unit), from joins[c] = (item, partials) of every CTA c (0
 // partials: none), in the order of their CTAs: every CTA of a join kernel makes the same list. An item has

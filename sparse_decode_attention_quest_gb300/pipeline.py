@@ -21,7 +21,8 @@ from typing import Optional, Sequence
 import torch
 
 from . import (APPEND_OVERLAP_PREVIOUS, paged_kv, se_block_tables_extend, se_block_tables_release, se_copy_async,
-               se_paged_decode, se_paged_decode_workspace_size, se_paged_kv_store, se_quest_build_summaries, se_quest_fused_step,
+               se_paged_decode, se_paged_decode_workspace_size, se_paged_kv_store, se_quest_build_summaries,
+               se_quest_fused_step,
                se_quest_kept_pages_max, se_quest_score_pages, se_quest_score_pages_ws, se_quest_score_workspace_size,
                se_quest_topk_pages_windowed, se_quest_update_summaries,
                se_quest_update_summaries_ex, se_snapkv_score_and_compact_windowed,
