@@ -322,6 +322,8 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
   const uint32_t ring0 = smem_addr(ring);
   const uint32_t plane = (uint32_t)heads * kPageSize * 128;  // 64 dims of a page's rows
   const uint32_t page_bytes = plane * C::kChunks;
+  const uint32_t k_off = swz128(lane & 15, lane >> 4);
+  const uint32_t v_off = swz128((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
   int j = 0, step = 0;
   const Neighbours share = neighbours_of(slices, blockIdx.x, slice);  // while the first copies are on their way
   int item0 = 0, item1 = 0;  // the items of the partials in slots 0 and 1
@@ -364,27 +366,29 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
         const uint32_t blk = pg * page_bytes + (uint32_t)hc * kPageSize * 128;
         uint32_t pb[kNt][2];
         if (mask) {
-          const uint32_t kt = ring0 + sk * kSlotBytes + blk;
-          // S^T in two accumulators: shorter chains of dependent products.
-          float s2[kNt][2][4];
+          // The swizzle is an exclusive or of the 16-byte chunk with the row: two chunks further is one of bit 5 on.
+          const uint32_t ka = ring0 + sk * kSlotBytes + blk + k_off;
+          // S^T of one column tile in two accumulators: shorter chains of dependent products.
+          constexpr int kAcc = kNt == 1 ? 2 : 1;
+          float s2[kNt][kAcc][4];
 #pragma unroll
           for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s2[nt][0][e] = s2[nt][1][e] = 0.f;
+            for (int e = 0; e < 4; ++e) s2[nt][0][e] = s2[nt][kAcc - 1][e] = 0.f;
 #pragma unroll
           for (int ks = 0; ks < kD / 16; ++ks) {
             uint32_t r0, r1, r2, r3;
-            ldmatrix_x4(r0, r1, r2, r3, kt + (ks >> 2) * plane + swz128(lane & 15, ((ks & 3) << 1) + (lane >> 4)));
+            ldmatrix_x4(r0, r1, r2, r3, (ka ^ ((ks & 3) << 5)) + (ks >> 2) * plane);
 #pragma unroll
             for (int nt = 0; nt < kNt; ++nt)
-              mma_bf16_16816(s2[nt][ks & 1], r0, r1, r2, r3, qb[ks][nt][0], qb[ks][nt][1]);
+              mma_bf16_16816(s2[nt][ks % kAcc], r0, r1, r2, r3, qb[ks][nt][0], qb[ks][nt][1]);
           }
           // Tokens g (0, 1) and g + 8 (2, 3), heads 2 t and 2 t + 1.
           float z[kNt][4];
 #pragma unroll
           for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[nt][e] = (s2[nt][0][e] + s2[nt][1][e]) * a.scale_log2;
+            for (int e = 0; e < 4; ++e) z[nt][e] = (kAcc == 2 ? s2[nt][0][e] + s2[nt][1][e] : s2[nt][0][e]) * a.scale_log2;
           if (!mask_is_full(mask)) {
             const bool k0 = in_mask(mask, g), k1 = in_mask(mask, g + 8);
 #pragma unroll
@@ -457,12 +461,11 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
             zeroed = true;
             __syncwarp();
           }
+          const uint32_t va = vt + v_off;
 #pragma unroll
           for (int i = 0; i < kD / 16; ++i) {
-            const int chunk = 2 * i + ((lane >> 3) & 1);
             uint32_t r0, r1, r2, r3;
-            ldmatrix_x4_trans(r0, r1, r2, r3,
-                              vt + (chunk >> 3) * plane + swz128((lane & 7) + ((lane >> 4) << 3), chunk & 7));
+            ldmatrix_x4_trans(r0, r1, r2, r3, (va ^ ((i & 3) << 5)) + (i >> 2) * plane);
 #pragma unroll
             for (int nt = 0; nt < kNt; ++nt) mma_bf16_16816(o[i][nt], r0, r1, r2, r3, pb[nt][0], pb[nt][1]);
           }
