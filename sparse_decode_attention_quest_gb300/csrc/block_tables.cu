@@ -12,8 +12,10 @@
 //
 // The work is a prefix sum over the batch and one write per token: a few KB to a
 // few MB, so a call is bound by its launch and by the latency of a chain of
-// dependent loads (lengths, then a free page, then the stores). Hence one
-// launch: every CTA sums the prefixes of the whole batch by itself (the lengths
+// dependent loads (lengths, then a free page, then the stores): with cold caches
+// 7.6 us for one token in each of 32 requests, 6.8 us for four prompts of 32K
+// tokens (64 CTAs), 9.2 us for 312,000 tokens of 250 requests, 5.0 to 5.9 us for the
+// releases of the three. Hence one launch: every CTA sums the prefixes of the whole batch by itself (the lengths
 // are a few KB in L2) and fills its share of the slot map. A new page is taken
 // from the stack by each of its tokens (the index is arithmetic on the
 // prefixes); the token at slot 0 also writes the table entry, so no CTA waits for
@@ -28,26 +30,37 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 
-// Inclusive prefix over the CTA of one value per thread, and the CTA's total (64 bits: lengths
-// are 31-bit, and a batch of them needs more).
-__device__ __forceinline__ long long cta_inclusive(long long x, long long* sums, long long* total) {
+// Inclusive prefixes over the CTA of two values per thread, and the CTA's totals (64 bits: lengths are 31-bit, and
+// a batch of them needs more).
+struct Pair {
+  long long tokens, pages;
+};
+__device__ __forceinline__ Pair cta_inclusive(Pair x, Pair* sums, Pair* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const long long t = __shfl_up_sync(0xffffffffu, x.tokens, o), p = __shfl_up_sync(0xffffffffu, x.pages, o);
+    if (lane >= o) {
+      x.tokens += t;
+      x.pages += p;
+    }
   }
   __syncthreads();  // the previous use of sums is over
   if (lane == 31) sums[warp] = x;
   __syncthreads();
-  long long before = 0, all = 0;
+  Pair before = {0, 0}, all = {0, 0};
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += sums[w];
-    all += sums[w];
+    const Pair s = sums[w];
+    if (w < warp) {
+      before.tokens += s.tokens;
+      before.pages += s.pages;
+    }
+    all.tokens += s.tokens;
+    all.pages += s.pages;
   }
   *total = all;
-  return x + before;
+  return {x.tokens + before.tokens, x.pages + before.pages};
 }
 
 // The number of free pages, from the pool's state (a count outside [0, num_pages] is reported and clipped).
@@ -64,6 +77,7 @@ __device__ __forceinline__ int free_count(const int32_t* pool_state, int num_pag
 __device__ __forceinline__ bool arrive_last(int32_t* pool_state) {
   __shared__ int s_last;
   __syncthreads();
+  if (gridDim.x == 1) return true;
   if (threadIdx.x == 0) {
     const uint32_t before = atomic_add_acq_rel_gpu(reinterpret_cast<uint32_t*>(pool_state) + 1, 1u);
     s_last = before == gridDim.x - 1;
@@ -91,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const int32_t* __restr
                                                           int32_t* positions, int32_t max_new_tokens, unsigned* err) {
   pdl_enter();
   extern __shared__ int smem[];
-  __shared__ long long sums[kWarps];
+  __shared__ Pair sums[kWarps];
   __shared__ int s_taken;
   int* start = smem;              // [batch + 1] first new token of each request
   int* off = start + batch + 1;   // [batch] first page of its share of the stack, -1: not served
@@ -109,14 +123,15 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const int32_t* __restr
       ok = bf >= 0 && nw >= 0 && (long long)bf + nw <= (long long)bt_stride * kPageSize;
       before[b] = bf;
     }
-    const long long tokens = nw > 0 ? nw : 0;
-    long long tok_total, page_total;
-    const long long tok_incl = tok0 + cta_inclusive(tokens, sums, &tok_total);
-    const bool fits = tok_incl <= max_new_tokens;
-    if (b < batch && !(ok && fits) && blockIdx.x == 0) raise_error(err, SE_DEVERR_LENGTH);
-    ok = ok && fits;
+    // Requests from the first that ends behind the map on are not served, so that what they would take changes
+    // nothing for those before.
     const int need = ok ? (bf + nw + kPageSize - 1) / kPageSize - (bf + kPageSize - 1) / kPageSize : 0;
-    const long long incl = page0 + cta_inclusive(need, sums, &page_total);
+    const long long tokens = nw > 0 ? nw : 0;
+    Pair total;
+    const Pair in = cta_inclusive({tokens, need}, sums, &total);
+    const long long tok_incl = tok0 + in.tokens, incl = page0 + in.pages;
+    if (b < batch && !(ok && tok_incl <= max_new_tokens) && blockIdx.x == 0) raise_error(err, SE_DEVERR_LENGTH);
+    ok = ok && tok_incl <= max_new_tokens;
     if (b < batch) {
       // In batch order: once a request finds too few pages left, no later one gets any.
       const bool served = ok && (need == 0 || incl <= f);
@@ -126,8 +141,8 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const int32_t* __restr
       off[b] = served ? (int)(need == 0 ? 0 : incl - need) : -1;
       if (served && need > 0) atomicMax(&s_taken, (int)incl);
     }
-    tok0 += tok_total;
-    page0 += page_total;
+    tok0 += total.tokens;
+    page0 += total.pages;
   }
   if (threadIdx.x == 0) start[batch] = (int)(tok0 < max_new_tokens ? tok0 : max_new_tokens);
   __syncthreads();
@@ -190,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) release_kernel(int32_t* free_pages, 
                                                            unsigned* err) {
   pdl_enter();
   extern __shared__ int smem[];
-  __shared__ long long sums[kWarps];
+  __shared__ Pair sums[kWarps];
   int* start = smem;               // [batch + 1] first page of each request in the returned sequence
   int* first = start + batch + 1;  // [batch] its first returned logical page
   const int f = free_count(pool_state, num_pages, err);
@@ -207,14 +222,14 @@ __global__ void __launch_bounds__(kThreads) release_kernel(int32_t* free_pages, 
         raise_error(err, SE_DEVERR_LENGTH);
       }
     }
-    long long page_total;
-    const long long incl = page0 + cta_inclusive(n, sums, &page_total);
+    Pair total;
+    const long long incl = page0 + cta_inclusive({0, n}, sums, &total).pages;
     if (b < batch) {
       const long long s = incl - n;
       start[b] = (int)(s < num_pages ? s : num_pages);
       first[b] = fp;
     }
-    page0 += page_total;
+    page0 += total.pages;
   }
   // More pages than the pool lacks cannot come back: nothing is returned.
   const bool sane = page0 <= num_pages - f;
@@ -234,8 +249,8 @@ __global__ void __launch_bounds__(kThreads) release_kernel(int32_t* free_pages, 
   if (arrive_last(pool_state) && threadIdx.x == 0) pool_state[0] = f + total;
 }
 
-int grid_for(long long elements, int sm_count) {
-  const long long g = (elements + kThreads * 4 - 1) / (kThreads * 4);
+int grid_for(long long elements, int per_thread, int sm_count) {
+  const long long g = (elements + kThreads * per_thread - 1) / (kThreads * per_thread);
   return (int)(g < 1 ? 1 : g > sm_count ? sm_count : g);
 }
 
@@ -252,7 +267,7 @@ cudaError_t launch_block_tables_extend(const int32_t* free_pages, int32_t* pool_
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(extend_kernel, (3 * block_tables_max_batch() + 1) * (int)sizeof(int), allowed);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(extend_kernel, dim3(grid_for(max_new_tokens, sm_count)), dim3(kThreads), smem, stream, free_pages,
+  e = launch_pdl(extend_kernel, dim3(grid_for(max_new_tokens, 4, sm_count)), dim3(kThreads), smem, stream, free_pages,
                  pool_state, num_pages, block_table, bt_stride, seq_lens, new_lens, batch, seq_lens_after,
                  token_start, slot_map, positions, max_new_tokens, err);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -267,7 +282,7 @@ cudaError_t launch_block_tables_release(int32_t* free_pages, int32_t* pool_state
   cudaError_t e = allow_smem(release_kernel, (2 * block_tables_max_batch() + 1) * (int)sizeof(int), allowed);
   if (e != cudaSuccess) return e;
   const long long most = (long long)batch * bt_stride < num_pages ? (long long)batch * bt_stride : num_pages;
-  e = launch_pdl(release_kernel, dim3(grid_for(most, sm_count)), dim3(kThreads), smem, stream, free_pages, pool_state,
+  e = launch_pdl(release_kernel, dim3(grid_for(most, 1, sm_count)), dim3(kThreads), smem, stream, free_pages, pool_state,
                  num_pages, block_table, bt_stride, seq_lens, keep_lens, batch, err);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
