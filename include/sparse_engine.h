@@ -9,7 +9,10 @@
  *     Figure 3 caption, Tables 8-12, Table 14);
  *   - SnapKV: eviction at the end of prefill from observation-window attention
  *     scores with max-pooling, keeping the selected tokens plus the window in
- *     compacted pages (Figure 2 caption, Table 8, Table 10, Table 15 note).
+ *     compacted pages (Figure 2 caption, Table 8, Table 10, Table 15 note);
+ *   - the dense paged path around them: pages, block tables and slot maps from
+ *     request lengths, the rows of new tokens into their pages, and attention of one
+ *     new token over a whole cache or a sink and a recent window (Table 7, Tables 9-12).
  * The pages do not print either method's equations; each entry point below
  * states the computation it performs.
  *
