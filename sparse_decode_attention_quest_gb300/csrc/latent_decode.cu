@@ -549,12 +549,18 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
             tmem_ld_wait();
             const int d = mt * 128 + 32 * q4 + lane;
             if (!split) {
+              // Two lanes exchange halves: the even one stores both dims of head cc, the odd one those of the next.
 #pragma unroll
-              for (int cc = 0; cc < 32; ++cc) {
-                const int h = 32 * (warp >> 2) + cc;
-                if (h < Hq)
-                  a.out[((size_t)b * Hq + h) * kDv + d] =
-                      (uint16_t)(pack_bf16x2(__uint_as_float(o[cc]) * linv[h], 0.f) & 0xffffu);
+              for (int cc = 0; cc < 32; cc += 2) {
+                const int h = 32 * (warp >> 2) + cc + (lane & 1);
+                const float mine = __uint_as_float(lane & 1 ? o[cc + 1] : o[cc]);
+                const float give = __uint_as_float(lane & 1 ? o[cc] : o[cc + 1]);
+                const float got = __shfl_xor_sync(0xffffffffu, give, 1);
+                if (h < Hq) {
+                  const float f = linv[h];
+                  *reinterpret_cast<uint32_t*>(a.out + ((size_t)b * Hq + h) * kDv + (d & ~1)) =
+                      lane & 1 ? pack_bf16x2(got * f, mine * f) : pack_bf16x2(mine * f, got * f);
+                }
               }
             } else {
               // Four heads of a dim in one 16-byte store.
