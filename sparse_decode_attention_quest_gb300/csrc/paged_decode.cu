@@ -33,7 +33,7 @@
 //    warps share the pages of a step when the heads do not fill the warps. S^T =
 //    K Q^T and O^T += V^T P^T are m16n8k16 bf16 MMAs with fp32 accumulators: the
 //    page's 16 tokens, or 16 dims, are the rows, and up to 8 query heads the
-//    columns (two column tiles for 9 to 16), so that a group of up to eight heads
+//    columns (two column tiles where a warp takes 16), so that a group of up to eight heads
 //    wastes no rows: the other way round, with heads as rows, half of the MMAs
 //    and of the exponentials were for rows that do not exist, and a block took
 //    a warp 450 instructions (8 x 16K tokens, 4 KV heads: 50.7 us). P^T goes from
@@ -224,8 +224,8 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
   uint32_t* meta = reinterpret_cast<uint32_t*>(ml + C::kWarps * 32);    // [kMetaRing][kMaxPages]
   uint64_t* full = reinterpret_cast<uint64_t*>(meta + kMetaRing * kMaxPages);
   uint64_t* empty = full + kSlots;
-  int* flags = reinterpret_cast<int*>(empty + kSlots);  // [4]
-  int* prefix = flags + 4;                              // [batch + 1]
+  int* flags = reinterpret_cast<int*>(empty + kSlots);  // [8]: joins to make, the items of slots 0 and 1, neighbours
+  int* prefix = flags + 8;                              // [batch + 1]
   int* lens = prefix + a.batch + 1;                     // [batch]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int heads = a.heads, G = a.group, rows = heads * G, HG = a.head_groups, Pg = a.step_pages;
@@ -325,8 +325,15 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
   const uint32_t k_off = swz128(lane & 15, lane >> 4);
   const uint32_t v_off = swz128((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
   int j = 0, step = 0;
-  const Neighbours share = neighbours_of(slices, blockIdx.x, slice);  // while the first copies are on their way
-  int item0 = 0, item1 = 0;  // the items of the partials in slots 0 and 1
+  if (warp == 0) {  // while the first copies are on their way; in shared memory, as the loop needs its registers
+    const Neighbours share = neighbours_of(slices, blockIdx.x, slice);
+    if (lane == 0) {
+      flags[2] = flags[3] = 0;
+      flags[4] = share.first0;
+      flags[5] = share.parts0;
+      flags[6] = share.parts1;
+    }
+  }
   bool handed = false;
 
   while (seg.next()) {
@@ -479,8 +486,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
     // ---- the end of a segment: this CTA's share of item (b, hg) is done
     const bool split = seg.split();
     const int slot = seg.lo > 0 ? 0 : 1, item = seg.b * HG + seg.group;
-    if (split && slot == 0) item0 = item;
-    if (split && slot == 1) item1 = item;
+    if (split && threadIdx.x == 0) flags[2 + slot] = item;
     const size_t out_row0 = (size_t)seg.b * a.num_q_heads + (size_t)seg.group * rows;
     const size_t part_row0 = (size_t)(2 * blockIdx.x + slot) * rows;
     // The R warps of a (head, tile) stage their states, eight query heads at a time, and share the sums and the
@@ -575,18 +581,20 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
     }
   }
   if (dead && lane == 0) raise_error(a.err, SE_DEVERR_WAIT_TIMEOUT);
-  if (a.deferred && threadIdx.x == 0) a.joins[blockIdx.x] = make_int2(item1, share.parts1);
+  if (a.deferred && threadIdx.x == 0) a.joins[blockIdx.x] = make_int2(flags[3], flags[6]);
 
   // ---- Publish: count this CTA in on the (at most two) items it shares with few others; whoever completes
   // an item's count merges its partials (written by other CTAs: read past L1) and resets the counter.
-  if (a.deferred || (share.parts0 == 0 && share.parts1 == 0)) return;  // the same for all consumers
+  if (a.deferred) return;
   __threadfence();
   named_bar_sync(1, C::kConsumers);
+  const int first0 = flags[4], parts0 = flags[5], parts1 = flags[6];
+  if (parts0 == 0 && parts1 == 0) return;  // the same for all consumers
   if (threadIdx.x < 2) {
-    const int parts = threadIdx.x ? share.parts1 : share.parts0;
+    const int parts = threadIdx.x ? parts1 : parts0;
     int last = 0;
     if (parts > 0) {
-      uint32_t* cnt = a.arrivals + (threadIdx.x ? (int)blockIdx.x : share.first0);
+      uint32_t* cnt = a.arrivals + (threadIdx.x ? (int)blockIdx.x : first0);
       last = atomic_add_acq_rel_gpu(cnt, 1u) == (uint32_t)parts - 1;
       if (last) *cnt = 0;
     }
@@ -598,11 +606,11 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
 #pragma unroll 1
   for (int s = 0; s < 2; ++s) {
     if (!flags[s]) continue;
-    const int first = s ? (int)blockIdx.x : share.first0, parts = s ? share.parts1 : share.parts0;
+    const int first = s ? (int)blockIdx.x : first0, parts = s ? parts1 : parts0, item = flags[2 + s];
     const int warps = min(C::kWarps, share_of(parts));
     for (int r0 = 0; r0 < rows; r0 += C::kWarps / warps)
-      join_rows<kD, C::kWarps>(a.o_part, a.lse_part, first, parts, s ? item1 : item0, rows, r0, warps, *join_smem,
-                               a.out, a.out_lse, [] { named_bar_sync(1, C::kConsumers); });
+      join_rows<kD, C::kWarps>(a.o_part, a.lse_part, first, parts, item, rows, r0, warps, *join_smem, a.out,
+                               a.out_lse, [] { named_bar_sync(1, C::kConsumers); });
   }
 }
 
@@ -633,13 +641,22 @@ struct HeadPlan {
   bool deferred;
 };
 
+// Query heads per KV head up to which a tile holds eight of them, above it sixteen. A warp of sixteen heads reads K
+// and V once for both, but its state spills (nine warps leave 168 registers): it is the better one where shared
+// memory or the tensor pipe would be read twice over at the full rate, that is in long caches of 64 dims (16 heads
+// per KV head at 800 MB: 151 us, tiles of eight 176) and for many heads (128 dims, 32 heads: 182 against 222). Up to
+// here eights are faster where latency counts (32 requests of 2.5K tokens, 4 KV heads of 128 dims with 16 heads
+// each: 33.6 us against 40.8; 2 of 256 dims: 34.9 against 44.8) and even at 800 MB (131 against 135, 134 against 138;
+// 32 heads of 256 dims: 223 against 217, and 32.5 against 41.8 for the 32 requests).
+int eights_up_to(int head_dim) { return head_dim == 64 ? 8 : head_dim == 128 ? 16 : 32; }
+
 // As many heads per box as leave at most an eighth of a slot empty (ten heads: boxes of two, not of five; 4 KB boxes
 // of one head read at 91% of the measured copy rate, slots five eighths full at 73%), and no more than `most_heads`.
 HeadPlan head_plan(int num_kv_heads, int group, int head_dim, int most_heads) {
   const int warps = head_dim == 256 ? Cfg<256>::kWarps : Cfg<128>::kWarps;
   const int blocks = kSlotBytes / (kPageSize * head_dim * 2);
   HeadPlan p;
-  p.mtiles = group <= 8 ? 1 : (group + 15) / 16;
+  p.mtiles = group <= eights_up_to(head_dim) ? (group + 7) / 8 : (group + 15) / 16;
   for (int c = 1; c <= most_heads && c * p.mtiles <= warps; ++c) {
     if (num_kv_heads % c) continue;
     const int r = warps / (c * p.mtiles), pages = blocks / c / r * r;
@@ -697,11 +714,12 @@ template <int kD>
 cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const PagedArgs& a, int grid,
                    cudaStream_t stream) {
   const bool solo = a.replicas == 1;
-  if (a.group <= 8)
+  if (a.group <= 8 * a.mtiles)
     return solo ? launch_as<kD, 1, true>(kmap, vmap, a, grid, stream)
                 : launch_as<kD, 1, false>(kmap, vmap, a, grid, stream);
-  return solo ? launch_as<kD, 2, true>(kmap, vmap, a, grid, stream)
-              : launch_as<kD, 2, false>(kmap, vmap, a, grid, stream);
+  if constexpr (kD < 256)  // at 256 dims three or four tiles of sixteen leave no second warp to any
+    if (!solo) return launch_as<kD, 2, false>(kmap, vmap, a, grid, stream);
+  return launch_as<kD, 2, true>(kmap, vmap, a, grid, stream);
 }
 
 }  // namespace

@@ -144,6 +144,15 @@ def test_windows(cuda_device, sink, recent, shape):
            recent=recent, seed=3).check()
 
 
+@pytest.mark.parametrize("batch,lo,hi", [(1, 20011, 20011), (5, 0, 3000), (150, 1, 70)])
+@pytest.mark.parametrize("shape", [(16, 1, 128), (36, 3, 128), (34, 2, 128), (32, 2, 64), (30, 1, 256), (40, 1, 256)])
+def test_many_heads_over_split_items(cuda_device, batch, lo, hi, shape):
+    """Tiles of eight and of sixteen query heads, alone in their warp and sharing pages, whole and joined."""
+    g = torch.Generator().manual_seed(batch + hi)
+    lens = torch.randint(lo, hi + 1, (batch,), generator=g).tolist()
+    Inputs(cuda_device, lens, *shape, seed=batch).check()
+
+
 @pytest.mark.parametrize("batch,lo,hi", [(1, 4096, 4096), (1, 20011, 20011), (3, 1, 9000), (70, 0, 400), (300, 0, 64),
                                          (51, 208, 208), (160, 330, 350), (200, 1, 17), (33, 1500, 1600), (2, 1, 30000)])
 @pytest.mark.parametrize("shape", [(8, 2, 128), (4, 1, 64), (16, 8, 64), (2, 1, 256), (64, 1, 576)])
