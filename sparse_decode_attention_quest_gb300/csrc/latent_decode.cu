@@ -17,7 +17,8 @@
 //  * Work: the requests follow one another on a line, each as long as its kept
 //    pages and an overhead, which the CTAs share equally in tiles of 64 tokens (4
 //    pages). An item that spans CTAs leaves a partial per CTA (at most two per
-//    CTA, whatever the lengths), and a second kernel joins them.
+//    CTA, whatever the lengths), and a second kernel joins them. Batches that would
+//    leave CTAs without work are cut into one or two tiles per CTA.
 //  * A tile is eight groups of 8 rows, each group nine 64-dim chunks of 8 rows x
 //    128 bytes, 128-byte swizzled: one 3-D TMA box per group. The queries (72 KB)
 //    leave room for two tiles, 144 KB, which must cover the copies' latency as
@@ -76,6 +77,7 @@ constexpr int kOCol = 256;                              // O^T M-tile mt: column
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kSoftBar = 1;
 constexpr int kItemPages = 8;                           // what starting and finishing a request costs, in pages
+constexpr int kPieces = 64;                             // of an item, where the batch leaves CTAs over
 constexpr int kMaxBatch = 512;
 constexpr int kJoinWarps = 8;
 constexpr int kTaskDims = 128;                          // dims of a join task
@@ -90,8 +92,8 @@ constexpr int kMrowOff = 3328;    // [64]
 constexpr int kLinvOff = 3584;    // [64]
 constexpr int kLseOff = 3840;     // [64]
 constexpr int kSumsOff = 4096;    // [12] 64-bit
-constexpr int kPrefixOff = 4224;  // [batch + 1]
-constexpr int kSmemMax = 1024 + kMiscOff + kPrefixOff + (2 * kMaxBatch + 1) * 4;
+constexpr int kPrefixOff = 4224;  // [batch + 1], and what kept_prefix puts behind it
+constexpr int kSmemMax = 1024 + kMiscOff + kPrefixOff + kept_ints(kMaxBatch) * 4;
 static_assert(kSmemMax <= 227 * 1024, "the largest batch fits");
 
 struct LatentArgs {
@@ -206,12 +208,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
   float* linv = reinterpret_cast<float*>(misc + kLinvOff);
   float* lse_s = reinterpret_cast<float*>(misc + kLseOff);
   int* prefix = reinterpret_cast<int*>(misc + kPrefixOff);
-  int* lens = prefix + a.batch + 1;  // [batch]
+  int* lens = prefix + a.batch + 1;  // [batch], then the pages of each
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hq = a.Hq;
 
-  kept_prefix<kThreads>(a.seq_lens, a.batch, a.bt_stride, a.sink, a.recent, kItemPages, kMaxPlaces, prefix, lens,
-                        reinterpret_cast<long long*>(misc + kSumsOff), a.err);
+  const int piece =
+      kept_prefix<kThreads>(a.seq_lens, a.batch, 1, a.bt_stride, a.sink, a.recent, kItemPages, kTilePages, kPieces,
+                            gridDim.x, kMaxPlaces, prefix, lens, reinterpret_cast<long long*>(misc + kSumsOff), a.err);
   for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
     if (prefix[b + 1] != prefix[b]) continue;  // no kept token: the empty sum
     uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)b * Hq * kDv);
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
       for (int i = threadIdx.x; i < Hq; i += kThreads) a.out_lse[(size_t)b * Hq + i] = -INFINITY;
   }
   Slices slices;
-  slices.init(prefix, a.batch, 1, kItemPages, kTilePages, gridDim.x);
+  slices.init(prefix, a.batch, 1, kItemPages, kTilePages, gridDim.x, piece);
   const int2 slice = slice_of(slices, blockIdx.x);
   if (slice.x >= slice.y) {
     if (threadIdx.x == 0) a.joins[blockIdx.x] = make_int2(0, 0);
@@ -733,7 +736,7 @@ cudaError_t launch_paged_latent(const CUtensorMap& kvmap, const CUtensorMap& qma
   a.lse_part = a.o_part + 2 * kMaxCtas * (size_t)num_q_heads * kDv;
   a.err = err;
   const int grid = std::min(sm_count, kMaxCtas);
-  const size_t smem = 1024 + kMiscOff + kPrefixOff + (size_t)(2 * batch + 1) * 4;
+  const size_t smem = 1024 + kMiscOff + kPrefixOff + kept_ints(batch) * 4;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(latent_decode_kernel, kSmemMax, allowed);
   if (e != cudaSuccess) return e;

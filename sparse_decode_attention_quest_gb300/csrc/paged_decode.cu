@@ -12,7 +12,8 @@
 //
 //  * Work: (request, KV head group) items follow one another on a line, each as
 //    long as its kept pages and a step's worth of overhead; the CTAs (one per SM)
-//    take equal slices: ragged lengths balance, and a single long request spreads
+//    take equal slices (or, where those leave CTAs over, pieces of one step each):
+//    ragged lengths balance, and a single long request spreads
 //    over every SM. An item that spans CTAs leaves a partial (output,
 //    log-sum-exp) per CTA; a CTA has at most two, for the item it starts inside
 //    and the item it ends inside, so the workspace does not grow with the lengths.
@@ -74,7 +75,7 @@ struct Cfg {
   static constexpr int kStageFloats = kWarps * 8 * kD;               // states handed over at a segment's end
   static constexpr int kFixed = 1024 + kSlots * kSlotBytes + kStageFloats * 4 + kWarps * 32 * 4 +
                                 kMetaRing * kMaxPages * 4 + 2 * kSlots * 8 + 64;
-  static constexpr int kMaxSmem = kFixed + (2 * kMaxBatch + 1) * 4;
+  static constexpr int kMaxSmem = kFixed + kept_ints(kMaxBatch) * 4;
 };
 
 struct PagedArgs {
@@ -226,13 +227,17 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
   uint64_t* empty = full + kSlots;
   int* flags = reinterpret_cast<int*>(empty + kSlots);  // [8]: joins to make, the items of slots 0 and 1, neighbours
   int* prefix = flags + 8;                              // [batch + 1]
-  int* lens = prefix + a.batch + 1;                     // [batch]
+  int* lens = prefix + a.batch + 1;                     // [batch], then the pages of each
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int heads = a.heads, G = a.group, rows = heads * G, HG = a.head_groups, Pg = a.step_pages;
   const int combos = heads * a.mtiles, active = combos * a.replicas;
 
-  kept_prefix<C::kThreads>(a.seq_lens, a.batch, a.bt_stride, a.sink, a.recent, Pg, kMaxPlaces / HG, prefix, lens,
-                           reinterpret_cast<long long*>(stage), a.err);
+  // Pieces of a step: of up to eight query heads a CTA takes a second one in less time than more partials take to
+  // join (1 x 1,000 tokens, 8 KV heads: 10.6 us with 32 partials an item, 10.0 with 16), of more it does not (1 x 4K,
+  // 32 heads over one: 14.6 us with 32, 17.8 with 16).
+  const int piece = kept_prefix<C::kThreads>(a.seq_lens, a.batch, HG, a.bt_stride, a.sink, a.recent, Pg, Pg,
+                                             G > 8 ? 32 : 8, gridDim.x, kMaxPlaces / HG, prefix, lens,
+                                             reinterpret_cast<long long*>(stage), a.err);
   // Requests without a kept token: the empty sum.
   for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
     if (prefix[b + 1] != prefix[b]) continue;
@@ -243,7 +248,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
       for (int i = threadIdx.x; i < a.num_q_heads; i += C::kThreads) a.out_lse[r0 + i] = -INFINITY;
   }
   Slices slices;
-  slices.init(prefix, a.batch, HG, Pg, Pg, gridDim.x);
+  slices.init(prefix, a.batch, HG, Pg, Pg, gridDim.x, piece);
   const int2 slice = slice_of(slices, blockIdx.x);
   if (slice.x >= slice.y) {
     if (a.deferred && threadIdx.x == 0) a.joins[blockIdx.x] = make_int2(0, 0);
@@ -696,7 +701,7 @@ int ctas_of(int sm_count) { return sm_count < kMaxCtas ? sm_count : kMaxCtas; }
 template <int kD, int kNt, bool kSolo>
 cudaError_t launch_as(const CUtensorMap& kmap, const CUtensorMap& vmap, const PagedArgs& a, int grid,
                    cudaStream_t stream) {
-  const size_t smem = Cfg<kD>::kFixed + (size_t)(2 * a.batch + 1) * 4;
+  const size_t smem = Cfg<kD>::kFixed + kept_ints(a.batch) * 4;
   static_assert(Cfg<kD>::kMaxSmem <= 227 * 1024, "the largest batch fits");
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(paged_decode_kernel<kD, kNt, kSolo>, Cfg<kD>::kMaxSmem, allowed);

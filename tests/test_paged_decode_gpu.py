@@ -153,6 +153,16 @@ def test_many_heads_over_split_items(cuda_device, batch, lo, hi, shape):
     Inputs(cuda_device, lens, *shape, seed=batch).check()
 
 
+@pytest.mark.parametrize("batch", [19, 76, 151, 152, 153, 160, 161])
+@pytest.mark.parametrize("shape", [(8, 2, 128), (9, 3, 64), (8, 8, 128), (12, 1, 256), (16, 1, 576)])
+def test_about_one_short_request_per_cta(cuda_device, batch, shape):
+    """Around the batch sizes at which every piece of a request still gets a CTA of its own."""
+    Hq, H, D = shape
+    lens = [(0, 1, 64, 65, 128, 129, 16, 200, 0, 33, 7)[(b * b + b // 5) % 11] for b in range(batch)]
+    Inputs(cuda_device, lens, Hq, H, D, latent=D == 576, seed=batch).check()
+    Inputs(cuda_device, [100] * batch, Hq, H, D, latent=D == 576, seed=batch, sink=4, recent=70).check()
+
+
 @pytest.mark.parametrize("batch,lo,hi", [(1, 4096, 4096), (1, 20011, 20011), (3, 1, 9000), (70, 0, 400), (300, 0, 64),
                                          (51, 208, 208), (160, 330, 350), (200, 1, 17), (33, 1500, 1600), (2, 1, 30000)])
 @pytest.mark.parametrize("shape", [(8, 2, 128), (4, 1, 64), (16, 8, 64), (2, 1, 256), (64, 1, 576)])
