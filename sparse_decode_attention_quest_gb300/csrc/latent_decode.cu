@@ -81,6 +81,8 @@ constexpr int kPieces = 64;                             // of an item, where the
 constexpr int kMaxBatch = 512;
 constexpr int kJoinWarps = 8;
 constexpr int kTaskDims = 128;                          // dims of a join task
+constexpr int kOutRow = kDv * 2 + 16;                   // bytes between a whole item's output rows in shared memory
+static_assert(kQRows * kOutRow <= kStageBytes, "the output rows fit into a stage");
 
 // Shared memory behind the queries.
 constexpr int kBarOff = 0;        // mbarriers
@@ -379,7 +381,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
           mma_elected(tmem + kOCol + mt * 64, dv + mt * kMt + ks * kStep, dp + ks * kStep, idesc, ks > 0 ? 1u : acc0);
-      commit_elected(&empty[s]);
+      // The epilogue of a whole item passes its rows through the stage and frees it.
+      if (!c.last() || c.sg.split()) commit_elected(&empty[s]);
       if (c.last()) commit_elected(o_last);
     }
     commit_elected(fin);
@@ -438,10 +441,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
       }
       // After the segment's first tile, a tile whose scores all stay within 2^8 of the running maxima changes
       // nothing but P and l. Otherwise the tile maxima are exchanged and the running maxima recomputed.
-      bool need = t == 0 || dead;
+      bool need = dead;
 #pragma unroll
       for (int i = 0; i < 16; ++i) need = need || x[i] > kRescaleLog2;
-      if (bar_red_or(kSoftBar, kSoftThreads, need)) {
+      if (t == 0 || bar_red_or(kSoftBar, kSoftThreads, need)) {
         float v[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = tok_ok && hh + i < Hq ? __uint_as_float(r[i]) * a.scale_log2 : -INFINITY;
@@ -522,8 +525,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
       if (c.last()) {
         // ---- epilogue of the segment: O = O^T / l per head, or a partial
         const int b = c.sg.b;
-        const bool ok_e = __all_sync(0xffffffffu, mbar_wait(o_last, c.seg & 1));
-        dead = dead || !ok_e;
         float w[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) w[i] = l_h[i];
@@ -540,10 +541,42 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
           lse_s[h] = l == 0.f ? -INFINITY : mrow[h] + log2f(l);
         }
         named_bar_sync(kSoftBar, kSoftThreads);
+        const bool ok_e = __all_sync(0xffffffffu, mbar_wait(o_last, c.seg & 1));
+        dead = dead || !ok_e;
         const bool split = c.sg.split();
         const int slot = 2 * blockIdx.x + (c.sg.lo > 0 ? 0 : 1);
         if (c.sg.lo == 0 && split) join = make_int2(b, parts1);
-        if (ok_e) {
+        if (ok_e && !split) {
+          // Whole rows: transposed in pairs of 8 x 8 tiles into rows of the last tile's stage, which no product reads
+          // any more, and from there by bulk copies of a row each.
+          tc05_fence_after();
+          const int h0 = 32 * (warp >> 2);
+          float2 inv[4];  // of this thread's columns: heads h0 + 8 i + 2 (lane % 4) and the next
+#pragma unroll
+          for (int i = 0; i < 4; ++i) inv[i] = *reinterpret_cast<const float2*>(linv + h0 + 8 * i + 2 * (lane & 3));
+          const uint32_t to = smem0 + s * kStageBytes + (h0 + 8 * (lane >> 4) + (lane & 7)) * kOutRow +
+                              (32 * q4 + (lane & 8)) * 2;
+          if (h0 < Hq) {
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {  // 16 dims
+                uint32_t o[16];
+                tmem_ld16x256b_x4(tmem + lane_base + ((uint32_t)(16 * x) << 16) + kOCol + mt * 64 + h0, o);
+                tmem_ld_wait();
+                uint32_t y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  y[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * inv[i >> 1].x,
+                                     __uint_as_float(o[2 * i + 1]) * inv[i >> 1].y);
+                const uint32_t at = to + (mt * 128 + 16 * x) * 2;
+                stmatrix_x4_trans(at, y[0], y[1], y[2], y[3]);
+                stmatrix_x4_trans(at + 16 * kOutRow, y[4], y[5], y[6], y[7]);
+              }
+          }
+          fence_proxy_async_smem();
+        }
+        if (ok_e && split) {
           tc05_fence_after();
 #pragma unroll 1
           for (int mt = 0; mt < 4; ++mt) {
@@ -551,31 +584,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
             tmem_ld32(tmem + lane_base + kOCol + mt * 64 + 32 * (warp >> 2), o);
             tmem_ld_wait();
             const int d = mt * 128 + 32 * q4 + lane;
-            if (!split) {
-              // Two lanes exchange halves: the even one stores both dims of head cc, the odd one those of the next.
+            // Four heads of a dim in one 16-byte store.
 #pragma unroll
-              for (int cc = 0; cc < 32; cc += 2) {
-                const int h = 32 * (warp >> 2) + cc + (lane & 1);
-                const float mine = __uint_as_float(lane & 1 ? o[cc + 1] : o[cc]);
-                const float give = __uint_as_float(lane & 1 ? o[cc] : o[cc + 1]);
-                const float got = __shfl_xor_sync(0xffffffffu, give, 1);
-                if (h < Hq) {
-                  const float f = linv[h];
-                  *reinterpret_cast<uint32_t*>(a.out + ((size_t)b * Hq + h) * kDv + (d & ~1)) =
-                      lane & 1 ? pack_bf16x2(got * f, mine * f) : pack_bf16x2(mine * f, got * f);
-                }
-              }
-            } else {
-              // Four heads of a dim in one 16-byte store.
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const int h = 32 * (warp >> 2) + 4 * k;
-                if (h < Hq) {
-                  const float4 val =
-                      make_float4(__uint_as_float(o[4 * k]) * linv[h], __uint_as_float(o[4 * k + 1]) * linv[h + 1],
-                                  __uint_as_float(o[4 * k + 2]) * linv[h + 2], __uint_as_float(o[4 * k + 3]) * linv[h + 3]);
-                  *reinterpret_cast<float4*>(a.o_part + (((size_t)slot * (Hq / 4) + h / 4) * kDv + d) * 4) = val;
-                }
+            for (int k = 0; k < 8; ++k) {
+              const int h = 32 * (warp >> 2) + 4 * k;
+              if (h < Hq) {
+                const float4 val =
+                    make_float4(__uint_as_float(o[4 * k]) * linv[h], __uint_as_float(o[4 * k + 1]) * linv[h + 1],
+                                __uint_as_float(o[4 * k + 2]) * linv[h + 2], __uint_as_float(o[4 * k + 3]) * linv[h + 3]);
+                *reinterpret_cast<float4*>(a.o_part + (((size_t)slot * (Hq / 4) + h / 4) * kDv + d) * 4) = val;
               }
             }
           }
@@ -589,8 +606,21 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         tc05_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(o_free);
+        if (!split) {
+          named_bar_sync(kSoftBar, kSoftThreads);  // the rows are complete
+          if (warp == 0) {
+            if (ok_e)
+              for (int h = lane; h < Hq; h += 32)
+                tma_store_bulk(a.out + ((size_t)b * Hq + h) * kDv, smem0 + s * kStageBytes + h * kOutRow, kDv * 2);
+            tma_store_commit();
+            tma_store_wait_read();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[s]);
+          }
+        }
       }
     }
+    if (warp == 0) tma_store_wait();
     if (threadIdx.x == 0) a.joins[blockIdx.x] = join;
   }
   if (dead && lane == 0) raise_error(a.err, SE_DEVERR_WAIT_TIMEOUT);
