@@ -217,7 +217,6 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
                                                                            const __grid_constant__ CUtensorMap vmap,
                                                                            const PagedArgs a) {
   using C = Cfg<kD>;
-  pdl_enter();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* stage = reinterpret_cast<float*>(ring + kSlots * kSlotBytes);  // [warps][8][D]
@@ -232,6 +231,19 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
   const int heads = a.heads, G = a.group, rows = heads * G, HG = a.head_groups, Pg = a.step_pages;
   const int combos = heads * a.mtiles, active = combos * a.replicas;
 
+  // What needs no input comes before the wait for the previous kernel; kept_prefix's barriers publish it.
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], active);
+    }
+    mbar_fence_init();
+  }
+  if (warp == C::kWarps && lane == 0) {
+    tma_prefetch_map(&kmap);
+    tma_prefetch_map(&vmap);
+  }
+  pdl_enter();
   // Pieces of a step: of up to eight query heads a CTA takes a second one in less time than more partials take to
   // join (1 x 1,000 tokens, 8 KV heads: 10.6 us with 32 partials an item, 10.0 with 16), of more it does not (1 x 4K,
   // 32 heads over one: 14.6 us with 32, 17.8 with 16).
@@ -255,14 +267,6 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
     return;
   }
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], active);
-    }
-    mbar_fence_init();
-  }
-  __syncthreads();
   Segments seg;
   seg.init(slices, slice.x, slice.y);
   bool dead = false;  // a bounded wait gave up: no further waits or products, but every barrier

@@ -204,30 +204,41 @@ __device__ __forceinline__ int kept_prefix(const int32_t* seq_lens, int batch, i
   constexpr int kOne = 40;  // sums of pages, and from this bit on of requests that have any
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto weight = [&](long long v) { return (v & ((1ll << kOne) - 1)) + (int)(v >> kOne) * over; };
+  // The sum of v over the threads up to this one, and over all. Of up to 32 requests every warp sums all itself.
+  const bool alone = batch <= 32;
+  const int me = alone ? lane : threadIdx.x;
+  auto scan = [&](auto v, auto* part, auto& all) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const auto t = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += t;
+    }
+    if (alone) {
+      all = __shfl_sync(0xffffffffu, v, 31);
+      return v;
+    }
+    if (lane == 31) part[warp] = v;
+    __syncthreads();
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) v += part[w];
+      all += part[w];
+    }
+    __syncthreads();
+    return v;
+  };
+  const bool writes = !alone || warp == 0;
   long long at = 0;
   int pages = 0;
   for (int base = 0; base < batch; base += kThreads) {
-    const int b = base + threadIdx.x;
+    const int b = base + me;
     const int L = b < batch ? seq_lens[b] : 0;
-    if (b < batch) lens[b] = L;
+    if (writes && b < batch) lens[b] = L;
     pages = kept_of(L, bt_stride, sink, recent, err).n;
-    long long incl = pages > 0 ? pages + (1ll << kOne) : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
-    }
-    if (lane == 31) sums[warp] = incl;
-    __syncthreads();
-    long long before = at, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += sums[w];
-      all += sums[w];
-    }
-    __syncthreads();
-    incl = weight(incl + before);
-    if (b < batch) prefix[b + 1] = (int)(incl < most ? incl : -1);
+    long long all;
+    const long long incl = weight(at + scan(pages > 0 ? pages + (1ll << kOne) : 0ll, sums, all));
+    if (writes && b < batch) prefix[b + 1] = (int)(incl < most ? incl : -1);
     at += all;
   }
   if (threadIdx.x == 0) prefix[0] = 0;
@@ -238,27 +249,16 @@ __device__ __forceinline__ int kept_prefix(const int32_t* seq_lens, int batch, i
   if (batch <= kPieceBatch && places <= (2 * over + 1) * ctas && places - items * over <= bound * widest) {
     // The requests' pieces of unit and of 2 unit pages, summed in the halves of a word.
     const int units = (pages + unit - 1) / unit;
-    unsigned incl = units | (units + 1) / 2 << 16, all = 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
-    }
-    unsigned* unit_sums = reinterpret_cast<unsigned*>(sums);
-    if (lane == 31) unit_sums[warp] = incl;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) incl += unit_sums[w];
-      all += unit_sums[w];
-    }
+    unsigned all;
+    const unsigned incl =
+        scan((unsigned)units | (unsigned)(units + 1) / 2 << 16, reinterpret_cast<unsigned*>(sums), all);
     if ((int)(all & 0xffff) * groups <= bound)
       piece = unit;
     else if (widest > unit && (int)(all >> 16) * groups <= bound)
       piece = widest;
-    if (piece > 0 && threadIdx.x < batch) {
-      prefix[threadIdx.x + 1] = (piece == unit ? incl & 0xffff : incl >> 16) * piece;
-      lens[batch + threadIdx.x] = pages;
+    if (piece > 0 && writes && me < batch) {
+      prefix[me + 1] = (piece == unit ? incl & 0xffff : incl >> 16) * piece;
+      lens[batch + me] = pages;
     }
   }
   __syncthreads();
