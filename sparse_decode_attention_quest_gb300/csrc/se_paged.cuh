@@ -105,7 +105,7 @@ struct Slices {
   }
   // Where CTA k's slice begins (CTA k - 1's ends).
   __device__ __forceinline__ int cut(int k) const {
-    if (total == 0 || k > (total - 1) / span) return total;
+    if ((long long)k * span >= total) return total;
     const int p = k * span;
     if (over == 0) return p;
     const int b = request_at(p), base = prefix[b] * groups, w = prefix[b + 1] - prefix[b];
