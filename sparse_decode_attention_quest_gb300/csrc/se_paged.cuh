@@ -244,7 +244,8 @@ __device__ __forceinline__ int kept_prefix(const int32_t* seq_lens, int batch, i
   if (threadIdx.x == 0) prefix[0] = 0;
   const long long total = weight(at);
   const int widest = 2 * unit <= over + 1 ? 2 * unit : unit, items = (int)(at >> kOne) * groups;
-  const int bound = min(ctas, items * pieces), places = (int)min(total, 1ll << 20) * groups;
+  const int bound = min(ctas, items * pieces);
+  const long long places = min(total, 1ll << 20) * groups;  // many heads: beyond 32 bits
   int piece = 0;
   if (batch <= kPieceBatch && places <= (2 * over + 1) * ctas && places - items * over <= bound * widest) {
     // The requests' pieces of unit and of 2 unit pages, summed in the halves of a word.

@@ -153,6 +153,13 @@ def test_many_heads_over_split_items(cuda_device, batch, lo, hi, shape):
     Inputs(cuda_device, lens, *shape, seed=batch).check()
 
 
+@pytest.mark.parametrize("Hq,H,D", [(1000, 1000, 64), (130, 65, 128)])
+def test_many_kv_heads(cuda_device, Hq, H, D):
+    """More (request, head group) items than CTAs from few requests, and about as many."""
+    Inputs(cuda_device, [100, 0, 17], Hq, H, D, seed=H).check()
+    Inputs(cuda_device, [33], Hq, H, D, seed=H).check()
+
+
 @pytest.mark.parametrize("batch", [19, 76, 151, 152, 153, 160, 161])
 @pytest.mark.parametrize("shape", [(8, 2, 128), (9, 3, 64), (8, 8, 128), (12, 1, 256), (16, 1, 576)])
 def test_about_one_short_request_per_cta(cuda_device, batch, shape):
