@@ -398,6 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
     const int parts1 = neighbours_of(slices, blockIdx.x, slice).parts1;
     int2 join = make_int2(0, 0);              // the item that goes on behind the slice
     float m_h[16], b_h[16], l_h[16];
+    bool unset = false;                       // one of the heads has no finite maximum yet
 #pragma unroll
     for (int i = 0; i < 16; ++i) m_h[i] = b_h[i] = l_h[i] = 0.f;
     for (; c.valid; c.next()) {
@@ -440,8 +441,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
           for (int k = 0; k < 8; ++k) st_shared_v4(st + ch * kChunkBytes + swz128(row % kGroupRows, k), 0u, 0u, 0u, 0u);
       }
       // After the segment's first tile, a tile whose scores all stay within 2^8 of the running maxima changes
-      // nothing but P and l. Otherwise the tile maxima are exchanged and the running maxima recomputed.
-      bool need = dead;
+      // nothing but P and l. Otherwise, and while a head has seen nothing but -inf (its base of 0 is no maximum),
+      // the tile maxima are exchanged and the running maxima recomputed.
+      bool need = dead || unset;
 #pragma unroll
       for (int i = 0; i < 16; ++i) need = need || x[i] > kRescaleLog2;
       if (t == 0 || bar_red_or(kSoftBar, kSoftThreads, need)) {
@@ -458,6 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         }
         float f[16];
         bool moved = false;
+        unset = false;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float4 w0 = *reinterpret_cast<const float4*>(xm + hh + 4 * k);
@@ -475,6 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
             f[i] = mv ? fast_exp2(mo - mn) : 1.f;
             moved = moved || mv;
             m_h[i] = mn;
+            unset = unset || (mn == -INFINITY && hh + i < Hq);
             l_h[i] = t == 0 ? 0.f : l_h[i] * f[i];
             b_h[i] = finite_base(mn);
             x[i] = tok_ok && hh + i < Hq ? fmaf(__uint_as_float(r[i]), a.scale_log2, -b_h[i]) : -INFINITY;
