@@ -39,7 +39,9 @@ def new_summary(k_cache: torch.Tensor) -> torch.Tensor:
 
 
 class DenseAttention:
-    """se_paged_decode's buffers for a cache view: output, log-sum-exp and workspace of ``batch`` requests."""
+    """se_paged_decode's buffers for a cache view: output, log-sum-exp and workspace of ``batch`` requests. The
+    workspace is filled on the current stream here, so this is made before the calls that use it, on whatever
+    stream those run, and outside a recording."""
 
     def __init__(self, kv, batch: int, num_q_heads: int, device, sm_scale: Optional[float] = None):
         self.kv = kv
@@ -135,7 +137,7 @@ class QuestDecodeStep:
         ws = se_sparse_decode_workspace_size(self.B, self.Hq, self.H, self.Dv, self.sel_stride)
         # zero-filled once: the decode's split-merge counters start at zero and every call leaves them so
         self.workspace = torch.zeros(max(ws, 16), dtype=torch.uint8, device=dev)
-        self.dense: Optional[DenseAttention] = None
+        self.dense = DenseAttention(self.kv, self.B, self.Hq, dev, self.sm_scale)
         self.score_ws = None
         if score_workspace:
             sws = se_quest_score_workspace_size(self.B, self.H, self.D)
@@ -173,8 +175,6 @@ class QuestDecodeStep:
     def attend_dense(self, q, seq_lens, stream=None):
         """Attention over every page of the cache instead of the selected ones: a layer that stays dense.
         The output is a buffer of its own (``self.dense.out``)."""
-        if self.dense is None:
-            self.dense = DenseAttention(self.kv, self.B, self.Hq, self.k_cache.device, self.sm_scale)
         return self.dense.run(q, self.block_table, seq_lens, stream=stream)
 
     def run_fused(self, q, seq_lens, k_new=None, v_new=None, stream=None):
@@ -250,7 +250,7 @@ class SnapKVDecodeCache:
         self.live = 0
         self.lens = torch.zeros(batch, dtype=torch.int32, device=device)
         self.q_window = torch.zeros(batch, window, num_q_heads, head_dim, dtype=torch.bfloat16, device=device)
-        self.attention: Optional[DenseAttention] = None
+        self.attention = DenseAttention(self.kv(), batch, num_q_heads, device, self.sm_scale)
         self.kept = torch.empty(batch, num_kv_heads, self.kept_max, dtype=torch.int32, device=device)
         self.counts = torch.empty(batch, num_kv_heads, dtype=torch.int32, device=device)
         self.steps = 0
@@ -289,6 +289,4 @@ class SnapKVDecodeCache:
     def attend(self, q, stream=None):
         """Attention of one query per request q [B][Hq][D] over its tokens in the live pool: the decode of a
         compacted cache."""
-        if self.attention is None:
-            self.attention = DenseAttention(self.kv(), self.B, self.Hq, self.lens.device, self.sm_scale)
         return self.attention.run(q, self.block_table, self.lens, stream=stream, kv=self.kv())
