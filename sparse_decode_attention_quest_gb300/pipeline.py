@@ -38,6 +38,13 @@ def new_summary(k_cache: torch.Tensor) -> torch.Tensor:
     return torch.empty(P, H, 2, D, dtype=torch.bfloat16, device=k_cache.device)
 
 
+def _on(stream):
+    """The context in which torch's own work goes to ``stream``, as the library's calls do (None: the current one)."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 class DenseAttention:
     """se_paged_decode's buffers for a cache view: output, log-sum-exp and workspace of ``batch`` requests. The
     workspace is filled on the current stream here, so this is made before the calls that use it, on whatever
@@ -264,24 +271,32 @@ class SnapKVDecodeCache:
         """Compacts (cache, lengths, the window's queries) into the pool that is not live and
         makes it live: the prefill eviction (the prompt's cache) and every periodic one."""
         dst = 1 - self.live
-        ws = torch.empty(max(se_snapkv_workspace_size(self.B, self.H, self.W, max_len), 16), dtype=torch.uint8,
-                         device=self.lens.device)
-        se_snapkv_score_and_compact_windowed(src_kv, q_window, src_block_table, lens, max_len, self.pool, self.keep,
-                                             self.sink, self.recent, self.sm_scale, self.kv(dst), self.block_table,
-                                             self.kept, self.counts, ws, stream)
-        self.lens = self.counts[:, 0].contiguous()  # every KV head of a request keeps as many positions
+        with _on(stream):  # the workspace goes back to this stream's memory, behind the calls that use it
+            ws = torch.empty(max(se_snapkv_workspace_size(self.B, self.H, self.W, max_len), 16), dtype=torch.uint8,
+                             device=self.lens.device)
+            se_snapkv_score_and_compact_windowed(src_kv, q_window, src_block_table, lens, max_len, self.pool, self.keep,
+                                                 self.sink, self.recent, self.sm_scale, self.kv(dst), self.block_table,
+                                                 self.kept, self.counts, ws, stream)
+            # every KV head of a request keeps as many positions
+            self._set_lens(self.counts[:, 0].contiguous())
         self.live = dst
         self.steps = 0
         self.evictions += 1
 
+    def _set_lens(self, lens):
+        if self.lens.is_cuda:  # calls in flight on this stream read the old ones
+            self.lens.record_stream(torch.cuda.current_stream())
+        self.lens = lens
+
     def append(self, k_new, v_new, q, stream=None):
         """One decode step: K/V rows of the new token (k_new, v_new [B][Hkv][D]) and its query
-        q [B][Hq][D]; evicts when the period is complete."""
+        q [B][Hq][D]; evicts when the period is complete. All of it runs on ``stream``."""
         se_quest_update_summaries(self.kv(), k_new, v_new, self.block_table, self.lens, stream)
         first = self.period - self.W
-        if self.steps >= first:
-            self.q_window[:, self.steps - first].copy_(q)
-        self.lens = self.lens + 1
+        with _on(stream):
+            if self.steps >= first:
+                self.q_window[:, self.steps - first].copy_(q)
+            self._set_lens(self.lens + 1)
         self.steps += 1
         if self.steps == self.period:
             self.evict_from(self.kv(), self.block_table, self.lens, self.q_window, self.max_len, stream)

@@ -1,7 +1,10 @@
 """Host side of the dense paged path's buffers: a step's calls only launch. What they need is made when the step
 is, so that its fills are not left on another stream than the call's, nor inside a recording."""
+import contextlib
+
 import pytest
 import torch
+from torch.overrides import TorchFunctionMode
 
 import sparse_decode_attention_quest_gb300 as se
 from sparse_decode_attention_quest_gb300 import pipeline
@@ -51,3 +54,40 @@ def test_attend_over_a_compacted_cache_makes_no_buffers(calls, monkeypatch):
     for stream in (11, 12):
         assert cache.attend(q, stream=stream) is cache.attention.out
     assert [s for _, s in calls] == [11, 12] and all(ws is cache.attention.workspace for ws, _ in calls)
+
+
+class _Ops(TorchFunctionMode):
+    """Names of torch's calls, with the stream that was current for each."""
+
+    def __init__(self):
+        self.seen, self.current = [], None
+
+    def __torch_function__(self, func, types, args=(), kwargs=None):
+        self.seen.append((getattr(func, "__name__", ""), self.current))
+        return func(*args, **(kwargs or {}))
+
+    @contextlib.contextmanager
+    def stream(self, s):
+        before, self.current = self.current, s if s is not None else self.current
+        try:
+            yield
+        finally:
+            self.current = before
+
+
+def test_a_compacted_cache_keeps_to_the_calls_stream(calls, monkeypatch):
+    """append and evict_from compute lengths and keep queries with torch: on the stream that their kernels use."""
+    cache = pipeline.SnapKVDecodeCache(2, 2, 8, 128, 4, 7, 24, 4, 8, 6, "cpu")
+    rows, q = torch.zeros(2, 2, 128, dtype=torch.bfloat16), torch.zeros(2, 8, 128, dtype=torch.bfloat16)
+    ops, mine = _Ops(), object()
+    monkeypatch.setattr(torch.cuda, "stream", ops.stream)
+    for name in ("se_quest_update_summaries", "se_snapkv_score_and_compact_windowed"):
+        monkeypatch.setattr(pipeline, name, lambda *a, **kw: None)
+    monkeypatch.setattr(pipeline, "se_snapkv_workspace_size", lambda *a: 64)
+    with ops:
+        for _ in range(cache.period):
+            cache.append(rows, rows, q, stream=mine)
+    assert cache.evictions == 1
+    work = [(name, s) for name, s in ops.seen if name in ("add", "__add__", "copy_", "contiguous", "empty", "zeros")]
+    assert {name for name, _ in work} >= {"copy_", "contiguous", "empty"} and len(work) >= cache.period + 6
+    assert all(s is mine for _, s in work)

@@ -101,3 +101,42 @@ def test_first_call_over_a_compacted_cache_on_a_side_stream(cuda_device):
     s.synchronize()
     with torch.cuda.stream(s):
         assert _equal(out, want)
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_steps_of_a_compacted_cache_on_a_side_stream(cuda_device, as_handle):
+    """Appends, the periodic evictions and the attention between them, none of it on the busy current stream."""
+    dev, g = cuda_device, torch.Generator().manual_seed(3)
+    B, H, Hq, D, W, n, period = 2, 2, 8, 128, 4, 90, 6
+    pages = -(-n // PAGE)
+    k, v = _bf16((B * pages, H, PAGE, D), g, dev), _bf16((B * pages, H, PAGE, D), g, dev)
+    table = torch.arange(B * pages, dtype=torch.int32, device=dev).view(B, pages)
+    lens = torch.full((B,), n, dtype=torch.int32, device=dev)
+    window = _bf16((B, W, Hq, D), g, dev)
+    rows = [(_bf16((B, H, D), g, dev), _bf16((B, H, D), g, dev), _bf16((B, Hq, D), g, dev))
+            for _ in range(2 * period + 1)]
+
+    def steps(stream):
+        cache = SnapKVDecodeCache(B, H, Hq, D, W, 7, 24, 4, 8, period, dev)
+        torch.cuda.synchronize()
+        if stream is not None:
+            torch.cuda._sleep(BUSY)
+        given = stream.cuda_stream if as_handle and stream is not None else stream
+        outs = []
+        with torch.cuda.stream(stream):
+            copies = [torch.empty(B, Hq, D, dtype=torch.bfloat16, device=dev) for _ in rows]
+        cache.evict_from(se.paged_kv(k, v, None), table, lens, window, n, given)
+        for (kn, vn, q), copy in zip(rows, copies):
+            cache.append(kn, vn, q, given)
+            out = cache.attend(q, given)
+            with torch.cuda.stream(stream):
+                outs.append(copy.copy_(out))
+        if stream is not None:
+            stream.synchronize()
+        torch.cuda.synchronize()
+        assert cache.evictions == 3
+        return outs, cache.lens.tolist()
+
+    want, n_want = steps(None)
+    got, n_got = steps(torch.cuda.Stream())
+    assert n_got == n_want and all(_equal(a, b) for a, b in zip(got, want))
