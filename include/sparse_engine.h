@@ -381,6 +381,10 @@ SE_API se_status_t se_sparse_paged_decode(const se_paged_kv_t* kv, const void* q
  * returned once. Lengths out of order or beyond the table: SE_DEVERR_LENGTH, nothing of that
  * request is returned. More pages than the pool lacks: SE_DEVERR_PAGE_RANGE, nothing is
  * returned. A page id out of range: SE_DEVERR_PAGE_RANGE, and -1 in its place on the stack.
+ *
+ * se_block_tables_release_ex -- the same, and the lengths that the release leaves:
+ *   seq_lens_after int32 [batch]: keep_lens[b], or seq_lens[b] where nothing of the request was
+ *     returned because of the lengths or of the pool; may be seq_lens or keep_lens itself.
  */
 SE_API se_status_t se_block_tables_extend(const int32_t* free_pages, int32_t* pool_state, int32_t num_pages,
                                           int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
@@ -390,6 +394,10 @@ SE_API se_status_t se_block_tables_extend(const int32_t* free_pages, int32_t* po
 SE_API se_status_t se_block_tables_release(int32_t* free_pages, int32_t* pool_state, int32_t num_pages,
                                            const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
                                            const int32_t* keep_lens, int32_t batch, void* stream);
+SE_API se_status_t se_block_tables_release_ex(int32_t* free_pages, int32_t* pool_state, int32_t num_pages,
+                                              const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
+                                              const int32_t* keep_lens, int32_t batch, int32_t* seq_lens_after,
+                                              void* stream);
 
 /*
  * se_paged_kv_store -- the K and V rows of a ragged batch of new tokens (a prompt,

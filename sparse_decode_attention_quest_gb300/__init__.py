@@ -28,7 +28,7 @@ __all__ = [
     "se_sparse_paged_decode_noalloc", "se_snapkv_workspace_size", "se_snapkv_window_scores", "se_snapkv_select",
     "se_snapkv_compact", "se_snapkv_score_and_compact", "se_snapkv_select_windowed",
     "se_snapkv_score_and_compact_windowed", "se_debug_snapkv_wait_probe", "SEGraph", "se_capture_begin",
-    "se_capture_end", "se_block_tables_extend", "se_block_tables_release", "se_paged_kv_store",
+    "se_capture_end", "se_block_tables_extend", "se_block_tables_release", "se_block_tables_release_ex", "se_paged_kv_store",
     "se_paged_decode_workspace_size", "se_paged_decode", "exported_symbols",
 ]
 
@@ -88,6 +88,7 @@ _SIGNATURES = {
     "se_sparse_paged_decode_noalloc": (ctypes.c_int, [_KV, _P, _I, _P, _I, _P, _I, _P, _P, _I, _F, _P, _P, _P]),
     "se_block_tables_extend": (ctypes.c_int, [_P, _P, _I, _P, _I, _P, _P, _I, _P, _P, _P, _P, _I, _P]),
     "se_block_tables_release": (ctypes.c_int, [_P, _P, _I, _P, _I, _P, _P, _I, _P]),
+    "se_block_tables_release_ex": (ctypes.c_int, [_P, _P, _I, _P, _I, _P, _P, _I, _P, _P]),
     "se_paged_kv_store": (ctypes.c_int, [_KV, _P, _L, _P, _L, _P, _I, _P]),
     "se_paged_decode_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
     "se_paged_decode": (ctypes.c_int, [_KV, _P, _L, _I, _P, _I, _P, _I, _I, _I, _F, _P, _P, _P, _Z, _P]),
@@ -477,6 +478,18 @@ def se_block_tables_release(free_pages, pool_state, block_table, seq_lens, keep_
         _arg(free_pages, i32, "free_pages", dev), _vec(pool_state, 4, i32, "pool_state", dev), free_pages.numel(),
         table, width, _vec(seq_lens, batch, i32, "seq_lens", dev),
         None if keep_lens is None else _vec(keep_lens, batch, i32, "keep_lens", dev), batch, _stream(stream, dev)))
+
+
+def se_block_tables_release_ex(free_pages, pool_state, block_table, seq_lens, keep_lens, seq_lens_after, stream=None):
+    """se_block_tables_release that also writes the lengths it leaves: keep_lens[b] (0 when None), or seq_lens[b] where
+    the request's release was refused. ``seq_lens_after`` may be ``seq_lens`` or ``keep_lens``."""
+    lib, dev, i32 = load_library(), torch.cuda.current_device(), torch.int32
+    table, batch, width = _table(block_table, "block_table", dev)
+    _check(lib.se_block_tables_release_ex(
+        _arg(free_pages, i32, "free_pages", dev), _vec(pool_state, 4, i32, "pool_state", dev), free_pages.numel(),
+        table, width, _vec(seq_lens, batch, i32, "seq_lens", dev),
+        None if keep_lens is None else _vec(keep_lens, batch, i32, "keep_lens", dev), batch,
+        _vec(seq_lens_after, batch, i32, "seq_lens_after", dev), _stream(stream, dev)))
 
 
 def se_paged_kv_store(kv: SEPagedKV, k_new, v_new, slot_map, stream=None):

@@ -775,6 +775,29 @@ se_status_t check_decode_call(const char* fn, const se_paged_kv_t* kv, const voi
 }  // namespace se
 
 // ------------------------------------------------ page pool, row store, dense paged decode
+// Both release calls (seq_lens_after NULL: the lengths are the caller's).
+static se_status_t release(int32_t* free_pages, int32_t* pool_state, int32_t num_pages, const int32_t* block_table,
+                           int32_t bt_stride, const int32_t* seq_lens, const int32_t* keep_lens, int32_t batch,
+                           int32_t* seq_lens_after, void* stream, const char* fn) {
+  if (batch < 0 || num_pages < 0 || bt_stride < 1)
+    return fail(SE_ERR_INVALID_ARG, fn, "negative size or bt_stride < 1");
+  if (!pool_state || (num_pages > 0 && !free_pages) || (batch > 0 && (!block_table || !seq_lens)))
+    return fail(SE_ERR_INVALID_ARG, fn, "NULL pointer");
+  if (!aligned16(free_pages) || !aligned16(pool_state) || !aligned16(block_table) || !aligned16(seq_lens) ||
+      !aligned16(keep_lens) || !aligned16(seq_lens_after))
+    return fail(SE_ERR_INVALID_ARG, fn, "pointers must be 16-byte aligned");
+  if (batch > se::block_tables_max_batch()) return fail(SE_ERR_UNSUPPORTED, fn, "batch > 16384");
+  if (num_pages >= (1 << 27) || bt_stride >= (1 << 27))
+    return fail(SE_ERR_UNSUPPORTED, fn, "2^27 or more pages (slots are 32-bit)");
+  if (batch == 0) return SE_OK;
+  DeviceInfo* d = nullptr;
+  cudaError_t e = current_device(&d);
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  e = se::launch_block_tables_release(free_pages, pool_state, num_pages, block_table, bt_stride, seq_lens, keep_lens,
+                                      batch, seq_lens_after, d->sm_count, d->err, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SE_OK : cuda_fail(fn, e);
+}
+
 extern "C" {
 
 se_status_t se_block_tables_extend(const int32_t* free_pages, int32_t* pool_state, int32_t num_pages,
@@ -807,24 +830,18 @@ se_status_t se_block_tables_extend(const int32_t* free_pages, int32_t* pool_stat
 se_status_t se_block_tables_release(int32_t* free_pages, int32_t* pool_state, int32_t num_pages,
                                     const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
                                     const int32_t* keep_lens, int32_t batch, void* stream) {
-  static const char* fn = "se_block_tables_release";
-  if (batch < 0 || num_pages < 0 || bt_stride < 1)
-    return fail(SE_ERR_INVALID_ARG, fn, "negative size or bt_stride < 1");
-  if (!pool_state || (num_pages > 0 && !free_pages) || (batch > 0 && (!block_table || !seq_lens)))
-    return fail(SE_ERR_INVALID_ARG, fn, "NULL pointer");
-  if (!aligned16(free_pages) || !aligned16(pool_state) || !aligned16(block_table) || !aligned16(seq_lens) ||
-      !aligned16(keep_lens))
-    return fail(SE_ERR_INVALID_ARG, fn, "pointers must be 16-byte aligned");
-  if (batch > se::block_tables_max_batch()) return fail(SE_ERR_UNSUPPORTED, fn, "batch > 16384");
-  if (num_pages >= (1 << 27) || bt_stride >= (1 << 27))
-    return fail(SE_ERR_UNSUPPORTED, fn, "2^27 or more pages (slots are 32-bit)");
-  if (batch == 0) return SE_OK;
-  DeviceInfo* d = nullptr;
-  cudaError_t e = current_device(&d);
-  if (e != cudaSuccess) return cuda_fail(fn, e);
-  e = se::launch_block_tables_release(free_pages, pool_state, num_pages, block_table, bt_stride, seq_lens, keep_lens,
-                                      batch, d->sm_count, d->err, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? SE_OK : cuda_fail(fn, e);
+  return release(free_pages, pool_state, num_pages, block_table, bt_stride, seq_lens, keep_lens, batch, nullptr, stream,
+                 "se_block_tables_release");
+}
+
+se_status_t se_block_tables_release_ex(int32_t* free_pages, int32_t* pool_state, int32_t num_pages,
+                                       const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
+                                       const int32_t* keep_lens, int32_t batch, int32_t* seq_lens_after,
+                                       void* stream) {
+  static const char* fn = "se_block_tables_release_ex";
+  if (batch > 0 && !seq_lens_after) return fail(SE_ERR_INVALID_ARG, fn, "NULL pointer");
+  return release(free_pages, pool_state, num_pages, block_table, bt_stride, seq_lens, keep_lens, batch, seq_lens_after,
+                 stream, fn);
 }
 
 se_status_t se_paged_kv_store(const se_paged_kv_t* kv, const void* k_new, int64_t k_stride, const void* v_new,

@@ -197,12 +197,17 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const int32_t* __restr
   if (threadIdx.x == 0) pool_state[0] = f - s_taken;
 }
 
+// Whether lengths can shrink from len to keep.
+__device__ __forceinline__ bool can_release(int len, int keep, int32_t bt_stride) {
+  return keep >= 0 && keep <= len && len <= (long long)bt_stride * kPageSize;
+}
+
 __global__ void __launch_bounds__(kThreads) release_kernel(int32_t* free_pages, int32_t* pool_state,
                                                            int32_t num_pages,
                                                            const int32_t* __restrict__ block_table,
-                                                           int32_t bt_stride, const int32_t* __restrict__ seq_lens,
-                                                           const int32_t* __restrict__ keep_lens, int32_t batch,
-                                                           unsigned* err) {
+                                                           int32_t bt_stride, const int32_t* seq_lens,
+                                                           const int32_t* keep_lens, int32_t batch,
+                                                           int32_t* seq_lens_after, unsigned* err) {
   pdl_enter();
   extern __shared__ int smem[];
   __shared__ Pair sums[kWarps];
@@ -215,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) release_kernel(int32_t* free_pages, 
     int n = 0, fp = 0;
     if (b < batch) {
       const int len = seq_lens[b], keep = keep_lens ? keep_lens[b] : 0;
-      if (keep >= 0 && keep <= len && len <= (long long)bt_stride * kPageSize) {
+      if (can_release(len, keep, bt_stride)) {
         fp = keep / kPageSize + (keep % kPageSize != 0);
         n = len / kPageSize + (len % kPageSize != 0) - fp;
       } else if (blockIdx.x == 0) {
@@ -246,7 +251,14 @@ __global__ void __launch_bounds__(kThreads) release_kernel(int32_t* free_pages, 
     }
     free_pages[f + total - 1 - (int)i] = phys;
   }
-  if (arrive_last(pool_state) && threadIdx.x == 0) pool_state[0] = f + total;
+  if (!arrive_last(pool_state)) return;
+  // Every CTA has read the lengths, and a thread reads a request's before it writes them: in place is fine.
+  if (seq_lens_after)
+    for (int b = threadIdx.x; b < batch; b += kThreads) {
+      const int len = seq_lens[b], keep = keep_lens ? keep_lens[b] : 0;
+      seq_lens_after[b] = sane && can_release(len, keep, bt_stride) ? keep : len;
+    }
+  if (threadIdx.x == 0) pool_state[0] = f + total;
 }
 
 int grid_for(long long elements, int per_thread, int sm_count) {
@@ -275,15 +287,15 @@ cudaError_t launch_block_tables_extend(const int32_t* free_pages, int32_t* pool_
 
 cudaError_t launch_block_tables_release(int32_t* free_pages, int32_t* pool_state, int32_t num_pages,
                                         const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
-                                        const int32_t* keep_lens, int32_t batch, int sm_count, unsigned* err,
-                                        cudaStream_t stream) {
+                                        const int32_t* keep_lens, int32_t batch, int32_t* seq_lens_after,
+                                        int sm_count, unsigned* err, cudaStream_t stream) {
   const size_t smem = (2 * (size_t)batch + 1) * sizeof(int);
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(release_kernel, (2 * block_tables_max_batch() + 1) * (int)sizeof(int), allowed);
   if (e != cudaSuccess) return e;
   const long long most = (long long)batch * bt_stride < num_pages ? (long long)batch * bt_stride : num_pages;
   e = launch_pdl(release_kernel, dim3(grid_for(most, 1, sm_count)), dim3(kThreads), smem, stream, free_pages, pool_state,
-                 num_pages, block_table, bt_stride, seq_lens, keep_lens, batch, err);
+                 num_pages, block_table, bt_stride, seq_lens, keep_lens, batch, seq_lens_after, err);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

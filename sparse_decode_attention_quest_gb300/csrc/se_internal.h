@@ -171,8 +171,8 @@ cudaError_t launch_block_tables_extend(const int32_t* free_pages, int32_t* pool_
                                        int32_t max_new_tokens, int sm_count, unsigned* err, cudaStream_t stream);
 cudaError_t launch_block_tables_release(int32_t* free_pages, int32_t* pool_state, int32_t num_pages,
                                         const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
-                                        const int32_t* keep_lens, int32_t batch, int sm_count, unsigned* err,
-                                        cudaStream_t stream);
+                                        const int32_t* keep_lens, int32_t batch, int32_t* seq_lens_after,
+                                        int sm_count, unsigned* err, cudaStream_t stream);
 
 // ---- kv_store.cu: rows of new tokens into their slots (+ summaries when kv.summary is set)
 cudaError_t launch_kv_store(const KvView& kv, uint16_t* k_mut, uint16_t* v_mut, const uint16_t* k_new,

@@ -11,7 +11,7 @@ or all four in one launch (se_quest_fused_step, run_fused).
 
 PagedCache is the cache's life around that step: pages from a pool, the rows of new tokens
 into their slots, dense attention over the cache, and the pages back
-(se_block_tables_extend, se_paged_kv_store, se_paged_decode, se_block_tables_release).
+(se_block_tables_extend, se_paged_kv_store, se_paged_decode, se_block_tables_release_ex).
 """
 from __future__ import annotations
 
@@ -20,7 +20,7 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import (APPEND_OVERLAP_PREVIOUS, paged_kv, se_block_tables_extend, se_block_tables_release, se_copy_async,
+from . import (APPEND_OVERLAP_PREVIOUS, paged_kv, se_block_tables_extend, se_block_tables_release_ex,
                se_paged_decode, se_paged_decode_workspace_size, se_paged_kv_store, se_quest_build_summaries,
                se_quest_fused_step,
                se_quest_kept_pages_max, se_quest_score_pages, se_quest_score_pages_ws, se_quest_score_workspace_size,
@@ -87,7 +87,6 @@ class PagedCache:
         self.pool_state = torch.tensor([num_pages, 0, 0, 0], **i32)
         self.block_table = torch.zeros(batch, max(1, (max_len + PAGE - 1) // PAGE), **i32)
         self.lens = torch.zeros(batch, **i32)
-        self.no_tokens = torch.zeros(batch, **i32)
         self.token_start = torch.zeros(batch + 1, **i32)
         self.slot_map = torch.full((max_new_tokens,), -1, **i32)
         self.positions = torch.zeros(max_new_tokens, **i32)
@@ -106,10 +105,11 @@ class PagedCache:
         return self.attention.run(q, self.block_table, self.lens, sink_tokens, recent_tokens, stream)
 
     def release(self, keep_lens=None, stream=None):
-        """The pages behind keep_lens[b] tokens (None: all of them) back to the pool; the lengths shrink. A page
-        that keep_lens ends in keeps its summary, which bounds the dropped keys too."""
-        se_block_tables_release(self.free_pages, self.pool_state, self.block_table, self.lens, keep_lens, stream)
-        se_copy_async(self.lens, self.no_tokens if keep_lens is None else keep_lens, stream)
+        """The pages behind keep_lens[b] tokens (None: all of them) back to the pool; the lengths shrink, except of
+        requests whose release is refused (and reported): a keep_lens[b] below 0 or above the length. A page that
+        keep_lens ends in keeps its summary, which bounds the dropped keys too."""
+        se_block_tables_release_ex(self.free_pages, self.pool_state, self.block_table, self.lens, keep_lens, self.lens,
+                                   stream)
 
 
 class QuestDecodeStep:
