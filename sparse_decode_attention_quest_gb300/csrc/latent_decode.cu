@@ -614,8 +614,17 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
           named_bar_sync(kSoftBar, kSoftThreads);  // the rows are complete
           if (warp == 0) {
             if (ok_e)
-              for (int h = lane; h < Hq; h += 32)
-                tma_store_bulk(a.out + ((size_t)b * Hq + h) * kDv, smem0 + s * kStageBytes + h * kOutRow, kDv * 2);
+              for (int h = lane; h < Hq; h += 32) {
+                const uint32_t from = smem0 + s * kStageBytes + h * kOutRow;
+                if (linv[h] == 0.f) {
+                  // No finite logit: 0 whatever the values hold (0 times them need not be; a partial keeps that
+                  // product, as the sum over a row with other tokens does).
+#pragma unroll 1
+                  for (int i = 0; i < kDv * 2; i += 16) st_shared_v4(from + i, 0u, 0u, 0u, 0u);
+                  fence_proxy_async_smem();
+                }
+                tma_store_bulk(a.out + ((size_t)b * Hq + h) * kDv, from, kDv * 2);
+              }
             tma_store_commit();
             tma_store_wait_read();
             __syncwarp();
@@ -726,10 +735,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const floa
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
       auto at = [&](const float4& v) { return h == 0 ? v.x : h == 1 ? v.y : h == 2 ? v.z : v.w; };
-      const float inv = ll[h] == 0.f ? 0.f : 1.f / ll[h];
-      *reinterpret_cast<uint2*>(out + (row + h) * kDv + d) = make_uint2(
-          pack_bf16x2(at(acc[0]) * inv, at(acc[1]) * inv), pack_bf16x2(at(acc[2]) * inv, at(acc[3]) * inv));
-      if (out_lse && d == 0) out_lse[row + h] = ll[h] == 0.f ? -INFINITY : (mm[h] + log2f(ll[h])) * kLn2;
+      const bool none = ll[h] == 0.f;
+      const float inv = 1.f / ll[h];
+      *reinterpret_cast<uint2*>(out + (row + h) * kDv + d) =
+          none ? make_uint2(0u, 0u)
+               : make_uint2(pack_bf16x2(at(acc[0]) * inv, at(acc[1]) * inv),
+                            pack_bf16x2(at(acc[2]) * inv, at(acc[3]) * inv));
+      if (out_lse && d == 0) out_lse[row + h] = none ? -INFINITY : (mm[h] + log2f(ll[h])) * kLn2;
     }
   }
 }

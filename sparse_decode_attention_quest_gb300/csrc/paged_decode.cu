@@ -174,11 +174,13 @@ __device__ __forceinline__ void join_rows(const float* o_part, const float* lse_
   if (share == 1) {
     if (r0 + warp >= rows) return;
     const size_t orow = (size_t)item * rows + r;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const bool none = l == 0.f;
+    const float inv = 1.f / l;
 #pragma unroll
     for (int x = 0; x < kV; x += 2)
-      *reinterpret_cast<uint32_t*>(out + orow * kD + lane * kV + x) = pack_bf16x2(acc[x] * inv, acc[x + 1] * inv);
-    if (out_lse && lane == 0) out_lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+      *reinterpret_cast<uint32_t*>(out + orow * kD + lane * kV + x) =
+          none ? 0u : pack_bf16x2(acc[x] * inv, acc[x + 1] * inv);
+    if (out_lse && lane == 0) out_lse[orow] = none ? -INFINITY : (M + log2f(l)) * kLn2;
     return;
   }
   sync();  // the previous rows' sums are read
@@ -204,9 +206,10 @@ __device__ __forceinline__ void join_rows(const float* o_part, const float* lse_
       y += f * sm.acc[w0 + k][d + 1];
     }
     const size_t orow = (size_t)item * rows + row;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    *reinterpret_cast<uint32_t*>(out + orow * kD + d) = pack_bf16x2(x * inv, y * inv);
-    if (out_lse && d == 0) out_lse[orow] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    const bool none = sum == 0.f;
+    const float inv = 1.f / sum;
+    *reinterpret_cast<uint32_t*>(out + orow * kD + d) = none ? 0u : pack_bf16x2(x * inv, y * inv);
+    if (out_lse && d == 0) out_lse[orow] = none ? -INFINITY : (top + log2f(sum)) * kLn2;
   }
 }
 
@@ -498,6 +501,8 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
     if (split && threadIdx.x == 0) flags[2 + slot] = item;
     const size_t out_row0 = (size_t)seg.b * a.num_q_heads + (size_t)seg.group * rows;
     const size_t part_row0 = (size_t)(2 * blockIdx.x + slot) * rows;
+    // A whole row without a finite logit is 0 whatever its values hold (0 times them need not be); a partial of one
+    // keeps that product, as the sum over a row with other tokens does.
     // The R warps of a (head, tile) stage their states, eight query heads at a time, and share the sums and the
     // output. Named barriers of the R warps: 2 + 2 combo, the states are there; 3 + 2 combo, they are read.
     if (!works) continue;
@@ -516,13 +521,14 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
         const int hd = 2 * t + e;
         if constexpr (kSolo) {
           // No other states: the row is final.
-          const float inv = l[nt][e] == 0.f ? 0.f : 1.f / l[nt][e];
-          const float lse2 = l[nt][e] == 0.f ? -INFINITY : m[nt][e] + log2f(l[nt][e]);
+          const bool none = l[nt][e] == 0.f;
+          const float inv = none ? 0.f : 1.f / l[nt][e];
+          const float lse2 = none ? -INFINITY : m[nt][e] + log2f(l[nt][e]);
           const int qr = tile_head + nt * 8 + hd, r = hc * G + qr;
 #pragma unroll
           for (int i = 0; i < kD / 16; ++i) {
-            o[i][nt][e] *= inv;
-            o[i][nt][2 + e] *= inv;
+            o[i][nt][e] = none && !split ? 0.f : o[i][nt][e] * inv;
+            o[i][nt][2 + e] = none && !split ? 0.f : o[i][nt][2 + e] * inv;
           }
           if (g == 0 && qr < G) {
             if (split)
@@ -572,14 +578,15 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
           const float4 v = *reinterpret_cast<const float4*>(stage + w * 8 * kD + stage_at<kD>(hd, d));
           acc = make_float4(acc.x + f * v.x, acc.y + f * v.y, acc.z + f * v.z, acc.w + f * v.w);
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum, lse2 = sum == 0.f ? -INFINITY : M + log2f(sum);
+        const bool none = sum == 0.f;
+        const float inv = none ? 0.f : 1.f / sum, lse2 = none ? -INFINITY : M + log2f(sum);
         const size_t r = r0 + hd;
         acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         if (split)
           *reinterpret_cast<float4*>(a.o_part + (part_row0 + r) * kD + d) = acc;
         else
           *reinterpret_cast<uint2*>(a.out + (out_row0 + r) * kD + d) =
-              make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+              none ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
         if (d == 0) {
           if (split)
             a.lse_part[part_row0 + r] = lse2;
