@@ -163,7 +163,8 @@ def _stream(stream, dev=None):
 
 def paged_kv(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor], summary: Optional[torch.Tensor],
              head_dim_v: Optional[int] = None) -> SEPagedKV:
-    """se_paged_kv_t for bf16 caches [P][Hkv][16][row]. ``v_cache`` None = latent cache (v aliases k)."""
+    """se_paged_kv_t for bf16 caches [P][Hkv][16][row]. ``v_cache`` None = latent cache (v aliases k). ``.device``
+    of the result is their CUDA device's index."""
     _ptr(k_cache, torch.bfloat16, "k_cache")
     P, H, ps, row_k = k_cache.shape
     if v_cache is None:
@@ -175,8 +176,13 @@ def paged_kv(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor], summary: Op
         v_ptr, row_v, dv = v_cache.data_ptr(), v_cache.shape[-1], v_cache.shape[-1]
     if summary is not None:
         _ptr(summary, torch.bfloat16, "summary")
-    return SEPagedKV(k_cache.data_ptr(), v_ptr, None if summary is None else summary.data_ptr(),
-                     P, H, ps, row_k, dv, row_k, row_v)
+    for t, name in ((v_cache, "v_cache"), (summary, "summary")):
+        if t is not None and t.get_device() != k_cache.get_device():
+            raise ValueError(f"{name}: is on cuda:{t.get_device()}, k_cache on cuda:{k_cache.get_device()}")
+    kv = SEPagedKV(k_cache.data_ptr(), v_ptr, None if summary is None else summary.data_ptr(),
+                   P, H, ps, row_k, dv, row_k, row_v)
+    kv.device = k_cache.get_device()
+    return kv
 
 
 class SEGraph:
@@ -441,6 +447,13 @@ def _table(t, name: str, dev: int):
     return p, t.shape[0], t.shape[1]
 
 
+def _cache(kv: SEPagedKV, dev: int):
+    """A reference to a cache view on the current device (a view of the caller's own making names no device)."""
+    if getattr(kv, "device", dev) != dev:
+        raise ValueError(f"kv: is on cuda:{kv.device}, the current device is cuda:{dev}")
+    return ctypes.byref(kv)
+
+
 def _rows_ptr(t, heads: int, width: int, dtype, name: str, dev: int):
     """(pointer, row stride) of [N][heads][width] rows whose heads are dense; the N rows may be
     any distance apart (columns of a fused projection's output, say)."""
@@ -503,7 +516,7 @@ def se_paged_kv_store(kv: SEPagedKV, k_new, v_new, slot_map, stream=None):
         vp, vs = _rows_ptr(v_new, kv.num_kv_heads, kv.head_dim_v, torch.bfloat16, "v_new", dev)
     if k_new.shape[0] != tokens or (v_new is not None and v_new.shape[0] != tokens):
         raise ValueError("k_new, v_new and slot_map differ in tokens")
-    _check(lib.se_paged_kv_store(ctypes.byref(kv), kp, ks, vp, vs, _arg(slot_map, torch.int32, "slot_map", dev), tokens,
+    _check(lib.se_paged_kv_store(_cache(kv, dev), kp, ks, vp, vs, _arg(slot_map, torch.int32, "slot_map", dev), tokens,
                                  _stream(stream, dev)))
 
 
@@ -527,7 +540,7 @@ def se_paged_decode(kv: SEPagedKV, q, block_table, seq_lens, sm_scale: float, ou
     if rows != batch:
         raise ValueError(f"block_table: expected {batch} rows, got {rows}")
     _check(lib.se_paged_decode(
-        ctypes.byref(kv), qp, qs, hq, table, width, _vec(seq_lens, batch, torch.int32, "seq_lens", dev), batch,
+        _cache(kv, dev), qp, qs, hq, table, width, _vec(seq_lens, batch, torch.int32, "seq_lens", dev), batch,
         sink_tokens, recent_tokens, sm_scale, _vec(out, batch * hq * kv.head_dim_v, torch.bfloat16, "out", dev),
         None if out_lse is None else _vec(out_lse, batch * hq, torch.float32, "out_lse", dev),
         None if workspace is None else _arg(workspace, torch.uint8, "workspace", dev),
