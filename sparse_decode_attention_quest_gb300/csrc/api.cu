@@ -874,8 +874,9 @@ size_t se_paged_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_
                                       int32_t head_dim_v) {
   if (batch < 0 || num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads) return 0;
   if (se::paged_latent_supported(num_kv_heads, head_dim, head_dim_v, num_q_heads))
-    return round16(se::paged_latent_workspace_bytes(num_q_heads));
+    return batch > se::paged_latent_max_batch() ? 0 : round16(se::paged_latent_workspace_bytes(num_q_heads));
   if (!se::paged_decode_supported(num_kv_heads, head_dim, head_dim_v, num_q_heads)) return 0;
+  if (batch > se::paged_decode_max_batch()) return 0;
   return round16(se::paged_decode_workspace_bytes(num_q_heads, num_kv_heads, head_dim));
 }
 
