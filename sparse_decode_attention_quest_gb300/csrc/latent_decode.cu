@@ -131,31 +131,6 @@ __device__ __forceinline__ void commit_elected(uint64_t* bar) {
       : "memory");
 }
 
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-
-// Reduction of 16 values over the 16 lanes of a half-warp by halving exchanges (15 shuffles). Afterwards v[0]
-// holds the result for the value with index reduced_index(lane).
-template <bool kMax>
-__device__ __forceinline__ void half_warp_reduce16(float (&v)[16], int lane) {
-#pragma unroll
-  for (int st = 0; st < 4; ++st) {
-    const int b = 1 << st, w = 8 >> st;
-    const bool up = (lane & b) != 0;
-#pragma unroll
-    for (int i = 0; i < w; ++i) {
-      const float send = up ? v[i] : v[i + w];
-      const float keep = up ? v[i + w] : v[i];
-      const float got = __shfl_xor_sync(0xffffffffu, send, b);
-      v[i] = kMax ? fmaxf(keep, got) : keep + got;
-    }
-  }
-}
-__device__ __forceinline__ int reduced_index(int lane) {
-  return 8 * (lane & 1) + 4 * ((lane >> 1) & 1) + 2 * ((lane >> 2) & 1) + ((lane >> 3) & 1);
-}
-
 // The tiles of a CTA's slice in order: its segments, cut into tiles of 4 pages.
 struct TileCursor {
   Segments sg;

@@ -164,7 +164,6 @@ struct Segments {
     end = stop;
     b = start < stop ? sl.request_at(start) : 0;
   }
-  __device__ __forceinline__ bool more() const { return x < end; }
   __device__ __forceinline__ bool next() {
     if (x >= end) return false;
     while (sl.prefix[b + 1] * sl.groups <= x) ++b;
