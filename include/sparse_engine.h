@@ -86,8 +86,9 @@ typedef struct {
   int32_t num_pages;       /* physical pages in the pool */
   int32_t num_kv_heads;
   int32_t page_size;       /* must be 16 */
-  int32_t head_dim;        /* key/query width: 128, or 576 for a latent cache */
-  int32_t head_dim_v;      /* value width: 128, or 512 for a latent cache */
+  int32_t head_dim;        /* key/query width: 128, or 576 for a latent cache, in the Quest and SnapKV calls; 64, 128, 256 or
+                              576 in se_paged_decode; any multiple of 8 up to 576 in se_paged_kv_store */
+  int32_t head_dim_v;      /* value width: head_dim, or 512 for a latent cache (se_paged_kv_store: any multiple of 8 up to 576) */
   int32_t row_stride_k;    /* elements between consecutive token rows of k (>= head_dim, multiple of 8) */
   int32_t row_stride_v;    /* elements between consecutive token rows of v (>= head_dim_v, multiple of 8) */
 } se_paged_kv_t;
@@ -410,7 +411,9 @@ SE_API se_status_t se_block_tables_release_ex(int32_t* free_pages, int32_t* pool
  *     the rows can be columns of a fused projection's output.
  * With kv->summary, the page summaries are updated as se_quest_update_summaries does
  * token by token: from the new keys alone for a page whose slot 0 is among them,
- * otherwise together with the page's present summary. The new tokens of one page stand
+ * otherwise together with the page's present summary. A NaN counts for neither bound; of a
+ * channel in which a new page's keys are all NaN they are +inf and -inf, as
+ * se_quest_build_summaries leaves them. The new tokens of one page stand
  * next to each other in the batch, as in the slot map of se_block_tables_extend, and a
  * slot is named once. A slot named twice in neighbouring tokens of one page keeps the
  * later row; elsewhere it holds pieces of either.
@@ -432,6 +435,9 @@ SE_API se_status_t se_paged_kv_store(const se_paged_kv_t* kv, const void* k_new,
  *     z_j = sm_scale * q[b][a] . k_j
  *     out[b][a]  = sum_j softmax(z)_j v_j       (bf16, round to nearest even)
  *     out_lse[b][a] = log sum_j exp(z_j)        (fp32, natural log; optional)
+ * Logits, maxima, sums, partial outputs and joins are fp32. A weight exp(z_j - max) is rounded to
+ * bf16 (half a step, 2^-8 of it) where it meets its value row, as in se_sparse_paged_decode, but
+ * not in the sum that divides the output nor in out_lse.
  * A request without tokens (and a row whose logits are all -inf) writes out = 0 and
  * lse = -inf. Cache rows that are not kept are never used, whatever they hold.
  *   q: bf16, query head a of request b at q + b * q_stride + a * head_dim (elements;

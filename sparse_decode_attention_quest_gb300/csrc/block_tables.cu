@@ -14,14 +14,14 @@
 // few MB, so a call is bound by its launch and by the latency of a chain of
 // dependent loads (lengths, then a free page, then the stores): with cold caches
 // 7.6 us for one token in each of 32 requests, 6.8 us for four prompts of 32K
-// tokens (64 CTAs), 9.2 us for 312,000 tokens of 250 requests, 5.0 to 5.9 us for the
+// tokens (64 CTAs), 9.2 us for 312,000 tokens of 250 requests, 5.1 to 5.7 us for the
 // releases of the three. Hence one launch: every CTA sums the prefixes of the whole batch by itself (the lengths
 // are a few KB in L2) and fills its share of the slot map. A new page is taken
 // from the stack by each of its tokens (the index is arithmetic on the
 // prefixes); the token at slot 0 also writes the table entry, so no CTA waits for
 // another's table entries. The CTA that arrives last, when every CTA has read
 // the lengths and the count, writes the new lengths and the count back: the
-// lengths may be updated in place.
+// lengths may be updated in place, by a release (se_block_tables_release_ex) too.
 #include "se_ptx.cuh"
 
 namespace se {

@@ -17,14 +17,19 @@
 //    over every SM. An item that spans CTAs leaves a partial (output,
 //    log-sum-exp) per CTA; a CTA has at most two, for the item it starts inside
 //    and the item it ends inside, so the workspace does not grow with the lengths.
-//  * Join: where the table's (or the windows') width bounds an item's partials to
-//    kInlineBytes, if need be with fewer KV heads per item, the CTA that publishes
-//    an item's last partial merges them in the order of the pages. Otherwise a
-//    second kernel does, a warp per row: one CTA reads partials from L2 at some 60
-//    bytes a clock, and merging 32 of 16 KB took it 25 of 46 us (4 requests of 2.5K
-//    tokens, 32 query heads). 48 windows of 1,064 tokens: 27.5 us, against 29.0 with
-//    the second kernel and 29.5 with a bound of 100 KB; one request of 4K tokens:
-//    10.0 us, against 10.8 with the second kernel.
+//  * Join: where the partials that an item of the table's (or the windows') width
+//    has in slices of the least length stay within kInlineBytes, if need be with
+//    fewer KV heads per item, the CTA that publishes an item's last partial merges
+//    them in the order of the pages. Otherwise a second kernel does, a warp per row:
+//    one CTA reads partials from L2 at some 60 bytes a clock, and merging 32 of 16 KB
+//    took it 25 of 46 us (4 requests of 2.5K tokens, 32 query heads). 48
+//    windows of 1,064 tokens: 27.5 us, against 29.0 with the second kernel and 29.5
+//    with a bound of 100 KB. The table's width is its capacity, so the same lengths
+//    behind a wider one may take the second kernel: one request of 4K tokens 9.6 us
+//    behind a table of 256 pages, 11.9 behind one of 8,192. In pieces an item can have
+//    about twice the partials that the bound counts: one request of 4K tokens beside
+//    19 of one token, 32 partials of 2 KB, takes 10.5 us joined here and 11.8 by the
+//    second kernel.
 //  * Copies: a page's rows of one KV head are 16 x D bf16, and the heads of a
 //    group of Hc lie next to each other, so that one TMA box of 64 dims x
 //    16 Hc rows x D / 64 brings a whole page of the group (16 to 32 KB for 4 to 8
@@ -54,7 +59,7 @@ constexpr int kSlotBytes = 32 * 1024;
 constexpr int kMetaRing = 4;     // steps whose page masks are held (at most three are in flight)
 constexpr int kMaxPages = 16;    // pages of a step
 constexpr int kMaxBatch = 4096;  // requests whose prefix fits beside the ring
-constexpr int kInlineBytes = 48 * 1024;  // partials of an item, at most, where one CTA merges them
+constexpr int kInlineBytes = 48 * 1024;  // partials of an item, in slices, where one CTA merges them
 constexpr int kInlineWidth = 32;          // pages of an item from which smaller boxes are taken for that
 constexpr int kJoinWarps = 8;
 
@@ -686,8 +691,8 @@ HeadPlan head_plan(int num_kv_heads, int group, int head_dim, int most_heads) {
   return p;
 }
 
-// The largest boxes, unless the table's (or the windows') width bounds an item's partials so far that smaller ones
-// let the decode kernel join them: fewer heads per item are fewer rows to join and more CTAs that join. Not
+// The largest boxes, unless the table's (or the windows') width keeps an item's partials, counted in slices of the
+// least length, so few that smaller ones let the decode kernel join them: fewer heads per item are fewer rows to join and more CTAs that join. Not
 // for short items, which are seldom split: more of them cost more than the join (64 requests of up to 19 pages, 8 KV
 // heads of 64 dims: 16.8 us, 21.9 in boxes of four; up to 157 pages, 4 heads of 128 dims: 31.6, and 30.0 in boxes of
 // one).
