@@ -235,7 +235,8 @@ class SnapKVDecodeCache:
     recent + period tokens). A decode step appends its token's K/V rows to the live pool and
     keeps its query if it is among the last ``window`` of the period, in order: the
     observation window of the next eviction. Host orchestration only; appends and
-    evictions run in the library's kernels.
+    evictions run in the library's kernels. Lengths, pools and the window's place change
+    from call to call, so append and evict_from refuse to be recorded.
     """
 
     def __init__(self, batch: int, num_kv_heads: int, num_q_heads: int, head_dim: int, window: int,
@@ -270,6 +271,7 @@ class SnapKVDecodeCache:
     def evict_from(self, src_kv, src_block_table, lens, q_window, max_len: int, stream=None):
         """Compacts (cache, lengths, the window's queries) into the pool that is not live and
         makes it live: the prefill eviction (the prompt's cache) and every periodic one."""
+        self._refuse_recording(stream)
         dst = 1 - self.live
         with _on(stream):  # the workspace goes back to this stream's memory, behind the calls that use it
             ws = torch.empty(max(se_snapkv_workspace_size(self.B, self.H, self.W, max_len), 16), dtype=torch.uint8,
@@ -283,6 +285,13 @@ class SnapKVDecodeCache:
         self.steps = 0
         self.evictions += 1
 
+    def _refuse_recording(self, stream):
+        if self.lens.is_cuda:
+            with _on(stream):
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("append and evict_from cannot be recorded: a replay would repeat one step's "
+                                       "lengths and pools")
+
     def _set_lens(self, lens):
         if self.lens.is_cuda:  # calls in flight on this stream read the old ones
             self.lens.record_stream(torch.cuda.current_stream())
@@ -291,6 +300,7 @@ class SnapKVDecodeCache:
     def append(self, k_new, v_new, q, stream=None):
         """One decode step: K/V rows of the new token (k_new, v_new [B][Hkv][D]) and its query
         q [B][Hq][D]; evicts when the period is complete. All of it runs on ``stream``."""
+        self._refuse_recording(stream)
         se_quest_update_summaries(self.kv(), k_new, v_new, self.block_table, self.lens, stream)
         first = self.period - self.W
         with _on(stream):

@@ -140,3 +140,37 @@ def test_steps_of_a_compacted_cache_on_a_side_stream(cuda_device, as_handle):
     want, n_want = steps(None)
     got, n_got = steps(torch.cuda.Stream())
     assert n_got == n_want and all(_equal(a, b) for a, b in zip(got, want))
+
+
+def test_steps_of_a_compacted_cache_refuse_to_be_recorded(cuda_device):
+    """Before anything is recorded or changed; the recording and the cache go on."""
+    dev, g = cuda_device, torch.Generator().manual_seed(4)
+    B, H, Hq, D = 2, 2, 8, 128
+    cache = SnapKVDecodeCache(B, H, Hq, D, 4, 7, 24, 4, 8, 6, dev)
+    kn, vn, q = _bf16((B, H, D), g, dev), _bf16((B, H, D), g, dev), _bf16((B, Hq, D), g, dev)
+    k = _bf16((B, H, PAGE, D), g, dev)
+    table, lens = torch.arange(B, dtype=torch.int32, device=dev).view(B, 1), torch.full((B,), 16, dtype=torch.int32, device=dev)
+    window = _bf16((B, 4, Hq, D), g, dev)
+    cache.append(kn, vn, q)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for given in (s, s.cuda_stream):
+        se.se_capture_begin(s)
+        with pytest.raises(RuntimeError, match="recorded"):
+            cache.append(kn, vn, q, given)
+        with pytest.raises(RuntimeError, match="recorded"):
+            cache.evict_from(se.paged_kv(k, k, None), table, lens, window, 16, given)
+        cache.attend(q, given)
+        graph = se.se_capture_end(s)
+        assert cache.steps == 1 and cache.evictions == 0 and cache.lens.tolist() == [1, 1]
+        cache.attention.out.fill_(7.0)
+        torch.cuda.synchronize()
+        graph.launch(s)
+        s.synchronize()
+        # One token: its weight is 1.
+        assert _equal(cache.attention.out, vn.repeat_interleave(Hq // H, 1))
+        graph.destroy()
+    cache.append(kn, vn, q, s)
+    s.synchronize()
+    with torch.cuda.stream(s):
+        assert cache.lens.tolist() == [2, 2]
