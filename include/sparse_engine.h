@@ -12,7 +12,8 @@
  *     compacted pages (Figure 2 caption, Table 8, Table 10, Table 15 note);
  *   - the dense paged path around them: pages, block tables and slot maps from
  *     request lengths, the rows of new tokens into their pages, and attention of one
- *     new token over a whole cache or a sink and a recent window (Table 7, Tables 9-12).
+ *     new token over a whole cache or a sink and a recent window (Table 7, Tables 9-12);
+ *   - rotary positions, and the dense paged path with the cache in 8 bits.
  * The pages do not print either method's equations; each entry point below
  * states the computation it performs.
  *
@@ -463,6 +464,136 @@ SE_API se_status_t se_paged_decode(const se_paged_kv_t* kv, const void* q, int64
                                    const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
                                    int32_t batch, int32_t sink_tokens, int32_t recent_tokens, float sm_scale,
                                    void* out, float* out_lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rotary positions: query and key rows turned by their tokens' positions before they are
+ * stored and attended to. The queries and keys of the Quest, SnapKV and dense calls are
+ * taken as they are; these calls make them from a projection's output.
+ *
+ * se_rotary -- for token t of num_tokens, every query head and key head, and every pair
+ * i < rotary_dim / 2 of the dims from rotary_offset on, with p = positions[t]:
+ *     angle = p * freqs[i] / 2^64 turns (the product taken modulo 2^64, so that it is exact
+ *             for every position),
+ *     y0 = amplitude * (x0 cos(angle) - x1 sin(angle)),
+ *     y1 = amplitude * (x1 cos(angle) + x0 sin(angle)).
+ *   (x0, x1) are dims rotary_offset + (i, i + rotary_dim / 2), or with SE_ROTARY_INTERLEAVED
+ *   rotary_offset + (2 i, 2 i + 1). SE_ROTARY_INVERSE turns by -angle. fp32, rounded once to
+ *   bf16; the other dims are copied (or left alone, in place).
+ *   q: bf16, query head a of token t at q + t * q_stride + a * head_dim (elements), k alike;
+ *     either may be NULL with 0 heads. Strides are multiples of 8 and at least heads * head_dim, so
+ *     that the rows can be columns of a fused projection's output.
+ *   q_out, k_out: as q and k; the same pointer and stride as the input (in place), or memory that
+ *     overlaps neither input.
+ *   freqs: uint64 [rotary_dim / 2], turns per position times 2^64 (se_rotary_frequencies);
+ *   positions: int32 [num_tokens], as se_block_tables_extend writes them;
+ *   num_valid: int32 (4-byte aligned) or NULL: rows at and behind *num_valid are left as they are
+ *     (token_start + batch of se_block_tables_extend: the padded end of a batch). Rows with a negative
+ *     position are left as they are too.
+ * head_dim: a multiple of 8 up to 576; rotary_offset and rotary_dim: multiples of 8, rotary_dim >= 8,
+ * within head_dim; at most 1024 heads in all.
+ *
+ * se_rotary_frequencies (host) -- freqs of the angles p * w_i, w_i = base^(-2 i / rotary_dim) radians
+ * per position, or scaled for contexts `factor` times as long as the ones trained for:
+ *   SE_ROTARY_SCALING_NONE: w_i;   SE_ROTARY_SCALING_LINEAR: w_i / factor;
+ *   SE_ROTARY_SCALING_NTK: base replaced by base * factor^(rotary_dim / (rotary_dim - 2)) (rotary_dim > 2);
+ *   SE_ROTARY_SCALING_YARN: w_i g + w_i / factor (1 - g), g = clamp((turns - 1) / (32 - 1), 0, 1) with
+ *     turns = original_len * w_i / (2 pi), and *amplitude = 0.1 ln(factor) + 1 (1 otherwise).
+ *   freqs: uint64 [rotary_dim / 2] on the host; amplitude: float on the host.
+ * rotary_dim: a positive multiple of 2; base > 1; factor >= 1; original_len > 0 for YARN. Computed in
+ * 64-bit floating point.
+ */
+#define SE_ROTARY_INTERLEAVED 0x1u
+#define SE_ROTARY_INVERSE     0x2u
+#define SE_ROTARY_SCALING_NONE   0
+#define SE_ROTARY_SCALING_LINEAR 1
+#define SE_ROTARY_SCALING_NTK    2
+#define SE_ROTARY_SCALING_YARN   3
+SE_API se_status_t se_rotary_frequencies(int32_t rotary_dim, double base, int32_t scaling, double factor,
+                                         int32_t original_len, uint64_t* freqs, float* amplitude);
+SE_API se_status_t se_rotary(const void* q, int64_t q_stride, int32_t num_q_heads, const void* k, int64_t k_stride,
+                             int32_t num_kv_heads, int32_t head_dim, int32_t rotary_offset, int32_t rotary_dim,
+                             uint32_t flags, const uint64_t* freqs, float amplitude, const int32_t* positions,
+                             const int32_t* num_valid, int32_t num_tokens, void* q_out, int64_t q_out_stride,
+                             void* k_out, int64_t k_out_stride, void* stream);
+
+/*
+ * Paged KV cache view in 8 bits. A value is code * scale: the codes are e4m3 (1-4-3, bias 7, no infinity,
+ * largest 448), and the 16 tokens of a page share a scale for each KV head, K and V apart. Token slot t of
+ * (physical page p, KV head h) starts at byte ((p * num_kv_heads + h) * 16 + t) * head_dim of `k` (resp. `v`); its
+ * scale is k_scale[p * num_kv_heads + h]. The pool, block tables, slot maps and positions are those of the bf16
+ * cache (se_block_tables_extend, se_block_tables_release).
+ */
+typedef struct {
+  void* k;                 /* e4m3 [num_pages][num_kv_heads][16][head_dim] */
+  void* v;
+  float* k_scale;          /* fp32 [num_pages][num_kv_heads] */
+  float* v_scale;
+  int32_t num_pages;
+  int32_t num_kv_heads;
+  int32_t page_size;       /* must be 16 */
+  int32_t head_dim;        /* 64, 128 or 256, K and V alike */
+} se_paged_kv8_t;
+
+/*
+ * se_paged_kv8_store -- se_paged_kv_store for a cache in 8 bits: the K and V rows of a ragged batch of new
+ * tokens quantised into their slots.
+ * The new tokens of one page (they stand next to each other in the batch) and one KV head, K and V apart: with
+ * amax the largest finite magnitude of their rows,
+ *     need = the least power of two s with amax <= 448 s, no less than 2^-100,
+ *     scale = need when slot 0 of the page is among them, otherwise max(need, the page's present scale),
+ *     code = x / scale rounded to nearest even (fp32: x times the scale's reciprocal).
+ * Where a page takes a scale other than its present one and slot 0 is not among the new tokens, the codes of its
+ * other slots are moved to it, code * (old / new) rounded to nearest even: exact for powers of two but for values that
+ * fall below 2^-6 of the new scale. So a page's scale only grows while it fills, and a page filled token by
+ * token holds (but for those small values) what it holds filled at once.
+ * NaN and infinities are stored as NaN and do not count for amax.
+ *   k_new, v_new: bf16 rows and strides as se_paged_kv_store's; slot_map: as there (negative: padding, skipped).
+ * A slot is named once; a slot named twice in neighbouring tokens of one page keeps the later row. A slot at or behind
+ * num_pages * 16 sets SE_DEVERR_PAGE_RANGE and is skipped.
+ */
+SE_API se_status_t se_paged_kv8_store(const se_paged_kv8_t* kv, const void* k_new, int64_t k_stride,
+                                      const void* v_new, int64_t v_stride, const int32_t* slot_map,
+                                      int32_t num_tokens, void* stream);
+
+/*
+ * se_paged_kv8_load -- rows of an 8-bit cache back as bf16 (code * scale, rounded to nearest even: exact where the
+ * scale is a power of two within bf16's range), request after request: for a prompt's next chunk, or for a move into
+ * a bf16 cache.
+ * Row t with token_start[b] <= t < token_start[b + 1] is position first[b] + t - token_start[b] of request b (first
+ * NULL: 0), read from page block_table[b][position / 16].
+ *   token_start: int32 [batch + 1], ascending from 0 (an exclusive prefix sum, as se_block_tables_extend writes it);
+ *   num_rows: rows that the outputs hold (host); rows at and behind min(token_start[batch], num_rows) are left
+ *     as they are;
+ *   k_out, v_out: bf16, the row of KV head h at k_out + t * k_stride + h * head_dim (elements; strides multiples
+ *     of 8, at least num_kv_heads * head_dim).
+ * A position outside [0, 16 * bt_stride) sets SE_DEVERR_LENGTH, a page id out of range SE_DEVERR_PAGE_RANGE; such rows
+ * are left as they are. batch <= 16384.
+ */
+SE_API se_status_t se_paged_kv8_load(const se_paged_kv8_t* kv, const int32_t* block_table, int32_t bt_stride,
+                                     const int32_t* first, const int32_t* token_start, int32_t batch,
+                                     int32_t num_rows, void* k_out, int64_t k_stride, void* v_out, int64_t v_stride,
+                                     void* stream);
+
+/*
+ * se_paged_kv8_decode -- se_paged_decode over a cache in 8 bits: attention of one new token per request over its
+ * cached tokens, all of them or the first sink_tokens and the last recent_tokens, with k_j = code * scale and
+ * v_j alike. Same arguments, windows, errors, splitting and repeatability; half the bytes.
+ * Logits, maxima, sums, partial outputs and joins are fp32. A query row enters the products as two e4m3 numbers a
+ * dim, together within 2^-21 of the row's largest magnitude; a weight exp(z_j - max) meets its value row as fp16
+ * (half a step, 2^-11 of it), but not the sum that divides the output nor out_lse. A query row that holds
+ * an infinity or a NaN gives NaN.
+ * Shapes: head_dim 64, 128 or 256 with 1..64 query heads per KV head; batch <= 4096. Scales are positive and finite
+ * (those of pages that no kept token lies in are not read).
+ *   workspace: se_paged_kv8_decode_workspace_size bytes (0: not supported), zero-filled before its first use. It
+ *     may be shared with se_paged_decode calls that do not overlap on the GPU.
+ */
+SE_API size_t se_paged_kv8_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                                 int32_t head_dim);
+SE_API se_status_t se_paged_kv8_decode(const se_paged_kv8_t* kv, const void* q, int64_t q_stride, int32_t num_q_heads,
+                                       const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
+                                       int32_t batch, int32_t sink_tokens, int32_t recent_tokens, float sm_scale,
+                                       void* out, float* out_lse, void* workspace, size_t workspace_bytes,
+                                       void* stream);
 
 /*
  * SnapKV eviction at the end of prefill (SparseEngine: Sparse-First Inference

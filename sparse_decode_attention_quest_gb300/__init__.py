@@ -29,7 +29,9 @@ __all__ = [
     "se_snapkv_compact", "se_snapkv_score_and_compact", "se_snapkv_select_windowed",
     "se_snapkv_score_and_compact_windowed", "se_debug_snapkv_wait_probe", "SEGraph", "se_capture_begin",
     "se_capture_end", "se_block_tables_extend", "se_block_tables_release", "se_block_tables_release_ex", "se_paged_kv_store",
-    "se_paged_decode_workspace_size", "se_paged_decode", "exported_symbols",
+    "se_paged_decode_workspace_size", "se_paged_decode", "ROTARY_SCALINGS", "se_rotary_frequencies", "se_rotary",
+    "SEPagedKV8", "paged_kv8", "se_paged_kv8_store", "se_paged_kv8_load", "se_paged_kv8_decode_workspace_size",
+    "se_paged_kv8_decode", "exported_symbols",
 ]
 
 SE_OK = 0
@@ -37,6 +39,7 @@ DEVERR_PAGE_RANGE = 0x1
 DEVERR_LENGTH = 0x2
 DEVERR_WAIT_TIMEOUT = 0x4
 DEVERR_NO_PAGES = 0x8
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 APPEND_OVERLAP_PREVIOUS = 0x1  # se_quest_update_summaries_ex: may run alongside the previous kernel
 
 
@@ -55,12 +58,22 @@ class SEPagedKV(ctypes.Structure):
                 ("row_stride_v", ctypes.c_int32)]
 
 
+class SEPagedKV8(ctypes.Structure):
+    """Mirror of se_paged_kv8_t."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _F = ctypes.c_float
 _Z = ctypes.c_size_t
 _L = ctypes.c_int64
+_U = ctypes.c_uint32
+_D = ctypes.c_double
 _KV = ctypes.POINTER(SEPagedKV)
+_KV8 = ctypes.POINTER(SEPagedKV8)
 
 _SIGNATURES = {
     "se_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -92,6 +105,12 @@ _SIGNATURES = {
     "se_paged_kv_store": (ctypes.c_int, [_KV, _P, _L, _P, _L, _P, _I, _P]),
     "se_paged_decode_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
     "se_paged_decode": (ctypes.c_int, [_KV, _P, _L, _I, _P, _I, _P, _I, _I, _I, _F, _P, _P, _P, _Z, _P]),
+    "se_rotary_frequencies": (ctypes.c_int, [_I, _D, _I, _D, _I, _P, _P]),
+    "se_rotary": (ctypes.c_int, [_P, _L, _I, _P, _L, _I, _I, _I, _I, _U, _P, _F, _P, _P, _I, _P, _L, _P, _L, _P]),
+    "se_paged_kv8_store": (ctypes.c_int, [_KV8, _P, _L, _P, _L, _P, _I, _P]),
+    "se_paged_kv8_load": (ctypes.c_int, [_KV8, _P, _I, _P, _P, _I, _I, _P, _L, _P, _L, _P]),
+    "se_paged_kv8_decode_workspace_size": (_Z, [_I, _I, _I, _I]),
+    "se_paged_kv8_decode": (ctypes.c_int, [_KV8, _P, _L, _I, _P, _I, _P, _I, _I, _I, _F, _P, _P, _P, _Z, _P]),
     "se_snapkv_workspace_size": (_Z, [_I, _I, _I, _I]),
     "se_snapkv_window_scores": (ctypes.c_int, [_KV, _P, _I, _I, _P, _I, _P, _I, _I, _F, _P, _I, _P, _P, _Z, _P]),
     "se_snapkv_select": (ctypes.c_int, [_P, _I, _P, _I, _I, _I, _I, _I, _I, _P, _I, _P, _P]),
@@ -542,6 +561,145 @@ def se_paged_decode(kv: SEPagedKV, q, block_table, seq_lens, sm_scale: float, ou
     _check(lib.se_paged_decode(
         _cache(kv, dev), qp, qs, hq, table, width, _vec(seq_lens, batch, torch.int32, "seq_lens", dev), batch,
         sink_tokens, recent_tokens, sm_scale, _vec(out, batch * hq * kv.head_dim_v, torch.bfloat16, "out", dev),
+        None if out_lse is None else _vec(out_lse, batch * hq, torch.float32, "out_lse", dev),
+        None if workspace is None else _arg(workspace, torch.uint8, "workspace", dev),
+        0 if workspace is None else workspace.numel(), _stream(stream, dev)))
+
+
+# ------------------------------------------- rotary positions, the cache in 8 bits
+def se_rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                          original_len: int = 0):
+    """(freqs, amplitude) for se_rotary: turns per position of each pair of dims times 2^64, as the bits of an int64
+    CPU tensor [rotary_dim / 2], and what the cosines and sines are multiplied by. ``scaling``: "none", "linear",
+    "ntk" or "yarn" (ROTARY_SCALINGS), for contexts ``factor`` times as long as the ``original_len`` trained for."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling: expected one of {', '.join(ROTARY_SCALINGS)}, got {scaling!r}")
+    freqs = torch.zeros(max(int(rotary_dim) // 2, 1), dtype=torch.int64)
+    amplitude = _F(0.0)
+    _check(load_library().se_rotary_frequencies(int(rotary_dim), float(base), ROTARY_SCALINGS[scaling], float(factor),
+                                                int(original_len), freqs.data_ptr(), ctypes.byref(amplitude)))
+    return freqs, amplitude.value
+
+
+def _rotary_side(x, out, name: str, tokens: int, dev: int):
+    """(rows, stride, heads, output, its stride) of the queries or keys of se_rotary."""
+    if x is None:
+        if out is not None:
+            raise ValueError(f"{name}_out: without {name}")
+        return None, 0, 0, None, 0
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError(f"{name}: expected [tokens][heads][head_dim]")
+    heads, dim = x.shape[1], x.shape[2]
+    if x.shape[0] != tokens:
+        raise ValueError(f"{name}: expected {tokens} rows, got {x.shape[0]}")
+    p, stride = _rows_ptr(x, heads, dim, torch.bfloat16, name, dev)
+    if out is None or out is x:
+        return p, stride, heads, p, stride
+    po, so = _rows_ptr(out, heads, dim, torch.bfloat16, name + "_out", dev)
+    if out.shape[0] != tokens:
+        raise ValueError(f"{name}_out: expected {tokens} rows, got {out.shape[0]}")
+    return p, stride, heads, po, so
+
+
+def se_rotary(q, k, positions, freqs, q_out=None, k_out=None, rotary_offset: int = 0, interleaved: bool = False,
+              inverse: bool = False, amplitude: float = 1.0, num_valid=None, stream=None):
+    """q [T][Hq][D] and k [T][Hkv][D] (tokens any stride apart; one of them may be None) turned by positions [T], over
+    the 2 freqs.numel() dims from ``rotary_offset`` on; in place where no output is given. ``freqs`` and ``amplitude``:
+    se_rotary_frequencies (freqs on the device). ``num_valid`` (int32 [1] on the device): rows behind it are left."""
+    lib, dev = load_library(), torch.cuda.current_device()
+    pp = _arg(positions, torch.int32, "positions", dev)
+    tokens = positions.numel()
+    qp, qs, hq, qo, qos = _rotary_side(q, q_out, "q", tokens, dev)
+    kp, ks, hk, ko, kos = _rotary_side(k, k_out, "k", tokens, dev)
+    if q is None and k is None:
+        raise ValueError("q, k: neither is given")
+    dim = (k if q is None else q).shape[2]
+    if q is not None and k is not None and k.shape[2] != dim:
+        raise ValueError(f"k: expected rows of {dim} dims, got {k.shape[2]}")
+    _check(lib.se_rotary(qp, qs, hq, kp, ks, hk, dim, rotary_offset, 2 * freqs.numel(),
+                         (1 if interleaved else 0) | (2 if inverse else 0), _arg(freqs, torch.int64, "freqs", dev),
+                         amplitude, pp, None if num_valid is None else _vec(num_valid, 1, torch.int32, "num_valid", dev),
+                         tokens, qo, qos, ko, kos, _stream(stream, dev)))
+
+
+def paged_kv8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+              v_scale: torch.Tensor) -> SEPagedKV8:
+    """se_paged_kv8_t for float8_e4m3fn caches [P][Hkv][16][D] and their fp32 scales [P][Hkv]. ``.device`` of the
+    result is their CUDA device's index."""
+    _ptr(k_cache, torch.float8_e4m3fn, "k_cache")
+    if k_cache.dim() != 4 or k_cache.shape[2] != 16:
+        raise ValueError("k_cache: expected [pages][heads][16][head_dim]")
+    P, H, ps, D = k_cache.shape
+    for t, name, shape, dtype in ((v_cache, "v_cache", (P, H, ps, D), torch.float8_e4m3fn),
+                                  (k_scale, "k_scale", (P, H), torch.float32),
+                                  (v_scale, "v_scale", (P, H), torch.float32)):
+        if t is None:
+            raise TypeError(f"{name}: expected a torch.Tensor")
+        _ptr(t, dtype, name)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
+        if t.get_device() != k_cache.get_device():
+            raise ValueError(f"{name}: is on cuda:{t.get_device()}, k_cache on cuda:{k_cache.get_device()}")
+    kv = SEPagedKV8(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, H, ps, D)
+    kv.device = k_cache.get_device()
+    return kv
+
+
+def _cache8(kv, dev: int):
+    if not isinstance(kv, SEPagedKV8):
+        raise TypeError("kv: expected an 8-bit cache view (paged_kv8)")
+    return _cache(kv, dev)
+
+
+def se_paged_kv8_store(kv: SEPagedKV8, k_new, v_new, slot_map, stream=None):
+    """The bf16 rows k_new and v_new [T][Hkv][D] (tokens any stride apart) of slot_map.numel() new tokens quantised
+    into their slots, and the scales of the pages they touch."""
+    lib, dev = load_library(), torch.cuda.current_device()
+    view, tokens = _cache8(kv, dev), slot_map.numel()
+    kp, ks = _rows_ptr(k_new, kv.num_kv_heads, kv.head_dim, torch.bfloat16, "k_new", dev)
+    vp, vs = _rows_ptr(v_new, kv.num_kv_heads, kv.head_dim, torch.bfloat16, "v_new", dev)
+    if k_new.shape[0] != tokens or v_new.shape[0] != tokens:
+        raise ValueError("k_new, v_new and slot_map differ in tokens")
+    _check(lib.se_paged_kv8_store(view, kp, ks, vp, vs, _arg(slot_map, torch.int32, "slot_map", dev), tokens,
+                                  _stream(stream, dev)))
+
+
+def se_paged_kv8_load(kv: SEPagedKV8, block_table, token_start, k_out, v_out, first=None, stream=None):
+    """Rows of the cache back as bf16 into k_out and v_out [T][Hkv][D] (rows any stride apart): request b's positions
+    from first[b] (None: 0) on at rows token_start[b] .. token_start[b + 1] - 1; rows behind the last are left."""
+    lib, dev, i32 = load_library(), torch.cuda.current_device(), torch.int32
+    view = _cache8(kv, dev)
+    table, batch, width = _table(block_table, "block_table", dev)
+    kp, ks = _rows_ptr(k_out, kv.num_kv_heads, kv.head_dim, torch.bfloat16, "k_out", dev)
+    vp, vs = _rows_ptr(v_out, kv.num_kv_heads, kv.head_dim, torch.bfloat16, "v_out", dev)
+    if k_out.shape[0] != v_out.shape[0]:
+        raise ValueError("k_out and v_out differ in rows")
+    _check(lib.se_paged_kv8_load(view, table, width, None if first is None else _vec(first, batch, i32, "first", dev),
+                                 _vec(token_start, batch + 1, i32, "token_start", dev), batch, k_out.shape[0], kp, ks,
+                                 vp, vs, _stream(stream, dev)))
+
+
+def se_paged_kv8_decode_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    """Bytes of se_paged_kv8_decode's workspace, whatever the lengths (0: shape not supported)."""
+    return int(load_library().se_paged_kv8_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim))
+
+
+def se_paged_kv8_decode(kv: SEPagedKV8, q, block_table, seq_lens, sm_scale: float, out, out_lse, workspace,
+                        sink_tokens: int = 0, recent_tokens: int = 0, stream=None):
+    """se_paged_decode over a cache in 8 bits: q [B][Hq][D] (requests any stride apart) -> out [B][Hq][D] in bf16,
+    out_lse [B][Hq] or None. ``workspace``: uint8, zeroed once."""
+    lib, dev = load_library(), torch.cuda.current_device()
+    view = _cache8(kv, dev)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q: expected [batch][num_q_heads][head_dim]")
+    batch, hq = q.shape[0], q.shape[1]
+    qp, qs = _rows_ptr(q, hq, kv.head_dim, torch.bfloat16, "q", dev)
+    table, rows, width = _table(block_table, "block_table", dev)
+    if rows != batch:
+        raise ValueError(f"block_table: expected {batch} rows, got {rows}")
+    _check(lib.se_paged_kv8_decode(
+        view, qp, qs, hq, table, width, _vec(seq_lens, batch, torch.int32, "seq_lens", dev), batch, sink_tokens,
+        recent_tokens, sm_scale, _vec(out, batch * hq * kv.head_dim, torch.bfloat16, "out", dev),
         None if out_lse is None else _vec(out_lse, batch * hq, torch.float32, "out_lse", dev),
         None if workspace is None else _arg(workspace, torch.uint8, "workspace", dev),
         0 if workspace is None else workspace.numel(), _stream(stream, dev)))

@@ -20,7 +20,7 @@ LIB_NAME = "libsparse_engine.so"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "quest_summary.cu", "quest_score.cu", "quest_topk.cu", "sparse_decode.cu", "mla_decode.cu", "quest_fused.cu",
            "decode_noalloc.cu", "snapkv.cu", "graph.cu", "block_tables.cu", "kv_store.cu", "paged_decode.cu",
-           "latent_decode.cu"]
+           "latent_decode.cu", "rotary.cu", "kv8_store.cu", "kv8_decode.cu"]
 
 
 def _nvcc():

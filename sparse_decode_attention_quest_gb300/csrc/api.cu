@@ -109,6 +109,22 @@ bool encode_row_chunks_map(CUtensorMap* map, const void* base, long long rows, i
   return r == CUDA_SUCCESS;
 }
 
+// 3-D view of an 8-bit cache of `rows` rows of `dim` bytes as (128 bytes, line, 128-byte chunk of a row): a line is a
+// row, or two rows of 64. Boxes of box_rows rows, every chunk, into [chunk][line][128 bytes] with 128-byte swizzle.
+bool encode_byte_rows_map(CUtensorMap* map, const void* base, long long rows, int dim, int box_rows) {
+  auto fn = encode_tiled();
+  if (!fn) return false;
+  const int per_line = dim < 128 ? 128 / dim : 1, chunks = dim < 128 ? 1 : dim / 128;
+  cuuint64_t dims[3] = {128, (cuuint64_t)(rows / per_line), (cuuint64_t)chunks};
+  cuuint64_t strides[2] = {(cuuint64_t)(dim * per_line), 128};
+  cuuint32_t box[3] = {128, (cuuint32_t)(box_rows / per_line), (cuuint32_t)chunks};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // 4-D view of SnapKV window queries bf16 [batch][window][num_q_heads][128]: boxes of
 // 64 dims x `group` heads x `window` positions x 1 request (128-byte swizzle), so one
 // box holds a KV head's window rows r = w * group + g for 64 of the dims.
@@ -183,6 +199,29 @@ KvView view_of(const se_paged_kv_t* kv) {
   v.row_stride_k = kv->row_stride_k;
   v.row_stride_v = kv->row_stride_v;
   return v;
+}
+
+// Checks of an 8-bit cache view.
+se_status_t check_kv8(const char* fn, const se_paged_kv8_t* kv) {
+  if (!kv) return fail(SE_ERR_INVALID_ARG, fn, "kv is NULL");
+  if (!kv->k || !kv->v || !kv->k_scale || !kv->v_scale)
+    return fail(SE_ERR_INVALID_ARG, fn, "kv->k / v / k_scale / v_scale is NULL");
+  if (!aligned16(kv->k) || !aligned16(kv->v) || !aligned16(kv->k_scale) || !aligned16(kv->v_scale))
+    return fail(SE_ERR_INVALID_ARG, fn, "cache pointers must be 16-byte aligned");
+  if (kv->k == kv->v || kv->k_scale == kv->v_scale)
+    return fail(SE_ERR_INVALID_ARG, fn, "K and V must not share memory");
+  if (kv->page_size != se::kPageSize) return fail(SE_ERR_INVALID_ARG, fn, "page_size must be 16");
+  if (kv->num_pages < 0 || kv->num_kv_heads < 1) return fail(SE_ERR_INVALID_ARG, fn, "bad num_pages/num_kv_heads");
+  if (kv->head_dim != 64 && kv->head_dim != 128 && kv->head_dim != 256)
+    return fail(SE_ERR_UNSUPPORTED, fn, "head_dim must be 64, 128 or 256");
+  if ((long long)kv->num_pages * kv->num_kv_heads * se::kPageSize >= (1ll << 31))
+    return fail(SE_ERR_UNSUPPORTED, fn, "cache holds 2^31 or more token rows");
+  return SE_OK;
+}
+
+se::Kv8View view_of(const se_paged_kv8_t* kv) {
+  return {static_cast<uint8_t*>(kv->k), static_cast<uint8_t*>(kv->v), kv->k_scale, kv->v_scale, kv->num_pages,
+          kv->num_kv_heads, kv->head_dim};
 }
 
 size_t round16(size_t x) { return (x + 15) & ~size_t(15); }
@@ -939,6 +978,190 @@ se_status_t se_paged_decode(const se_paged_kv_t* kv, const void* q, int64_t q_st
                               block_table, bt_stride, seq_lens, batch, sink_tokens, recent_tokens, sm_scale,
                               static_cast<uint16_t*>(out), out_lse, workspace, d->sm_count, d->err,
                               static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SE_OK : cuda_fail(fn, e);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------ rotary positions, the cache in 8 bits
+extern "C" {
+
+se_status_t se_rotary_frequencies(int32_t rotary_dim, double base, int32_t scaling, double factor, int32_t original_len,
+                                  uint64_t* freqs, float* amplitude) {
+  static const char* fn = "se_rotary_frequencies";
+  if (rotary_dim < 2 || (rotary_dim % 2)) return fail(SE_ERR_INVALID_ARG, fn, "rotary_dim must be a positive multiple of 2");
+  if (!freqs || !amplitude) return fail(SE_ERR_INVALID_ARG, fn, "freqs/amplitude NULL");
+  if (!std::isfinite(base) || base <= 1.0) return fail(SE_ERR_INVALID_ARG, fn, "base must be above 1");
+  if (scaling < SE_ROTARY_SCALING_NONE || scaling > SE_ROTARY_SCALING_YARN)
+    return fail(SE_ERR_INVALID_ARG, fn, "unknown scaling");
+  if (!std::isfinite(factor) || factor < 1.0) return fail(SE_ERR_INVALID_ARG, fn, "factor must be at least 1");
+  if (scaling == SE_ROTARY_SCALING_YARN && original_len < 1)
+    return fail(SE_ERR_INVALID_ARG, fn, "original_len must be positive");
+  constexpr double kTwoPi = 6.283185307179586476925;
+  const double r = rotary_dim;
+  if (scaling == SE_ROTARY_SCALING_NTK && rotary_dim > 2) base *= std::pow(factor, r / (r - 2.0));
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    double w = std::pow(base, -2.0 * i / r);
+    if (scaling == SE_ROTARY_SCALING_LINEAR) w /= factor;
+    if (scaling == SE_ROTARY_SCALING_YARN) {
+      const double g = std::min(1.0, std::max(0.0, (original_len * w / kTwoPi - 1.0) / 31.0));
+      w = w * g + w / factor * (1.0 - g);
+    }
+    // Turns per position below 1/6 as a fraction of 2^64, to the nearest (the product is exact).
+    freqs[i] = (uint64_t)std::nearbyint(std::ldexp(w / kTwoPi, 64));
+  }
+  *amplitude = scaling == SE_ROTARY_SCALING_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+  return SE_OK;
+}
+
+se_status_t se_rotary(const void* q, int64_t q_stride, int32_t num_q_heads, const void* k, int64_t k_stride,
+                      int32_t num_kv_heads, int32_t head_dim, int32_t rotary_offset, int32_t rotary_dim, uint32_t flags,
+                      const uint64_t* freqs, float amplitude, const int32_t* positions, const int32_t* num_valid,
+                      int32_t num_tokens, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                      void* stream) {
+  static const char* fn = "se_rotary";
+  if (flags & ~(uint32_t)(SE_ROTARY_INTERLEAVED | SE_ROTARY_INVERSE)) return fail(SE_ERR_INVALID_ARG, fn, "unknown flags");
+  if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads < 0) return fail(SE_ERR_INVALID_ARG, fn, "negative size");
+  if (num_q_heads + (long long)num_kv_heads < 1) return fail(SE_ERR_INVALID_ARG, fn, "no heads");
+  if (num_q_heads + (long long)num_kv_heads > 1024) return fail(SE_ERR_UNSUPPORTED, fn, "more than 1024 heads");
+  if (head_dim < 8 || (head_dim % 8)) return fail(SE_ERR_INVALID_ARG, fn, "head_dim must be a positive multiple of 8");
+  if (head_dim > 576) return fail(SE_ERR_UNSUPPORTED, fn, "head_dim up to 576");
+  if (rotary_dim < 8 || (rotary_dim % 8) || rotary_offset < 0 || (rotary_offset % 8) ||
+      rotary_offset > head_dim - rotary_dim)
+    return fail(SE_ERR_INVALID_ARG, fn, "rotary_offset and rotary_dim must be multiples of 8 within head_dim");
+  if (!std::isfinite(amplitude)) return fail(SE_ERR_INVALID_ARG, fn, "amplitude not finite");
+  if (num_tokens == 0) return SE_OK;
+  const struct {
+    const void* in;
+    int64_t in_stride;
+    int32_t heads;
+    const void* out;
+    int64_t out_stride;
+  } side[2] = {{q, q_stride, num_q_heads, q_out, q_out_stride}, {k, k_stride, num_kv_heads, k_out, k_out_stride}};
+  for (const auto& s : side) {
+    if (s.heads == 0) {
+      if (s.in || s.out) return fail(SE_ERR_INVALID_ARG, fn, "rows without heads");
+      continue;
+    }
+    if (!s.in || !s.out) return fail(SE_ERR_INVALID_ARG, fn, "NULL pointer");
+    if (!aligned16(s.in) || !aligned16(s.out)) return fail(SE_ERR_INVALID_ARG, fn, "pointers must be 16-byte aligned");
+    const int64_t least = (int64_t)s.heads * head_dim;
+    if (s.in_stride < least || s.out_stride < least || (s.in_stride % 8) || (s.out_stride % 8))
+      return fail(SE_ERR_INVALID_ARG, fn, "token strides must cover the heads' rows and be multiples of 8");
+    if (s.in == s.out && s.in_stride != s.out_stride)
+      return fail(SE_ERR_INVALID_ARG, fn, "in place, both strides must be the same");
+  }
+  if (!freqs || !positions) return fail(SE_ERR_INVALID_ARG, fn, "freqs/positions NULL");
+  if (!aligned16(freqs) || !aligned16(positions)) return fail(SE_ERR_INVALID_ARG, fn, "pointers must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(num_valid) & 3u) return fail(SE_ERR_INVALID_ARG, fn, "num_valid not 4-byte aligned");
+  DeviceInfo* d = nullptr;
+  cudaError_t e = current_device(&d);
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  e = se::launch_rotary(static_cast<const uint16_t*>(q), q_stride, num_q_heads, static_cast<const uint16_t*>(k),
+                        k_stride, num_kv_heads, head_dim, rotary_offset, rotary_dim, flags & SE_ROTARY_INTERLEAVED,
+                        flags & SE_ROTARY_INVERSE, freqs, amplitude, positions, num_valid, num_tokens,
+                        static_cast<uint16_t*>(q_out), q_out_stride, static_cast<uint16_t*>(k_out), k_out_stride,
+                        d->sm_count, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SE_OK : cuda_fail(fn, e);
+}
+
+se_status_t se_paged_kv8_store(const se_paged_kv8_t* kv, const void* k_new, int64_t k_stride, const void* v_new,
+                               int64_t v_stride, const int32_t* slot_map, int32_t num_tokens, void* stream) {
+  static const char* fn = "se_paged_kv8_store";
+  const se_status_t st = check_kv8(fn, kv);
+  if (st != SE_OK) return st;
+  if (num_tokens < 0) return fail(SE_ERR_INVALID_ARG, fn, "num_tokens < 0");
+  if (num_tokens == 0) return SE_OK;
+  if (!k_new || !v_new || !slot_map) return fail(SE_ERR_INVALID_ARG, fn, "k_new/v_new/slot_map NULL");
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(slot_map))
+    return fail(SE_ERR_INVALID_ARG, fn, "pointers must be 16-byte aligned");
+  const int64_t least = (int64_t)kv->num_kv_heads * kv->head_dim;
+  if (k_stride < least || v_stride < least || (k_stride % 8) || (v_stride % 8))
+    return fail(SE_ERR_INVALID_ARG, fn, "token strides must cover the heads' rows and be multiples of 8");
+  DeviceInfo* d = nullptr;
+  cudaError_t e = current_device(&d);
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  e = se::launch_kv8_store(view_of(kv), static_cast<const uint16_t*>(k_new), k_stride,
+                           static_cast<const uint16_t*>(v_new), v_stride, slot_map, num_tokens, d->sm_count, d->err,
+                           static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SE_OK : cuda_fail(fn, e);
+}
+
+se_status_t se_paged_kv8_load(const se_paged_kv8_t* kv, const int32_t* block_table, int32_t bt_stride,
+                              const int32_t* first, const int32_t* token_start, int32_t batch, int32_t num_rows,
+                              void* k_out, int64_t k_stride, void* v_out, int64_t v_stride, void* stream) {
+  static const char* fn = "se_paged_kv8_load";
+  const se_status_t st = check_kv8(fn, kv);
+  if (st != SE_OK) return st;
+  if (batch < 0 || num_rows < 0 || bt_stride < 1)
+    return fail(SE_ERR_INVALID_ARG, fn, "negative size or bt_stride < 1");
+  if (batch > 16384) return fail(SE_ERR_UNSUPPORTED, fn, "batch > 16384");
+  if (bt_stride >= (1 << 27)) return fail(SE_ERR_UNSUPPORTED, fn, "2^27 or more pages per request");
+  if (batch == 0 || num_rows == 0) return SE_OK;
+  if (!block_table || !token_start || !k_out || !v_out) return fail(SE_ERR_INVALID_ARG, fn, "NULL pointer");
+  if (!aligned16(block_table) || !aligned16(first) || !aligned16(token_start) || !aligned16(k_out) || !aligned16(v_out))
+    return fail(SE_ERR_INVALID_ARG, fn, "pointers must be 16-byte aligned");
+  const int64_t least = (int64_t)kv->num_kv_heads * kv->head_dim;
+  if (k_stride < least || v_stride < least || (k_stride % 8) || (v_stride % 8))
+    return fail(SE_ERR_INVALID_ARG, fn, "row strides must cover the heads' rows and be multiples of 8");
+  DeviceInfo* d = nullptr;
+  cudaError_t e = current_device(&d);
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  e = se::launch_kv8_load(view_of(kv), block_table, bt_stride, first, token_start, batch, num_rows,
+                          static_cast<uint16_t*>(k_out), k_stride, static_cast<uint16_t*>(v_out), v_stride,
+                          d->sm_count, d->err, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SE_OK : cuda_fail(fn, e);
+}
+
+size_t se_paged_kv8_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
+  if (batch < 0 || num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads) return 0;
+  if (!se::kv8_decode_supported(num_kv_heads, head_dim, num_q_heads) || batch > se::kv8_decode_max_batch()) return 0;
+  return round16(se::kv8_decode_workspace_bytes(num_q_heads, num_kv_heads, head_dim));
+}
+
+se_status_t se_paged_kv8_decode(const se_paged_kv8_t* kv, const void* q, int64_t q_stride, int32_t num_q_heads,
+                                const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens, int32_t batch,
+                                int32_t sink_tokens, int32_t recent_tokens, float sm_scale, void* out, float* out_lse,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  static const char* fn = "se_paged_kv8_decode";
+  const se_status_t st = check_kv8(fn, kv);
+  if (st != SE_OK) return st;
+  if (batch < 0) return fail(SE_ERR_INVALID_ARG, fn, "batch < 0");
+  if (num_q_heads < 1 || num_q_heads % kv->num_kv_heads)
+    return fail(SE_ERR_INVALID_ARG, fn, "num_q_heads must be a positive multiple of num_kv_heads");
+  if (!se::kv8_decode_supported(kv->num_kv_heads, kv->head_dim, num_q_heads))
+    return fail(SE_ERR_UNSUPPORTED, fn, "more than 64 query heads per KV head");
+  if (sink_tokens < 0 || recent_tokens < 0) return fail(SE_ERR_INVALID_ARG, fn, "negative window");
+  if (sink_tokens > 0 && recent_tokens == 0)
+    return fail(SE_ERR_INVALID_ARG, fn, "sink_tokens without recent_tokens (0 keeps every token)");
+  if (!std::isfinite(sm_scale)) return fail(SE_ERR_INVALID_ARG, fn, "sm_scale not finite");
+  if (q_stride < (int64_t)num_q_heads * kv->head_dim || (q_stride % 8))
+    return fail(SE_ERR_INVALID_ARG, fn, "q_stride must cover the heads and be a multiple of 8");
+  if (bt_stride < 1) return fail(SE_ERR_INVALID_ARG, fn, "bt_stride < 1");
+  if (bt_stride >= (1 << 27)) return fail(SE_ERR_UNSUPPORTED, fn, "2^27 or more pages per request");
+  if (batch > se::kv8_decode_max_batch()) return fail(SE_ERR_UNSUPPORTED, fn, "batch > 4096");
+  if (batch == 0) return SE_OK;
+  if (!q || !block_table || !seq_lens || !out) return fail(SE_ERR_INVALID_ARG, fn, "NULL pointer");
+  if (!aligned16(q) || !aligned16(block_table) || !aligned16(seq_lens) || !aligned16(out) || !aligned16(out_lse) ||
+      !aligned16(workspace))
+    return fail(SE_ERR_INVALID_ARG, fn, "pointers must be 16-byte aligned");
+  if (workspace_bytes < se::kv8_decode_workspace_bytes(num_q_heads, kv->num_kv_heads, kv->head_dim))
+    return fail(SE_ERR_WORKSPACE, fn, "workspace too small");
+  if (!workspace) return fail(SE_ERR_INVALID_ARG, fn, "workspace NULL");
+  DeviceInfo* d = nullptr;
+  cudaError_t e = current_device(&d);
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  const long long rows = (long long)std::max(1, kv->num_pages) * kv->num_kv_heads * se::kPageSize;
+  const int box = se::kPageSize * se::kv8_decode_box_heads(kv->num_kv_heads, num_q_heads, kv->head_dim, bt_stride,
+                                                           sink_tokens, recent_tokens, d->sm_count);
+  CUtensorMap kmap, vmap;
+  if (!encode_byte_rows_map(&kmap, kv->k, rows, kv->head_dim, box) ||
+      !encode_byte_rows_map(&vmap, kv->v, rows, kv->head_dim, box))
+    return fail(SE_ERR_CUDA, fn, "cuTensorMapEncodeTiled failed");
+  e = se::launch_kv8_decode(kmap, vmap, view_of(kv), static_cast<const uint16_t*>(q), q_stride, num_q_heads,
+                            block_table, bt_stride, seq_lens, batch, sink_tokens, recent_tokens, sm_scale,
+                            static_cast<uint16_t*>(out), out_lse, workspace, d->sm_count, d->err,
+                            static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SE_OK : cuda_fail(fn, e);
 }
 

@@ -1,0 +1,696 @@
+// Attention of one new token per request over its whole 8-bit paged cache, or over its
+// first sink and last recent tokens: se_paged_decode's computation with rows that are
+// e4m3 codes, 16 tokens of a page and one KV head to a scale:
+//
+//     z_j = sm_scale s_k(page of j) q . c_j over the kept positions j < L,
+//     out = sum_j exp(z_j - m) s_v(page of j) d_j / l,  l = sum_j exp(z_j - m),  lse = m + log l.
+//
+// The floor is the time of the codes from HBM, half that of the bf16 cache, and the
+// share-out of the work, the joins and the ring of TMA boxes are its (paged_decode.cu). What
+// differs is what has to happen to twice as many rows in the same time:
+//
+//  * K is not converted. S^T = K Q^T takes the codes as they lie, in m16n8k32 e4m3 MMAs, and the
+//    query row is split into two e4m3 numbers a dim instead: scaled by a power of two to at most
+//    448, high = rne(q), low = rne(16 (q - high)). A bf16 number has eight significant bits
+//    and a code four, so the two hold it exactly down to 2^-6 of the scale, and within 2^-21 of the
+//    row's largest magnitude below. Two accumulators, z = (high + low / 16) times the scales.
+//  * V is converted to fp16 (exact) on its way from shared memory. The 8 x 8 transposes of
+//    ldmatrix move pairs of codes, two dims of a token; a byte permutation and two conversions make
+//    of them the A operands of the even and of the odd dims, whose rows are then 2 g and 2 g + 1 of
+//    sixteen dims instead of g and g + 8: nothing but the epilogue sees it.
+//  * V's scales go into the weights before they are rounded to fp16. The output sums have a maximum of their own, of
+//    z_j + log2 s_v: a weight enters as exp2(z_j + log2 s_v - that + 14), at most 2^14, so that it is
+//    rounded by half a step of 2^-11 down to 2^-28 of the largest product of weight and scale, whatever the scales of
+//    pages that carry no weight. l keeps the maximum of z. One more exponential per logit.
+//  * Scales travel with their slot: a 4-byte asynchronous copy per (page, head) that arrives on the slot's barrier.
+//  * Rows that are not kept: their logits become -inf, and their value rows are
+//    zeroed in shared memory first, since 0 * NaN is not 0.
+#include <algorithm>
+
+#include "se_kv8.cuh"
+#include "se_paged_join.cuh"
+
+namespace se {
+namespace {
+
+constexpr int kSlotBytes = 32 * 1024;
+constexpr int kMetaRing = 4;     // steps whose page masks are held (at most three are in flight)
+constexpr int kMaxPages = 32;    // pages of a step
+constexpr int kMaxBatch = 4096;  // requests whose prefix fits beside the ring
+constexpr int kInlineBytes = 48 * 1024;  // partials of an item, in slices, where one CTA merges them
+constexpr int kInlineWidth = 32;          // pages of an item from which smaller boxes are taken for that
+
+constexpr float kWeightTop = 14.f;  // log2 of the largest weight that meets V
+
+template <int kD>
+struct Cfg {
+  static constexpr int kWarps = 8;  // consumers
+  static constexpr int kConsumers = kWarps * 32;
+  static constexpr int kThreads = kConsumers + 32;
+  static constexpr int kSlots = kD == 256 ? 4 : 5;
+  static constexpr int kBlocks = kSlotBytes / (kPageSize * kD);  // (page, head) blocks of a slot
+  static constexpr int kStageFloats = kWarps * 8 * kD;           // states handed over at a segment's end
+  static constexpr int kFixed = 1024 + kSlots * kSlotBytes + kStageFloats * 4 + kWarps * 16 * 4 +
+                                kMetaRing * kMaxPages * 4 + kSlots * kBlocks * 4 + 2 * kSlots * 8 + 64;
+  static constexpr int kMaxSmem = kFixed + kept_ints(kMaxBatch) * 4;
+};
+
+// Byte offset of 16-byte chunk c of a block's row r: lines of 128 bytes, swizzled, `plane` bytes between the lines'
+// first and second 128 bytes of a row; two rows of 64 dims share a line.
+template <int kD>
+__device__ __forceinline__ uint32_t row_chunk(int r, int c, uint32_t plane) {
+  if constexpr (kD == 64) return swz128(r >> 1, (r & 1) * 4 + c);
+  return (c >> 3) * plane + swz128(r, c & 7);
+}
+
+struct Kv8Args {
+  const float* k_scale;
+  const float* v_scale;
+  const uint16_t* q;
+  long long q_stride;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t group;        // query heads per KV head
+  int32_t heads;        // KV heads of an item (Hc)
+  int32_t head_groups;  // items per request
+  int32_t mtiles;       // tiles of 8 or 16 query heads per KV head
+  int32_t replicas;     // warps that share a (head, tile)
+  int32_t step_pages;   // pages of a step
+  int32_t num_pages;
+  int32_t batch;
+  const int32_t* block_table;
+  int32_t bt_stride;
+  const int32_t* seq_lens;
+  int32_t sink, recent;
+  float scale_log2;
+  uint16_t* out;
+  float* out_lse;
+  float* o_part;        // [2 * CTAs][heads * group][D]
+  float* lse_part;      // [2 * CTAs][heads * group], log2 domain
+  // An item that spans CTAs is the only one to go on behind its first CTA, so that CTA's index names it.
+  uint32_t* arrivals;   // [kMaxCtas] by first CTA, zero between calls
+  int2* joins;          // [CTAs] by first CTA: item and partials for the join kernel (0 partials: nothing to do)
+  bool deferred;        // the join kernel follows
+  unsigned* err;
+};
+
+// kNt: column tiles of eight query heads; kSolo: no two warps share a (head, tile) (code of its own: as a branch
+// beside the other it cost that one 0.8 us of 9.9).
+template <int kD, int kNt, bool kSolo>
+__global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap,
+                                                                           const __grid_constant__ CUtensorMap vmap,
+                                                                           const Kv8Args a) {
+  using C = Cfg<kD>;
+  constexpr int kSlots = C::kSlots;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* stage = reinterpret_cast<float*>(ring + kSlots * kSlotBytes);  // [warps][8][D]
+  float* ml = stage + C::kStageFloats;                                  // [warps][(m, l)][8]
+  uint32_t* meta = reinterpret_cast<uint32_t*>(ml + C::kWarps * 16);    // [kMetaRing][kMaxPages]
+  float* scales = reinterpret_cast<float*>(meta + kMetaRing * kMaxPages);  // [kSlots][kBlocks]
+  uint64_t* full = reinterpret_cast<uint64_t*>(scales + kSlots * C::kBlocks);
+  uint64_t* empty = full + kSlots;
+  int* flags = reinterpret_cast<int*>(empty + kSlots);  // [8]: joins to make, the items of slots 0 and 1, neighbours
+  int* prefix = flags + 8;                              // [batch + 1]
+  int* lens = prefix + a.batch + 1;                     // [batch], then the pages of each
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int heads = a.heads, G = a.group, rows = heads * G, HG = a.head_groups, Pg = a.step_pages;
+  const int combos = heads * a.mtiles, active = combos * a.replicas;
+
+  // What needs no input comes before the wait for the previous kernel; kept_prefix's barriers publish it.
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&full[s], 1 + 32);  // the copies of the codes, and each lane's of the scales
+      mbar_init(&empty[s], active);
+    }
+    mbar_fence_init();
+  }
+  if (warp == C::kWarps && lane == 0) {
+    tma_prefetch_map(&kmap);
+    tma_prefetch_map(&vmap);
+  }
+  pdl_enter();
+  // Pieces of a step: of up to eight query heads a CTA takes a second one in less time than more partials take to
+  // join (1 x 1,000 tokens, 8 KV heads: 10.6 us with 32 partials an item, 10.0 with 16), of more it does not (1 x 4K,
+  // 32 heads over one: 14.6 us with 32, 17.8 with 16).
+  const int piece = kept_prefix<C::kThreads>(a.seq_lens, a.batch, HG, a.bt_stride, a.sink, a.recent, Pg, Pg,
+                                             G > 8 ? 32 : 8, gridDim.x, kMaxPlaces / HG, prefix, lens,
+                                             reinterpret_cast<long long*>(stage), a.err);
+  // Requests without a kept token: the empty sum.
+  for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+    if (prefix[b + 1] != prefix[b]) continue;
+    const size_t r0 = (size_t)b * a.num_q_heads;
+    uint4* o = reinterpret_cast<uint4*>(a.out + r0 * kD);
+    for (int i = threadIdx.x; i < a.num_q_heads * kD / 8; i += C::kThreads) o[i] = make_uint4(0, 0, 0, 0);
+    if (a.out_lse)
+      for (int i = threadIdx.x; i < a.num_q_heads; i += C::kThreads) a.out_lse[r0 + i] = -INFINITY;
+  }
+  Slices slices;
+  slices.init(prefix, a.batch, HG, Pg, Pg, gridDim.x, piece);
+  const int2 slice = slice_of(slices, blockIdx.x);
+  if (slice.x >= slice.y) {
+    if (a.deferred && threadIdx.x == 0) a.joins[blockIdx.x] = make_int2(0, 0);
+    return;
+  }
+
+  Segments seg;
+  seg.init(slices, slice.x, slice.y);
+  bool dead = false;  // a bounded wait gave up: no further waits or products, but every barrier
+
+  if (warp == C::kWarps) {
+    // ------------------------------------------------------------ TMA producer
+    const uint64_t policy = l2_evict_first_policy();
+    const uint32_t page_bytes = (uint32_t)heads * kPageSize * kD;
+    const int my_page = lane / heads, my_head = lane - my_page * heads;  // the block whose scales this lane copies
+    int j = 0, step = 0;
+    while (!dead && seg.next()) {
+      const Kept k = kept_of(lens[seg.b], a.bt_stride, a.sink, a.recent, nullptr);
+      const int32_t* bt = a.block_table + (size_t)seg.b * a.bt_stride;
+      auto entry = [&](int i) { return i < seg.hi ? bt[k.logical(i)] : -1; };
+      // Two windows of 32 table entries, one per lane: the second is loaded while the first is copied.
+      int base = seg.lo, cur = entry(base + lane), nxt = entry(base + 32 + lane);
+      for (int i0 = seg.lo; i0 < seg.hi && !dead; i0 += Pg, ++step) {
+        if (i0 >= base + 32) {
+          base += 32;
+          cur = nxt;
+          nxt = entry(base + 32 + lane);
+        }
+        const int i = i0 + lane;
+        const int pc = __shfl_sync(0xffffffffu, cur, (i - base) & 31);
+        const int pn = __shfl_sync(0xffffffffu, nxt, (i - base) & 31);
+        const int phys = i < base + 32 ? pc : pn;
+        const bool mine = lane < Pg && i < seg.hi;
+        const bool ok = mine && phys >= 0 && phys < a.num_pages;
+        if (mine && !ok) raise_error(a.err, SE_DEVERR_PAGE_RANGE);
+        const int block_page = __shfl_sync(0xffffffffu, ok ? phys : -1, my_page);
+        const bool scaled = lane < Pg * heads && block_page >= 0;
+        const size_t block = (size_t)max(block_page, 0) * a.num_kv_heads + seg.group * heads + my_head;
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ok)) * page_bytes;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++j) {
+          const int s = j % kSlots;
+          if (lane == 0 && j >= kSlots && !mbar_wait(&empty[s], (j / kSlots - 1) & 1)) dead = true;
+          dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
+          if (dead) break;
+          if (kv == 0 && lane < Pg)
+            meta[(step % kMetaRing) * kMaxPages + lane] = ok ? page_mask(k, a.sink, k.logical(i)) : 0u;
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
+          __syncwarp();
+          if (ok)
+            tma_load_3d(ring + s * kSlotBytes + lane * page_bytes, kv ? &vmap : &kmap, 0,
+                        (phys * a.num_kv_heads + seg.group * heads) * (kPageSize * min(kD, 128) / 128), 0, &full[s],
+                        policy);
+          if (scaled) cp_async_4(smem_addr(scales + s * C::kBlocks + lane), (kv ? a.v_scale : a.k_scale) + block);
+          mbar_arrive_copies(&full[s]);
+        }
+      }
+    }
+    // Every copy has landed before the CTA leaves.
+    if (lane == 0) {
+      for (int u = max(0, j - kSlots); u < j; ++u)
+        if (!mbar_wait(&full[u % kSlots], (u / kSlots) & 1)) dead = true;
+      if (dead) raise_error(a.err, SE_DEVERR_WAIT_TIMEOUT);
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const bool works = warp < active;
+  const int combo = warp % combos, replica = warp / combos;
+  const int hc = combo / a.mtiles, mt = combo % a.mtiles;
+  const int g = lane >> 2, t = lane & 3;
+  const int tile_head = mt * 8 * kNt;  // first query head of the tile, in its KV head's group
+  const uint32_t ring0 = smem_addr(ring);
+  const uint32_t plane = (uint32_t)heads * kPageSize * 128;  // 128 dims of a page's rows
+  const uint32_t page_bytes = (uint32_t)heads * kPageSize * kD;
+  const uint32_t off = row_chunk<kD>(lane & 15, lane >> 4, plane);  // of ldmatrix: 16 rows, two chunks
+  int j = 0, step = 0;
+  if (warp == 0) {  // while the first copies are on their way; in shared memory, as the loop needs its registers
+    const Neighbours share = neighbours_of(slices, blockIdx.x, slice);
+    if (lane == 0) {
+      flags[2] = flags[3] = 0;
+      flags[4] = share.first0;
+      flags[5] = share.parts0;
+      flags[6] = share.parts1;
+    }
+  }
+  bool handed = false;
+
+  while (seg.next()) {
+    // Q^T as the B operand, high and low parts: head g of each column tile, dims 4 t .. 4 t + 3 and 16 more.
+    uint32_t qh[kD / 32][kNt][2], ql[kD / 32][kNt][2];
+    float zf[kNt][2];  // what turns the products of heads 2 t and 2 t + 1 into logits in base 2, but for K's scale
+#pragma unroll
+    for (int nt = 0; nt < kNt; ++nt) {
+      const int hd = tile_head + nt * 8 + g;
+      const bool real = works && hd < G;
+      const int row = (seg.group * heads + hc) * G + (real ? hd : 0);
+      const uint16_t* qr = a.q + (size_t)seg.b * a.q_stride + (size_t)row * kD + 4 * t;
+      uint2 x[kD / 16];
+      uint32_t top = 0, odd = 0;
+#pragma unroll
+      for (int i = 0; i < kD / 16; ++i) {
+        x[i] = real ? *reinterpret_cast<const uint2*>(qr + i * 16) : make_uint2(0u, 0u);
+        top = max_abs_bf16x2(max_abs_bf16x2(top, x[i].x), x[i].y);
+        odd |= not_finite_bf16x2(x[i].x) | not_finite_bf16x2(x[i].y);
+      }
+      top = max_abs_bf16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max_abs_bf16x2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      odd |= __shfl_xor_sync(0xffffffffu, odd, 1);
+      odd |= __shfl_xor_sync(0xffffffffu, odd, 2);
+      // A row that is not finite is NaN throughout.
+      const float qs = odd ? 1.f : scale_for(max(top & 0xffffu, top >> 16)), inv = odd ? NAN : 1.f / qs;
+#pragma unroll
+      for (int i = 0; i < kD / 16; ++i) {
+        const float f0 = bf16_lo(x[i].x) * inv, f1 = bf16_hi(x[i].x) * inv;
+        const float f2 = bf16_lo(x[i].y) * inv, f3 = bf16_hi(x[i].y) * inv;
+        const uint32_t high = to_e4m3x4(f0, f1, f2, f3);
+        float b[4];
+        from_e4m3x4(high, b);
+        qh[i / 2][nt][i & 1] = high;
+        ql[i / 2][nt][i & 1] =
+            to_e4m3x4((f0 - b[0]) * 16.f, (f1 - b[1]) * 16.f, (f2 - b[2]) * 16.f, (f3 - b[3]) * 16.f);
+      }
+      zf[nt][0] = __shfl_sync(0xffffffffu, qs, 8 * t) * a.scale_log2;
+      zf[nt][1] = __shfl_sync(0xffffffffu, qs, 8 * t + 4) * a.scale_log2;
+    }
+    // O^T: dims 16 i + 2 g (0, 1) and the next (2, 3), heads 2 t and 2 t + 1 of each column tile, times 2^(14 - mo);
+    // mo, m and l of those heads (l: the thread's tokens only).
+    float o[kD / 16][kNt][4], mo[kNt][2], m[kNt][2], l[kNt][2];
+#pragma unroll
+    for (int nt = 0; nt < kNt; ++nt) {
+#pragma unroll
+      for (int i = 0; i < kD / 16; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+      mo[nt][0] = mo[nt][1] = m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+
+    for (int i0 = seg.lo; i0 < seg.hi; i0 += Pg, ++step, j += 2) {
+      if (!works) continue;
+      const int sk = j % kSlots, sv = (j + 1) % kSlots;
+      if (!dead && !__all_sync(0xffffffffu, mbar_wait(&full[sk], (j / kSlots) & 1))) dead = true;
+      bool v_here = false, zeroed = false;
+      for (int pg = replica; pg < Pg; pg += a.replicas) {
+        const uint32_t mask = dead || i0 + pg >= seg.hi ? 0u : meta[(step % kMetaRing) * kMaxPages + pg];
+        const bool last = pg + a.replicas >= Pg;
+        const uint32_t blk = pg * page_bytes + (uint32_t)hc * kPageSize * min(kD, 128);
+        float z[kNt][4], top[kNt][2];
+        if (mask) {
+          // The swizzle is an exclusive or of the 16-byte chunk with the line: two chunks further is one of bit 5 on.
+          const uint32_t ka = ring0 + sk * kSlotBytes + blk + off;
+          float high[kNt][4], low[kNt][4];
+#pragma unroll
+          for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) high[nt][e] = low[nt][e] = 0.f;
+#pragma unroll
+          for (int ks = 0; ks < kD / 32; ++ks) {
+            uint32_t r0, r1, r2, r3;
+            ldmatrix_x4(r0, r1, r2, r3, (ka ^ ((ks & 3) << 5)) + (ks >> 2) * plane);
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt) {
+              mma_e4m3_16832(high[nt], r0, r1, r2, r3, qh[ks][nt][0], qh[ks][nt][1]);
+              mma_e4m3_16832(low[nt], r0, r1, r2, r3, ql[ks][nt][0], ql[ks][nt][1]);
+            }
+          }
+          // Tokens g (0, 1) and g + 8 (2, 3), heads 2 t and 2 t + 1.
+          const float ks = scales[sk * C::kBlocks + pg * heads + hc];
+#pragma unroll
+          for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[nt][e] = fmaf(low[nt][e], 0.0625f, high[nt][e]) * zf[nt][e & 1] * ks;
+          if (!mask_is_full(mask)) {
+            const bool k0 = in_mask(mask, g), k1 = in_mask(mask, g + 8);
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt) {
+              z[nt][0] = k0 ? z[nt][0] : -INFINITY;
+              z[nt][1] = k0 ? z[nt][1] : -INFINITY;
+              z[nt][2] = k1 ? z[nt][2] : -INFINITY;
+              z[nt][3] = k1 ? z[nt][3] : -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              top[nt][e] = fmaxf(z[nt][e], z[nt][2 + e]);
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1)
+                top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xffffffffu, top[nt][e], x));
+              // A head that has seen nothing but -inf keeps m = -inf and takes 0 as its base.
+              const float mn = fmaxf(m[nt][e], top[nt][e]), base = finite_base(mn);
+              l[nt][e] = l[nt][e] * fast_exp2(m[nt][e] - base) + (fast_exp2(z[nt][e] - base) + fast_exp2(z[nt][2 + e] - base));
+              m[nt][e] = mn;
+            }
+        }
+        if (last) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[sk]);
+        }
+        if (!v_here) {
+          if (!dead && !__all_sync(0xffffffffu, mbar_wait(&full[sv], ((j + 1) / kSlots) & 1))) dead = true;
+          v_here = true;
+        }
+        if (mask && !dead) {
+          const uint32_t vt = ring0 + sv * kSlotBytes + blk;
+          if (!mask_is_full(mask)) {
+            // Stale rows may hold NaN: zero them (two lanes per row).
+            const int r = lane >> 1;
+            if (!in_mask(mask, r))
+              for (int c = lane & 1; c < kD / 16; c += 2)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + row_chunk<kD>(r, c, plane)), "r"(0u)
+                             : "memory");
+            zeroed = true;
+            __syncwarp();
+          }
+          // The weights with V's scale, as fp16 (half a step, 2^-11 of each); l sums them unrounded.
+          const float vs = log2f(scales[sv * C::kBlocks + pg * heads + hc]);
+          bool moved = false;
+#pragma unroll
+          for (int nt = 0; nt < kNt; ++nt) moved = moved || top[nt][0] + vs > mo[nt][0] || top[nt][1] + vs > mo[nt][1];
+          if (__any_sync(0xffffffffu, moved)) {
+            // Some head's maximum moves: its sums follow.
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float mn = fmaxf(mo[nt][e], top[nt][e] + vs), f = fast_exp2(mo[nt][e] - finite_base(mn));
+                mo[nt][e] = mn;
+#pragma unroll
+                for (int i = 0; i < kD / 16; ++i) {
+                  o[i][nt][e] *= f;
+                  o[i][nt][2 + e] *= f;
+                }
+              }
+          }
+          uint32_t pb[kNt][2];
+#pragma unroll
+          for (int nt = 0; nt < kNt; ++nt) {
+            const float w0 = vs + kWeightTop - finite_base(mo[nt][0]), w1 = vs + kWeightTop - finite_base(mo[nt][1]);
+            pb[nt][0] = transpose_8x8_b16(pack_f16x2(fast_exp2(z[nt][0] + w0), fast_exp2(z[nt][1] + w1)));
+            pb[nt][1] = transpose_8x8_b16(pack_f16x2(fast_exp2(z[nt][2] + w0), fast_exp2(z[nt][3] + w1)));
+          }
+          const uint32_t va = vt + off;
+#pragma unroll
+          for (int i = 0; i < kD / 32; ++i) {
+            // Two chunks of 16 dims, tokens 0-7 and 8-15 of each: (2 dims of token 2 t, 2 dims of the next) a word.
+            uint32_t r[4], even[4], odd[4];
+            ldmatrix_x4_trans(r[0], r[1], r[2], r[3], (va ^ ((i & 3) << 5)) + (i >> 2) * plane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) e4m3x4_to_f16(__byte_perm(r[k], 0u, 0x3120), even[k], odd[k]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int nt = 0; nt < kNt; ++nt)
+                mma_f16_16816(o[2 * i + c][nt], even[2 * c], odd[2 * c], even[2 * c + 1], odd[2 * c + 1], pb[nt][0],
+                              pb[nt][1]);
+          }
+        }
+      }
+      if (zeroed) fence_proxy_async_smem();  // before the next copy into the slot
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[sv]);
+    }
+
+    // ---- the end of a segment: this CTA's share of item (b, hg) is done
+    const bool split = seg.split();
+    const int slot = seg.lo > 0 ? 0 : 1, item = seg.b * HG + seg.group;
+    if (split && threadIdx.x == 0) flags[2 + slot] = item;
+    const size_t out_row0 = (size_t)seg.b * a.num_q_heads + (size_t)seg.group * rows;
+    const size_t part_row0 = (size_t)(2 * blockIdx.x + slot) * rows;
+    // A whole row without a finite logit is 0 whatever its values hold (0 times them need not be); a partial of one
+    // keeps that product, as the sum over a row with other tokens does.
+    // The R warps of a (head, tile) stage their states, eight query heads at a time, and share the sums and the
+    // output. Named barriers of the R warps: 2 + 2 combo, the states are there; 3 + 2 combo, they are read.
+    if (!works) continue;
+    const uint32_t threads = a.replicas * 32;
+#pragma unroll
+    for (int nt = 0; nt < kNt; ++nt) {
+      if (tile_head + nt * 8 >= G) continue;
+      if (!kSolo && handed) named_bar_sync(3 + 2 * combo, threads);
+      __syncwarp();
+      handed = true;
+      float* dst = stage + warp * 8 * kD;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
+        const int hd = 2 * t + e;
+        if constexpr (kSolo) {
+          // No other states: the row is final.
+          const bool none = l[nt][e] == 0.f;
+          const float inv = none ? 0.f : fast_exp2(mo[nt][e] - kWeightTop - finite_base(m[nt][e])) / l[nt][e];
+          const float lse2 = none ? -INFINITY : m[nt][e] + log2f(l[nt][e]);
+          const int qr = tile_head + nt * 8 + hd, r = hc * G + qr;
+#pragma unroll
+          for (int i = 0; i < kD / 16; ++i) {
+            o[i][nt][e] = none && !split ? 0.f : o[i][nt][e] * inv;
+            o[i][nt][2 + e] = none && !split ? 0.f : o[i][nt][2 + e] * inv;
+          }
+          if (g == 0 && qr < G) {
+            if (split)
+              a.lse_part[part_row0 + r] = lse2;
+            else if (a.out_lse)
+              a.out_lse[out_row0 + r] = lse2 * kLn2;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kD / 16; ++i) {
+          const float f = kSolo ? 1.f : fast_exp2(mo[nt][e] - kWeightTop - finite_base(m[nt][e]));
+          *reinterpret_cast<float2*>(dst + stage_at<kD>(hd, 16 * i + 2 * g)) =
+              make_float2(o[i][nt][e] * f, o[i][nt][2 + e] * f);
+        }
+        if (g == 0) {
+          ml[warp * 16 + hd] = m[nt][e];
+          ml[warp * 16 + 8 + hd] = l[nt][e];
+        }
+      }
+      const int hds = min(8, G - tile_head - nt * 8);
+      const size_t r0 = hc * G + tile_head + nt * 8;
+      if constexpr (kSolo) {
+        __syncwarp();
+#pragma unroll 4
+        for (int e = lane; e < hds * (kD / 4); e += 32) {
+          const int d = e % (kD / 4) * 4, hd = e / (kD / 4);
+          const float4 v = *reinterpret_cast<const float4*>(dst + stage_at<kD>(hd, d));
+          if (split)
+            *reinterpret_cast<float4*>(a.o_part + (part_row0 + r0 + hd) * kD + d) = v;
+          else
+            *reinterpret_cast<uint2*>(a.out + (out_row0 + r0 + hd) * kD + d) =
+                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        }
+        continue;
+      }
+      named_bar_sync(2 + 2 * combo, threads);
+#pragma unroll 4
+      for (int e = replica * 32 + lane; e < hds * (kD / 4); e += threads) {
+        const int d = e % (kD / 4) * 4, hd = e / (kD / 4);
+        float M = -INFINITY;
+        for (int w = combo; w < active; w += combos) M = fmaxf(M, ml[w * 16 + hd]);
+        const float base = finite_base(M);
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = combo; w < active; w += combos) {
+          const float f = fast_exp2(ml[w * 16 + hd] - base);
+          sum += f * ml[w * 16 + 8 + hd];
+          const float4 v = *reinterpret_cast<const float4*>(stage + w * 8 * kD + stage_at<kD>(hd, d));
+          acc = make_float4(acc.x + f * v.x, acc.y + f * v.y, acc.z + f * v.z, acc.w + f * v.w);
+        }
+        const bool none = sum == 0.f;
+        const float inv = none ? 0.f : 1.f / sum, lse2 = none ? -INFINITY : M + log2f(sum);
+        const size_t r = r0 + hd;
+        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (split)
+          *reinterpret_cast<float4*>(a.o_part + (part_row0 + r) * kD + d) = acc;
+        else
+          *reinterpret_cast<uint2*>(a.out + (out_row0 + r) * kD + d) =
+              none ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+        if (d == 0) {
+          if (split)
+            a.lse_part[part_row0 + r] = lse2;
+          else if (a.out_lse)
+            a.out_lse[out_row0 + r] = lse2 * kLn2;
+        }
+      }
+    }
+  }
+  if (dead && lane == 0) raise_error(a.err, SE_DEVERR_WAIT_TIMEOUT);
+  if (a.deferred && threadIdx.x == 0) a.joins[blockIdx.x] = make_int2(flags[3], flags[6]);
+
+  // ---- Publish: count this CTA in on the (at most two) items it shares with few others; whoever completes
+  // an item's count merges its partials (written by other CTAs: read past L1) and resets the counter.
+  if (a.deferred) return;
+  __threadfence();
+  named_bar_sync(1, C::kConsumers);
+  const int first0 = flags[4], parts0 = flags[5], parts1 = flags[6];
+  if (parts0 == 0 && parts1 == 0) return;  // the same for all consumers
+  if (threadIdx.x < 2) {
+    const int parts = threadIdx.x ? parts1 : parts0;
+    int last = 0;
+    if (parts > 0) {
+      uint32_t* cnt = a.arrivals + (threadIdx.x ? (int)blockIdx.x : first0);
+      last = atomic_add_acq_rel_gpu(cnt, 1u) == (uint32_t)parts - 1;
+      if (last) *cnt = 0;
+    }
+    flags[threadIdx.x] = last;
+  }
+  named_bar_sync(1, C::kConsumers);
+  auto* join_smem = reinterpret_cast<JoinSmem<kD, C::kWarps>*>(stage);  // the states staged there are read
+  static_assert(sizeof(JoinSmem<kD, C::kWarps>) <= (C::kStageFloats + C::kWarps * 16) * 4, "the join's sums fit");
+#pragma unroll 1
+  for (int s = 0; s < 2; ++s) {
+    if (!flags[s]) continue;
+    const int first = s ? (int)blockIdx.x : first0, parts = s ? parts1 : parts0, item = flags[2 + s];
+    const int warps = min(C::kWarps, share_of(parts));
+    for (int r0 = 0; r0 < rows; r0 += C::kWarps / warps)
+      join_rows<kD, C::kWarps>(a.o_part, a.lse_part, first, parts, item, rows, r0, warps, *join_smem, a.out,
+                               a.out_lse, [] { named_bar_sync(1, C::kConsumers); });
+  }
+}
+
+// How the heads of a call are laid over the consumer warps, and where its joins run.
+struct HeadPlan {
+  int heads, head_groups, mtiles, replicas, step_pages;
+  bool deferred;
+};
+
+// Query heads per KV head up to which a tile holds eight of them, above it sixteen.
+int eights_up_to(int head_dim) { return head_dim == 256 ? 64 : 8; }
+
+// As many heads per box as leave at most an eighth of a slot empty, and no more than `most_heads`.
+HeadPlan head_plan(int num_kv_heads, int group, int head_dim, int most_heads) {
+  const int warps = Cfg<128>::kWarps, blocks = kSlotBytes / (kPageSize * head_dim);
+  HeadPlan p;
+  p.mtiles = group <= eights_up_to(head_dim) ? (group + 7) / 8 : (group + 15) / 16;
+  for (int c = 1; c <= most_heads && c * p.mtiles <= warps; ++c) {
+    if (num_kv_heads % c) continue;
+    const int r = warps / (c * p.mtiles), pages = blocks / c / r * r;
+    if (c > 1 && pages * c * 8 < blocks * 7) continue;
+    p.heads = c;
+    p.replicas = r;
+    p.step_pages = pages;
+  }
+  p.head_groups = num_kv_heads / p.heads;
+  p.deferred = true;
+  return p;
+}
+
+// The largest boxes, unless the table's (or the windows') width keeps an item's partials, counted in slices of the
+// least length, so few that smaller ones let the decode kernel join them. Not for short items, which are seldom split.
+HeadPlan call_plan(int num_kv_heads, int group, int head_dim, int32_t bt_stride, int32_t sink_tokens,
+                   int32_t recent_tokens, int ctas) {
+  long long width = bt_stride;
+  if (recent_tokens > 0)
+    width = std::min(width, ((long long)sink_tokens + kPageSize - 1) / kPageSize + recent_tokens / kPageSize + 2);
+  for (int c = 8; c > 0;) {
+    HeadPlan p = head_plan(num_kv_heads, group, head_dim, c);
+    if (c < 8 && width < kInlineWidth) break;
+    const long long parts = std::min<long long>(ctas, (width + p.step_pages) / (2 * p.step_pages + 1) + 2);
+    p.deferred = parts * p.heads * group * head_dim * (long long)sizeof(float) > kInlineBytes;
+    if (!p.deferred) return p;
+    c = p.heads - 1;
+  }
+  return head_plan(num_kv_heads, group, head_dim, 8);
+}
+
+int ctas_of(int sm_count) { return sm_count < kMaxCtas ? sm_count : kMaxCtas; }
+
+template <int kD, int kNt, bool kSolo>
+cudaError_t launch_as(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8Args& a, int grid,
+                   cudaStream_t stream) {
+  const size_t smem = Cfg<kD>::kFixed + kept_ints(a.batch) * 4;
+  static_assert(Cfg<kD>::kMaxSmem <= 227 * 1024, "the largest batch fits");
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(kv8_decode_kernel<kD, kNt, kSolo>, Cfg<kD>::kMaxSmem, allowed);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kv8_decode_kernel<kD, kNt, kSolo>, dim3(grid), dim3(Cfg<kD>::kThreads), smem, stream, kmap, vmap, a);
+  if (e != cudaSuccess || !a.deferred) return e;
+  const int rows = a.heads * a.group;
+  // An item has at most `rows` units, and no more items than CTAs reach beyond a slice.
+  const int units = std::min(grid, a.batch * a.head_groups) * rows;
+  return launch_pdl(paged_join_kernel<kD>, dim3(std::min(units, 8 * grid)), dim3(kJoinWarps * 32), 0, stream,
+                    a.o_part, a.lse_part, a.joins, grid, rows, a.out, a.out_lse);
+}
+
+template <int kD>
+cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8Args& a, int grid,
+                   cudaStream_t stream) {
+  const bool solo = a.replicas == 1;
+  if (a.group <= 8 * a.mtiles)
+    return solo ? launch_as<kD, 1, true>(kmap, vmap, a, grid, stream)
+                : launch_as<kD, 1, false>(kmap, vmap, a, grid, stream);
+  if constexpr (kD < 256)  // 256 dims: tiles of eight alone
+    return solo ? launch_as<kD, 2, true>(kmap, vmap, a, grid, stream)
+                : launch_as<kD, 2, false>(kmap, vmap, a, grid, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+int kv8_decode_max_batch() { return kMaxBatch; }
+
+bool kv8_decode_supported(int num_kv_heads, int head_dim, int num_q_heads) {
+  return (head_dim == 64 || head_dim == 128 || head_dim == 256) &&
+         num_q_heads / num_kv_heads <= 64;
+}
+
+int kv8_decode_box_heads(int num_kv_heads, int num_q_heads, int head_dim, int32_t bt_stride, int32_t sink_tokens,
+                           int32_t recent_tokens, int sm_count) {
+  return call_plan(num_kv_heads, num_q_heads / num_kv_heads, head_dim, bt_stride, sink_tokens, recent_tokens,
+                   ctas_of(sm_count)).heads;
+}
+
+size_t kv8_decode_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
+  const HeadPlan p = head_plan(num_kv_heads, num_q_heads / num_kv_heads, head_dim, 8);  // the most rows of an item
+  const size_t rows = (size_t)p.heads * (num_q_heads / num_kv_heads);
+  return kCounterBytes + 2 * kMaxCtas * rows * (head_dim + 1) * sizeof(float);
+}
+
+cudaError_t launch_kv8_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8View& kv, const uint16_t* q,
+                                long long q_stride, int32_t num_q_heads, const int32_t* block_table,
+                                int32_t bt_stride, const int32_t* seq_lens, int32_t batch, int32_t sink_tokens,
+                                int32_t recent_tokens, float sm_scale, uint16_t* out, float* out_lse, void* workspace,
+                                int sm_count, unsigned* err, cudaStream_t stream) {
+  const int group = num_q_heads / kv.num_kv_heads;
+  const int grid = ctas_of(sm_count);
+  const HeadPlan p = call_plan(kv.num_kv_heads, group, kv.head_dim, bt_stride, sink_tokens, recent_tokens, grid);
+  Kv8Args a;
+  a.k_scale = kv.k_scale;
+  a.v_scale = kv.v_scale;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = kv.num_kv_heads;
+  a.group = group;
+  a.heads = p.heads;
+  a.head_groups = p.head_groups;
+  a.mtiles = p.mtiles;
+  a.replicas = p.replicas;
+  a.step_pages = p.step_pages;
+  a.num_pages = kv.num_pages;
+  a.batch = batch;
+  a.block_table = block_table;
+  a.bt_stride = bt_stride;
+  a.seq_lens = seq_lens;
+  a.sink = sink_tokens;
+  a.recent = recent_tokens;
+  a.scale_log2 = sm_scale * 1.4426950408889634f;
+  a.out = out;
+  a.out_lse = out_lse;
+  const size_t rows = (size_t)p.heads * group;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.arrivals = reinterpret_cast<uint32_t*>(ws);
+  a.joins = reinterpret_cast<int2*>(ws + kArrivalBytes);
+  a.o_part = reinterpret_cast<float*>(ws + kCounterBytes);
+  a.lse_part = a.o_part + 2 * kMaxCtas * rows * kv.head_dim;
+  a.err = err;
+  a.deferred = p.deferred;
+  switch (kv.head_dim) {
+    case 64: return launch<64>(kmap, vmap, a, grid, stream);
+    case 128: return launch<128>(kmap, vmap, a, grid, stream);
+    default: return launch<256>(kmap, vmap, a, grid, stream);
+  }
+}
+
+}  // namespace se

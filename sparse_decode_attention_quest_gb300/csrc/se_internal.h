@@ -62,6 +62,17 @@ struct KvView {
   int32_t row_stride_v;
 };
 
+// The same of an 8-bit cache.
+struct Kv8View {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t num_pages;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+};
+
 // ---- quest_summary.cu
 cudaError_t launch_build_summaries(const KvView& kv, const int32_t* block_table, int32_t bt_stride,
                                    const int32_t* seq_lens, int32_t batch, int32_t max_seq_len, unsigned* err,
@@ -205,6 +216,37 @@ cudaError_t launch_paged_latent(const CUtensorMap& kvmap, const CUtensorMap& qma
                                 const int32_t* seq_lens, int32_t batch, int32_t sink_tokens, int32_t recent_tokens,
                                 float sm_scale, uint16_t* out, float* out_lse, void* workspace, int sm_count,
                                 unsigned* err, cudaStream_t stream);
+
+// ---- rotary.cu: positions into query and key rows
+cudaError_t launch_rotary(const uint16_t* q, long long q_stride, int32_t q_heads, const uint16_t* k, long long k_stride,
+                          int32_t kv_heads, int32_t dim, int32_t offset, int32_t rot, bool interleaved, bool inverse,
+                          const uint64_t* freqs, float amplitude, const int32_t* positions, const int32_t* num_valid,
+                          int32_t num_tokens, uint16_t* q_out, long long q_out_stride, uint16_t* k_out,
+                          long long k_out_stride, int sm_count, cudaStream_t stream);
+
+// ---- kv8_store.cu: rows of new tokens into an 8-bit cache, and rows of it back
+cudaError_t launch_kv8_store(const Kv8View& kv, const uint16_t* k_new, long long k_stride, const uint16_t* v_new,
+                             long long v_stride, const int32_t* slot_map, int32_t num_tokens, int sm_count,
+                             unsigned* err, cudaStream_t stream);
+cudaError_t launch_kv8_load(const Kv8View& kv, const int32_t* block_table, int32_t bt_stride, const int32_t* first,
+                            const int32_t* token_start, int32_t batch, int32_t num_rows, uint16_t* k_out,
+                            long long k_stride, uint16_t* v_out, long long v_stride, int sm_count, unsigned* err,
+                            cudaStream_t stream);
+
+// ---- kv8_decode.cu: one new token over an 8-bit cache
+int kv8_decode_max_batch();
+bool kv8_decode_supported(int num_kv_heads, int head_dim, int num_q_heads);
+// KV heads per TMA box of a call.
+int kv8_decode_box_heads(int num_kv_heads, int num_q_heads, int head_dim, int32_t bt_stride, int32_t sink_tokens,
+                         int32_t recent_tokens, int sm_count);
+size_t kv8_decode_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim);
+// kmap, vmap: the caches as (128 bytes, line, 128-byte chunk of a row), 128-byte swizzle; a line is a row (two rows of
+// 64 dims), a box the lines of a page's kv8_decode_box_heads heads, all chunks.
+cudaError_t launch_kv8_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8View& kv, const uint16_t* q,
+                              long long q_stride, int32_t num_q_heads, const int32_t* block_table, int32_t bt_stride,
+                              const int32_t* seq_lens, int32_t batch, int32_t sink_tokens, int32_t recent_tokens,
+                              float sm_scale, uint16_t* out, float* out_lse, void* workspace, int sm_count,
+                              unsigned* err, cudaStream_t stream);
 
 // ---- api.cu: per-device context and helpers shared with other entry points
 cudaError_t device_context(int* sm_count, unsigned** err);
