@@ -9,19 +9,24 @@
 // share-out of the work, the joins and the ring of TMA boxes are its (paged_decode.cu). What
 // differs is what has to happen to twice as many rows in the same time:
 //
-//  * K is not converted. S^T = K Q^T takes the codes as they lie, in m16n8k32 e4m3 MMAs, and the
-//    query row is split into two e4m3 numbers a dim instead: scaled by a power of two to at most
-//    448, high = rne(q), low = rne(16 (q - high)). A bf16 number has eight significant bits
-//    and a code four, so the two hold it exactly down to 2^-6 of the scale, and within 2^-21 of the
-//    row's largest magnitude below. Two accumulators, z = (high + low / 16) times the scales.
-//  * V is converted to fp16 (exact) on its way from shared memory. The 8 x 8 transposes of
-//    ldmatrix move pairs of codes, two dims of a token; a byte permutation and two conversions make
+//  * Codes become fp16 (exact) on their way from shared memory, two conversions a word, and both products
+//    are m16n8k16 fp16 MMAs. Neither operand's order matters as long as both have it: K's words keep
+//    four dims of a token together, so Q^T is loaded in that order. V comes through the 8 x 8 transposes of
+//    ldmatrix, which move pairs of codes, two dims of a token; a byte permutation and the conversions make
 //    of them the A operands of the even and of the odd dims, whose rows are then 2 g and 2 g + 1 of
-//    sixteen dims instead of g and g + 8: nothing but the epilogue sees it.
-//  * V's scales go into the weights before they are rounded to fp16. The output sums have a maximum of their own, of
-//    z_j + log2 s_v: a weight enters as exp2(z_j + log2 s_v - that + 14), at most 2^14, so that it is
-//    rounded by half a step of 2^-11 down to 2^-28 of the largest product of weight and scale, whatever the scales of
-//    pages that carry no weight. l keeps the maximum of z. One more exponential per logit.
+//    sixteen dims instead of g and g + 8: nothing but the epilogue sees it. (m16n8k32 e4m3 MMAs on the codes
+//    themselves are expanded into the same conversions, of Q too and every time: 454 instructions a block of
+//    16 tokens and one head, with the query split into two e4m3 numbers; 691 us for 3.2 GB.)
+//  * A query row is scaled by a power of two to at most 448 and held as fp16: exact for dims down to 2^-25 of the
+//    row's largest magnitude, within 2^-32 of it below.
+//  * V's scales go into the weights before they are rounded to fp16: a weight enters as
+//    w_j = exp2(z_j - m + log2 s_v - d + 14), with m + d a reference of their product's maximum, so that it is rounded
+//    by half a step of 2^-11 down to 2^-28 of the largest, whatever the scales of pages that carry no weight. The
+//    sum l takes the same exponentials, times exp2(d - log2 s_v - 14) for each page.
+//  * m and m + d need not be the maxima: a weight may reach 2^15.9. A page whose weights stay below costs no exchange
+//    between lanes, just a vote; any other (the first ones, mostly) moves both references to the maxima, and
+//    the sums follow.
+//  * A warp takes two pages at once where its registers allow: two independent chains of products.
 //  * Scales travel with their slot: a 4-byte asynchronous copy per (page, head) that arrives on the slot's barrier.
 //  * Rows that are not kept: their logits become -inf, and their value rows are
 //    zeroed in shared memory first, since 0 * NaN is not 0.
@@ -40,7 +45,9 @@ constexpr int kMaxBatch = 4096;  // requests whose prefix fits beside the ring
 constexpr int kInlineBytes = 48 * 1024;  // partials of an item, in slices, where one CTA merges them
 constexpr int kInlineWidth = 32;          // pages of an item from which smaller boxes are taken for that
 
-constexpr float kWeightTop = 14.f;  // log2 of the largest weight that meets V
+constexpr float kWeightTop = 14.f;    // log2 of the weight at the reference
+constexpr float kWeightMost = 15.9f;  // log2 of the largest weight, within fp16
+constexpr float kLowest = -3.4e38f;   // m and d before any logit
 
 template <int kD>
 struct Cfg {
@@ -225,6 +232,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
   const uint32_t plane = (uint32_t)heads * kPageSize * 128;  // 128 dims of a page's rows
   const uint32_t page_bytes = (uint32_t)heads * kPageSize * kD;
   const uint32_t off = row_chunk<kD>(lane & 15, lane >> 4, plane);  // of ldmatrix: 16 rows, two chunks
+  constexpr int kPp = kD <= 128 && kNt == 1 ? 2 : 1;  // pages at once
   int j = 0, step = 0;
   if (warp == 0) {  // while the first copies are on their way; in shared memory, as the loop needs its registers
     const Neighbours share = neighbours_of(slices, blockIdx.x, slice);
@@ -238,8 +246,8 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
   bool handed = false;
 
   while (seg.next()) {
-    // Q^T as the B operand, high and low parts: head g of each column tile, dims 4 t .. 4 t + 3 and 16 more.
-    uint32_t qh[kD / 32][kNt][2], ql[kD / 32][kNt][2];
+    // Q^T as the B operand: head g of each column tile, dims 4 t, 4 t + 1 and the next two of each sixteen.
+    uint32_t qb[kD / 16][kNt][2];
     float zf[kNt][2];  // what turns the products of heads 2 t and 2 t + 1 into logits in base 2, but for K's scale
 #pragma unroll
     for (int nt = 0; nt < kNt; ++nt) {
@@ -247,42 +255,38 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
       const bool real = works && hd < G;
       const int row = (seg.group * heads + hc) * G + (real ? hd : 0);
       const uint16_t* qr = a.q + (size_t)seg.b * a.q_stride + (size_t)row * kD + 4 * t;
-      uint2 x[kD / 16];
       uint32_t top = 0, odd = 0;
 #pragma unroll
       for (int i = 0; i < kD / 16; ++i) {
-        x[i] = real ? *reinterpret_cast<const uint2*>(qr + i * 16) : make_uint2(0u, 0u);
-        top = max_abs_bf16x2(max_abs_bf16x2(top, x[i].x), x[i].y);
-        odd |= not_finite_bf16x2(x[i].x) | not_finite_bf16x2(x[i].y);
+        const uint2 x = real ? *reinterpret_cast<const uint2*>(qr + i * 16) : make_uint2(0u, 0u);
+        qb[i][nt][0] = x.x;
+        qb[i][nt][1] = x.y;
+        top = max_abs_bf16x2(max_abs_bf16x2(top, x.x), x.y);
+        odd |= not_finite_bf16x2(x.x) | not_finite_bf16x2(x.y);
       }
-      top = max_abs_bf16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max_abs_bf16x2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      odd |= __shfl_xor_sync(0xffffffffu, odd, 1);
-      odd |= __shfl_xor_sync(0xffffffffu, odd, 2);
+#pragma unroll
+      for (int x = 1; x < 4; x <<= 1) {
+        top = max_abs_bf16x2(top, __shfl_xor_sync(0xffffffffu, top, x));
+        odd |= __shfl_xor_sync(0xffffffffu, odd, x);
+      }
       // A row that is not finite is NaN throughout.
       const float qs = odd ? 1.f : scale_for(max(top & 0xffffu, top >> 16)), inv = odd ? NAN : 1.f / qs;
 #pragma unroll
-      for (int i = 0; i < kD / 16; ++i) {
-        const float f0 = bf16_lo(x[i].x) * inv, f1 = bf16_hi(x[i].x) * inv;
-        const float f2 = bf16_lo(x[i].y) * inv, f3 = bf16_hi(x[i].y) * inv;
-        const uint32_t high = to_e4m3x4(f0, f1, f2, f3);
-        float b[4];
-        from_e4m3x4(high, b);
-        qh[i / 2][nt][i & 1] = high;
-        ql[i / 2][nt][i & 1] =
-            to_e4m3x4((f0 - b[0]) * 16.f, (f1 - b[1]) * 16.f, (f2 - b[2]) * 16.f, (f3 - b[3]) * 16.f);
-      }
+      for (int i = 0; i < kD / 16; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          qb[i][nt][k] = pack_f16x2(bf16_lo(qb[i][nt][k]) * inv, bf16_hi(qb[i][nt][k]) * inv);
       zf[nt][0] = __shfl_sync(0xffffffffu, qs, 8 * t) * a.scale_log2;
       zf[nt][1] = __shfl_sync(0xffffffffu, qs, 8 * t + 4) * a.scale_log2;
     }
-    // O^T: dims 16 i + 2 g (0, 1) and the next (2, 3), heads 2 t and 2 t + 1 of each column tile, times 2^(14 - mo);
-    // mo, m and l of those heads (l: the thread's tokens only).
-    float o[kD / 16][kNt][4], mo[kNt][2], m[kNt][2], l[kNt][2];
+    // O^T: dims 16 i + 2 g (0, 1) and the next (2, 3), heads 2 t and 2 t + 1 of each column tile, times
+    // 2^(14 - m - d); m, d and l (times 2^-m, the thread's tokens only) of those heads.
+    float o[kD / 16][kNt][4], m[kNt][2], d[kNt][2], l[kNt][2];
 #pragma unroll
     for (int nt = 0; nt < kNt; ++nt) {
 #pragma unroll
       for (int i = 0; i < kD / 16; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
-      mo[nt][0] = mo[nt][1] = m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = d[nt][0] = d[nt][1] = kLowest;
       l[nt][0] = l[nt][1] = 0.f;
     }
 
@@ -291,58 +295,62 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
       const int sk = j % kSlots, sv = (j + 1) % kSlots;
       if (!dead && !__all_sync(0xffffffffu, mbar_wait(&full[sk], (j / kSlots) & 1))) dead = true;
       bool v_here = false, zeroed = false;
-      for (int pg = replica; pg < Pg; pg += a.replicas) {
-        const uint32_t mask = dead || i0 + pg >= seg.hi ? 0u : meta[(step % kMetaRing) * kMaxPages + pg];
-        const bool last = pg + a.replicas >= Pg;
-        const uint32_t blk = pg * page_bytes + (uint32_t)hc * kPageSize * min(kD, 128);
-        float z[kNt][4], top[kNt][2];
-        if (mask) {
-          // The swizzle is an exclusive or of the 16-byte chunk with the line: two chunks further is one of bit 5 on.
-          const uint32_t ka = ring0 + sk * kSlotBytes + blk + off;
-          float high[kNt][4], low[kNt][4];
+      for (int pg0 = replica; pg0 < Pg; pg0 += kPp * a.replicas) {
+        uint32_t mask[kPp], at[kPp];  // the page's kept tokens, and where its block begins in its slot
+        int blk[kPp];
+        bool any = false;
 #pragma unroll
-          for (int nt = 0; nt < kNt; ++nt)
+        for (int u = 0; u < kPp; ++u) {
+          const int pg = pg0 + u * a.replicas;
+          mask[u] = dead || pg >= Pg || i0 + pg >= seg.hi ? 0u : meta[(step % kMetaRing) * kMaxPages + pg];
+          blk[u] = pg * heads + hc;
+          at[u] = pg * page_bytes + hc * (kPageSize * min(kD, 128));
+          any = any || mask[u];
+        }
+        if constexpr (kPp == 2) {
+          // A page that is not there is the other one over again, without a weight.
+          if (!mask[0]) blk[0] = blk[1], at[0] = at[1];
+          if (!mask[1]) blk[1] = blk[0], at[1] = at[0];
+        }
+        const bool last = pg0 + kPp * a.replicas >= Pg;
+        // Products of tokens g (0, 1) and g + 8 (2, 3), heads 2 t and 2 t + 1, times their factors; K's scale.
+        float s[kPp][kNt][4], ks[kPp];
+        if (any) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) high[nt][e] = low[nt][e] = 0.f;
+          for (int u = 0; u < kPp; ++u)
 #pragma unroll
-          for (int ks = 0; ks < kD / 32; ++ks) {
-            uint32_t r0, r1, r2, r3;
-            ldmatrix_x4(r0, r1, r2, r3, (ka ^ ((ks & 3) << 5)) + (ks >> 2) * plane);
+            for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < kNt; ++nt) {
-              mma_e4m3_16832(high[nt], r0, r1, r2, r3, qh[ks][nt][0], qh[ks][nt][1]);
-              mma_e4m3_16832(low[nt], r0, r1, r2, r3, ql[ks][nt][0], ql[ks][nt][1]);
+              for (int e = 0; e < 4; ++e) s[u][nt][e] = 0.f;
+#pragma unroll
+          for (int c = 0; c < kD / 32; ++c) {
+#pragma unroll
+            for (int u = 0; u < kPp; ++u) {
+              // The swizzle is an exclusive or of the 16-byte chunk with the line: two chunks further is one of bit 5 on.
+              uint32_t r[4], lo[4], hi[4];
+              ldmatrix_x4(r[0], r[1], r[2], r[3],
+                          ((ring0 + sk * kSlotBytes + at[u] + off) ^ ((c & 3) << 5)) + (c >> 2) * plane);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) e4m3x4_to_f16(r[k], lo[k], hi[k]);
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int nt = 0; nt < kNt; ++nt)
+                  mma_f16_16816(s[u][nt], lo[2 * k], lo[2 * k + 1], hi[2 * k], hi[2 * k + 1], qb[2 * c + k][nt][0],
+                                qb[2 * c + k][nt][1]);
             }
           }
-          // Tokens g (0, 1) and g + 8 (2, 3), heads 2 t and 2 t + 1.
-          const float ks = scales[sk * C::kBlocks + pg * heads + hc];
 #pragma unroll
-          for (int nt = 0; nt < kNt; ++nt)
+          for (int u = 0; u < kPp; ++u) {
+            ks[u] = scales[sk * C::kBlocks + blk[u]];
+            const bool whole = mask_is_full(mask[u]);
+            const bool k0 = whole || in_mask(mask[u], g), k1 = whole || in_mask(mask[u], g + 8);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[nt][e] = fmaf(low[nt][e], 0.0625f, high[nt][e]) * zf[nt][e & 1] * ks;
-          if (!mask_is_full(mask)) {
-            const bool k0 = in_mask(mask, g), k1 = in_mask(mask, g + 8);
+            for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < kNt; ++nt) {
-              z[nt][0] = k0 ? z[nt][0] : -INFINITY;
-              z[nt][1] = k0 ? z[nt][1] : -INFINITY;
-              z[nt][2] = k1 ? z[nt][2] : -INFINITY;
-              z[nt][3] = k1 ? z[nt][3] : -INFINITY;
-            }
+              for (int e = 0; e < 4; ++e)
+                s[u][nt][e] = (e < 2 ? k0 : k1) ? s[u][nt][e] * zf[nt][e & 1] : -INFINITY;
           }
-#pragma unroll
-          for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              top[nt][e] = fmaxf(z[nt][e], z[nt][2 + e]);
-#pragma unroll
-              for (int x = 4; x < 32; x <<= 1)
-                top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xffffffffu, top[nt][e], x));
-              // A head that has seen nothing but -inf keeps m = -inf and takes 0 as its base.
-              const float mn = fmaxf(m[nt][e], top[nt][e]), base = finite_base(mn);
-              l[nt][e] = l[nt][e] * fast_exp2(m[nt][e] - base) + (fast_exp2(z[nt][e] - base) + fast_exp2(z[nt][2 + e] - base));
-              m[nt][e] = mn;
-            }
         }
         if (last) {
           __syncwarp();
@@ -352,59 +360,108 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
           if (!dead && !__all_sync(0xffffffffu, mbar_wait(&full[sv], ((j + 1) / kSlots) & 1))) dead = true;
           v_here = true;
         }
-        if (mask && !dead) {
-          const uint32_t vt = ring0 + sv * kSlotBytes + blk;
-          if (!mask_is_full(mask)) {
-            // Stale rows may hold NaN: zero them (two lanes per row).
-            const int r = lane >> 1;
-            if (!in_mask(mask, r))
-              for (int c = lane & 1; c < kD / 16; c += 2)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + row_chunk<kD>(r, c, plane)), "r"(0u)
-                             : "memory");
-            zeroed = true;
-            __syncwarp();
-          }
-          // The weights with V's scale, as fp16 (half a step, 2^-11 of each); l sums them unrounded.
-          const float vs = log2f(scales[sv * C::kBlocks + pg * heads + hc]);
+        if (any && !dead) {
+          float vs[kPp], x[kPp][kNt][4], lg[kPp][kNt][2];
           bool moved = false;
 #pragma unroll
-          for (int nt = 0; nt < kNt; ++nt) moved = moved || top[nt][0] + vs > mo[nt][0] || top[nt][1] + vs > mo[nt][1];
-          if (__any_sync(0xffffffffu, moved)) {
-            // Some head's maximum moves: its sums follow.
+          for (int u = 0; u < kPp; ++u) {
+            vs[u] = fast_log2(scales[sv * C::kBlocks + blk[u]]);
 #pragma unroll
             for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float mn = fmaxf(mo[nt][e], top[nt][e] + vs), f = fast_exp2(mo[nt][e] - finite_base(mn));
-                mo[nt][e] = mn;
+                const float w = vs[u] + kWeightTop - d[nt][e];
+                x[u][nt][e] = fmaf(s[u][nt][e], ks[u], -m[nt][e]) + w;
+                x[u][nt][2 + e] = fmaf(s[u][nt][2 + e], ks[u], -m[nt][e]) + w;
+                // l's exponentials over the weights; beyond 2^60 (a V scale far below the others') they have their own.
+                lg[u][nt][e] = fast_exp2(-w);
+                moved = moved || !(fmaxf(x[u][nt][e], x[u][nt][2 + e]) <= kWeightMost) || w < -60.f;
+              }
+          }
+          if (__any_sync(0xffffffffu, moved)) {
+            // References to the maxima; the sums follow. l takes its own exponentials here.
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float z[kPp][2], top = m[nt][e];
+#pragma unroll
+                for (int u = 0; u < kPp; ++u) {
+                  z[u][0] = s[u][nt][e] * ks[u];
+                  z[u][1] = s[u][nt][2 + e] * ks[u];
+                  top = fmaxf(top, fmaxf(z[u][0], z[u][1]));
+                }
+#pragma unroll
+                for (int i = 4; i < 32; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+                const float back = m[nt][e] - top;
+                float over = fmaxf(d[nt][e] + back, kLowest);
+#pragma unroll
+                for (int u = 0; u < kPp; ++u) over = fmaxf(over, fmaxf(z[u][0], z[u][1]) - top + vs[u]);
+#pragma unroll
+                for (int i = 4; i < 32; i <<= 1) over = fmaxf(over, __shfl_xor_sync(0xffffffffu, over, i));
+                const float f = fast_exp2(back + (d[nt][e] - over));
+                l[nt][e] *= fast_exp2(back);
+                m[nt][e] = top;
+                d[nt][e] = over;
 #pragma unroll
                 for (int i = 0; i < kD / 16; ++i) {
                   o[i][nt][e] *= f;
                   o[i][nt][2 + e] *= f;
                 }
+#pragma unroll
+                for (int u = 0; u < kPp; ++u) {
+                  const float z0 = z[u][0] - top, z1 = z[u][1] - top, w = vs[u] + kWeightTop - over;
+                  x[u][nt][e] = z0 + w;
+                  x[u][nt][2 + e] = z1 + w;
+                  l[nt][e] += fast_exp2(z0) + fast_exp2(z1);
+                  lg[u][nt][e] = 0.f;
+                }
               }
           }
-          uint32_t pb[kNt][2];
+          uint32_t pb[kPp][kNt][2];
 #pragma unroll
-          for (int nt = 0; nt < kNt; ++nt) {
-            const float w0 = vs + kWeightTop - finite_base(mo[nt][0]), w1 = vs + kWeightTop - finite_base(mo[nt][1]);
-            pb[nt][0] = transpose_8x8_b16(pack_f16x2(fast_exp2(z[nt][0] + w0), fast_exp2(z[nt][1] + w1)));
-            pb[nt][1] = transpose_8x8_b16(pack_f16x2(fast_exp2(z[nt][2] + w0), fast_exp2(z[nt][3] + w1)));
+          for (int u = 0; u < kPp; ++u)
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt) {
+              const float w0 = fast_exp2(x[u][nt][0]), w1 = fast_exp2(x[u][nt][1]);
+              const float w2 = fast_exp2(x[u][nt][2]), w3 = fast_exp2(x[u][nt][3]);
+              l[nt][0] = fmaf(lg[u][nt][0], w0 + w2, l[nt][0]);
+              l[nt][1] = fmaf(lg[u][nt][1], w1 + w3, l[nt][1]);
+              // Weights meet V as fp16 (half a step, 2^-11 of each); l sums them unrounded.
+              pb[u][nt][0] = transpose_8x8_b16(pack_f16x2(w0, w1));
+              pb[u][nt][1] = transpose_8x8_b16(pack_f16x2(w2, w3));
+            }
+#pragma unroll
+          for (int u = 0; u < kPp; ++u) {
+            if (!mask[u] || mask_is_full(mask[u])) continue;
+            // Stale rows may hold NaN: zero them (two lanes per row).
+            const int r = lane >> 1;
+            if (!in_mask(mask[u], r))
+              for (int c = lane & 1; c < kD / 16; c += 2)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                 ring0 + sv * kSlotBytes + at[u] + row_chunk<kD>(r, c, plane)),
+                             "r"(0u)
+                             : "memory");
+            zeroed = true;
           }
-          const uint32_t va = vt + off;
+          __syncwarp();
 #pragma unroll
-          for (int i = 0; i < kD / 32; ++i) {
-            // Two chunks of 16 dims, tokens 0-7 and 8-15 of each: (2 dims of token 2 t, 2 dims of the next) a word.
-            uint32_t r[4], even[4], odd[4];
-            ldmatrix_x4_trans(r[0], r[1], r[2], r[3], (va ^ ((i & 3) << 5)) + (i >> 2) * plane);
+          for (int c = 0; c < kD / 32; ++c) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) e4m3x4_to_f16(__byte_perm(r[k], 0u, 0x3120), even[k], odd[k]);
+            for (int u = 0; u < kPp; ++u) {
+              // Two chunks of 16 dims, tokens 0-7 and 8-15 of each: (2 dims of token 2 t, 2 dims of the next) a word.
+              uint32_t r[4], even[4], odd[4];
+              ldmatrix_x4_trans(r[0], r[1], r[2], r[3],
+                                ((ring0 + sv * kSlotBytes + at[u] + off) ^ ((c & 3) << 5)) + (c >> 2) * plane);
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+              for (int k = 0; k < 4; ++k) e4m3x4_to_f16(__byte_perm(r[k], 0u, 0x3120), even[k], odd[k]);
 #pragma unroll
-              for (int nt = 0; nt < kNt; ++nt)
-                mma_f16_16816(o[2 * i + c][nt], even[2 * c], odd[2 * c], even[2 * c + 1], odd[2 * c + 1], pb[nt][0],
-                              pb[nt][1]);
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int nt = 0; nt < kNt; ++nt)
+                  mma_f16_16816(o[2 * c + k][nt], even[2 * k], odd[2 * k], even[2 * k + 1], odd[2 * k + 1],
+                                pb[u][nt][0], pb[u][nt][1]);
+            }
           }
         }
       }
@@ -440,7 +497,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
         if constexpr (kSolo) {
           // No other states: the row is final.
           const bool none = l[nt][e] == 0.f;
-          const float inv = none ? 0.f : fast_exp2(mo[nt][e] - kWeightTop - finite_base(m[nt][e])) / l[nt][e];
+          const float inv = none ? 0.f : fast_exp2(d[nt][e] - kWeightTop) / l[nt][e];
           const float lse2 = none ? -INFINITY : m[nt][e] + log2f(l[nt][e]);
           const int qr = tile_head + nt * 8 + hd, r = hc * G + qr;
 #pragma unroll
@@ -457,7 +514,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
         }
 #pragma unroll
         for (int i = 0; i < kD / 16; ++i) {
-          const float f = kSolo ? 1.f : fast_exp2(mo[nt][e] - kWeightTop - finite_base(m[nt][e]));
+          const float f = kSolo ? 1.f : fast_exp2(d[nt][e] - kWeightTop);
           *reinterpret_cast<float2*>(dst + stage_at<kD>(hd, 16 * i + 2 * g)) =
               make_float2(o[i][nt][e] * f, o[i][nt][2 + e] * f);
         }

@@ -1,12 +1,13 @@
 """Decode over an 8-bit cache on the GPU against the fp64 oracle over the values that its codes stand for.
 
-Error bounds, from the arithmetic. A query element enters as two e4m3 numbers, together within 2^-14 of it where the
-row's largest magnitude is scaled to at least 224: 2^-21 of that magnitude M. Their products with codes are exact and summed
-in fp32 (each of the D additions off by at most 2^-23 of the running magnitude, truncation allowed for, in two
-sums), then scaled in four multiplications; exp2 is good to 2^-22; a weight meets its value row as fp16 (half a
-step, 2^-11 of it, or 2^-25 where the largest product of weight and V scale is 2^14: 2^-39 of that, S, against codes up to 448)
-while l sums the unrounded ones; every other sum and the merge of splits are fp32; the output is rounded to bf16 once.
-With dz = |s| (2^-21 M max_j sum_c |k_jc| + (D + 12) 2^-23 max_j sum_c |q_c k_jc|) and A = sum_j alpha_j |v_j|,
+Error bounds, from the arithmetic. A query row is scaled by a power of two to a largest magnitude M of 224 to 448 and
+enters as fp16, exact or within 2^-25: 2^-32 of M. Its products with codes are exact and summed in fp32 (each of
+the D additions off by at most 2^-23 of the running magnitude, truncation allowed for), then scaled in three
+multiplications; exp2 is good to 2^-22; a weight meets its value row as fp16 (half a step, 2^-11 of it, or 2^-25 where the largest
+product of weight and V scale is 2^14 at least: 2^-39 of that, S, against codes up to 448) while l sums the unrounded ones;
+its exponent, up to 2^7 where the scales of pages differ widely, is rounded by 2^-18 (2^-17 of the weight, which the n + 64
+roundings below are 2^-17 or more for); every other sum and the merge of splits are fp32; the output is rounded to bf16 once.
+With dz = |s| (2^-32 M max_j sum_c |k_jc| + (D + 12) 2^-23 max_j sum_c |q_c k_jc|) and A = sum_j alpha_j |v_j|,
     |out - exact| <= (2^-11 + 2 dz + (n + 64) 2^-23) A + n 2^-39 448 S + 2^-8 |exact| (1 + 2^-7) + 2^-133,
     |lse - exact| <= dz + (n + 64) 2^-23 + 2^-21 (1 + |exact|).
 """
@@ -110,7 +111,7 @@ class Inputs:
                 w = np.exp(z - np.where(np.isneginf(rlse[b]), 0, rlse[b]).reshape(self.H, G))
                 top[b] = (w * self.s["v"].numpy()[page][:, :, None]).max(0).reshape(-1)
         n = np.array([len(op.kept_positions(L, self.sink, self.recent)) for L in self.lens])[:, None]
-        dz = abs(self.scale) * 2.0 ** -21 * np.abs(q).max(2) * kmag + (self.D + 12) * 2.0 ** -23 * zmag
+        dz = abs(self.scale) * 2.0 ** -32 * np.abs(q).max(2) * kmag + (self.D + 12) * 2.0 ** -23 * zmag
         tol = (2.0 ** -11 + 2 * dz + (n + 64) * 2.0 ** -23)[..., None] * mag + (n * 2.0 ** -39 * 448 * top)[..., None]
         tol = tol + 2.0 ** -8 * np.abs(ref) * (1 + 2.0 ** -7) + 2.0 ** -133
         ltol = dz + (n + 64) * 2.0 ** -23 + 2.0 ** -21 * (1 + np.abs(np.where(np.isneginf(rlse), 0, rlse)))
