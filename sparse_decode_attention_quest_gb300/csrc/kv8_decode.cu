@@ -70,6 +70,10 @@ __device__ __forceinline__ uint32_t row_chunk(int r, int c, uint32_t plane) {
   return (c >> 3) * plane + swz128(r, c & 7);
 }
 
+// A page's mask with its top bit set where all tokens are kept.
+constexpr uint32_t kWhole = 0x80000000u;
+__device__ __forceinline__ uint32_t tagged(uint32_t mask) { return mask_is_full(mask) ? mask | kWhole : mask; }
+
 struct Kv8Args {
   const float* k_scale;
   const float* v_scale;
@@ -200,7 +204,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
           dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
           if (dead) break;
           if (kv == 0 && lane < Pg)
-            meta[(step % kMetaRing) * kMaxPages + lane] = ok ? page_mask(k, a.sink, k.logical(i)) : 0u;
+            meta[(step % kMetaRing) * kMaxPages + lane] = ok ? tagged(page_mask(k, a.sink, k.logical(i))) : 0u;
           __syncwarp();
           if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
           __syncwarp();
@@ -233,7 +237,8 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
   const uint32_t page_bytes = (uint32_t)heads * kPageSize * kD;
   const uint32_t off = row_chunk<kD>(lane & 15, lane >> 4, plane);  // of ldmatrix: 16 rows, two chunks
   constexpr int kPp = kD <= 128 && kNt == 1 ? 2 : 1;  // pages at once
-  int j = 0, step = 0;
+  int sk = 0, step = 0;   // K's slot of the step, and the parity of its use
+  uint32_t phase = 0;
   if (warp == 0) {  // while the first copies are on their way; in shared memory, as the loop needs its registers
     const Neighbours share = neighbours_of(slices, blockIdx.x, slice);
     if (lane == 0) {
@@ -290,10 +295,12 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
       l[nt][0] = l[nt][1] = 0.f;
     }
 
-    for (int i0 = seg.lo; i0 < seg.hi; i0 += Pg, ++step, j += 2) {
-      if (!works) continue;
-      const int sk = j % kSlots, sv = (j + 1) % kSlots;
-      if (!dead && !__all_sync(0xffffffffu, mbar_wait(&full[sk], (j / kSlots) & 1))) dead = true;
+    for (int i0 = seg.lo; i0 < seg.hi && works; i0 += Pg, ++step) {
+      const bool wraps = sk + 1 == kSlots;
+      const int sv = wraps ? 0 : sk + 1;
+      const uint32_t phase_v = phase ^ (uint32_t)wraps;
+      if (!dead && !__all_sync(0xffffffffu, mbar_wait(&full[sk], phase))) dead = true;
+      const uint32_t* masks = meta + (step % kMetaRing) * kMaxPages;
       bool v_here = false, zeroed = false;
       for (int pg0 = replica; pg0 < Pg; pg0 += kPp * a.replicas) {
         uint32_t mask[kPp], at[kPp];  // the page's kept tokens, and where its block begins in its slot
@@ -302,7 +309,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
 #pragma unroll
         for (int u = 0; u < kPp; ++u) {
           const int pg = pg0 + u * a.replicas;
-          mask[u] = dead || pg >= Pg || i0 + pg >= seg.hi ? 0u : meta[(step % kMetaRing) * kMaxPages + pg];
+          mask[u] = dead || pg >= Pg ? 0u : masks[pg];
           blk[u] = pg * heads + hc;
           at[u] = pg * page_bytes + hc * (kPageSize * min(kD, 128));
           any = any || mask[u];
@@ -313,6 +320,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
           if (!mask[1]) blk[1] = blk[0], at[1] = at[0];
         }
         const bool last = pg0 + kPp * a.replicas >= Pg;
+        const bool whole = (mask[0] & mask[kPp - 1] & kWhole) != 0;
         // Products of tokens g (0, 1) and g + 8 (2, 3), heads 2 t and 2 t + 1, times their factors; K's scale.
         float s[kPp][kNt][4], ks[kPp];
         if (any) {
@@ -343,13 +351,17 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
 #pragma unroll
           for (int u = 0; u < kPp; ++u) {
             ks[u] = scales[sk * C::kBlocks + blk[u]];
-            const bool whole = mask_is_full(mask[u]);
-            const bool k0 = whole || in_mask(mask[u], g), k1 = whole || in_mask(mask[u], g + 8);
 #pragma unroll
             for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                s[u][nt][e] = (e < 2 ? k0 : k1) ? s[u][nt][e] * zf[nt][e & 1] : -INFINITY;
+              for (int e = 0; e < 4; ++e) s[u][nt][e] *= zf[nt][e & 1];
+            if (!whole) {
+              const bool k0 = in_mask(mask[u] & ~kWhole, g), k1 = in_mask(mask[u] & ~kWhole, g + 8);
+#pragma unroll
+              for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[u][nt][e] = (e < 2 ? k0 : k1) ? s[u][nt][e] : -INFINITY;
+            }
           }
         }
         if (last) {
@@ -357,7 +369,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
           if (lane == 0) mbar_arrive(&empty[sk]);
         }
         if (!v_here) {
-          if (!dead && !__all_sync(0xffffffffu, mbar_wait(&full[sv], ((j + 1) / kSlots) & 1))) dead = true;
+          if (!dead && !__all_sync(0xffffffffu, mbar_wait(&full[sv], phase_v))) dead = true;
           v_here = true;
         }
         if (any && !dead) {
@@ -431,20 +443,22 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
               pb[u][nt][0] = transpose_8x8_b16(pack_f16x2(w0, w1));
               pb[u][nt][1] = transpose_8x8_b16(pack_f16x2(w2, w3));
             }
+          if (!whole) {
 #pragma unroll
-          for (int u = 0; u < kPp; ++u) {
-            if (!mask[u] || mask_is_full(mask[u])) continue;
-            // Stale rows may hold NaN: zero them (two lanes per row).
-            const int r = lane >> 1;
-            if (!in_mask(mask[u], r))
-              for (int c = lane & 1; c < kD / 16; c += 2)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                 ring0 + sv * kSlotBytes + at[u] + row_chunk<kD>(r, c, plane)),
-                             "r"(0u)
-                             : "memory");
-            zeroed = true;
+            for (int u = 0; u < kPp; ++u) {
+              if (!mask[u] || (mask[u] & kWhole)) continue;
+              // Stale rows may hold NaN: zero them (two lanes per row).
+              const int r = lane >> 1;
+              if (!in_mask(mask[u], r))
+                for (int c = lane & 1; c < kD / 16; c += 2)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                   ring0 + sv * kSlotBytes + at[u] + row_chunk<kD>(r, c, plane)),
+                               "r"(0u)
+                               : "memory");
+              zeroed = true;
+            }
+            __syncwarp();
           }
-          __syncwarp();
 #pragma unroll
           for (int c = 0; c < kD / 32; ++c) {
 #pragma unroll
@@ -468,6 +482,8 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
       if (zeroed) fence_proxy_async_smem();  // before the next copy into the slot
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[sv]);
+      sk = sv + 1 == kSlots ? 0 : sv + 1;
+      phase = phase_v ^ (uint32_t)(sk == 0);
     }
 
     // ---- the end of a segment: this CTA's share of item (b, hg) is done
