@@ -582,23 +582,22 @@ def se_rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str =
 
 
 def _rotary_side(x, out, name: str, tokens: int, dev: int):
-    """(rows, stride, heads, output, its stride) of the queries or keys of se_rotary."""
-    if x is None:
-        if out is not None:
-            raise ValueError(f"{name}_out: without {name}")
-        return None, 0, 0, None, 0
+    """(rows, stride, heads, output, its stride, head_dim) of the queries or keys of se_rotary."""
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError(f"{name}: expected [tokens][heads][head_dim]")
-    heads, dim = x.shape[1], x.shape[2]
-    if x.shape[0] != tokens:
-        raise ValueError(f"{name}: expected {tokens} rows, got {x.shape[0]}")
+    rows, heads, dim = x.shape
+    if rows != tokens:
+        raise ValueError(f"{name}: expected {tokens} rows, got {rows}")
     p, stride = _rows_ptr(x, heads, dim, torch.bfloat16, name, dev)
     if out is None or out is x:
-        return p, stride, heads, p, stride
+        return p, stride, heads, p, stride, dim
     po, so = _rows_ptr(out, heads, dim, torch.bfloat16, name + "_out", dev)
     if out.shape[0] != tokens:
         raise ValueError(f"{name}_out: expected {tokens} rows, got {out.shape[0]}")
-    return p, stride, heads, po, so
+    return p, stride, heads, po, so, dim
+
+
+_NO_ROWS = (None, 0, 0, None, 0, None)
 
 
 def se_rotary(q, k, positions, freqs, q_out=None, k_out=None, rotary_offset: int = 0, interleaved: bool = False,
@@ -609,13 +608,16 @@ def se_rotary(q, k, positions, freqs, q_out=None, k_out=None, rotary_offset: int
     lib, dev = load_library(), torch.cuda.current_device()
     pp = _arg(positions, torch.int32, "positions", dev)
     tokens = positions.numel()
-    qp, qs, hq, qo, qos = _rotary_side(q, q_out, "q", tokens, dev)
-    kp, ks, hk, ko, kos = _rotary_side(k, k_out, "k", tokens, dev)
-    if q is None and k is None:
-        raise ValueError("q, k: neither is given")
-    dim = (k if q is None else q).shape[2]
-    if q is not None and k is not None and k.shape[2] != dim:
-        raise ValueError(f"k: expected rows of {dim} dims, got {k.shape[2]}")
+    if (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError("q_out, k_out: an output without its rows")
+    qp, qs, hq, qo, qos, dim = _NO_ROWS if q is None else _rotary_side(q, q_out, "q", tokens, dev)
+    kp, ks, hk, ko, kos, k_dim = _NO_ROWS if k is None else _rotary_side(k, k_out, "k", tokens, dev)
+    if dim is None:
+        if k_dim is None:
+            raise ValueError("q, k: neither is given")
+        dim = k_dim
+    elif k_dim is not None and k_dim != dim:
+        raise ValueError(f"k: expected rows of {dim} dims, got {k_dim}")
     _check(lib.se_rotary(qp, qs, hq, kp, ks, hk, dim, rotary_offset, 2 * freqs.numel(),
                          (1 if interleaved else 0) | (2 if inverse else 0), _arg(freqs, torch.int64, "freqs", dev),
                          amplitude, pp, None if num_valid is None else _vec(num_valid, 1, torch.int32, "num_valid", dev),

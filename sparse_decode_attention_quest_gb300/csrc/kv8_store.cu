@@ -49,6 +49,62 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
   return to_e4m3x4(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
 }
 
+// Eight values with NaN for infinities, which the conversion alone would take to 448.
+__device__ __forceinline__ uint4 without_inf(uint4 x) {
+  return make_uint4(x.x | not_finite_bf16x2(x.x), x.y | not_finite_bf16x2(x.y), x.z | not_finite_bf16x2(x.z),
+                    x.w | not_finite_bf16x2(x.w));
+}
+
+// A run of n tokens of one page and KV head, by a warp: lane's columns of the page and of the first token's row.
+template <int kD>
+struct Run {
+  uint8_t* rows;
+  const uint16_t* from;
+  long long stride;
+  float* scale;
+  int n, sub, lane;
+
+  // The page's scale for rows whose largest magnitudes the lanes hold, and which slots they take; the other slots'
+  // codes follow. Returns its reciprocal; loud: there are infinities among them.
+  __device__ __forceinline__ float take_scale(uint32_t amax, uint32_t written, bool& loud) const {
+    constexpr int kRows = 256 / kD;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = max_abs_bf16x2(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    uint32_t top = max(amax & 0xffffu, amax >> 16);
+    loud = top >= 0x7f80u;
+    if (loud) {
+      // The largest finite magnitude instead, the same for all lanes.
+      uint32_t m = 0;
+      for (int k = sub; k < n; k += kRows) {
+        const uint4 y = ld_stream_v4(reinterpret_cast<const uint4*>(from + k * stride));
+        m = max_abs_bf16x8(m, make_uint4(y.x & ~not_finite_bf16x2(y.x), y.y & ~not_finite_bf16x2(y.y),
+                                         y.z & ~not_finite_bf16x2(y.z), y.w & ~not_finite_bf16x2(y.w)));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
+      top = max(m & 0xffffu, m >> 16);
+    }
+    float s = scale_for(top);
+    if (written & 1u) {
+      if (lane == 0) *scale = s;
+    } else {
+      const float old = *scale;
+      s = fmaxf(s, old);
+      if (s != old) {
+        const float ratio = old / s;
+        for (int r = sub; r < kPageSize; r += kRows) {
+          if (written >> r & 1u) continue;
+          uint2* c = reinterpret_cast<uint2*>(rows + r * kD);
+          *c = make_uint2(rescale4(c->x, ratio), rescale4(c->y, ratio));
+        }
+        __syncwarp();
+        if (lane == 0) *scale = s;
+      }
+    }
+    return 1.f / s;
+  }
+};
+
 template <int kD>
 __global__ void __launch_bounds__(kWarps * 32, kD == 256 ? 2 : 3) kv8_store_kernel(const Kv8StoreArgs a) {
   constexpr int kLanes = kD / 8;          // lanes of a row, 8 dims each
@@ -83,8 +139,7 @@ __global__ void __launch_bounds__(kWarps * 32, kD == 256 ? 2 : 3) kv8_store_kern
     runs &= runs - 1;
     const int page = __shfl_sync(0xffffffffu, pg, i0);
     const size_t block = (size_t)page * a.kv.num_kv_heads + h;
-    uint8_t* rows = cache + block * kPageSize * kD;
-    const float old = scales[block];
+    uint8_t* rows = cache + block * kPageSize * kD + x0;
     // The run's length: as far as the lanes see it, and from memory behind them.
     const uint32_t same = __ballot_sync(0xffffffffu, pg == page) >> i0;
     const int seen = same == (0xffffffffu >> i0) ? 32 - i0 : __ffs(~same) - 1;
@@ -97,71 +152,55 @@ __global__ void __launch_bounds__(kWarps * 32, kD == 256 ? 2 : 3) kv8_store_kern
     // Rows one after another in the page, as a slot map built from lengths has them.
     const bool ordered = n == seen && (inrow & ((1u << seen) - 1)) == (1u << seen) - 1;
     const int r0 = s0 % kPageSize;
-    uint4 x[kLoads];
-    uint32_t amax = 0, written = 0;
-    if (ordered) {
-      written = ((1u << n) - 1) << r0;
+    const Run<kD> run{rows, from, stride, scales + block, n, sub, lane};
+    if (ordered && n == kPageSize) {
+      uint4 x[kLoads];
+      const uint16_t* p = from + sub * stride;
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u, p += kRows * stride) x[u] = ld_stream_v4(reinterpret_cast<const uint4*>(p));
+      uint32_t amax = 0;
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) amax = max_abs_bf16x8(amax, x[u]);
+      bool loud;
+      const float inv = run.take_scale(amax, 0xffffu, loud);
+      uint8_t* q = rows + sub * kD;
+      if (loud)
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) x[u] = without_inf(x[u]);
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) *reinterpret_cast<uint2*>(q + u * kRows * kD) = quantise8(x[u], inv);
+    } else if (ordered) {
+      uint4 x[kLoads];
 #pragma unroll
       for (int u = 0; u < kLoads; ++u) {
         x[u] = make_uint4(0u, 0u, 0u, 0u);
         if (u * kRows + sub < n) x[u] = ld_stream_v4(reinterpret_cast<const uint4*>(from + (u * kRows + sub) * stride));
       }
+      uint32_t amax = 0;
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) amax = max_abs_bf16x8(amax, x[u]);
+      bool loud;
+      const float inv = run.take_scale(amax, ((1u << n) - 1) << r0, loud);
 #pragma unroll
       for (int u = 0; u < kLoads; ++u)
-        amax = max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(amax, x[u].x), x[u].y), x[u].z), x[u].w);
+        if (u * kRows + sub < n)
+          *reinterpret_cast<uint2*>(rows + (r0 + u * kRows + sub) * kD) = quantise8(loud ? without_inf(x[u]) : x[u], inv);
     } else {
       // Rows in any order, and a run of more tokens than a page has (slots named twice).
+      uint32_t amax = 0, written = 0;
       for (int k = 0; k < n; ++k) {
         written |= 1u << a.slot_map[first + k] % kPageSize;
-        if (sub == 0) {
-          const uint4 y = ld_stream_v4(reinterpret_cast<const uint4*>(from + k * stride));
-          amax = max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(amax, y.x), y.y), y.z), y.w);
-        }
+        if (sub == 0) amax = max_abs_bf16x8(amax, ld_stream_v4(reinterpret_cast<const uint4*>(from + k * stride)));
+      }
+      bool loud;
+      const float inv = run.take_scale(amax, written, loud);
+      if (sub > 0) continue;
+      for (int k = 0; k < n; ++k) {
+        const uint4 x = ld_stream_v4(reinterpret_cast<const uint4*>(from + k * stride));
+        *reinterpret_cast<uint2*>(rows + a.slot_map[first + k] % kPageSize * kD) =
+            quantise8(loud ? without_inf(x) : x, inv);
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = max_abs_bf16x2(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    uint32_t top = max(amax & 0xffffu, amax >> 16);
-    bool loud = top >= 0x7f80u;
-    if (loud) {
-      // An infinity (or nothing but NaN): the largest finite magnitude instead, the same for all lanes.
-      uint32_t m = 0;
-      for (int k = sub; k < n; k += kRows) {
-        const uint4 y = ld_stream_v4(reinterpret_cast<const uint4*>(from + k * stride));
-        m = max_abs_bf16x2(max_abs_bf16x2(m, y.x & ~not_finite_bf16x2(y.x)), y.y & ~not_finite_bf16x2(y.y));
-        m = max_abs_bf16x2(max_abs_bf16x2(m, y.z & ~not_finite_bf16x2(y.z)), y.w & ~not_finite_bf16x2(y.w));
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
-      top = max(m & 0xffffu, m >> 16);
-    }
-    const bool opened = written & 1u;
-    const float need = scale_for(top), scale = opened ? need : fmaxf(need, old);
-    if (!opened && scale != old) {
-      const float ratio = old / scale;
-      for (int r = sub; r < kPageSize; r += kRows) {
-        if (written >> r & 1u) continue;
-        uint2* c = reinterpret_cast<uint2*>(rows + r * kD + x0);
-        *c = make_uint2(rescale4(c->x, ratio), rescale4(c->y, ratio));
-      }
-    }
-    const float inv = 1.f / scale;
-    // An infinity becomes NaN: the conversion alone would take it to 448.
-    auto put = [&](int row, uint4 y) {
-      if (loud)
-        y = make_uint4(y.x | not_finite_bf16x2(y.x), y.y | not_finite_bf16x2(y.y), y.z | not_finite_bf16x2(y.z),
-                       y.w | not_finite_bf16x2(y.w));
-      *reinterpret_cast<uint2*>(rows + row * kD + x0) = quantise8(y, inv);
-    };
-    if (ordered) {
-#pragma unroll
-      for (int u = 0; u < kLoads; ++u)
-        if (u * kRows + sub < n) put(r0 + u * kRows + sub, x[u]);
-    } else if (sub == 0) {
-      for (int k = 0; k < n; ++k)
-        put(a.slot_map[first + k] % kPageSize, ld_stream_v4(reinterpret_cast<const uint4*>(from + k * stride)));
-    }
-    if (lane == 0 && scale != old) scales[block] = scale;
   }
 }
 
@@ -180,10 +219,10 @@ struct Kv8LoadArgs {
 };
 
 template <int kD>
-__global__ void __launch_bounds__(kLoadThreads) kv8_load_kernel(const Kv8LoadArgs a) {
+__global__ void __launch_bounds__(kLoadThreads, 3) kv8_load_kernel(const Kv8LoadArgs a) {
   constexpr int kLanes = kD / 16;        // lanes of a row, 16 codes each
   constexpr int kRows = 32 / kLanes;     // rows of a warp's load
-  constexpr int kLoads = 4;              // loads in flight
+  constexpr int kLoads = 8;              // loads in flight
   __shared__ int slots[kMaxWindow];      // of the window's rows, -1: none
   pdl_enter();
   const int total = min(a.token_start[a.batch], a.num_rows), t0 = blockIdx.x * a.window;

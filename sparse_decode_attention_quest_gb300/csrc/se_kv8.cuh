@@ -7,9 +7,12 @@ namespace se {
 
 // Larger of the magnitudes so far and a word's two; a NaN beside a number is dropped.
 __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t m, uint32_t x) {
-  const uint32_t ax = x & 0x7fff7fffu;
-  __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&m), *reinterpret_cast<const __nv_bfloat162*>(&ax));
+  const __nv_bfloat162 a = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x));
+  __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&m), a);
   return *reinterpret_cast<uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t max_abs_bf16x8(uint32_t m, uint4 x) {
+  return max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(m, x.x), x.y), x.z), x.w);
 }
 
 // A word's infinities and NaN, by mask 0xffff each.
