@@ -1153,7 +1153,7 @@ se_status_t se_paged_kv8_decode(const se_paged_kv8_t* kv, const void* q, int64_t
   if (e != cudaSuccess) return cuda_fail(fn, e);
   const long long rows = (long long)std::max(1, kv->num_pages) * kv->num_kv_heads * se::kPageSize;
   const int box = se::kPageSize * se::kv8_decode_box_heads(kv->num_kv_heads, num_q_heads, kv->head_dim, bt_stride,
-                                                           sink_tokens, recent_tokens, d->sm_count);
+                                                           sink_tokens, recent_tokens, batch, d->sm_count);
   CUtensorMap kmap, vmap;
   if (!encode_byte_rows_map(&kmap, kv->k, rows, kv->head_dim, box) ||
       !encode_byte_rows_map(&vmap, kv->v, rows, kv->head_dim, box))

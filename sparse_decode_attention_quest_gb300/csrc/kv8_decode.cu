@@ -44,6 +44,7 @@ constexpr int kMaxPages = 32;    // pages of a step
 constexpr int kMaxBatch = 4096;  // requests whose prefix fits beside the ring
 constexpr int kInlineBytes = 48 * 1024;  // partials of an item, in slices, where one CTA merges them
 constexpr int kInlineWidth = 32;          // pages of an item from which smaller boxes are taken for that
+constexpr long long kSmallBoxBytes = 128 << 20;  // codes of a full table up to which they are
 
 constexpr float kWeightTop = 14.f;    // log2 of the weight at the reference
 constexpr float kWeightMost = 15.9f;  // log2 of the largest weight, within fp16
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
   const uint32_t plane = (uint32_t)heads * kPageSize * 128;  // 128 dims of a page's rows
   const uint32_t page_bytes = (uint32_t)heads * kPageSize * kD;
   const uint32_t off = row_chunk<kD>(lane & 15, lane >> 4, plane);  // of ldmatrix: 16 rows, two chunks
-  constexpr int kPp = kD <= 128 && kNt == 1 ? 2 : 1;  // pages at once
+  constexpr int kPp = kNt > 1 || kD > 128 ? 1 : kD == 128 ? 2 : 4;  // pages at once
   int sk = 0, step = 0;   // K's slot of the step, and the parity of its use
   uint32_t phase = 0;
   if (warp == 0) {  // while the first copies are on their way; in shared memory, as the loop needs its registers
@@ -314,13 +315,21 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
           at[u] = pg * page_bytes + hc * (kPageSize * min(kD, 128));
           any = any || mask[u];
         }
-        if constexpr (kPp == 2) {
-          // A page that is not there is the other one over again, without a weight.
-          if (!mask[0]) blk[0] = blk[1], at[0] = at[1];
-          if (!mask[1]) blk[1] = blk[0], at[1] = at[0];
+        if constexpr (kPp > 1) {
+          // A page that is not there is another one over again, without a weight.
+          int there = 0, there_at = 0;
+#pragma unroll
+          for (int u = kPp - 1; u >= 0; --u)
+            if (mask[u]) there = blk[u], there_at = at[u];
+#pragma unroll
+          for (int u = 0; u < kPp; ++u)
+            if (!mask[u]) blk[u] = there, at[u] = there_at;
         }
         const bool last = pg0 + kPp * a.replicas >= Pg;
-        const bool whole = (mask[0] & mask[kPp - 1] & kWhole) != 0;
+        uint32_t all = kWhole;
+#pragma unroll
+        for (int u = 0; u < kPp; ++u) all &= mask[u];
+        const bool whole = all != 0;
         // Products of tokens g (0, 1) and g + 8 (2, 3), heads 2 t and 2 t + 1, times their factors; K's scale.
         float s[kPp][kNt][4], ks[kPp];
         if (any) {
@@ -652,13 +661,14 @@ HeadPlan head_plan(int num_kv_heads, int group, int head_dim, int most_heads) {
 // The largest boxes, unless the table's (or the windows') width keeps an item's partials, counted in slices of the
 // least length, so few that smaller ones let the decode kernel join them. Not for short items, which are seldom split.
 HeadPlan call_plan(int num_kv_heads, int group, int head_dim, int32_t bt_stride, int32_t sink_tokens,
-                   int32_t recent_tokens, int ctas) {
+                   int32_t recent_tokens, int batch, int ctas) {
   long long width = bt_stride;
   if (recent_tokens > 0)
     width = std::min(width, ((long long)sink_tokens + kPageSize - 1) / kPageSize + recent_tokens / kPageSize + 2);
+  const bool little = batch * width * num_kv_heads * kPageSize * head_dim * 2 <= kSmallBoxBytes;
   for (int c = 8; c > 0;) {
     HeadPlan p = head_plan(num_kv_heads, group, head_dim, c);
-    if (c < 8 && width < kInlineWidth) break;
+    if (c < 8 && (width < kInlineWidth || !little)) break;
     const long long parts = std::min<long long>(ctas, (width + p.step_pages) / (2 * p.step_pages + 1) + 2);
     p.deferred = parts * p.heads * group * head_dim * (long long)sizeof(float) > kInlineBytes;
     if (!p.deferred) return p;
@@ -709,8 +719,8 @@ bool kv8_decode_supported(int num_kv_heads, int head_dim, int num_q_heads) {
 }
 
 int kv8_decode_box_heads(int num_kv_heads, int num_q_heads, int head_dim, int32_t bt_stride, int32_t sink_tokens,
-                           int32_t recent_tokens, int sm_count) {
-  return call_plan(num_kv_heads, num_q_heads / num_kv_heads, head_dim, bt_stride, sink_tokens, recent_tokens,
+                         int32_t recent_tokens, int batch, int sm_count) {
+  return call_plan(num_kv_heads, num_q_heads / num_kv_heads, head_dim, bt_stride, sink_tokens, recent_tokens, batch,
                    ctas_of(sm_count)).heads;
 }
 
@@ -727,7 +737,7 @@ cudaError_t launch_kv8_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, 
                                 int sm_count, unsigned* err, cudaStream_t stream) {
   const int group = num_q_heads / kv.num_kv_heads;
   const int grid = ctas_of(sm_count);
-  const HeadPlan p = call_plan(kv.num_kv_heads, group, kv.head_dim, bt_stride, sink_tokens, recent_tokens, grid);
+  const HeadPlan p = call_plan(kv.num_kv_heads, group, kv.head_dim, bt_stride, sink_tokens, recent_tokens, batch, grid);
   Kv8Args a;
   a.k_scale = kv.k_scale;
   a.v_scale = kv.v_scale;

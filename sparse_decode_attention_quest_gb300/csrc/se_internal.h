@@ -238,7 +238,7 @@ int kv8_decode_max_batch();
 bool kv8_decode_supported(int num_kv_heads, int head_dim, int num_q_heads);
 // KV heads per TMA box of a call.
 int kv8_decode_box_heads(int num_kv_heads, int num_q_heads, int head_dim, int32_t bt_stride, int32_t sink_tokens,
-                         int32_t recent_tokens, int sm_count);
+                         int32_t recent_tokens, int batch, int sm_count);
 size_t kv8_decode_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim);
 // kmap, vmap: the caches as (128 bytes, line, 128-byte chunk of a row), 128-byte swizzle; a line is a row (two rows of
 // 64 dims), a box the lines of a page's kv8_decode_box_heads heads, all chunks.
