@@ -63,6 +63,11 @@ struct Cfg {
   static constexpr int kMaxSmem = kFixed + kept_ints(kMaxBatch) * 4;
 };
 
+// Pages that a warp takes at once.
+__host__ __device__ constexpr int pages_at_once(int head_dim, int tiles) {
+  return tiles > 1 || head_dim > 128 ? 1 : head_dim == 128 ? 2 : 4;
+}
+
 // Byte offset of 16-byte chunk c of a block's row r: lines of 128 bytes, swizzled, `plane` bytes between the lines'
 // first and second 128 bytes of a row; two rows of 64 dims share a line.
 template <int kD>
@@ -237,7 +242,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
   const uint32_t plane = (uint32_t)heads * kPageSize * 128;  // 128 dims of a page's rows
   const uint32_t page_bytes = (uint32_t)heads * kPageSize * kD;
   const uint32_t off = row_chunk<kD>(lane & 15, lane >> 4, plane);  // of ldmatrix: 16 rows, two chunks
-  constexpr int kPp = kNt > 1 || kD > 128 ? 1 : kD == 128 ? 2 : 4;  // pages at once
+  constexpr int kPp = pages_at_once(kD, kNt);
   int sk = 0, step = 0;   // K's slot of the step, and the parity of its use
   uint32_t phase = 0;
   if (warp == 0) {  // while the first copies are on their way; in shared memory, as the loop needs its registers
@@ -640,18 +645,29 @@ struct HeadPlan {
 // Query heads per KV head up to which a tile holds eight of them, above it sixteen.
 int eights_up_to(int head_dim) { return head_dim == 256 ? 64 : 8; }
 
-// As many heads per box as leave at most an eighth of a slot empty, and no more than `most_heads`.
+// The KV heads of a box, up to `most_heads`: the count that the slower of copies and warps lets run fastest, the larger
+// of two alike. Boxes of 1 KB read at 48% of the measured copy rate, of 2 KB at 72%, from 4 KB on at 89%; every
+// warp that has pages carries an eighth of it (0.6 GB, 16K tokens a request: 7 heads of 128 dims 87% in one box, 5
+// heads 67%, 10 heads 89% in pairs, 67% in fives and 72% alone). A warp's pages are whole sets of those it takes at once.
 HeadPlan head_plan(int num_kv_heads, int group, int head_dim, int most_heads) {
   const int warps = Cfg<128>::kWarps, blocks = kSlotBytes / (kPageSize * head_dim);
+  const bool sixteens = group > eights_up_to(head_dim);
+  const int once = pages_at_once(head_dim, sixteens ? 2 : 1);
   HeadPlan p;
-  p.mtiles = group <= eights_up_to(head_dim) ? (group + 7) / 8 : (group + 15) / 16;
+  p.mtiles = sixteens ? (group + 15) / 16 : (group + 7) / 8;
+  int best = 0;
   for (int c = 1; c <= most_heads && c * p.mtiles <= warps; ++c) {
     if (num_kv_heads % c) continue;
-    const int r = warps / (c * p.mtiles), pages = blocks / c / r * r;
-    if (c > 1 && pages * c * 8 < blocks * 7) continue;
+    const int r = warps / (c * p.mtiles), box = c * kPageSize * head_dim;
+    int each = blocks / c / r;
+    if (each > once) each -= each % once;
+    const int copies = box >= 4096 ? 89 : box > 2048 ? 80 : box == 2048 ? 72 : 48;
+    const int rate = std::min(copies, c * p.mtiles * r * 100 / warps);
+    if (each == 0 || rate < best) continue;
+    best = rate;
     p.heads = c;
     p.replicas = r;
-    p.step_pages = pages;
+    p.step_pages = each * r;
   }
   p.head_groups = num_kv_heads / p.heads;
   p.deferred = true;
