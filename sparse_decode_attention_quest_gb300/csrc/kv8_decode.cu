@@ -147,11 +147,10 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
     tma_prefetch_map(&vmap);
   }
   pdl_enter();
-  // Pieces of a step: of up to eight query heads a CTA takes a second one in less time than more partials take to
-  // join (1 x 1,000 tokens, 8 KV heads: 10.6 us with 32 partials an item, 10.0 with 16), of more it does not (1 x 4K,
-  // 32 heads over one: 14.6 us with 32, 17.8 with 16).
+  // Pieces of a step: up to 32 partials an item, rather than two steps for a CTA (1 x 4K tokens, 4 heads over one: 9.5 us,
+  // 10.6 in eights; 32 over 8: 10.5 and 13.2).
   const int piece = kept_prefix<C::kThreads>(a.seq_lens, a.batch, HG, a.bt_stride, a.sink, a.recent, Pg, Pg,
-                                             G > 8 ? 32 : 8, gridDim.x, kMaxPlaces / HG, prefix, lens,
+                                             32, gridDim.x, kMaxPlaces / HG, prefix, lens,
                                              reinterpret_cast<long long*>(stage), a.err);
   // Requests without a kept token: the empty sum.
   for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
@@ -266,22 +265,19 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
       const bool real = works && hd < G;
       const int row = (seg.group * heads + hc) * G + (real ? hd : 0);
       const uint16_t* qr = a.q + (size_t)seg.b * a.q_stride + (size_t)row * kD + 4 * t;
-      uint32_t top = 0, odd = 0;
+      uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < kD / 16; ++i) {
         const uint2 x = real ? *reinterpret_cast<const uint2*>(qr + i * 16) : make_uint2(0u, 0u);
         qb[i][nt][0] = x.x;
         qb[i][nt][1] = x.y;
-        top = max_abs_bf16x2(max_abs_bf16x2(top, x.x), x.y);
-        odd |= not_finite_bf16x2(x.x) | not_finite_bf16x2(x.y);
+        top = max_abs_nan_bf16x2(max_abs_nan_bf16x2(top, x.x), x.y);
       }
 #pragma unroll
-      for (int x = 1; x < 4; x <<= 1) {
-        top = max_abs_bf16x2(top, __shfl_xor_sync(0xffffffffu, top, x));
-        odd |= __shfl_xor_sync(0xffffffffu, odd, x);
-      }
+      for (int x = 1; x < 4; x <<= 1) top = max_abs_nan_bf16x2(top, __shfl_xor_sync(0xffffffffu, top, x));
+      top = max(top & 0xffffu, top >> 16);
       // A row that is not finite is NaN throughout.
-      const float qs = odd ? 1.f : scale_for(max(top & 0xffffu, top >> 16)), inv = odd ? NAN : 1.f / qs;
+      const float qs = scale_for(top < 0x7f80u ? top : 0u), inv = top < 0x7f80u ? fast_rcp(qs) : NAN;
 #pragma unroll
       for (int i = 0; i < kD / 16; ++i)
 #pragma unroll
@@ -527,8 +523,8 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
         if constexpr (kSolo) {
           // No other states: the row is final.
           const bool none = l[nt][e] == 0.f;
-          const float inv = none ? 0.f : fast_exp2(d[nt][e] - kWeightTop) / l[nt][e];
-          const float lse2 = none ? -INFINITY : m[nt][e] + log2f(l[nt][e]);
+          const float inv = none ? 0.f : fast_exp2(d[nt][e] - kWeightTop) * fast_rcp(l[nt][e]);
+          const float lse2 = none ? -INFINITY : m[nt][e] + fast_log2(l[nt][e]);
           const int qr = tile_head + nt * 8 + hd, r = hc * G + qr;
 #pragma unroll
           for (int i = 0; i < kD / 16; ++i) {
@@ -557,7 +553,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
       const size_t r0 = hc * G + tile_head + nt * 8;
       if constexpr (kSolo) {
         __syncwarp();
-#pragma unroll 4
+#pragma unroll 1
         for (int e = lane; e < hds * (kD / 4); e += 32) {
           const int d = e % (kD / 4) * 4, hd = e / (kD / 4);
           const float4 v = *reinterpret_cast<const float4*>(dst + stage_at<kD>(hd, d));
@@ -570,7 +566,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
         continue;
       }
       named_bar_sync(2 + 2 * combo, threads);
-#pragma unroll 4
+#pragma unroll 1
       for (int e = replica * 32 + lane; e < hds * (kD / 4); e += threads) {
         const int d = e % (kD / 4) * 4, hd = e / (kD / 4);
         float M = -INFINITY;
@@ -585,7 +581,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
           acc = make_float4(acc.x + f * v.x, acc.y + f * v.y, acc.z + f * v.z, acc.w + f * v.w);
         }
         const bool none = sum == 0.f;
-        const float inv = none ? 0.f : 1.f / sum, lse2 = none ? -INFINITY : M + log2f(sum);
+        const float inv = none ? 0.f : fast_rcp(sum), lse2 = none ? -INFINITY : M + fast_log2(sum);
         const size_t r = r0 + hd;
         acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         if (split)
@@ -631,7 +627,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
     const int first = s ? (int)blockIdx.x : first0, parts = s ? parts1 : parts0, item = flags[2 + s];
     const int warps = min(C::kWarps, share_of(parts));
     for (int r0 = 0; r0 < rows; r0 += C::kWarps / warps)
-      join_rows<kD, C::kWarps>(a.o_part, a.lse_part, first, parts, item, rows, r0, warps, *join_smem, a.out,
+      join_rows<kD, C::kWarps, 4, true>(a.o_part, a.lse_part, first, parts, item, rows, r0, warps, *join_smem, a.out,
                                a.out_lse, [] { named_bar_sync(1, C::kConsumers); });
   }
 }
@@ -642,8 +638,11 @@ struct HeadPlan {
   bool deferred;
 };
 
-// Query heads per KV head up to which a tile holds eight of them, above it sixteen.
-int eights_up_to(int head_dim) { return head_dim == 256 ? 64 : 8; }
+// Query heads per KV head up to which a tile holds eight of them, above it (128 dims alone) sixteen. Sixteen
+// share the conversions of K and V but take one page at a time and spill: of 0.3 GB in 16K tokens a request, 32 heads
+// over one 134 us against 156, 16 heads over each of 4 82 against 76; 32 requests of 2K tokens with 16 heads over each
+// of 4 42 against 32. Of 64 dims 64 heads over one 309 against 313, those 32 requests 34 against 28.
+int eights_up_to(int head_dim) { return head_dim == 128 ? 16 : 64; }
 
 // The KV heads of a box, up to `most_heads`: the count that the slower of copies and warps lets run fastest, the larger
 // of two alike. Boxes of 1 KB read at 48% of the measured copy rate, of 2 KB at 72%, from 4 KB on at 89%; every
@@ -719,7 +718,7 @@ cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8Ar
   if (a.group <= 8 * a.mtiles)
     return solo ? launch_as<kD, 1, true>(kmap, vmap, a, grid, stream)
                 : launch_as<kD, 1, false>(kmap, vmap, a, grid, stream);
-  if constexpr (kD < 256)  // 256 dims: tiles of eight alone
+  if constexpr (kD == 128)  // the others have tiles of eight alone
     return solo ? launch_as<kD, 2, true>(kmap, vmap, a, grid, stream)
                 : launch_as<kD, 2, false>(kmap, vmap, a, grid, stream);
   return cudaErrorInvalidValue;

@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
     const int first = s ? (int)blockIdx.x : first0, parts = s ? parts1 : parts0, item = flags[2 + s];
     const int warps = min(C::kWarps, share_of(parts));
     for (int r0 = 0; r0 < rows; r0 += C::kWarps / warps)
-      join_rows<kD, C::kWarps>(a.o_part, a.lse_part, first, parts, item, rows, r0, warps, *join_smem, a.out,
+      join_rows<kD, C::kWarps, 8, false>(a.o_part, a.lse_part, first, parts, item, rows, r0, warps, *join_smem, a.out,
                                a.out_lse, [] { named_bar_sync(1, C::kConsumers); });
   }
 }

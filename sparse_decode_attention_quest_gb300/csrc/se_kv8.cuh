@@ -15,6 +15,13 @@ __device__ __forceinline__ uint32_t max_abs_bf16x8(uint32_t m, uint4 x) {
   return max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(m, x.x), x.y), x.z), x.w);
 }
 
+// The same with NaN above all numbers.
+__device__ __forceinline__ uint32_t max_abs_nan_bf16x2(uint32_t m, uint32_t x) {
+  const __nv_bfloat162 a = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x));
+  __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&m), a);
+  return *reinterpret_cast<uint32_t*>(&r) & 0x7fff7fffu;
+}
+
 // A word's infinities and NaN, by mask 0xffff each.
 __device__ __forceinline__ uint32_t not_finite_bf16x2(uint32_t x) {
   return ((x & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((x & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);

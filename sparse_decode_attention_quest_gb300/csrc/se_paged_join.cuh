@@ -21,12 +21,14 @@ __device__ __forceinline__ int stage_at(int head, int dim) {
 // warp per row, or `share` of them when a row has many partials, joined in their order. With M the largest
 // log-sum-exp of a row,
 //     out = sum_i exp2(lse_i - M) o_i / sum_i exp2(lse_i - M).
+// kBatch: partials in flight (a power of two). kLean: quotients and logarithms by the hardware approximations, which
+// take less code: what a CTA runs once costs it the fetching of its instructions.
 template <int kD, int kW>
 struct JoinSmem {
   float acc[kW][kD];
   float m[kW], l[kW];
 };
-template <int kD, int kW, typename Sync>
+template <int kD, int kW, int kBatch, bool kLean, typename Sync>
 __device__ __forceinline__ void join_rows(const float* o_part, const float* lse_part, int first, int parts, int item,
                                           int rows, int r0, int share, JoinSmem<kD, kW>& sm, uint16_t* out,
                                           float* out_lse, Sync sync) {
@@ -39,11 +41,11 @@ __device__ __forceinline__ void join_rows(const float* o_part, const float* lse_
   float M = -INFINITY, l = 0.f, acc[kV];
 #pragma unroll
   for (int x = 0; x < kV; ++x) acc[x] = 0.f;
-  // Batches of eight partials, their loads in flight beside those of their log-sum-exps.
-  for (int k0 = 0; k0 < n; k0 += 8) {
-    float v[8][kV];
+  // Batches of partials, their loads in flight beside those of their log-sum-exps.
+  for (int k0 = 0; k0 < n; k0 += kBatch) {
+    float v[kBatch][kV];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kBatch; ++k) {
       if (k0 + k >= n) continue;
       const float* p = o_part + part(sub + share * (k0 + k)) * kD + lane * kV;
       if constexpr (kV == 2) {
@@ -62,10 +64,10 @@ __device__ __forceinline__ void join_rows(const float* o_part, const float* lse_
       }
     }
     const int mine = sub + share * (k0 + lane);
-    const float ls = lane < 8 && mine < parts ? __ldcg(lse_part + part(mine)) : -INFINITY;
+    const float ls = lane < kBatch && mine < parts ? __ldcg(lse_part + part(mine)) : -INFINITY;
     float top = ls;
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int o = kBatch / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     top = fmaxf(M, __shfl_sync(0xffffffffu, top, 0));
     const float base = finite_base(top), f0 = fast_exp2(M - base), w = fast_exp2(ls - base);
     M = top;
@@ -73,7 +75,7 @@ __device__ __forceinline__ void join_rows(const float* o_part, const float* lse_
 #pragma unroll
     for (int x = 0; x < kV; ++x) acc[x] *= f0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kBatch; ++k) {
       if (k0 + k >= n) continue;
       const float f = __shfl_sync(0xffffffffu, w, k);
       l += f;
@@ -85,12 +87,12 @@ __device__ __forceinline__ void join_rows(const float* o_part, const float* lse_
     if (r0 + warp >= rows) return;
     const size_t orow = (size_t)item * rows + r;
     const bool none = l == 0.f;
-    const float inv = 1.f / l;
+    const float inv = kLean ? fast_rcp(l) : 1.f / l;
 #pragma unroll
     for (int x = 0; x < kV; x += 2)
       *reinterpret_cast<uint32_t*>(out + orow * kD + lane * kV + x) =
           none ? 0u : pack_bf16x2(acc[x] * inv, acc[x + 1] * inv);
-    if (out_lse && lane == 0) out_lse[orow] = none ? -INFINITY : (M + log2f(l)) * kLn2;
+    if (out_lse && lane == 0) out_lse[orow] = none ? -INFINITY : (M + (kLean ? fast_log2(l) : log2f(l))) * kLn2;
     return;
   }
   sync();  // the previous rows' sums are read
@@ -117,9 +119,9 @@ __device__ __forceinline__ void join_rows(const float* o_part, const float* lse_
     }
     const size_t orow = (size_t)item * rows + row;
     const bool none = sum == 0.f;
-    const float inv = 1.f / sum;
+    const float inv = kLean ? fast_rcp(sum) : 1.f / sum;
     *reinterpret_cast<uint32_t*>(out + orow * kD + d) = none ? 0u : pack_bf16x2(x * inv, y * inv);
-    if (out_lse && d == 0) out_lse[orow] = none ? -INFINITY : (top + log2f(sum)) * kLn2;
+    if (out_lse && d == 0) out_lse[orow] = none ? -INFINITY : (top + (kLean ? fast_log2(sum) : log2f(sum))) * kLn2;
   }
 }
 
@@ -139,7 +141,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const float
   for (int u = blockIdx.x; u < n.y; u += gridDim.x) {
     const int4 j = join_of(todo, n.x, u);
     const int share = share_of(j.z);
-    join_rows<kD, kJoinWarps>(o_part, lse_part, j.x, j.z, j.y, rows, (u - j.w) * (kJoinWarps / share), share, sm, out,
+    join_rows<kD, kJoinWarps, 8, false>(o_part, lse_part, j.x, j.z, j.y, rows, (u - j.w) * (kJoinWarps / share), share, sm, out,
                               out_lse, [] { __syncthreads(); });
   }
 }

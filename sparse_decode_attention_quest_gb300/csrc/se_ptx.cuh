@@ -296,6 +296,13 @@ __device__ __forceinline__ float fast_log2(float x) {
   return y;
 }
 
+// 1 / x with the hardware approximation (relative error 2^-23; subnormals are zero).
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
