@@ -583,9 +583,10 @@ def se_rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str =
 
 def _rotary_side(x, out, name: str, tokens: int, dev: int):
     """(rows, stride, heads, output, its stride, head_dim) of the queries or keys of se_rotary."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+    shape = x.shape if isinstance(x, torch.Tensor) else ()
+    if len(shape) != 3:
         raise ValueError(f"{name}: expected [tokens][heads][head_dim]")
-    rows, heads, dim = x.shape
+    rows, heads, dim = shape
     if rows != tokens:
         raise ValueError(f"{name}: expected {tokens} rows, got {rows}")
     p, stride = _rows_ptr(x, heads, dim, torch.bfloat16, name, dev)

@@ -10,8 +10,12 @@
 //
 // Bound by reading and writing the rows once. A CTA takes a few tokens: it computes
 // their cosines and sines once into shared memory (every head of a token uses
-// the same ones), then each thread takes 16-byte pieces of the rows, both halves of
-// eight pairs (or four pairs, interleaved), a batch of loads in flight.
+// the same ones), then each thread takes pieces of the rows, two 16-byte vectors each:
+// both halves of eight pairs, or a vector of the first and one of the second half of
+// the interleaved pairs, so that the lanes' vectors lie next to each other, a batch
+// of them in flight. Dims that are not turned are copied in a loop of their own
+// (beside the others, in the same one, a row of 128 dims with 64 turned took
+// 4 x 32K tokens of 40 heads 519 us for a floor of 401).
 #include "se_ptx.cuh"
 
 namespace se {
@@ -19,8 +23,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBatch = 4;          // units a thread has in flight
-constexpr int kMaxPairs = 288;     // of a row
-constexpr int kMaxTile = 8;        // tokens of a CTA
+constexpr int kMaxAngles = 2304;   // of a CTA: eight tokens of the widest rows
+constexpr int kMaxTile = 64;       // tokens of a CTA
 
 struct RotaryArgs {
   const uint16_t* in[2];   // queries, keys
@@ -29,9 +33,10 @@ struct RotaryArgs {
   long long out_stride[2];
   int32_t q_heads, heads;  // of queries, of both
   int32_t dim, offset, pairs;
-  int32_t rot_units;       // pieces of a row's turned dims
-  int32_t units;           // and of all its dims that are written
-  uint32_t units_magic;    // of the divisions by units and by the heads of a CTA (magic_of)
+  int32_t units;           // pieces of a row's turned dims
+  int32_t copies;          // vectors of a row that are not turned but written
+  uint32_t units_magic;    // of the divisions by units, by copies and by the heads of a CTA (magic_of)
+  uint32_t copies_magic;
   uint32_t heads_magic;
   int32_t tile;            // tokens of a CTA
   int32_t tile_heads;      // heads of a CTA
@@ -69,15 +74,25 @@ __device__ __forceinline__ uint32_t turn_pair(uint32_t w, float c, float s) {
   return pack_bf16x2(x0 * c - x1 * s, x1 * c + x0 * s);
 }
 
+__device__ __forceinline__ uint4 turn_pairs(uint4 x, float4 c, float4 s) {
+  return make_uint4(turn_pair(x.x, c.x, s.x), turn_pair(x.y, c.y, s.y), turn_pair(x.z, c.z, s.z),
+                    turn_pair(x.w, c.w, s.w));
+}
+// The first dim of vector v (eight dims) of those that are not turned.
+__device__ __forceinline__ int beside(const RotaryArgs& a, int v) {
+  return v * 8 < a.offset ? v * 8 : v * 8 + 2 * a.pairs;
+}
+
 // n / d by its magic_of(d).
 __device__ __forceinline__ int quotient(int n, uint32_t magic) { return magic ? (int)__umulhi((uint32_t)n, magic) : n; }
 
-enum Layout { kHalf8, kHalf4, kInterleaved };  // pairs of a piece: eight, four (rotary_dim / 2 no multiple of 8), four
+// Pieces of eight pairs, and of four (8-byte vectors, and one vector) where the pairs are no multiple of eight.
+enum Layout { kHalf8, kHalf4, kInterleaved8, kInterleaved4 };
 
 template <int kLayout>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
-  __shared__ __align__(16) float cosines[kMaxTile * kMaxPairs];
-  __shared__ __align__(16) float sines[kMaxTile * kMaxPairs];
+  __shared__ __align__(16) float cosines[kMaxAngles];
+  __shared__ __align__(16) float sines[kMaxAngles];
   __shared__ bool live[kMaxTile];
   pdl_enter();
   const int t0 = blockIdx.x * a.tile;
@@ -85,41 +100,44 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
   const int tokens = min(a.tile, valid - t0);
   if (tokens <= 0) return;
   const int h0 = blockIdx.y * a.tile_heads, heads = min(a.tile_heads, a.heads - h0);
-  const int total = tokens * heads * a.units;
+  // Piece e of `each` a row: where it is, and its place in the row.
+  struct Place {
+    int token, piece, is_k;
+    long long in, out;
+  };
+  auto place_of = [&](int e, int each, uint32_t magic) {
+    Place p;
+    const int row = quotient(e, magic);
+    p.piece = e - row * each;
+    p.token = heads == a.tile_heads ? quotient(row, a.heads_magic) : row / heads;
+    const int h = h0 + row - p.token * heads, t = t0 + p.token;
+    p.is_k = h >= a.q_heads;
+    const long long head = (long long)(p.is_k ? h - a.q_heads : h) * a.dim;
+    p.in = t * a.in_stride[p.is_k] + head;
+    p.out = t * a.out_stride[p.is_k] + head;
+    return p;
+  };
 
   // The first pieces are on their way while the angles are computed.
+  constexpr int kDims = kLayout == kHalf4 ? 4 : 8;  // of a vector
+  const int total = tokens * heads * a.units;
   uint4 x[kBatch], y[kBatch];
-  long long to[kBatch];
-  int token[kBatch], unit[kBatch];
+  Place at[kBatch];
   auto load = [&](int first) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int e = first + u * kThreads;
-      unit[u] = -1;
-      if (e >= total) continue;
-      const int row = quotient(e, a.units_magic);
-      const int tk = heads == a.tile_heads ? quotient(row, a.heads_magic) : row / heads;
-      const int h = h0 + row - tk * heads, t = t0 + tk;
-      const bool is_k = h >= a.q_heads;
-      const int hh = is_k ? h - a.q_heads : h;
-      unit[u] = e - row * a.units;
-      token[u] = tk;
-      // A piece's first dim: of the turned ones, then of those before and behind them.
-      const int r = unit[u] - a.rot_units;
-      const int d = r >= 0 ? (r * 8 < a.offset ? r * 8 : r * 8 + 2 * a.pairs)
-                           : a.offset + unit[u] * (kLayout == kHalf4 ? 4 : 8);
-      const uint16_t* from = a.in[is_k] + t * a.in_stride[is_k] + (long long)hh * a.dim + d;
-      to[u] = t * a.out_stride[is_k] + (long long)hh * a.dim + d;
-      if (is_k) unit[u] |= 1 << 30;
-      if (r >= 0 || kLayout == kInterleaved) {
-        x[u] = ld_row_v4(from);
-      } else if (kLayout == kHalf8) {
-        x[u] = ld_row_v4(from);
-        y[u] = ld_row_v4(from + a.pairs);
-      } else {
+      if (first + u * kThreads >= total) continue;
+      at[u] = place_of(first + u * kThreads, a.units, a.units_magic);
+      const int d = a.offset + at[u].piece * kDims;
+      const uint16_t* from = a.in[at[u].is_k] + at[u].in + d;
+      at[u].out += d;
+      if (kLayout == kHalf4) {
         const uint2 lo = ld_row_v2(from), hi = ld_row_v2(from + a.pairs);
         x[u] = make_uint4(lo.x, lo.y, 0u, 0u);
         y[u] = make_uint4(hi.x, hi.y, 0u, 0u);
+      } else {
+        x[u] = ld_row_v4(from);
+        if (kLayout != kInterleaved4) y[u] = ld_row_v4(from + a.pairs);
       }
     }
   };
@@ -140,20 +158,18 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
     if (first != threadIdx.x) load(first);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      if (unit[u] < 0 || !live[token[u]]) continue;
-      uint16_t* out = a.out[unit[u] >> 30] + to[u];
-      const int un = unit[u] & ~(1 << 30);
-      if (un >= a.rot_units) {
-        *reinterpret_cast<uint4*>(out) = x[u];
-        continue;
-      }
+      if (first + u * kThreads >= total || !live[at[u].token]) continue;
+      uint16_t* out = a.out[at[u].is_k] + at[u].out;
       constexpr int kPairs = kLayout == kHalf8 ? 8 : 4;
-      const float* cs = cosines + token[u] * a.pairs + un * kPairs;
-      const float* sn = sines + token[u] * a.pairs + un * kPairs;
+      const float* cs = cosines + at[u].token * a.pairs + at[u].piece * kPairs;
+      const float* sn = sines + at[u].token * a.pairs + at[u].piece * kPairs;
       const float4 c0 = *reinterpret_cast<const float4*>(cs), s0 = *reinterpret_cast<const float4*>(sn);
-      if constexpr (kLayout == kInterleaved) {
-        *reinterpret_cast<uint4*>(out) = make_uint4(turn_pair(x[u].x, c0.x, s0.x), turn_pair(x[u].y, c0.y, s0.y),
-                                                    turn_pair(x[u].z, c0.z, s0.z), turn_pair(x[u].w, c0.w, s0.w));
+      if constexpr (kLayout == kInterleaved8 || kLayout == kInterleaved4) {
+        *reinterpret_cast<uint4*>(out) = turn_pairs(x[u], c0, s0);
+        if constexpr (kLayout == kInterleaved8)
+          *reinterpret_cast<uint4*>(out + a.pairs) =
+              turn_pairs(y[u], *reinterpret_cast<const float4*>(cs + a.pairs / 2),
+                         *reinterpret_cast<const float4*>(sn + a.pairs / 2));
       } else {
         turn_halves(x[u].x, y[u].x, make_float2(c0.x, c0.y), make_float2(s0.x, s0.y));
         turn_halves(x[u].y, y[u].y, make_float2(c0.z, c0.w), make_float2(s0.z, s0.w));
@@ -169,6 +185,22 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
         }
       }
     }
+  }
+
+  const int copied = tokens * heads * a.copies;
+  for (int first = threadIdx.x; first < copied; first += kBatch * kThreads) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (first + u * kThreads >= copied) continue;
+      at[u] = place_of(first + u * kThreads, a.copies, a.copies_magic);
+      const int d = beside(a, at[u].piece);
+      x[u] = ld_row_v4(a.in[at[u].is_k] + at[u].in + d);
+      at[u].out += d;
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (first + u * kThreads < copied && live[at[u].token])
+        *reinterpret_cast<uint4*>(a.out[at[u].is_k] + at[u].out) = x[u];
   }
 }
 
@@ -196,17 +228,19 @@ cudaError_t launch_rotary(const uint16_t* q, long long q_stride, int32_t q_heads
   a.dim = dim;
   a.offset = offset;
   a.pairs = rot / 2;
-  const int layout = interleaved ? kInterleaved : a.pairs % 8 == 0 ? kHalf8 : kHalf4;
-  a.rot_units = layout == kHalf8 ? a.pairs / 8 : a.pairs / 4;
+  const int layout = interleaved ? (a.pairs % 8 == 0 ? kInterleaved8 : kInterleaved4) : a.pairs % 8 == 0 ? kHalf8 : kHalf4;
+  a.units = a.pairs / (a.pairs % 8 == 0 ? 8 : 4);
   // In place nothing else is written. (Queries in place and keys not, or the other way round: copied onto themselves.)
   const bool in_place = (q_heads == 0 || q_out == q) && (kv_heads == 0 || k_out == k);
-  a.units = a.rot_units + (in_place ? 0 : (dim - rot) / 8);
+  a.copies = in_place ? 0 : (dim - rot) / 8;
   a.units_magic = magic_of(a.units);
+  a.copies_magic = a.copies ? magic_of(a.copies) : 0u;
   // A few tokens per CTA where there are many; one, its heads shared by several CTAs, where there are few.
   a.tile = 1;
   a.tile_heads = a.heads;
   if (num_tokens >= 16 * sm_count) {
-    while (a.tile < kMaxTile && a.tile * a.heads * a.units < kBatch * kThreads) a.tile *= 2;
+    while (a.tile < kMaxTile && 2 * a.tile * a.pairs <= kMaxAngles && a.tile * a.heads * a.units < kBatch * kThreads)
+      a.tile *= 2;
   } else {
     while (a.tile_heads > 1 && a.tile_heads * a.units > kThreads &&
            (long long)num_tokens * ((a.heads + a.tile_heads - 1) / a.tile_heads) < 2 * sm_count)
@@ -223,7 +257,8 @@ cudaError_t launch_rotary(const uint16_t* q, long long q_stride, int32_t q_heads
   switch (layout) {
     case kHalf8: return launch_pdl(rotary_kernel<kHalf8>, grid, dim3(kThreads), 0, stream, a);
     case kHalf4: return launch_pdl(rotary_kernel<kHalf4>, grid, dim3(kThreads), 0, stream, a);
-    default: return launch_pdl(rotary_kernel<kInterleaved>, grid, dim3(kThreads), 0, stream, a);
+    case kInterleaved8: return launch_pdl(rotary_kernel<kInterleaved8>, grid, dim3(kThreads), 0, stream, a);
+    default: return launch_pdl(rotary_kernel<kInterleaved4>, grid, dim3(kThreads), 0, stream, a);
   }
 }
 
