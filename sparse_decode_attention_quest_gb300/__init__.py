@@ -581,21 +581,29 @@ def se_rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str =
     return freqs, amplitude.value
 
 
-def _rotary_side(x, out, name: str, tokens: int, dev: int):
-    """(rows, stride, heads, output, its stride, head_dim) of the queries or keys of se_rotary."""
+def _rotary_rows(x, name: str, tokens: int, dev: int):
+    """(pointer, row stride, shape) of rows [tokens][heads][head_dim] whose heads are dense."""
+    if isinstance(x, torch.Tensor) and x.dtype is torch.bfloat16 and x.get_device() == dev:
+        shape, stride = x.shape, x.stride()
+        if len(shape) == 3 and shape[0] == tokens > 1 and stride[2] == 1 and stride[1] == shape[2]:
+            return x.data_ptr(), stride[0], shape
     shape = x.shape if isinstance(x, torch.Tensor) else ()
     if len(shape) != 3:
         raise ValueError(f"{name}: expected [tokens][heads][head_dim]")
-    rows, heads, dim = shape
-    if rows != tokens:
-        raise ValueError(f"{name}: expected {tokens} rows, got {rows}")
-    p, stride = _rows_ptr(x, heads, dim, torch.bfloat16, name, dev)
+    if shape[0] != tokens:
+        raise ValueError(f"{name}: expected {tokens} rows, got {shape[0]}")
+    return *_rows_ptr(x, shape[1], shape[2], torch.bfloat16, name, dev), shape
+
+
+def _rotary_side(x, out, name: str, tokens: int, dev: int):
+    """(rows, stride, heads, output, its stride, head_dim) of the queries or keys of se_rotary."""
+    p, stride, shape = _rotary_rows(x, name, tokens, dev)
     if out is None or out is x:
-        return p, stride, heads, p, stride, dim
-    po, so = _rows_ptr(out, heads, dim, torch.bfloat16, name + "_out", dev)
-    if out.shape[0] != tokens:
-        raise ValueError(f"{name}_out: expected {tokens} rows, got {out.shape[0]}")
-    return p, stride, heads, po, so, dim
+        return p, stride, shape[1], p, stride, shape[2]
+    po, so, out_shape = _rotary_rows(out, name + "_out", tokens, dev)
+    if out_shape != shape:
+        raise ValueError(f"{name}_out: expected shape {list(shape)}, got {list(out_shape)}")
+    return p, stride, shape[1], po, so, shape[2]
 
 
 _NO_ROWS = (None, 0, 0, None, 0, None)
