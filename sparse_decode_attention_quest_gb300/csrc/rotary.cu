@@ -16,6 +16,8 @@
 // of them in flight. Dims that are not turned are copied in a loop of their own
 // (beside the others, in the same one, a row of 128 dims with 64 turned took
 // 4 x 32K tokens of 40 heads 519 us for a floor of 401).
+#include <algorithm>
+
 #include "se_ptx.cuh"
 
 namespace se {
@@ -239,8 +241,7 @@ cudaError_t launch_rotary(const uint16_t* q, long long q_stride, int32_t q_heads
   a.tile = 1;
   a.tile_heads = a.heads;
   if (num_tokens >= 16 * sm_count) {
-    while (a.tile < kMaxTile && 2 * a.tile * a.pairs <= kMaxAngles && a.tile * a.heads * a.units < kBatch * kThreads)
-      a.tile *= 2;
+    a.tile = std::max(1, std::min({kMaxTile, kMaxAngles / a.pairs, kBatch * kThreads / (a.heads * a.units)}));
   } else {
     while (a.tile_heads > 1 && a.tile_heads * a.units > kThreads &&
            (long long)num_tokens * ((a.heads + a.tile_heads - 1) / a.tile_heads) < 2 * sm_count)
