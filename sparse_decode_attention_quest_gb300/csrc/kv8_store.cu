@@ -55,7 +55,23 @@ __device__ __forceinline__ uint4 without_inf(uint4 x) {
                     x.w | not_finite_bf16x2(x.w));
 }
 
-// A run of n tokens of one page and KV head, by a warp: lane's columns of the page and of the first token's row.
+// How a warp takes rows of kD dims: 8 dims a lane, rows of two KV heads of 64 dims as one of 128.
+template <int kD>
+struct Lanes {
+  static constexpr int kHeads = kD == 64 ? 2 : 1;
+  static constexpr int kOfHead = kD / 8;            // lanes of a head's row
+  static constexpr int kOfRow = kHeads * kOfHead;   // and of a row
+  static constexpr int kRows = 32 / kOfRow;         // rows of a warp's load
+  // Over the lanes of a head.
+  static __device__ __forceinline__ uint32_t max_abs(uint32_t m) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (o < kOfHead || o >= kOfRow) m = max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return max(m & 0xffffu, m >> 16);
+  }
+};
+
+// A run of n tokens of one page, by a warp: a lane's columns of the page and of the first token's row.
 template <int kD>
 struct Run {
   uint8_t* rows;
@@ -63,57 +79,50 @@ struct Run {
   long long stride;
   float* scale;
   int n, sub, lane;
+  bool on;  // the lane has a head
 
-  // The page's scale for rows whose largest magnitudes the lanes hold, and which slots they take; the other slots'
-  // codes follow. Returns its reciprocal; loud: there are infinities among them.
-  __device__ __forceinline__ float take_scale(uint32_t amax, uint32_t written, bool& loud) const {
-    constexpr int kRows = 256 / kD;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = max_abs_bf16x2(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    uint32_t top = max(amax & 0xffffu, amax >> 16);
-    loud = top >= 0x7f80u;
+  // The page's scale for rows whose largest magnitudes the lanes hold, and which slots they take (old: its present one,
+  // where slot 0 is not among them); the other slots' codes follow. Returns its reciprocal; loud: a lane has infinities.
+  __device__ __forceinline__ float take_scale(uint32_t amax, uint32_t written, float old, bool& loud) const {
+    using L = Lanes<kD>;
+    uint32_t top = L::max_abs(amax);
+    loud = __any_sync(0xffffffffu, top >= 0x7f80u);
     if (loud) {
-      // The largest finite magnitude instead, the same for all lanes.
+      // The largest finite magnitudes instead.
       uint32_t m = 0;
-      for (int k = sub; k < n; k += kRows) {
+      for (int k = sub; k < n && on; k += L::kRows) {
         const uint4 y = ld_stream_v4(reinterpret_cast<const uint4*>(from + k * stride));
         m = max_abs_bf16x8(m, make_uint4(y.x & ~not_finite_bf16x2(y.x), y.y & ~not_finite_bf16x2(y.y),
                                          y.z & ~not_finite_bf16x2(y.z), y.w & ~not_finite_bf16x2(y.w)));
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
-      top = max(m & 0xffffu, m >> 16);
+      __syncwarp();
+      top = L::max_abs(m);
     }
     float s = scale_for(top);
-    if (written & 1u) {
-      if (lane == 0) *scale = s;
-    } else {
-      const float old = *scale;
-      s = fmaxf(s, old);
-      if (s != old) {
-        const float ratio = old / s;
-        for (int r = sub; r < kPageSize; r += kRows) {
-          if (written >> r & 1u) continue;
-          uint2* c = reinterpret_cast<uint2*>(rows + r * kD);
-          *c = make_uint2(rescale4(c->x, ratio), rescale4(c->y, ratio));
-        }
-        __syncwarp();
-        if (lane == 0) *scale = s;
+    const bool opened = written & 1u;
+    if (!opened) s = fmaxf(s, old);
+    if (on && !opened && s != old) {
+      const float ratio = old / s;
+      for (int r = sub; r < kPageSize; r += L::kRows) {
+        if (written >> r & 1u) continue;
+        uint2* c = reinterpret_cast<uint2*>(rows + r * kD);
+        *c = make_uint2(rescale4(c->x, ratio), rescale4(c->y, ratio));
       }
     }
+    __syncwarp();  // every lane has the present scale
+    if (on && lane % L::kOfHead == 0 && sub == 0 && (opened || s != old)) *scale = s;
     return 1.f / s;
   }
 };
 
 template <int kD>
 __global__ void __launch_bounds__(kWarps * 32, kD == 256 ? 2 : 3) kv8_store_kernel(const Kv8StoreArgs a) {
-  constexpr int kLanes = kD / 8;          // lanes of a row, 8 dims each
-  constexpr int kRows = 32 / kLanes;      // rows of a warp's load
-  constexpr int kLoads = kPageSize / kRows;
+  using L = Lanes<kD>;
+  constexpr int kRows = L::kRows, kLoads = kPageSize / kRows;
   pdl_enter();
   const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31, sub = lane / kLanes, x0 = lane % kLanes * 8;
-  const int groups = 2 * a.kv.num_kv_heads;
+  const int lane = threadIdx.x & 31, sub = lane / L::kOfRow, x0 = lane % L::kOfHead * 8;
+  const int groups = 2 * ((a.kv.num_kv_heads + L::kHeads - 1) / L::kHeads);
   const long long win = w / groups;
   if (win * a.window >= a.num_tokens) return;
   const int t0 = (int)win * a.window, T = a.num_tokens;
@@ -128,7 +137,9 @@ __global__ void __launch_bounds__(kWarps * 32, kD == 256 ? 2 : 3) kv8_store_kern
   const int prev = __shfl_up_sync(0xffffffffu, pg, 1);
   uint32_t runs = __ballot_sync(0xffffffffu, lane >= 1 && lane <= a.window && pg >= 0 && pg != prev);
 
-  const int cg = (int)(w % groups), is_v = cg & 1, h = cg >> 1;
+  const int cg = (int)(w % groups), is_v = cg & 1, mine = (cg >> 1) * L::kHeads + lane % L::kOfRow / L::kOfHead;
+  const bool on = mine < a.kv.num_kv_heads;
+  const int h = on ? mine : a.kv.num_kv_heads - 1;
   const uint16_t* src = (is_v ? a.in[1] : a.in[0]) + (long long)h * kD + x0;
   const long long stride = is_v ? a.stride[1] : a.stride[0];
   uint8_t* cache = is_v ? a.kv.v : a.kv.k;
@@ -152,7 +163,8 @@ __global__ void __launch_bounds__(kWarps * 32, kD == 256 ? 2 : 3) kv8_store_kern
     // Rows one after another in the page, as a slot map built from lengths has them.
     const bool ordered = n == seen && (inrow & ((1u << seen) - 1)) == (1u << seen) - 1;
     const int r0 = s0 % kPageSize;
-    const Run<kD> run{rows, from, stride, scales + block, n, sub, lane};
+    const Run<kD> run{rows, from, stride, scales + block, n, sub, lane, on};
+    const float old = r0 == 0 ? 0.f : scales[block];  // with the rows: it is needed where the run begins behind slot 0
     if (ordered && n == kPageSize) {
       uint4 x[kLoads];
       const uint16_t* p = from + sub * stride;
@@ -162,13 +174,14 @@ __global__ void __launch_bounds__(kWarps * 32, kD == 256 ? 2 : 3) kv8_store_kern
 #pragma unroll
       for (int u = 0; u < kLoads; ++u) amax = max_abs_bf16x8(amax, x[u]);
       bool loud;
-      const float inv = run.take_scale(amax, 0xffffu, loud);
+      const float inv = run.take_scale(amax, 0xffffu, 0.f, loud);
       uint8_t* q = rows + sub * kD;
       if (loud)
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) x[u] = without_inf(x[u]);
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u) *reinterpret_cast<uint2*>(q + u * kRows * kD) = quantise8(x[u], inv);
+      for (int u = 0; u < kLoads; ++u)
+        if (on) *reinterpret_cast<uint2*>(q + u * kRows * kD) = quantise8(x[u], inv);
     } else if (ordered) {
       uint4 x[kLoads];
 #pragma unroll
@@ -180,10 +193,10 @@ __global__ void __launch_bounds__(kWarps * 32, kD == 256 ? 2 : 3) kv8_store_kern
 #pragma unroll
       for (int u = 0; u < kLoads; ++u) amax = max_abs_bf16x8(amax, x[u]);
       bool loud;
-      const float inv = run.take_scale(amax, ((1u << n) - 1) << r0, loud);
+      const float inv = run.take_scale(amax, ((1u << n) - 1) << r0, old, loud);
 #pragma unroll
       for (int u = 0; u < kLoads; ++u)
-        if (u * kRows + sub < n)
+        if (on && u * kRows + sub < n)
           *reinterpret_cast<uint2*>(rows + (r0 + u * kRows + sub) * kD) = quantise8(loud ? without_inf(x[u]) : x[u], inv);
     } else {
       // Rows in any order, and a run of more tokens than a page has (slots named twice).
@@ -193,9 +206,8 @@ __global__ void __launch_bounds__(kWarps * 32, kD == 256 ? 2 : 3) kv8_store_kern
         if (sub == 0) amax = max_abs_bf16x8(amax, ld_stream_v4(reinterpret_cast<const uint4*>(from + k * stride)));
       }
       bool loud;
-      const float inv = run.take_scale(amax, written, loud);
-      if (sub > 0) continue;
-      for (int k = 0; k < n; ++k) {
+      const float inv = run.take_scale(amax, written, scales[block], loud);
+      for (int k = 0; k < n && on && sub == 0; ++k) {
         const uint4 x = ld_stream_v4(reinterpret_cast<const uint4*>(from + k * stride));
         *reinterpret_cast<uint2*>(rows + a.slot_map[first + k] % kPageSize * kD) =
             quantise8(loud ? without_inf(x) : x, inv);
@@ -309,7 +321,7 @@ cudaError_t launch_kv8_store(const Kv8View& kv, const uint16_t* k_new, long long
   a.slot_map = slot_map;
   a.num_tokens = num_tokens;
   a.err = err;
-  const int groups = 2 * kv.num_kv_heads;
+  const int groups = kv.head_dim == 64 ? 2 * ((kv.num_kv_heads + 1) / 2) : 2 * kv.num_kv_heads;
   // Windows of 16 tokens once they fill the SMs (24 warps each), shorter ones before.
   a.window = 16;
   while (a.window > 1 && (long long)num_tokens * groups < (long long)a.window * 24 * sm_count) a.window /= 2;
