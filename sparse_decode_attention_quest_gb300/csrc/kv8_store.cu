@@ -55,10 +55,9 @@ __device__ __forceinline__ uint4 without_inf(uint4 x) {
                     x.w | not_finite_bf16x2(x.w));
 }
 
-// How a warp takes rows of kD dims: 8 dims a lane, rows of two KV heads of 64 dims as one of 128.
-template <int kD>
+// How a warp takes rows of kD dims, 8 dims a lane: those of kHeads KV heads next to each other as one.
+template <int kD, int kHeads>
 struct Lanes {
-  static constexpr int kHeads = kD == 64 ? 2 : 1;
   static constexpr int kOfHead = kD / 8;            // lanes of a head's row
   static constexpr int kOfRow = kHeads * kOfHead;   // and of a row
   static constexpr int kRows = 32 / kOfRow;         // rows of a warp's load
@@ -72,7 +71,7 @@ struct Lanes {
 };
 
 // A run of n tokens of one page, by a warp: a lane's columns of the page and of the first token's row.
-template <int kD>
+template <int kD, int kHeads>
 struct Run {
   uint8_t* rows;
   const uint16_t* from;
@@ -84,7 +83,7 @@ struct Run {
   // The page's scale for rows whose largest magnitudes the lanes hold, and which slots they take (old: its present one,
   // where slot 0 is not among them); the other slots' codes follow. Returns its reciprocal; loud: a lane has infinities.
   __device__ __forceinline__ float take_scale(uint32_t amax, uint32_t written, float old, bool& loud) const {
-    using L = Lanes<kD>;
+    using L = Lanes<kD, kHeads>;
     uint32_t top = L::max_abs(amax);
     loud = __any_sync(0xffffffffu, top >= 0x7f80u);
     if (loud) {
@@ -115,14 +114,14 @@ struct Run {
   }
 };
 
-template <int kD>
-__global__ void __launch_bounds__(kWarps * 32, kD == 256 ? 2 : 3) kv8_store_kernel(const Kv8StoreArgs a) {
-  using L = Lanes<kD>;
+template <int kD, int kHeads>
+__global__ void __launch_bounds__(kWarps * 32, kD * kHeads == 256 ? 2 : 3) kv8_store_kernel(const Kv8StoreArgs a) {
+  using L = Lanes<kD, kHeads>;
   constexpr int kRows = L::kRows, kLoads = kPageSize / kRows;
   pdl_enter();
   const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31, sub = lane / L::kOfRow, x0 = lane % L::kOfHead * 8;
-  const int groups = 2 * ((a.kv.num_kv_heads + L::kHeads - 1) / L::kHeads);
+  const int groups = 2 * ((a.kv.num_kv_heads + kHeads - 1) / kHeads);
   const long long win = w / groups;
   if (win * a.window >= a.num_tokens) return;
   const int t0 = (int)win * a.window, T = a.num_tokens;
@@ -137,7 +136,7 @@ __global__ void __launch_bounds__(kWarps * 32, kD == 256 ? 2 : 3) kv8_store_kern
   const int prev = __shfl_up_sync(0xffffffffu, pg, 1);
   uint32_t runs = __ballot_sync(0xffffffffu, lane >= 1 && lane <= a.window && pg >= 0 && pg != prev);
 
-  const int cg = (int)(w % groups), is_v = cg & 1, mine = (cg >> 1) * L::kHeads + lane % L::kOfRow / L::kOfHead;
+  const int cg = (int)(w % groups), is_v = cg & 1, mine = (cg >> 1) * kHeads + lane % L::kOfRow / L::kOfHead;
   const bool on = mine < a.kv.num_kv_heads;
   const int h = on ? mine : a.kv.num_kv_heads - 1;
   const uint16_t* src = (is_v ? a.in[1] : a.in[0]) + (long long)h * kD + x0;
@@ -163,7 +162,7 @@ __global__ void __launch_bounds__(kWarps * 32, kD == 256 ? 2 : 3) kv8_store_kern
     // Rows one after another in the page, as a slot map built from lengths has them.
     const bool ordered = n == seen && (inrow & ((1u << seen) - 1)) == (1u << seen) - 1;
     const int r0 = s0 % kPageSize;
-    const Run<kD> run{rows, from, stride, scales + block, n, sub, lane, on};
+    const Run<kD, kHeads> run{rows, from, stride, scales + block, n, sub, lane, on};
     const float old = r0 == 0 ? 0.f : scales[block];  // with the rows: it is needed where the run begins behind slot 0
     if (ordered && n == kPageSize) {
       uint4 x[kLoads];
@@ -298,9 +297,15 @@ __global__ void __launch_bounds__(kLoadThreads, 3) kv8_load_kernel(const Kv8Load
   }
 }
 
-template <int kD>
-cudaError_t launch_store(const Kv8StoreArgs& a, unsigned grid, cudaStream_t stream) {
-  return launch_pdl(kv8_store_kernel<kD>, dim3(grid), dim3(kWarps * 32), 0, stream, a);
+template <int kD, int kHeads>
+cudaError_t launch_store(Kv8StoreArgs& a, int sm_count, cudaStream_t stream) {
+  const int groups = 2 * ((a.kv.num_kv_heads + kHeads - 1) / kHeads);
+  // Windows of 16 tokens once they fill the SMs (16 warps each), shorter ones before.
+  a.window = 16;
+  while (a.window > 1 && (long long)a.num_tokens * groups < (long long)a.window * 16 * sm_count) a.window /= 2;
+  const long long warps = ((long long)a.num_tokens + a.window - 1) / a.window * groups;
+  return launch_pdl(kv8_store_kernel<kD, kHeads>, dim3((unsigned)((warps + kWarps - 1) / kWarps)), dim3(kWarps * 32), 0,
+                    stream, a);
 }
 template <int kD>
 cudaError_t launch_load(const Kv8LoadArgs& a, unsigned grid, cudaStream_t stream) {
@@ -321,16 +326,12 @@ cudaError_t launch_kv8_store(const Kv8View& kv, const uint16_t* k_new, long long
   a.slot_map = slot_map;
   a.num_tokens = num_tokens;
   a.err = err;
-  const int groups = kv.head_dim == 64 ? 2 * ((kv.num_kv_heads + 1) / 2) : 2 * kv.num_kv_heads;
-  // Windows of 16 tokens once they fill the SMs (24 warps each), shorter ones before.
-  a.window = 16;
-  while (a.window > 1 && (long long)num_tokens * groups < (long long)a.window * 24 * sm_count) a.window /= 2;
-  const long long warps = ((long long)num_tokens + a.window - 1) / a.window * groups;
-  const unsigned grid = (unsigned)((warps + kWarps - 1) / kWarps);
+  // Rows of 256 dims to a warp where the heads allow: 8 KB in flight for each.
+  const int h = kv.num_kv_heads;
   switch (kv.head_dim) {
-    case 64: return launch_store<64>(a, grid, stream);
-    case 128: return launch_store<128>(a, grid, stream);
-    default: return launch_store<256>(a, grid, stream);
+    case 64: return h % 4 ? launch_store<64, 2>(a, sm_count, stream) : launch_store<64, 4>(a, sm_count, stream);
+    case 128: return h % 2 ? launch_store<128, 1>(a, sm_count, stream) : launch_store<128, 2>(a, sm_count, stream);
+    default: return launch_store<256, 1>(a, sm_count, stream);
   }
 }
 
