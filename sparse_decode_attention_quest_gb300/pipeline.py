@@ -11,7 +11,9 @@ or all four in one launch (se_quest_fused_step, run_fused).
 
 PagedCache is the cache's life around that step: pages from a pool, the rows of new tokens
 into their slots, dense attention over the cache, and the pages back
-(se_block_tables_extend, se_paged_kv_store, se_paged_decode, se_block_tables_release_ex).
+(se_block_tables_extend, se_paged_kv_store, se_paged_decode, se_block_tables_release_ex), the cache
+in bf16 or in 8 bits (se_paged_kv8_store, _load, _decode). Rotary turns the rows by their positions first
+(se_rotary).
 """
 from __future__ import annotations
 
@@ -20,12 +22,14 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import (APPEND_OVERLAP_PREVIOUS, paged_kv, se_block_tables_extend, se_block_tables_release_ex,
-               se_paged_decode, se_paged_decode_workspace_size, se_paged_kv_store, se_quest_build_summaries,
+from . import (APPEND_OVERLAP_PREVIOUS, SEPagedKV8, paged_kv, paged_kv8, se_block_tables_extend,
+               se_block_tables_release_ex, se_paged_decode, se_paged_decode_workspace_size, se_paged_kv8_decode,
+               se_paged_kv8_decode_workspace_size, se_paged_kv8_load, se_paged_kv8_store, se_paged_kv_store,
+               se_quest_build_summaries,
                se_quest_fused_step,
                se_quest_kept_pages_max, se_quest_score_pages, se_quest_score_pages_ws, se_quest_score_workspace_size,
                se_quest_topk_pages_windowed, se_quest_update_summaries,
-               se_quest_update_summaries_ex, se_snapkv_score_and_compact_windowed,
+               se_quest_update_summaries_ex, se_rotary, se_rotary_frequencies, se_snapkv_score_and_compact_windowed,
                se_snapkv_workspace_size, se_sparse_decode_plan, se_sparse_decode_workspace_size,
                se_sparse_paged_decode)
 
@@ -46,23 +50,47 @@ def _on(stream):
 
 
 class DenseAttention:
-    """se_paged_decode's buffers for a cache view: output, log-sum-exp and workspace of ``batch`` requests. The
-    workspace is filled on the current stream here, so this is made before the calls that use it, on whatever
-    stream those run, and outside a recording."""
+    """The buffers of se_paged_decode (se_paged_kv8_decode) for a cache view: output, log-sum-exp and workspace of
+    ``batch`` requests. The workspace is filled on the current stream here, so this is made before the calls that use
+    it, on whatever stream those run, and outside a recording."""
 
     def __init__(self, kv, batch: int, num_q_heads: int, device, sm_scale: Optional[float] = None):
         self.kv = kv
         self.sm_scale = sm_scale if sm_scale is not None else 1.0 / math.sqrt(kv.head_dim)
-        self.out = torch.empty(batch, num_q_heads, kv.head_dim_v, dtype=torch.bfloat16, device=device)
+        self.eight_bit = isinstance(kv, SEPagedKV8)
+        dim_v = kv.head_dim if self.eight_bit else kv.head_dim_v
+        self.out = torch.empty(batch, num_q_heads, dim_v, dtype=torch.bfloat16, device=device)
         self.lse = torch.empty(batch, num_q_heads, dtype=torch.float32, device=device)
-        ws = se_paged_decode_workspace_size(batch, num_q_heads, kv.num_kv_heads, kv.head_dim, kv.head_dim_v)
+        if self.eight_bit:
+            ws = se_paged_kv8_decode_workspace_size(batch, num_q_heads, kv.num_kv_heads, kv.head_dim)
+        else:
+            ws = se_paged_decode_workspace_size(batch, num_q_heads, kv.num_kv_heads, kv.head_dim, dim_v)
         # zero-filled once: the counters of the join start at zero and every call leaves them so
         self.workspace = torch.zeros(max(ws, 16), dtype=torch.uint8, device=device)
 
     def run(self, q, block_table, seq_lens, sink_tokens: int = 0, recent_tokens: int = 0, stream=None, kv=None):
-        se_paged_decode(self.kv if kv is None else kv, q, block_table, seq_lens, self.sm_scale, self.out, self.lse,
-                        self.workspace, sink_tokens, recent_tokens, stream)
+        decode = se_paged_kv8_decode if self.eight_bit else se_paged_decode
+        decode(self.kv if kv is None else kv, q, block_table, seq_lens, self.sm_scale, self.out, self.lse,
+               self.workspace, sink_tokens, recent_tokens, stream)
         return self.out
+
+
+class Rotary:
+    """The frequencies of rotary positions on a device, and which dims of a head they turn: ``rotary_dim`` of them from
+    ``offset`` on, pairs of a half's distance or next to each other (``interleaved``). ``scaling``, ``factor`` and
+    ``original_len``: se_rotary_frequencies."""
+
+    def __init__(self, rotary_dim: int, device, base: float = 10000.0, offset: int = 0, interleaved: bool = False,
+                 scaling: str = "none", factor: float = 1.0, original_len: int = 0):
+        freqs, self.amplitude = se_rotary_frequencies(rotary_dim, base, scaling, factor, original_len)
+        self.freqs = freqs.to(device)
+        self.offset, self.interleaved = offset, interleaved
+
+    def apply(self, q, k, positions, q_out=None, k_out=None, num_valid=None, inverse: bool = False, stream=None):
+        """Query and key rows [T][heads][D] turned by positions [T], in place without outputs; rows at and behind
+        num_valid (int32 [1] on the device) are left."""
+        se_rotary(q, k, positions, self.freqs, q_out, k_out, self.offset, self.interleaved, inverse, self.amplitude,
+                  num_valid, stream)
 
 
 class PagedCache:
@@ -72,17 +100,27 @@ class PagedCache:
     page summaries when the cache keeps them) and attend (one query per request over all its tokens, or over
     a sink and a recent window). Lengths live on the device and nothing depends on them on the host, so the
     calls of a step can be recorded once (se_capture_begin ... se_capture_end) and replayed. release returns
-    pages to the pool. ``head_dim_v`` (with ``latent``): the value is the first dims of the key row.
+    pages to the pool. ``head_dim_v`` (with ``latent``): the value is the first dims of the key row. ``eight_bit``: the
+    cache holds e4m3 codes with a scale for each page and KV head (head dims 64, 128 and 256; no latent cache, no
+    summaries), and load brings rows back. rotate turns a step's rows by the positions that extend gave them, before
+    store and attend.
     """
 
     def __init__(self, num_pages: int, batch: int, max_len: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                  max_new_tokens: int, device, latent: bool = False, head_dim_v: Optional[int] = None,
-                 summary: bool = False, sm_scale: Optional[float] = None):
+                 summary: bool = False, sm_scale: Optional[float] = None, eight_bit: bool = False):
+        if eight_bit and (latent or summary):
+            raise ValueError("an 8-bit cache is neither latent nor does it keep summaries")
         i32 = dict(dtype=torch.int32, device=device)
-        self.k = torch.zeros(num_pages, num_kv_heads, PAGE, head_dim, dtype=torch.bfloat16, device=device)
+        dtype = torch.float8_e4m3fn if eight_bit else torch.bfloat16
+        self.k = torch.zeros(num_pages, num_kv_heads, PAGE, head_dim, dtype=dtype, device=device)
         self.v = None if latent else torch.zeros_like(self.k)
         self.summary = new_summary(self.k) if summary else None
-        self.kv = paged_kv(self.k, self.v, self.summary, head_dim_v if latent else None)
+        if eight_bit:
+            self.k_scale, self.v_scale = (torch.ones(num_pages, num_kv_heads, device=device) for _ in range(2))
+            self.kv = paged_kv8(self.k, self.v, self.k_scale, self.v_scale)
+        else:
+            self.kv = paged_kv(self.k, self.v, self.summary, head_dim_v if latent else None)
         self.free_pages = torch.arange(num_pages, **i32)
         self.pool_state = torch.tensor([num_pages, 0, 0, 0], **i32)
         self.block_table = torch.zeros(batch, max(1, (max_len + PAGE - 1) // PAGE), **i32)
@@ -99,7 +137,21 @@ class PagedCache:
 
     def store(self, k_new, v_new=None, stream=None):
         """The rows [T][Hkv][D] of the tokens that extend placed, in batch order (T up to max_new_tokens)."""
-        se_paged_kv_store(self.kv, k_new, v_new, self.slot_map[:k_new.shape[0]], stream)
+        write = se_paged_kv8_store if isinstance(self.kv, SEPagedKV8) else se_paged_kv_store
+        write(self.kv, k_new, v_new, self.slot_map[:k_new.shape[0]], stream)
+
+    def rotate(self, rotary: Rotary, q, k, q_out=None, k_out=None, stream=None):
+        """The query and key rows [T][heads][D] of the tokens that extend placed, turned by their positions (in place
+        without outputs); the padded rows behind the batch's last token are left."""
+        rows = (k if q is None else q).shape[0]
+        rotary.apply(q, k, self.positions[:rows], q_out, k_out, self.token_start[-1:], stream=stream)
+
+    def load(self, token_start, k_out, v_out, first=None, stream=None):
+        """Rows of an 8-bit cache back as bf16 into k_out and v_out [T][Hkv][D]: request b's positions from first[b]
+        (None: 0) on at rows token_start[b] .. token_start[b + 1] - 1."""
+        if not isinstance(self.kv, SEPagedKV8):
+            raise ValueError("load: the cache is not in 8 bits")
+        se_paged_kv8_load(self.kv, self.block_table, token_start, k_out, v_out, first, stream)
 
     def attend(self, q, sink_tokens: int = 0, recent_tokens: int = 0, stream=None):
         return self.attention.run(q, self.block_table, self.lens, sink_tokens, recent_tokens, stream)
@@ -107,7 +159,7 @@ class PagedCache:
     def release(self, keep_lens=None, stream=None):
         """The pages behind keep_lens[b] tokens (None: all of them) back to the pool; the lengths shrink, except of
         requests whose release is refused (and reported): a keep_lens[b] below 0 or above the length. A page that
-        keep_lens ends in keeps its summary, which bounds the dropped keys too."""
+        keep_lens ends in keeps its summary, which bounds the dropped keys too, and its scales in 8 bits."""
         se_block_tables_release_ex(self.free_pages, self.pool_state, self.block_table, self.lens, keep_lens, self.lens,
                                    stream)
 
