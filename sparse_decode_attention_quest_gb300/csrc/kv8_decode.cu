@@ -11,12 +11,10 @@
 //
 //  * Codes become fp16 (exact) on their way from shared memory, two conversions a word, and both products
 //    are m16n8k16 fp16 MMAs. Neither operand's order matters as long as both have it: K's words keep
-//    four dims of a token together, so Q^T is loaded in that order. V comes through the 8 x 8 transposes of
-//    ldmatrix, which move pairs of codes, two dims of a token; a byte permutation and the conversions make
-//    of them the A operands of the even and of the odd dims, whose rows are then 2 g and 2 g + 1 of
-//    sixteen dims instead of g and g + 8: nothing but the epilogue sees it. (m16n8k32 e4m3 MMAs on the codes
-//    themselves are expanded into the same conversions, of Q too and every time: 454 instructions a block of
-//    16 tokens and one head, with the query split into two e4m3 numbers; 691 us for 3.2 GB.)
+//    four dims of a token together, so Q^T is loaded in that order; V's, transposed as bytes, four tokens of a dim, so
+//    P^T has them in that order, which the rows of K and V are read in such orders for (and without bank
+//    conflicts): no bytes are moved in registers. (m16n8k32 e4m3 MMAs on K's codes as they lie, the query split into
+//    two e4m3 numbers a dim, were slower: 454 instructions a block of 16 tokens and one head, 691 us for 3.2 GB.)
 //  * A query row is scaled by a power of two to at most 448 and held as fp16: exact for dims down to 2^-25 of the
 //    row's largest magnitude, within 2^-32 of it below.
 //  * V's scales go into the weights before they are rounded to fp16: a weight enters as
@@ -67,6 +65,14 @@ struct Cfg {
 __host__ __device__ constexpr int pages_at_once(int head_dim, int tiles) {
   return tiles > 1 || head_dim > 128 ? 1 : head_dim == 128 ? 2 : 4;
 }
+
+// The order in which the MMAs have a page's 16 tokens: row i of S^T is token k_row(i); V's rows are read as v_row(0),
+// v_row(1) .., and a lane's word of them is tokens v_row(4 t) .. v_row(4 t + 3). The transposes of P^T put rows 2 t and
+// 2 t + 1 of S^T's upper half into the first two of these places and of its lower half into the others, so
+//     k_row(2 t + j) = v_row(4 t + j),  k_row(8 + 2 t + j) = v_row(4 t + 2 + j),  j = 0, 1,
+// and any eight rows that are read at once have all residues modulo 8, which the swizzle spreads over all banks.
+__device__ __forceinline__ int k_row(int i) { return i < 8 ? i : 8 + (i & 7 ^ 4); }
+__device__ __forceinline__ int v_row(int i) { return k_row((i >> 2) * 2 + (i & 1) + (i & 2) * 4); }
 
 // Byte offset of 16-byte chunk c of a block's row r: lines of 128 bytes, swizzled, `plane` bytes between the lines'
 // first and second 128 bytes of a row; two rows of 64 dims share a line.
@@ -223,6 +229,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
       }
     }
     // Every copy has landed before the CTA leaves.
+    cp_async_wait_all();
     if (lane == 0) {
       for (int u = max(0, j - kSlots); u < j; ++u)
         if (!mbar_wait(&full[u % kSlots], (u / kSlots) & 1)) dead = true;
@@ -240,7 +247,9 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
   const uint32_t ring0 = smem_addr(ring);
   const uint32_t plane = (uint32_t)heads * kPageSize * 128;  // 128 dims of a page's rows
   const uint32_t page_bytes = (uint32_t)heads * kPageSize * kD;
-  const uint32_t off = row_chunk<kD>(lane & 15, lane >> 4, plane);  // of ldmatrix: 16 rows, two chunks
+  // Of ldmatrix: 16 rows, two chunks.
+  const uint32_t off_k = row_chunk<kD>(k_row(lane & 15), lane >> 4, plane);
+  const uint32_t off_v = row_chunk<kD>(v_row(lane & 15), lane >> 4, plane);
   constexpr int kPp = pages_at_once(kD, kNt);
   int sk = 0, step = 0;   // K's slot of the step, and the parity of its use
   uint32_t phase = 0;
@@ -286,7 +295,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
       zf[nt][0] = __shfl_sync(0xffffffffu, qs, 8 * t) * a.scale_log2;
       zf[nt][1] = __shfl_sync(0xffffffffu, qs, 8 * t + 4) * a.scale_log2;
     }
-    // O^T: dims 16 i + 2 g (0, 1) and the next (2, 3), heads 2 t and 2 t + 1 of each column tile, times
+    // O^T: dims 16 i + g (0, 1) and 8 more (2, 3), heads 2 t and 2 t + 1 of each column tile, times
     // 2^(14 - m - d); m, d and l (times 2^-m, the thread's tokens only) of those heads.
     float o[kD / 16][kNt][4], m[kNt][2], d[kNt][2], l[kNt][2];
 #pragma unroll
@@ -331,7 +340,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
 #pragma unroll
         for (int u = 0; u < kPp; ++u) all &= mask[u];
         const bool whole = all != 0;
-        // Products of tokens g (0, 1) and g + 8 (2, 3), heads 2 t and 2 t + 1, times their factors; K's scale.
+        // Products of tokens k_row(g) (0, 1) and k_row(g + 8) (2, 3), heads 2 t and 2 t + 1, times their factors; K's scale.
         float s[kPp][kNt][4], ks[kPp];
         if (any) {
 #pragma unroll
@@ -347,7 +356,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
               // The swizzle is an exclusive or of the 16-byte chunk with the line: two chunks further is one of bit 5 on.
               uint32_t r[4], lo[4], hi[4];
               ldmatrix_x4(r[0], r[1], r[2], r[3],
-                          ((ring0 + sk * kSlotBytes + at[u] + off) ^ ((c & 3) << 5)) + (c >> 2) * plane);
+                          ((ring0 + sk * kSlotBytes + at[u] + off_k) ^ ((c & 3) << 5)) + (c >> 2) * plane);
 #pragma unroll
               for (int k = 0; k < 4; ++k) e4m3x4_to_f16(r[k], lo[k], hi[k]);
 #pragma unroll
@@ -366,7 +375,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
 #pragma unroll
               for (int e = 0; e < 4; ++e) s[u][nt][e] *= zf[nt][e & 1];
             if (!whole) {
-              const bool k0 = in_mask(mask[u] & ~kWhole, g), k1 = in_mask(mask[u] & ~kWhole, g + 8);
+              const bool k0 = in_mask(mask[u] & ~kWhole, g), k1 = in_mask(mask[u] & ~kWhole, k_row(g + 8));
 #pragma unroll
               for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
@@ -473,18 +482,18 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
           for (int c = 0; c < kD / 32; ++c) {
 #pragma unroll
             for (int u = 0; u < kPp; ++u) {
-              // Two chunks of 16 dims, tokens 0-7 and 8-15 of each: (2 dims of token 2 t, 2 dims of the next) a word.
-              uint32_t r[4], even[4], odd[4];
-              ldmatrix_x4_trans(r[0], r[1], r[2], r[3],
-                                ((ring0 + sv * kSlotBytes + at[u] + off) ^ ((c & 3) << 5)) + (c >> 2) * plane);
+              // Two chunks of 16 dims: four tokens of dims g and g + 8 of each.
+              uint32_t r[4], lo[4], hi[4];
+              ldmatrix_x2_trans_b8(r[0], r[1], r[2], r[3],
+                                   ((ring0 + sv * kSlotBytes + at[u] + off_v) ^ ((c & 3) << 5)) + (c >> 2) * plane);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) e4m3x4_to_f16(__byte_perm(r[k], 0u, 0x3120), even[k], odd[k]);
+              for (int k = 0; k < 4; ++k) e4m3x4_to_f16(r[k], lo[k], hi[k]);
 #pragma unroll
               for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int nt = 0; nt < kNt; ++nt)
-                  mma_f16_16816(o[2 * c + k][nt], even[2 * k], odd[2 * k], even[2 * k + 1], odd[2 * k + 1],
-                                pb[u][nt][0], pb[u][nt][1]);
+                  mma_f16_16816(o[2 * c + k][nt], lo[2 * k], lo[2 * k + 1], hi[2 * k], hi[2 * k + 1], pb[u][nt][0],
+                                pb[u][nt][1]);
             }
           }
         }
@@ -541,8 +550,8 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
 #pragma unroll
         for (int i = 0; i < kD / 16; ++i) {
           const float f = kSolo ? 1.f : fast_exp2(d[nt][e] - kWeightTop);
-          *reinterpret_cast<float2*>(dst + stage_at<kD>(hd, 16 * i + 2 * g)) =
-              make_float2(o[i][nt][e] * f, o[i][nt][2 + e] * f);
+          dst[stage_at<kD>(hd, 16 * i + g)] = o[i][nt][e] * f;
+          dst[stage_at<kD>(hd, 16 * i + g + 8)] = o[i][nt][2 + e] * f;
         }
         if (g == 0) {
           ml[warp * 16 + hd] = m[nt][e];
