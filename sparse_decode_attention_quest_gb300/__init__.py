@@ -478,12 +478,13 @@ def _rows_ptr(t, heads: int, width: int, dtype, name: str, dev: int):
     any distance apart (columns of a fused projection's output, say)."""
     if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype:
         _refuse(t, dtype, name, dev)
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != width:
-        raise ValueError(f"{name}: expected shape [N][{heads}][{width}], got {list(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != width:
+        raise ValueError(f"{name}: expected shape [N][{heads}][{width}], got {list(shape)}")
     row, head, one = t.stride()
     if (width > 1 and one != 1) or (heads > 1 and head != width):
         raise ValueError(f"{name}: the heads of a row must be dense")
-    return t.data_ptr(), row if t.shape[0] > 1 else heads * width
+    return t.data_ptr(), row if shape[0] > 1 else heads * width
 
 
 def se_block_tables_extend(free_pages, pool_state, block_table, seq_lens, new_lens, seq_lens_after, token_start,
