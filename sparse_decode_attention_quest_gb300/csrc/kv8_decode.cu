@@ -341,14 +341,15 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
         for (int u = 0; u < kPp; ++u) all &= mask[u];
         const bool whole = all != 0;
         // Products of tokens k_row(g) (0, 1) and k_row(g + 8) (2, 3), heads 2 t and 2 t + 1, times their factors; K's scale.
-        float s[kPp][kNt][4], ks[kPp];
+        constexpr int kAcc = kPp * kNt == 1 ? 2 : 1;  // accumulators of a page's products where there is no other chain
+        float s[kPp][kNt][4], more[kPp][kNt][4], ks[kPp];
         if (any) {
 #pragma unroll
           for (int u = 0; u < kPp; ++u)
 #pragma unroll
             for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) s[u][nt][e] = 0.f;
+              for (int e = 0; e < 4; ++e) s[u][nt][e] = more[u][nt][e] = 0.f;
 #pragma unroll
           for (int c = 0; c < kD / 32; ++c) {
 #pragma unroll
@@ -363,8 +364,8 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
               for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int nt = 0; nt < kNt; ++nt)
-                  mma_f16_16816(s[u][nt], lo[2 * k], lo[2 * k + 1], hi[2 * k], hi[2 * k + 1], qb[2 * c + k][nt][0],
-                                qb[2 * c + k][nt][1]);
+                  mma_f16_16816(kAcc == 2 && k ? more[u][nt] : s[u][nt], lo[2 * k], lo[2 * k + 1], hi[2 * k],
+                                hi[2 * k + 1], qb[2 * c + k][nt][0], qb[2 * c + k][nt][1]);
             }
           }
 #pragma unroll
@@ -373,7 +374,8 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
 #pragma unroll
             for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) s[u][nt][e] *= zf[nt][e & 1];
+              for (int e = 0; e < 4; ++e)
+                s[u][nt][e] = (kAcc == 2 ? s[u][nt][e] + more[u][nt][e] : s[u][nt][e]) * zf[nt][e & 1];
             if (!whole) {
               const bool k0 = in_mask(mask[u] & ~kWhole, g), k1 = in_mask(mask[u] & ~kWhole, k_row(g + 8));
 #pragma unroll
