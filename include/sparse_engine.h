@@ -548,7 +548,8 @@ typedef struct {
  * token holds (but for those small values) what it holds filled at once.
  * NaN and infinities are stored as NaN and do not count for amax.
  *   k_new, v_new: bf16 rows and strides as se_paged_kv_store's; slot_map: as there (negative: padding, skipped).
- * A slot is named once; a slot named twice in neighbouring tokens of one page keeps the later row. A slot at or behind
+ * A slot is named once; a slot named twice in neighbouring tokens of one page keeps the later row. A page whose new tokens
+ * do not stand next to each other ends with codes and a scale that need not belong together. A slot at or behind
  * num_pages * 16 sets SE_DEVERR_PAGE_RANGE and is skipped.
  */
 SE_API se_status_t se_paged_kv8_store(const se_paged_kv8_t* kv, const void* k_new, int64_t k_stride,

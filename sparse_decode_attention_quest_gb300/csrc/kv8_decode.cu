@@ -40,9 +40,11 @@ constexpr int kSlotBytes = 32 * 1024;
 constexpr int kMetaRing = 4;     // steps whose page masks are held (at most three are in flight)
 constexpr int kMaxPages = 32;    // pages of a step
 constexpr int kMaxBatch = 4096;  // requests whose prefix fits beside the ring
-constexpr int kInlineBytes = 48 * 1024;  // partials of an item, in slices, where one CTA merges them
+// Partials of an item, in slices, where one CTA merges them (48 windows of 1,064 tokens, 32/4 heads: 22.5 us, with 32 KB
+// 21.9, with 192 KB 25.6; 8 requests of 4K tokens, 64/8 heads of 64 dims: 17.0, 19.1, 34.3).
+constexpr int kInlineBytes = 48 * 1024;
 constexpr int kInlineWidth = 32;          // pages of an item from which smaller boxes are taken for that
-constexpr long long kSmallBoxBytes = 128 << 20;  // codes of a full table up to which they are
+constexpr double kSmallBoxBytes = 64 << 20;  // codes of a full table up to which they are
 
 constexpr float kWeightTop = 14.f;    // log2 of the weight at the reference
 constexpr float kWeightMost = 15.9f;  // log2 of the largest weight, within fp16
@@ -685,13 +687,15 @@ HeadPlan head_plan(int num_kv_heads, int group, int head_dim, int most_heads) {
 }
 
 // The largest boxes, unless the table's (or the windows') width keeps an item's partials, counted in slices of the
-// least length, so few that smaller ones let the decode kernel join them. Not for short items, which are seldom split.
+// least length, so few that smaller ones let the decode kernel join them (4 requests of 2-3K tokens, 32/8 heads: 14.4 us
+// against 14.9 with the second kernel). Not for short items, which are seldom split, nor where a full table holds more
+// than kSmallBoxBytes, since the smaller boxes read more slowly (16 such requests 25.1 against 23.8, 32 39.8 against 35.6).
 HeadPlan call_plan(int num_kv_heads, int group, int head_dim, int32_t bt_stride, int32_t sink_tokens,
                    int32_t recent_tokens, int batch, int ctas) {
   long long width = bt_stride;
   if (recent_tokens > 0)
     width = std::min(width, ((long long)sink_tokens + kPageSize - 1) / kPageSize + recent_tokens / kPageSize + 2);
-  const bool little = batch * width * num_kv_heads * kPageSize * head_dim * 2 <= kSmallBoxBytes;
+  const bool little = (double)batch * width * num_kv_heads * (kPageSize * head_dim * 2) <= kSmallBoxBytes;
   for (int c = 8; c > 0;) {
     HeadPlan p = head_plan(num_kv_heads, group, head_dim, c);
     if (c < 8 && (width < kInlineWidth || !little)) break;
