@@ -393,6 +393,23 @@ def test_a_cache_of_more_than_two_to_the_31_bytes(cuda_device):
         assert bool(((out[b].double().cpu() - ref).abs() <= (2.0 ** -11 + 1e-4) * mag + 2.0 ** -8 * ref.abs() * 1.01).all())
 
 
+@pytest.mark.parametrize("shape", SHAPES)
+def test_calls_at_once_on_two_streams(cuda_device, shape):
+    """Calls that share neither workspace nor outputs may overlap; their results stay."""
+    x = Inputs(cuda_device, [5000, 3, 700], *shape, seed=21)
+    y = Inputs(cuda_device, [7, 2500, 64], *shape, seed=22)
+    want = [t.run()[0] for t in (x, y)]
+    outs = [torch.empty_like(w) for w in want]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for t, o, st in zip((x, y), outs, streams):
+            se.se_paged_kv8_decode(t.kv, t.dq, t.dt, t.dl, t.scale, o, None, t.ws, stream=st)
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert torch.equal(w.view(torch.int16), o.view(torch.int16))
+
+
 def test_binding_checks(cuda_device):
     x = Inputs(cuda_device, [5, 6], 8, 2, 128, seed=15)
     out = torch.empty(2, 8, 128, dtype=torch.bfloat16, device=cuda_device)

@@ -249,3 +249,63 @@ def test_streams(cuda_device):
     slots, pages = _slots(RUNS["ragged"], torch.Generator().manual_seed(8))
     _check(cuda_device, slots, pages, 2, 128, stream=s)
     _check_load(cuda_device, [33, 7], None, 2, 128, stream=s)
+
+
+def test_load_of_the_largest_batch(cuda_device):
+    """16,384 requests of up to three rows, a page each."""
+    dev, B = cuda_device, 16384
+    g = torch.Generator().manual_seed(11)
+    counts = torch.randint(0, 4, (B,), generator=g)
+    firsts = torch.randint(0, 14, (B,), generator=g)
+    c = Cache(dev, B, 1, 64, 11)
+    table = torch.randperm(B, generator=g).int()[:, None]
+    start = torch.cat([torch.zeros(1, dtype=torch.int64), torch.cumsum(counts, 0)]).int()
+    T = int(start[-1])
+    out = [torch.full((T + 5, 1, 64), 7.0, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    se.se_paged_kv8_load(c.kv, table.to(dev), start.to(dev), *out, firsts.int().to(dev))
+    r = torch.repeat_interleave(torch.arange(B), counts)
+    pos = (firsts[r] + torch.arange(T) - start[r]).numpy()
+    for n, o in zip("kv", out):
+        page = table[r, 0].numpy()
+        want = k8.VALUES[c.codes[n][page, :, pos]] * c.scale[n][page].astype(np.float64)[..., None]
+        np.testing.assert_array_equal(o[:T].double().cpu().numpy(), want)
+        assert bool((o[T:] == 7.0).all())
+    with pytest.raises(se.SparseEngineError, match="batch >"):
+        z = torch.zeros(B + 2, dtype=torch.int32, device=dev)
+        se.se_paged_kv8_load(c.kv, torch.zeros(B + 1, 1, dtype=torch.int32, device=dev), z, *out)
+
+
+def test_recorded_store_and_load(cuda_device):
+    """Recorded once; the replays take the slots, rows and spans that their buffers hold then."""
+    dev = cuda_device
+    s = torch.cuda.Stream(device=dev)
+    c = Cache(dev, 6, 2, 128, 12)
+    kn, vn = (torch.zeros(20, 2, 128, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    slots = torch.full((20,), -1, dtype=torch.int32, device=dev)
+    table = torch.arange(6, dtype=torch.int32, device=dev).view(2, 3)
+    start = torch.zeros(3, dtype=torch.int32, device=dev)
+    out = [torch.zeros(96, 2, 128, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    torch.cuda.synchronize()
+    se.se_capture_begin(s)
+    se.se_paged_kv8_store(c.kv, kn, vn, slots, s)
+    se.se_paged_kv8_load(c.kv, table, start, *out, stream=s)
+    step = se.se_capture_end(s)
+    g = torch.Generator().manual_seed(13)
+    for i, (a, b) in enumerate([(20, 0), (7, 13), (0, 16)]):
+        new = [_rows(g, 20, 2, 128) for _ in range(2)]
+        at = [16 * (i % 2) + j for j in range(a)] + [48 + 16 * i + j for j in range(b)] + [-1] * (20 - a - b)
+        slots.copy_(torch.tensor(at, dtype=torch.int32))
+        kn.copy_(new[0])
+        vn.copy_(new[1])
+        start.copy_(torch.tensor([0, 30 + i, 70], dtype=torch.int32))
+        for o in out:
+            o.fill_(7.0)
+        torch.cuda.synchronize()
+        step.launch(s)
+        s.synchronize()
+        c.store(*new, at)
+        c.check()
+        for n, o in zip("kv", out):
+            want, err = k8.load(c.codes[n], c.scale[n], table.cpu().numpy(), [0, 30 + i, 70], np.full(o.shape, 7.0))
+            assert err == 0
+            np.testing.assert_array_equal(o.double().cpu().numpy(), want)

@@ -134,6 +134,25 @@ def test_turning_back(cuda_device):
     assert bool(((z - x).float().abs() <= 2.0 ** -7 * 1.01 * size).all())
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_outputs_as_columns_of_a_wider_tensor(cuda_device, interleaved):
+    dev = cuda_device
+    g = torch.Generator().manual_seed(6)
+    q, k = (torch.randn(37, h, 128, generator=g).to(torch.bfloat16).to(dev) for h in (6, 2))
+    pos = (torch.arange(37, dtype=torch.int32) * 77).to(dev)
+    freqs = se.se_rotary_frequencies(64)[0].to(dev)
+    want = [torch.empty_like(t) for t in (q, k)]
+    se.se_rotary(q, k, pos, freqs, *want, rotary_offset=32, interleaved=interleaved)
+    wide = torch.full((37, 13, 128), 7.0, dtype=torch.bfloat16, device=dev)
+    se.se_rotary(q, k, pos, freqs, wide[:, 1:7], wide[:, 9:11], rotary_offset=32, interleaved=interleaved)
+    assert torch.equal(wide[:, 1:7], want[0]) and torch.equal(wide[:, 9:11], want[1])
+    assert bool((wide[:, [0, 7, 8, 11, 12]] == 7.0).all())
+    # One in place, the other not: the same bits, and dims that are not turned stay.
+    mixed = q.clone()
+    se.se_rotary(mixed, k, pos, freqs, None, wide[:, 9:11], rotary_offset=32, interleaved=interleaved)
+    assert torch.equal(mixed, want[0]) and torch.equal(wide[:, 9:11], want[1])
+
+
 def test_another_stream_and_a_recorded_step(cuda_device):
     dev = cuda_device
     s = torch.cuda.Stream(device=dev)
