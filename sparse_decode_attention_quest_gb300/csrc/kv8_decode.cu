@@ -16,7 +16,7 @@
 //    conflicts): no bytes are moved in registers. (m16n8k32 e4m3 MMAs on K's codes as they lie, the query split into
 //    two e4m3 numbers a dim, were slower: 454 instructions a block of 16 tokens and one head, 691 us for 3.2 GB.)
 //  * A query row is scaled by a power of two to at most 448 and held as fp16: exact for dims down to 2^-25 of the
-//    row's largest magnitude, within 2^-32 of it below.
+//    row's largest magnitude, within 2^-32 of it below (2^-125 where the power of two is the least, 2^-100).
 //  * V's scales go into the weights before they are rounded to fp16: a weight enters as
 //    w_j = exp2(z_j - m + log2 s_v - d + 14), with m + d a reference of their product's maximum, so that it is rounded
 //    by half a step of 2^-11 down to 2^-28 of the largest, whatever the scales of pages that carry no weight. The

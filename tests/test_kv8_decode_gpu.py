@@ -194,6 +194,17 @@ def test_scales_of_pages(cuda_device, shape, spread, odd):
 
 
 @pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("k_exp,v_exp", [(-100, -100), (-100, 100), (60, -100), (60, 100)])
+def test_least_and_large_scales(cuda_device, shape, k_exp, v_exp):
+    """The least scales that a store writes, and large ones; the queries make ordinary logits of them."""
+    x = Inputs(cuda_device, [70, 333, 17, 2500], *shape, seed=20, q_scale=2.0 ** (-7 - k_exp))
+    for n, e in (("k", k_exp), ("v", v_exp)):
+        x.s[n] = torch.exp2(torch.randint(e, e + 3, x.s[n].shape, generator=torch.Generator().manual_seed(e + 200)).float())
+    x.upload()
+    x.check()
+
+
+@pytest.mark.parametrize("shape", SHAPES)
 @pytest.mark.parametrize("scale,q_scale", [(0.0, 1.0), (-0.07, 1.0), (1.0, 0.1), (1e-3, 300.0), (1e20, 1e-21), (1e-9, 1e8)])
 def test_scales_of_queries(cuda_device, shape, scale, q_scale):
     Inputs(cuda_device, [70, 333, 17], *shape, scale=scale, q_scale=q_scale, seed=6).check()
