@@ -50,11 +50,18 @@ constexpr float kWeightTop = 14.f;    // log2 of the weight at the reference
 constexpr float kWeightMost = 15.9f;  // log2 of the largest weight, within fp16
 constexpr float kLowest = -3.4e38f;   // m and d before any logit
 
-template <int kD>
+// kMany: the kernel for many query heads per KV head. Nine warps, three of them on one scheduler, have 168 registers a thread;
+// twelve have as many, and four of them, of which one works, hand theirs to the consumers: tiles of sixteen
+// heads and two pages at once without spills (0.3 GB in 16K tokens a request, 32 heads of 128 dims over one: 118 us before,
+// 98 so; 64: 201 and 164; 16 over each of 4 of 64 dims: 80 and 71; 12 over each of 2 of 256 dims, 0.5 GB: 124 and 106).
+// What bounds it is the time of the MMAs (8 clocks each) with the conversions, which hardly overlap.
+template <int kD, bool kMany>
 struct Cfg {
   static constexpr int kWarps = 8;  // consumers
   static constexpr int kConsumers = kWarps * 32;
-  static constexpr int kThreads = kConsumers + 32;
+  static constexpr int kProducers = kMany ? 128 : 32;
+  static constexpr int kThreads = kConsumers + kProducers;
+  static constexpr int kProducerRegs = 56, kConsumerRegs = 224;  // kMany: a thread's, of 168 at launch
   static constexpr int kSlots = kD == 256 ? 4 : 5;
   static constexpr int kBlocks = kSlotBytes / (kPageSize * kD);  // (page, head) blocks of a slot
   static constexpr int kStageFloats = kWarps * 8 * kD;           // states handed over at a segment's end
@@ -63,10 +70,11 @@ struct Cfg {
   static constexpr int kMaxSmem = kFixed + kept_ints(kMaxBatch) * 4;
 };
 
-// Pages that a warp takes at once.
-__host__ __device__ constexpr int pages_at_once(int head_dim, int tiles) {
-  return tiles > 1 || head_dim > 128 ? 1 : head_dim == 128 ? 2 : 4;
+// Pages that a warp takes at once, and column tiles of eight query heads that it has.
+__host__ __device__ constexpr int pages_at_once(int head_dim, bool many) {
+  return many || head_dim == 128 ? 2 : head_dim == 64 ? 4 : 1;
 }
+__host__ __device__ constexpr int tiles_at_once(int head_dim, bool many) { return many && head_dim <= 128 ? 2 : 1; }
 
 // The order in which the MMAs have a page's 16 tokens: row i of S^T is token k_row(i); V's rows are read as v_row(0),
 // v_row(1) .., and a lane's word of them is tokens v_row(4 t) .. v_row(4 t + 3). The transposes of P^T put rows 2 t and
@@ -119,14 +127,14 @@ struct Kv8Args {
   unsigned* err;
 };
 
-// kNt: column tiles of eight query heads; kSolo: no two warps share a (head, tile) (code of its own: as a branch
+// kSolo: no two warps share a (head, tile) (code of its own: as a branch
 // beside the other it cost that one 0.8 us of 9.9).
-template <int kD, int kNt, bool kSolo>
-__global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap,
+template <int kD, bool kMany, bool kSolo>
+__global__ void __launch_bounds__(Cfg<kD, kMany>::kThreads, 1) kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                                                                            const __grid_constant__ CUtensorMap vmap,
                                                                            const Kv8Args a) {
-  using C = Cfg<kD>;
-  constexpr int kSlots = C::kSlots;
+  using C = Cfg<kD, kMany>;
+  constexpr int kSlots = C::kSlots, kNt = tiles_at_once(kD, kMany), kPp = pages_at_once(kD, kMany);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* stage = reinterpret_cast<float*>(ring + kSlots * kSlotBytes);  // [warps][8][D]
@@ -181,8 +189,12 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
   seg.init(slices, slice.x, slice.y);
   bool dead = false;  // a bounded wait gave up: no further waits or products, but every barrier
 
-  if (warp == C::kWarps) {
+  if (warp >= C::kWarps) {
     // ------------------------------------------------------------ TMA producer
+    if constexpr (kMany) {
+      set_max_registers<C::kProducerRegs, false>();
+      if (warp > C::kWarps) return;
+    }
     const uint64_t policy = l2_evict_first_policy();
     const uint32_t page_bytes = (uint32_t)heads * kPageSize * kD;
     const int my_page = lane / heads, my_head = lane - my_page * heads;  // the block whose scales this lane copies
@@ -241,6 +253,7 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
   }
 
   // -------------------------------------------------------------- consumers
+  if constexpr (kMany) set_max_registers<C::kConsumerRegs, true>();
   const bool works = warp < active;
   const int combo = warp % combos, replica = warp / combos;
   const int hc = combo / a.mtiles, mt = combo % a.mtiles;
@@ -252,7 +265,6 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) kv8_decode_kernel(const 
   // Of ldmatrix: 16 rows, two chunks.
   const uint32_t off_k = row_chunk<kD>(k_row(lane & 15), lane >> 4, plane);
   const uint32_t off_v = row_chunk<kD>(v_row(lane & 15), lane >> 4, plane);
-  constexpr int kPp = pages_at_once(kD, kNt);
   int sk = 0, step = 0;   // K's slot of the step, and the parity of its use
   uint32_t phase = 0;
   if (warp == 0) {  // while the first copies are on their way; in shared memory, as the loop needs its registers
@@ -651,22 +663,20 @@ struct HeadPlan {
   bool deferred;
 };
 
-// Query heads per KV head up to which a tile holds eight of them, above it (128 dims alone) sixteen. Sixteen
-// share the conversions of K and V but take one page at a time and spill: of 0.3 GB in 16K tokens a request, 32 heads
-// over one 134 us against 156, 16 heads over each of 4 82 against 76; 32 requests of 2K tokens with 16 heads over each
-// of 4 42 against 32. Of 64 dims 64 heads over one 309 against 313, those 32 requests 34 against 28.
-int eights_up_to(int head_dim) { return head_dim == 128 ? 16 : 64; }
+// Query heads per KV head from which the kernel for many is taken: 64 and 256 dims 9, 128 dims 17 (16 over each of 4, 0.3 GB in
+// 16K tokens a request: 65 us against 68; but 32 requests of 2K tokens 30 against 28).
+bool takes_many(int head_dim, int group) { return group > (head_dim == 128 ? 16 : 8); }
 
 // The KV heads of a box, up to `most_heads`: the count that the slower of copies and warps lets run fastest, the larger
 // of two alike. Boxes of 1 KB read at 48% of the measured copy rate, of 2 KB at 72%, from 4 KB on at 89%; every
 // warp that has pages carries an eighth of it (0.6 GB, 16K tokens a request: 7 heads of 128 dims 87% in one box, 5
 // heads 67%, 10 heads 89% in pairs, 67% in fives and 72% alone). A warp's pages are whole sets of those it takes at once.
 HeadPlan head_plan(int num_kv_heads, int group, int head_dim, int most_heads) {
-  const int warps = Cfg<128>::kWarps, blocks = kSlotBytes / (kPageSize * head_dim);
-  const bool sixteens = group > eights_up_to(head_dim);
-  const int once = pages_at_once(head_dim, sixteens ? 2 : 1);
+  const int warps = Cfg<128, false>::kWarps, blocks = kSlotBytes / (kPageSize * head_dim);
+  const bool many = takes_many(head_dim, group);
+  const int once = pages_at_once(head_dim, many), tile = 8 * tiles_at_once(head_dim, many);
   HeadPlan p;
-  p.mtiles = sixteens ? (group + 15) / 16 : (group + 7) / 8;
+  p.mtiles = (group + tile - 1) / tile;
   int best = 0;
   for (int c = 1; c <= most_heads && c * p.mtiles <= warps; ++c) {
     if (num_kv_heads % c) continue;
@@ -709,15 +719,24 @@ HeadPlan call_plan(int num_kv_heads, int group, int head_dim, int32_t bt_stride,
 
 int ctas_of(int sm_count) { return sm_count < kMaxCtas ? sm_count : kMaxCtas; }
 
-template <int kD, int kNt, bool kSolo>
+template <int kD, bool kMany, bool kSolo>
 cudaError_t launch_as(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8Args& a, int grid,
                    cudaStream_t stream) {
-  const size_t smem = Cfg<kD>::kFixed + kept_ints(a.batch) * 4;
-  static_assert(Cfg<kD>::kMaxSmem <= 227 * 1024, "the largest batch fits");
+  using C = Cfg<kD, kMany>;
+  const size_t smem = C::kFixed + kept_ints(a.batch) * 4;
+  static_assert(C::kMaxSmem <= 227 * 1024, "the largest batch fits");
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem(kv8_decode_kernel<kD, kNt, kSolo>, Cfg<kD>::kMaxSmem, allowed);
+  if (kMany && !allowed.load(std::memory_order_acquire)) {
+    // The consumers take their registers from the launch's: with fewer they would wait for them forever.
+    cudaFuncAttributes at;
+    const cudaError_t e = cudaFuncGetAttributes(&at, kv8_decode_kernel<kD, kMany, kSolo>);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs * C::kThreads < C::kProducerRegs * C::kProducers + C::kConsumerRegs * C::kConsumers)
+      return cudaErrorInvalidConfiguration;
+  }
+  cudaError_t e = allow_smem(kv8_decode_kernel<kD, kMany, kSolo>, C::kMaxSmem, allowed);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kv8_decode_kernel<kD, kNt, kSolo>, dim3(grid), dim3(Cfg<kD>::kThreads), smem, stream, kmap, vmap, a);
+  e = launch_pdl(kv8_decode_kernel<kD, kMany, kSolo>, dim3(grid), dim3(C::kThreads), smem, stream, kmap, vmap, a);
   if (e != cudaSuccess || !a.deferred) return e;
   const int rows = a.heads * a.group;
   // An item has at most `rows` units, and no more items than CTAs reach beyond a slice.
@@ -730,13 +749,11 @@ template <int kD>
 cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8Args& a, int grid,
                    cudaStream_t stream) {
   const bool solo = a.replicas == 1;
-  if (a.group <= 8 * a.mtiles)
-    return solo ? launch_as<kD, 1, true>(kmap, vmap, a, grid, stream)
-                : launch_as<kD, 1, false>(kmap, vmap, a, grid, stream);
-  if constexpr (kD == 128)  // the others have tiles of eight alone
-    return solo ? launch_as<kD, 2, true>(kmap, vmap, a, grid, stream)
-                : launch_as<kD, 2, false>(kmap, vmap, a, grid, stream);
-  return cudaErrorInvalidValue;
+  if (takes_many(kD, a.group))
+    return solo ? launch_as<kD, true, true>(kmap, vmap, a, grid, stream)
+                : launch_as<kD, true, false>(kmap, vmap, a, grid, stream);
+  return solo ? launch_as<kD, false, true>(kmap, vmap, a, grid, stream)
+              : launch_as<kD, false, false>(kmap, vmap, a, grid, stream);
 }
 
 }  // namespace

@@ -436,6 +436,15 @@ __device__ __forceinline__ int reduced_index(int lane) {
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
+// Registers a thread from here on, by all threads of a warpgroup (its four warps). An increase waits until the CTA's
+// other warpgroups have given back what it needs of the launch's registers.
+template <int kRegs, bool kMore>
+__device__ __forceinline__ void set_max_registers() {
+  if constexpr (kMore)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 // Arrive without waiting.
 __device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t count) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
