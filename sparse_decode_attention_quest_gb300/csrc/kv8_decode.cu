@@ -40,26 +40,25 @@ constexpr int kSlotBytes = 32 * 1024;
 constexpr int kMetaRing = 4;     // steps whose page masks are held (at most three are in flight)
 constexpr int kMaxPages = 32;    // pages of a step
 constexpr int kMaxBatch = 4096;  // requests whose prefix fits beside the ring
-// Partials of an item, in slices, where one CTA merges them (48 windows of 1,064 tokens, 32/4 heads: 22.5 us, with 32 KB
-// 21.9, with 192 KB 25.6; 8 requests of 4K tokens, 64/8 heads of 64 dims: 17.0, 19.1, 34.3).
-constexpr int kInlineBytes = 48 * 1024;
-constexpr int kInlineWidth = 32;          // pages of an item from which smaller boxes are taken for that
-constexpr double kSmallBoxBytes = 64 << 20;  // codes of a full table up to which they are
-
 constexpr float kWeightTop = 14.f;    // log2 of the weight at the reference
 constexpr float kWeightMost = 15.9f;  // log2 of the largest weight, within fp16
 constexpr float kLowest = -3.4e38f;   // m and d before any logit
 
-// kMany: the kernel for many query heads per KV head. Nine warps, three of them on one scheduler, have 168 registers a thread;
-// twelve have as many, and four of them, of which one works, hand theirs to the consumers: tiles of sixteen
-// heads and two pages at once without spills (0.3 GB in 16K tokens a request, 32 heads of 128 dims over one: 118 us before,
-// 98 so; 64: 201 and 164; 16 over each of 4 of 64 dims: 80 and 71; 12 over each of 2 of 256 dims, 0.5 GB: 124 and 106).
-// What bounds it is the time of the MMAs (8 clocks each) with the conversions, which hardly overlap.
+// Four warps issue the boxes, every fourth page each: a warp takes some 65 clocks to issue one and 35 more per KB, so
+// that one warp alone kept boxes of 1 KB to 48% of the copy rate and of 2 KB to 72% (0.3 GB in 32K tokens a request: one
+// head of 64 dims 49 us, of 128 dims 61; so 31 and 51; 5 heads of 128 dims, 0.7 GB: 133 and 108).
+//
+// kMany: the kernel for many query heads per KV head. The twelve warps have 168 registers a thread at launch; here those of
+// the issuers go to the consumers, for tiles of sixteen heads and two pages at once without spills (0.3 GB in 16K tokens a
+// request, 32 heads of 128 dims over one: 118 us before, 98 so; 64: 201 and 164; 16 over each of 4 of 64 dims: 80 and
+// 71; 12 over each of 2 of 256 dims, 0.5 GB: 124 and 106). What bounds it is the time of the MMAs (8 clocks each) with
+// the conversions, which hardly overlap.
 template <int kD, bool kMany>
 struct Cfg {
   static constexpr int kWarps = 8;  // consumers
   static constexpr int kConsumers = kWarps * 32;
-  static constexpr int kProducers = kMany ? 128 : 32;
+  static constexpr int kIssuers = 4;
+  static constexpr int kProducers = kIssuers * 32;
   static constexpr int kThreads = kConsumers + kProducers;
   static constexpr int kProducerRegs = 56, kConsumerRegs = 224;  // kMany: a thread's, of 168 at launch
   static constexpr int kSlots = kD == 256 ? 4 : 5;
@@ -153,7 +152,7 @@ __global__ void __launch_bounds__(Cfg<kD, kMany>::kThreads, 1) kv8_decode_kernel
   // What needs no input comes before the wait for the previous kernel; kept_prefix's barriers publish it.
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&full[s], 1 + 32);  // the copies of the codes, and each lane's of the scales
+      mbar_init(&full[s], C::kIssuers + 32);  // each issuer's boxes, and each lane's scales of the last one
       mbar_init(&empty[s], active);
     }
     mbar_fence_init();
@@ -190,11 +189,10 @@ __global__ void __launch_bounds__(Cfg<kD, kMany>::kThreads, 1) kv8_decode_kernel
   bool dead = false;  // a bounded wait gave up: no further waits or products, but every barrier
 
   if (warp >= C::kWarps) {
-    // ------------------------------------------------------------ TMA producer
-    if constexpr (kMany) {
-      set_max_registers<C::kProducerRegs, false>();
-      if (warp > C::kWarps) return;
-    }
+    // ------------------------------------------------------------ TMA producers: all go through all steps; the first
+    // writes the masks, the last copies the scales
+    if constexpr (kMany) set_max_registers<C::kProducerRegs, false>();
+    const int issuer = warp - C::kWarps;
     const uint64_t policy = l2_evict_first_policy();
     const uint32_t page_bytes = (uint32_t)heads * kPageSize * kD;
     const int my_page = lane / heads, my_head = lane - my_page * heads;  // the block whose scales this lane copies
@@ -217,28 +215,29 @@ __global__ void __launch_bounds__(Cfg<kD, kMany>::kThreads, 1) kv8_decode_kernel
         const int phys = i < base + 32 ? pc : pn;
         const bool mine = lane < Pg && i < seg.hi;
         const bool ok = mine && phys >= 0 && phys < a.num_pages;
+        const bool issues = ok && lane % C::kIssuers == issuer;
         if (mine && !ok) raise_error(a.err, SE_DEVERR_PAGE_RANGE);
         const int block_page = __shfl_sync(0xffffffffu, ok ? phys : -1, my_page);
-        const bool scaled = lane < Pg * heads && block_page >= 0;
+        const bool scaled = lane < Pg * heads && block_page >= 0 && issuer == C::kIssuers - 1;
         const size_t block = (size_t)max(block_page, 0) * a.num_kv_heads + seg.group * heads + my_head;
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ok)) * page_bytes;
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, issues)) * page_bytes;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++j) {
           const int s = j % kSlots;
           if (lane == 0 && j >= kSlots && !mbar_wait(&empty[s], (j / kSlots - 1) & 1)) dead = true;
           dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
           if (dead) break;
-          if (kv == 0 && lane < Pg)
+          if (kv == 0 && lane < Pg && issuer == 0)
             meta[(step % kMetaRing) * kMaxPages + lane] = ok ? tagged(page_mask(k, a.sink, k.logical(i))) : 0u;
           __syncwarp();
           if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
           __syncwarp();
-          if (ok)
+          if (issues)
             tma_load_3d(ring + s * kSlotBytes + lane * page_bytes, kv ? &vmap : &kmap, 0,
                         (phys * a.num_kv_heads + seg.group * heads) * (kPageSize * min(kD, 128) / 128), 0, &full[s],
                         policy);
           if (scaled) cp_async_4(smem_addr(scales + s * C::kBlocks + lane), (kv ? a.v_scale : a.k_scale) + block);
-          mbar_arrive_copies(&full[s]);
+          if (issuer == C::kIssuers - 1) mbar_arrive_copies(&full[s]);
         }
       }
     }
@@ -667,10 +666,9 @@ struct HeadPlan {
 // 16K tokens a request: 65 us against 68; but 32 requests of 2K tokens 30 against 28).
 bool takes_many(int head_dim, int group) { return group > (head_dim == 128 ? 16 : 8); }
 
-// The KV heads of a box, up to `most_heads`: the count that the slower of copies and warps lets run fastest, the larger
-// of two alike. Boxes of 1 KB read at 48% of the measured copy rate, of 2 KB at 72%, from 4 KB on at 89%; every
-// warp that has pages carries an eighth of it (0.6 GB, 16K tokens a request: 7 heads of 128 dims 87% in one box, 5
-// heads 67%, 10 heads 89% in pairs, 67% in fives and 72% alone). A warp's pages are whole sets of those it takes at once.
+// The KV heads of a box, up to `most_heads`: the count for which most warps have pages, the larger of two alike (0.6
+// GB, 16K tokens a request: 5 heads of 64 dims one to a box 61 us, five 86; 3 heads of 128 dims 70, 75). A warp's pages are
+// whole sets of those it takes at once.
 HeadPlan head_plan(int num_kv_heads, int group, int head_dim, int most_heads) {
   const int warps = Cfg<128, false>::kWarps, blocks = kSlotBytes / (kPageSize * head_dim);
   const bool many = takes_many(head_dim, group);
@@ -680,13 +678,11 @@ HeadPlan head_plan(int num_kv_heads, int group, int head_dim, int most_heads) {
   int best = 0;
   for (int c = 1; c <= most_heads && c * p.mtiles <= warps; ++c) {
     if (num_kv_heads % c) continue;
-    const int r = warps / (c * p.mtiles), box = c * kPageSize * head_dim;
+    const int r = warps / (c * p.mtiles);
     int each = blocks / c / r;
     if (each > once) each -= each % once;
-    const int copies = box >= 4096 ? 89 : box > 2048 ? 80 : box == 2048 ? 72 : 48;
-    const int rate = std::min(copies, c * p.mtiles * r * 100 / warps);
-    if (each == 0 || rate < best) continue;
-    best = rate;
+    if (each == 0 || c * p.mtiles * r < best) continue;
+    best = c * p.mtiles * r;
     p.heads = c;
     p.replicas = r;
     p.step_pages = each * r;
@@ -696,24 +692,26 @@ HeadPlan head_plan(int num_kv_heads, int group, int head_dim, int most_heads) {
   return p;
 }
 
-// The largest boxes, unless the table's (or the windows') width keeps an item's partials, counted in slices of the
-// least length, so few that smaller ones let the decode kernel join them (4 requests of 2-3K tokens, 32/8 heads: 14.4 us
-// against 14.9 with the second kernel). Not for short items, which are seldom split, nor where a full table holds more
-// than kSmallBoxBytes, since the smaller boxes read more slowly (16 such requests 25.1 against 23.8, 32 39.8 against 35.6).
+// Largest boxes of which an item's partials, counted in slices of the least length over the table's (or the windows')
+// width, have no more than 32 KB, so that the decode kernel joins them itself without delay; otherwise no more than 48
+// KB; otherwise the largest of all and a second kernel (48 windows of 1,064 tokens, 32/4 heads: 21.6 us, 22.6 with 48 KB
+// alone; 8 requests of 4K tokens, 64/8 heads of 64 dims: 15.5, 19.1, with 192 KB 34.3; but 1 request of 8K tokens, 32/8
+// heads: 12.0, 14.8 with 32 KB alone). More items than two to a CTA are not made for that: 300 requests of up to 1,000
+// tokens, 32/4 heads: 45 us, 63 in boxes of one head.
 HeadPlan call_plan(int num_kv_heads, int group, int head_dim, int32_t bt_stride, int32_t sink_tokens,
                    int32_t recent_tokens, int batch, int ctas) {
   long long width = bt_stride;
   if (recent_tokens > 0)
     width = std::min(width, ((long long)sink_tokens + kPageSize - 1) / kPageSize + recent_tokens / kPageSize + 2);
-  const bool little = (double)batch * width * num_kv_heads * (kPageSize * head_dim * 2) <= kSmallBoxBytes;
-  for (int c = 8; c > 0;) {
-    HeadPlan p = head_plan(num_kv_heads, group, head_dim, c);
-    if (c < 8 && (width < kInlineWidth || !little)) break;
-    const long long parts = std::min<long long>(ctas, (width + p.step_pages) / (2 * p.step_pages + 1) + 2);
-    p.deferred = parts * p.heads * group * head_dim * (long long)sizeof(float) > kInlineBytes;
-    if (!p.deferred) return p;
-    c = p.heads - 1;
-  }
+  for (const int most : {32 * 1024, 48 * 1024})
+    for (int c = 8; c > 0;) {
+      HeadPlan p = head_plan(num_kv_heads, group, head_dim, c);
+      if (c < 8 && (long long)batch * p.head_groups > 2 * ctas) break;
+      const long long parts = std::min<long long>(ctas, (width + p.step_pages) / (2 * p.step_pages + 1) + 2);
+      p.deferred = parts * p.heads * group * head_dim * (long long)sizeof(float) > most;
+      if (!p.deferred) return p;
+      c = p.heads - 1;
+    }
   return head_plan(num_kv_heads, group, head_dim, 8);
 }
 
