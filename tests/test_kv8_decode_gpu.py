@@ -169,6 +169,15 @@ def test_splits(cuda_device, batch, lo, hi, shape):
     Inputs(cuda_device, g.integers(lo, hi + 1, batch).tolist(), *shape, seed=4).check()
 
 
+@pytest.mark.parametrize("lens,sink,recent", [([20011], 0, 0), ([9000, 1, 0, 4095], 0, 0), ([330] * 160, 0, 0),
+                                              ([17, 40, 99, 5000, 333], 5, 100), (list(range(0, 200, 7)) * 3, 0, 0)])
+@pytest.mark.parametrize("shape", [(64, 1, 128), (48, 2, 128), (17, 1, 128), (136, 8, 128), (24, 2, 64), (64, 1, 64),
+                                   (128, 8, 64), (9, 1, 256), (64, 1, 256), (48, 4, 256)])
+def test_many_heads_in_splits_and_windows(cuda_device, shape, lens, sink, recent):
+    """More heads per KV head than a warp's tile of eight: tiles, replicas and boxes of every kind."""
+    Inputs(cuda_device, lens, *shape, seed=len(lens), sink=sink, recent=recent).check()
+
+
 @pytest.mark.parametrize("batch", [19, 76, 151, 152, 153, 160, 161])
 @pytest.mark.parametrize("shape", [(8, 2, 128), (9, 3, 64), (8, 8, 128), (12, 1, 256)])
 def test_about_one_short_request_per_cta(cuda_device, batch, shape):
