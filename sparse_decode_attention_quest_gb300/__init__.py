@@ -637,7 +637,7 @@ def se_rotary(q, k, positions, freqs, q_out=None, k_out=None, rotary_offset: int
 def paged_kv8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
               v_scale: torch.Tensor) -> SEPagedKV8:
     """se_paged_kv8_t for float8_e4m3fn caches [P][Hkv][16][D] and their fp32 scales [P][Hkv]. ``.device`` of the
-    result is their CUDA device's index."""
+    result is their CUDA device's index; it keeps the four tensors."""
     _ptr(k_cache, torch.float8_e4m3fn, "k_cache")
     if k_cache.dim() != 4 or k_cache.shape[2] != 16:
         raise ValueError("k_cache: expected [pages][heads][16][head_dim]")
@@ -654,6 +654,7 @@ def paged_kv8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tenso
             raise ValueError(f"{name}: is on cuda:{t.get_device()}, k_cache on cuda:{k_cache.get_device()}")
     kv = SEPagedKV8(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, H, ps, D)
     kv.device = k_cache.get_device()
+    kv.tensors = (k_cache, v_cache, k_scale, v_scale)
     return kv
 
 

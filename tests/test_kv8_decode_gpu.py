@@ -331,7 +331,8 @@ def test_one_workspace_for_other_lengths_streams_and_caches(cuda_device, shape):
     want, _ = x.run()
     y.check()
     k = torch.randn(400, H, 16, D, device=cuda_device).to(torch.bfloat16)
-    kv = se.paged_kv(k, k.clone(), None)
+    v = k.clone()
+    kv = se.paged_kv(k, v, None)
     out = torch.empty(2, Hq, D, dtype=torch.bfloat16, device=cuda_device)
     table = torch.arange(400, dtype=torch.int32, device=cuda_device).view(2, 200)
     lens = torch.tensor([3000, 77], dtype=torch.int32, device=cuda_device)
@@ -428,6 +429,16 @@ def test_calls_at_once_on_two_streams(cuda_device, shape):
     torch.cuda.synchronize()
     for w, o in zip(want, outs):
         assert torch.equal(w.view(torch.int16), o.view(torch.int16))
+
+
+def test_a_view_keeps_its_tensors(cuda_device):
+    x = Inputs(cuda_device, [5000, 3, 700], 8, 2, 128, seed=23)
+    want, _ = x.run()
+    x.kv = se.paged_kv8(x.d["k"].clone(), x.d["v"].clone(), x.ds["k"].clone(), x.ds["v"].clone())
+    # What was freed would be handed out again here.
+    taken = [torch.full_like(t.view(torch.uint8), 0x7F) for d in (x.d, x.ds) for t in d.values()]
+    got, _ = x.run()
+    assert len(taken) == 4 and torch.equal(got.view(torch.int16), want.view(torch.int16))
 
 
 def test_binding_checks(cuda_device):
