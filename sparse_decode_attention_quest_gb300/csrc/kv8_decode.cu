@@ -43,6 +43,8 @@ constexpr int kMaxBatch = 4096;  // requests whose prefix fits beside the ring
 constexpr float kWeightTop = 14.f;    // log2 of the weight at the reference
 constexpr float kWeightMost = 15.9f;  // log2 of the largest weight, within fp16
 constexpr float kLowest = -3.4e38f;   // m and d before any logit
+constexpr int kDown = 8;              // joins: up to 2^8 partials whose sum may pass fp32's largest
+static_assert(kMaxCtas <= 1 << kDown, "an item has no more partials than CTAs");
 
 // Four warps issue the boxes, every fourth page each: a warp takes some 65 clocks to issue one and 35 more per KB, so
 // that one warp alone kept boxes of 1 KB to 48% of the copy rate and of 2 KB to 72% (0.3 GB in 32K tokens a request: one
@@ -64,7 +66,7 @@ struct Cfg {
   static constexpr int kSlots = kD == 256 ? 4 : 5;
   static constexpr int kBlocks = kSlotBytes / (kPageSize * kD);  // (page, head) blocks of a slot
   static constexpr int kStageFloats = kWarps * 8 * kD;           // states handed over at a segment's end
-  static constexpr int kFixed = 1024 + kSlots * kSlotBytes + kStageFloats * 4 + kWarps * 16 * 4 +
+  static constexpr int kFixed = 1024 + kSlots * kSlotBytes + kStageFloats * 4 + kWarps * 8 * 4 +
                                 kMetaRing * kMaxPages * 4 + kSlots * kBlocks * 4 + 2 * kSlots * 8 + 64;
   static constexpr int kMaxSmem = kFixed + kept_ints(kMaxBatch) * 4;
 };
@@ -137,8 +139,8 @@ __global__ void __launch_bounds__(Cfg<kD, kMany>::kThreads, 1) kv8_decode_kernel
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* stage = reinterpret_cast<float*>(ring + kSlots * kSlotBytes);  // [warps][8][D]
-  float* ml = stage + C::kStageFloats;                                  // [warps][(m, l)][8]
-  uint32_t* meta = reinterpret_cast<uint32_t*>(ml + C::kWarps * 16);    // [kMetaRing][kMaxPages]
+  float* lses = stage + C::kStageFloats;                                // [warps][8], log2 domain
+  uint32_t* meta = reinterpret_cast<uint32_t*>(lses + C::kWarps * 8);   // [kMetaRing][kMaxPages]
   float* scales = reinterpret_cast<float*>(meta + kMetaRing * kMaxPages);  // [kSlots][kBlocks]
   uint64_t* full = reinterpret_cast<uint64_t*>(scales + kSlots * C::kBlocks);
   uint64_t* empty = full + kSlots;
@@ -544,34 +546,26 @@ __global__ void __launch_bounds__(Cfg<kD, kMany>::kThreads, 1) kv8_decode_kernel
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
         const int hd = 2 * t + e;
-        if constexpr (kSolo) {
+        // The average over the warp's own tokens (values near fp32's largest have no sum), 2^3 lower where it meets those of
+        // up to 2^3 warps.
+        const bool none = l[nt][e] == 0.f;
+        const float inv = none ? 0.f : fast_rcp(l[nt][e]);
+        const float f = fast_exp2(d[nt][e] - (kSolo ? kWeightTop : kWeightTop + 3.f));
+        const float lse2 = none ? -INFINITY : m[nt][e] + fast_log2(l[nt][e]);
+        if (kSolo && g == 0 && tile_head + nt * 8 + hd < G) {
           // No other states: the row is final.
-          const bool none = l[nt][e] == 0.f;
-          const float inv = none ? 0.f : fast_exp2(d[nt][e] - kWeightTop) * fast_rcp(l[nt][e]);
-          const float lse2 = none ? -INFINITY : m[nt][e] + fast_log2(l[nt][e]);
-          const int qr = tile_head + nt * 8 + hd, r = hc * G + qr;
-#pragma unroll
-          for (int i = 0; i < kD / 16; ++i) {
-            o[i][nt][e] = none && !split ? 0.f : o[i][nt][e] * inv;
-            o[i][nt][2 + e] = none && !split ? 0.f : o[i][nt][2 + e] * inv;
-          }
-          if (g == 0 && qr < G) {
-            if (split)
-              a.lse_part[part_row0 + r] = lse2;
-            else if (a.out_lse)
-              a.out_lse[out_row0 + r] = lse2 * kLn2;
-          }
+          const int r = hc * G + tile_head + nt * 8 + hd;
+          if (split)
+            a.lse_part[part_row0 + r] = lse2;
+          else if (a.out_lse)
+            a.out_lse[out_row0 + r] = lse2 * kLn2;
         }
 #pragma unroll
         for (int i = 0; i < kD / 16; ++i) {
-          const float f = kSolo ? 1.f : fast_exp2(d[nt][e] - kWeightTop);
-          dst[stage_at<kD>(hd, 16 * i + g)] = o[i][nt][e] * f;
-          dst[stage_at<kD>(hd, 16 * i + g + 8)] = o[i][nt][2 + e] * f;
+          dst[stage_at<kD>(hd, 16 * i + g)] = kSolo && none && !split ? 0.f : o[i][nt][e] * inv * f;
+          dst[stage_at<kD>(hd, 16 * i + g + 8)] = kSolo && none && !split ? 0.f : o[i][nt][2 + e] * inv * f;
         }
-        if (g == 0) {
-          ml[warp * 16 + hd] = m[nt][e];
-          ml[warp * 16 + 8 + hd] = l[nt][e];
-        }
+        if (!kSolo && g == 0) lses[warp * 8 + hd] = lse2;
       }
       const int hds = min(8, G - tile_head - nt * 8);
       const size_t r0 = hc * G + tile_head + nt * 8;
@@ -594,20 +588,20 @@ __global__ void __launch_bounds__(Cfg<kD, kMany>::kThreads, 1) kv8_decode_kernel
       for (int e = replica * 32 + lane; e < hds * (kD / 4); e += threads) {
         const int d = e % (kD / 4) * 4, hd = e / (kD / 4);
         float M = -INFINITY;
-        for (int w = combo; w < active; w += combos) M = fmaxf(M, ml[w * 16 + hd]);
+        for (int w = combo; w < active; w += combos) M = fmaxf(M, lses[w * 8 + hd]);
         const float base = finite_base(M);
         float sum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int w = combo; w < active; w += combos) {
-          const float f = fast_exp2(ml[w * 16 + hd] - base);
-          sum += f * ml[w * 16 + 8 + hd];
+          const float f = fast_exp2(lses[w * 8 + hd] - base);
+          sum += f;
           const float4 v = *reinterpret_cast<const float4*>(stage + w * 8 * kD + stage_at<kD>(hd, d));
           acc = make_float4(acc.x + f * v.x, acc.y + f * v.y, acc.z + f * v.z, acc.w + f * v.w);
         }
         const bool none = sum == 0.f;
-        const float inv = none ? 0.f : fast_rcp(sum), lse2 = none ? -INFINITY : M + fast_log2(sum);
-        const size_t r = r0 + hd;
+        const float inv = none ? 0.f : 8.f * fast_rcp(sum), lse2 = none ? -INFINITY : M + fast_log2(sum);
         acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        const size_t r = r0 + hd;
         if (split)
           *reinterpret_cast<float4*>(a.o_part + (part_row0 + r) * kD + d) = acc;
         else
@@ -644,15 +638,15 @@ __global__ void __launch_bounds__(Cfg<kD, kMany>::kThreads, 1) kv8_decode_kernel
   }
   named_bar_sync(1, C::kConsumers);
   auto* join_smem = reinterpret_cast<JoinSmem<kD, C::kWarps>*>(stage);  // the states staged there are read
-  static_assert(sizeof(JoinSmem<kD, C::kWarps>) <= (C::kStageFloats + C::kWarps * 16) * 4, "the join's sums fit");
+  static_assert(sizeof(JoinSmem<kD, C::kWarps>) <= (C::kStageFloats + C::kWarps * 8) * 4, "the join's sums fit");
 #pragma unroll 1
   for (int s = 0; s < 2; ++s) {
     if (!flags[s]) continue;
     const int first = s ? (int)blockIdx.x : first0, parts = s ? parts1 : parts0, item = flags[2 + s];
     const int warps = min(C::kWarps, share_of(parts));
     for (int r0 = 0; r0 < rows; r0 += C::kWarps / warps)
-      join_rows<kD, C::kWarps, 4, true>(a.o_part, a.lse_part, first, parts, item, rows, r0, warps, *join_smem, a.out,
-                               a.out_lse, [] { named_bar_sync(1, C::kConsumers); });
+      join_rows<kD, C::kWarps, 4, true, kDown>(a.o_part, a.lse_part, first, parts, item, rows, r0, warps, *join_smem,
+                                               a.out, a.out_lse, [] { named_bar_sync(1, C::kConsumers); });
   }
 }
 
@@ -739,7 +733,7 @@ cudaError_t launch_as(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv
   const int rows = a.heads * a.group;
   // An item has at most `rows` units, and no more items than CTAs reach beyond a slice.
   const int units = std::min(grid, a.batch * a.head_groups) * rows;
-  return launch_pdl(paged_join_kernel<kD>, dim3(std::min(units, 8 * grid)), dim3(kJoinWarps * 32), 0, stream,
+  return launch_pdl(paged_join_kernel<kD, kDown>, dim3(std::min(units, 8 * grid)), dim3(kJoinWarps * 32), 0, stream,
                     a.o_part, a.lse_part, a.joins, grid, rows, a.out, a.out_lse);
 }
 

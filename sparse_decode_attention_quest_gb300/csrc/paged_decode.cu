@@ -515,8 +515,8 @@ __global__ void __launch_bounds__(Cfg<kD>::kThreads, 1) paged_decode_kernel(cons
     const int first = s ? (int)blockIdx.x : first0, parts = s ? parts1 : parts0, item = flags[2 + s];
     const int warps = min(C::kWarps, share_of(parts));
     for (int r0 = 0; r0 < rows; r0 += C::kWarps / warps)
-      join_rows<kD, C::kWarps, 8, false>(a.o_part, a.lse_part, first, parts, item, rows, r0, warps, *join_smem, a.out,
-                               a.out_lse, [] { named_bar_sync(1, C::kConsumers); });
+      join_rows<kD, C::kWarps, 8, false, 0>(a.o_part, a.lse_part, first, parts, item, rows, r0, warps, *join_smem,
+                                            a.out, a.out_lse, [] { named_bar_sync(1, C::kConsumers); });
   }
 }
 
@@ -591,7 +591,7 @@ cudaError_t launch_as(const CUtensorMap& kmap, const CUtensorMap& vmap, const Pa
   const int rows = a.heads * a.group;
   // An item has at most `rows` units, and no more items than CTAs reach beyond a slice.
   const int units = std::min(grid, a.batch * a.head_groups) * rows;
-  return launch_pdl(paged_join_kernel<kD>, dim3(std::min(units, 8 * grid)), dim3(kJoinWarps * 32), 0, stream,
+  return launch_pdl(paged_join_kernel<kD, 0>, dim3(std::min(units, 8 * grid)), dim3(kJoinWarps * 32), 0, stream,
                     a.o_part, a.lse_part, a.joins, grid, rows, a.out, a.out_lse);
 }
 

@@ -22,17 +22,19 @@ __device__ __forceinline__ int stage_at(int head, int dim) {
 // log-sum-exp of a row,
 //     out = sum_i exp2(lse_i - M) o_i / sum_i exp2(lse_i - M).
 // kBatch: partials in flight (a power of two). kLean: quotients and logarithms by the hardware approximations, which
-// take less code: what a CTA runs once costs it the fetching of its instructions.
+// take less code: what a CTA runs once costs it the fetching of its instructions. kDown: weights and their sum are held
+// 2^kDown lower (exact, but for weights below 2^-118), so that the sum of so many partials near fp32's largest is finite.
 template <int kD, int kW>
 struct JoinSmem {
   float acc[kW][kD];
   float m[kW], l[kW];
 };
-template <int kD, int kW, int kBatch, bool kLean, typename Sync>
+template <int kD, int kW, int kBatch, bool kLean, int kDown, typename Sync>
 __device__ __forceinline__ void join_rows(const float* o_part, const float* lse_part, int first, int parts, int item,
                                           int rows, int r0, int share, JoinSmem<kD, kW>& sm, uint16_t* out,
                                           float* out_lse, Sync sync) {
   constexpr int kV = kD / 32;  // values per lane
+  constexpr float kUp = 1 << kDown;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = min(r0 + warp / share, rows - 1), sub = warp % share;
   // Partial i is in slot 1 of the item's first CTA (i = 0), in slot 0 of the others. Other CTAs wrote it: past L1.
@@ -69,7 +71,7 @@ __device__ __forceinline__ void join_rows(const float* o_part, const float* lse_
 #pragma unroll
     for (int o = kBatch / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     top = fmaxf(M, __shfl_sync(0xffffffffu, top, 0));
-    const float base = finite_base(top), f0 = fast_exp2(M - base), w = fast_exp2(ls - base);
+    const float base = finite_base(top), f0 = fast_exp2(M - base), w = fast_exp2(ls - base) * (1.f / kUp);
     M = top;
     l *= f0;
 #pragma unroll
@@ -87,12 +89,12 @@ __device__ __forceinline__ void join_rows(const float* o_part, const float* lse_
     if (r0 + warp >= rows) return;
     const size_t orow = (size_t)item * rows + r;
     const bool none = l == 0.f;
-    const float inv = kLean ? fast_rcp(l) : 1.f / l;
+    const float inv = kLean ? fast_rcp(l) : 1.f / l, log_l = kLean ? fast_log2(l * kUp) : log2f(l * kUp);
 #pragma unroll
     for (int x = 0; x < kV; x += 2)
       *reinterpret_cast<uint32_t*>(out + orow * kD + lane * kV + x) =
           none ? 0u : pack_bf16x2(acc[x] * inv, acc[x + 1] * inv);
-    if (out_lse && lane == 0) out_lse[orow] = none ? -INFINITY : (M + (kLean ? fast_log2(l) : log2f(l))) * kLn2;
+    if (out_lse && lane == 0) out_lse[orow] = none ? -INFINITY : (M + log_l) * kLn2;
     return;
   }
   sync();  // the previous rows' sums are read
@@ -119,14 +121,14 @@ __device__ __forceinline__ void join_rows(const float* o_part, const float* lse_
     }
     const size_t orow = (size_t)item * rows + row;
     const bool none = sum == 0.f;
-    const float inv = kLean ? fast_rcp(sum) : 1.f / sum;
+    const float inv = kLean ? fast_rcp(sum) : 1.f / sum, log_l = kLean ? fast_log2(sum * kUp) : log2f(sum * kUp);
     *reinterpret_cast<uint32_t*>(out + orow * kD + d) = none ? 0u : pack_bf16x2(x * inv, y * inv);
-    if (out_lse && d == 0) out_lse[orow] = none ? -INFINITY : (top + (kLean ? fast_log2(sum) : log2f(sum))) * kLn2;
+    if (out_lse && d == 0) out_lse[orow] = none ? -INFINITY : (top + log_l) * kLn2;
   }
 }
 
 // The join of the items that span many CTAs, a CTA per few rows of an item.
-template <int kD>
+template <int kD, int kDown>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const float* __restrict__ o_part,
                                                                     const float* __restrict__ lse_part,
                                                                     const int2* __restrict__ joins, int32_t ctas,
@@ -141,8 +143,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const float
   for (int u = blockIdx.x; u < n.y; u += gridDim.x) {
     const int4 j = join_of(todo, n.x, u);
     const int share = share_of(j.z);
-    join_rows<kD, kJoinWarps, 8, false>(o_part, lse_part, j.x, j.z, j.y, rows, (u - j.w) * (kJoinWarps / share), share, sm, out,
-                              out_lse, [] { __syncthreads(); });
+    join_rows<kD, kJoinWarps, 8, false, kDown>(o_part, lse_part, j.x, j.z, j.y, rows,
+                                               (u - j.w) * (kJoinWarps / share), share, sm, out, out_lse,
+                                               [] { __syncthreads(); });
   }
 }
 

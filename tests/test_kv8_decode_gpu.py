@@ -213,6 +213,23 @@ def test_least_and_large_scales(cuda_device, shape, k_exp, v_exp):
     x.check()
 
 
+# Shapes whose warps share a head's pages and shapes where each has its own, with one tile of heads and with many.
+EVERY_SPLIT = SHAPES + [(64, 8, 128), (32, 8, 64), (64, 1, 128), (64, 1, 64), (64, 1, 256), (48, 4, 256)]
+
+
+@pytest.mark.parametrize("shape", EVERY_SPLIT)
+@pytest.mark.parametrize("lens,sink,recent", [([70, 0, 333, 17, 2500], 0, 0), ([20011], 0, 0), ([9000, 1, 4095], 0, 0),
+                                              ([330] * 160, 0, 0), ([17, 40, 99, 5000, 333], 5, 100)])
+def test_values_near_the_largest(cuda_device, shape, lens, sink, recent):
+    """Values up to 448 2^119 = 0.875 2^128 of one sign, their weights nearly the same: the averages are finite, though the
+    sums of two values are not. (Positive codes: only averages this large could overflow on the way.)"""
+    x = Inputs(cuda_device, lens, *shape, seed=24, sink=sink, recent=recent, q_scale=0.01)
+    x.codes["v"] &= 0x7F
+    x.s["v"] = torch.exp2(torch.randint(118, 120, x.s["v"].shape, generator=torch.Generator().manual_seed(24)).float())
+    x.upload()
+    x.check()
+
+
 @pytest.mark.parametrize("shape", SHAPES)
 @pytest.mark.parametrize("scale,q_scale", [(0.0, 1.0), (-0.07, 1.0), (1.0, 0.1), (1e-3, 300.0), (1e20, 1e-21), (1e-9, 1e8)])
 def test_scales_of_queries(cuda_device, shape, scale, q_scale):
