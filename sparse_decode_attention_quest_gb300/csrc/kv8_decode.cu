@@ -355,9 +355,9 @@ __global__ void __launch_bounds__(Cfg<kD, kMany>::kThreads, 1) kv8_decode_kernel
 #pragma unroll
         for (int u = 0; u < kPp; ++u) all &= mask[u];
         const bool whole = all != 0;
-        // Products of tokens k_row(g) (0, 1) and k_row(g + 8) (2, 3), heads 2 t and 2 t + 1, times their factors; K's scale.
+        // Products, then logits in base 2, of tokens k_row(g) (0, 1) and k_row(g + 8) (2, 3), heads 2 t and 2 t + 1.
         constexpr int kAcc = kPp * kNt == 1 ? 2 : 1;  // accumulators of a page's products where there is no other chain
-        float s[kPp][kNt][4], more[kPp][kNt][4], ks[kPp];
+        float s[kPp][kNt][4], more[kPp][kNt][4];
         if (any) {
 #pragma unroll
           for (int u = 0; u < kPp; ++u)
@@ -385,12 +385,14 @@ __global__ void __launch_bounds__(Cfg<kD, kMany>::kThreads, 1) kv8_decode_kernel
           }
 #pragma unroll
           for (int u = 0; u < kPp; ++u) {
-            ks[u] = scales[sk * C::kBlocks + blk[u]];
+            // Both factors at once: the products times the query's alone pass fp32 where K's scale brings logits back. Rounded
+            // here, not in a fused subtraction of a maximum: equal logits stay equal, however large.
+            const float ks = scales[sk * C::kBlocks + blk[u]];
 #pragma unroll
             for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                s[u][nt][e] = (kAcc == 2 ? s[u][nt][e] + more[u][nt][e] : s[u][nt][e]) * zf[nt][e & 1];
+                s[u][nt][e] = __fmul_rn(kAcc == 2 ? s[u][nt][e] + more[u][nt][e] : s[u][nt][e], zf[nt][e & 1] * ks);
             if (!whole) {
               const bool k0 = in_mask(mask[u] & ~kWhole, g), k1 = in_mask(mask[u] & ~kWhole, k_row(g + 8));
 #pragma unroll
@@ -419,8 +421,8 @@ __global__ void __launch_bounds__(Cfg<kD, kMany>::kThreads, 1) kv8_decode_kernel
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const float w = vs[u] + kWeightTop - d[nt][e];
-                x[u][nt][e] = fmaf(s[u][nt][e], ks[u], -m[nt][e]) + w;
-                x[u][nt][2 + e] = fmaf(s[u][nt][2 + e], ks[u], -m[nt][e]) + w;
+                x[u][nt][e] = s[u][nt][e] - m[nt][e] + w;
+                x[u][nt][2 + e] = s[u][nt][2 + e] - m[nt][e] + w;
                 // l's exponentials over the weights; beyond 2^60 (a V scale far below the others') they have their own.
                 lg[u][nt][e] = fast_exp2(-w);
                 moved = moved || !(fmaxf(x[u][nt][e], x[u][nt][2 + e]) <= kWeightMost) || w < -60.f;
@@ -432,19 +434,15 @@ __global__ void __launch_bounds__(Cfg<kD, kMany>::kThreads, 1) kv8_decode_kernel
             for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                float z[kPp][2], top = m[nt][e];
+                float top = m[nt][e];
 #pragma unroll
-                for (int u = 0; u < kPp; ++u) {
-                  z[u][0] = s[u][nt][e] * ks[u];
-                  z[u][1] = s[u][nt][2 + e] * ks[u];
-                  top = fmaxf(top, fmaxf(z[u][0], z[u][1]));
-                }
+                for (int u = 0; u < kPp; ++u) top = fmaxf(top, fmaxf(s[u][nt][e], s[u][nt][2 + e]));
 #pragma unroll
                 for (int i = 4; i < 32; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
                 const float back = m[nt][e] - top;
                 float over = fmaxf(d[nt][e] + back, kLowest);
 #pragma unroll
-                for (int u = 0; u < kPp; ++u) over = fmaxf(over, fmaxf(z[u][0], z[u][1]) - top + vs[u]);
+                for (int u = 0; u < kPp; ++u) over = fmaxf(over, fmaxf(s[u][nt][e], s[u][nt][2 + e]) - top + vs[u]);
 #pragma unroll
                 for (int i = 4; i < 32; i <<= 1) over = fmaxf(over, __shfl_xor_sync(0xffffffffu, over, i));
                 const float f = fast_exp2(back + (d[nt][e] - over));
@@ -458,7 +456,7 @@ __global__ void __launch_bounds__(Cfg<kD, kMany>::kThreads, 1) kv8_decode_kernel
                 }
 #pragma unroll
                 for (int u = 0; u < kPp; ++u) {
-                  const float z0 = z[u][0] - top, z1 = z[u][1] - top, w = vs[u] + kWeightTop - over;
+                  const float z0 = s[u][nt][e] - top, z1 = s[u][nt][2 + e] - top, w = vs[u] + kWeightTop - over;
                   x[u][nt][e] = z0 + w;
                   x[u][nt][2 + e] = z1 + w;
                   l[nt][e] += fast_exp2(z0) + fast_exp2(z1);

@@ -230,6 +230,36 @@ def test_values_near_the_largest(cuda_device, shape, lens, sink, recent):
     x.check()
 
 
+@pytest.mark.parametrize("shape", EVERY_SPLIT)
+@pytest.mark.parametrize("recent", [0, 1])
+def test_large_queries_over_keys_of_the_least_scale(cuda_device, shape, recent):
+    """Queries near 2^122 over K scales of 2^-100: the logits are some 2^30, the products with the codes alone beyond fp32.
+    One kept token has all the weight, whatever its logit. Of more, whose logits and partial log-sum-exps are rounded in
+    steps of 2^7, no weight is known, but that they are an average's: with A the largest |v_j| of a dim, the output lies
+    within min_j v_j and max_j v_j but for (2^-11 + (n + 64) 2^-23) A (weights in fp16, sums) and the rounding to bf16."""
+    lens = [1, 40, 0, 5000, 9000] if recent else [70, 0, 333, 17, 5000]
+    x = Inputs(cuda_device, lens, *shape, seed=25, recent=recent, q_scale=2.0 ** 120)
+    x.s["k"] = torch.full_like(x.s["k"], 2.0 ** -100)
+    x.upload()
+    out, lse = x.run()
+    _, rlse, _, ltol = x.bounds()
+    got = lse.double().cpu().numpy()
+    empty = np.isneginf(rlse)
+    assert (np.isneginf(got) == empty).all()
+    assert (np.abs(np.where(empty, 0, got) - np.where(empty, 0, rlse)) <= ltol).all()
+    v, got = x.value("v"), out.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    for b, L in enumerate(lens):
+        j = op.kept_positions(L, 0, recent)
+        if len(j) == 0:
+            assert (got[b] == 0).all()
+            continue
+        kept = np.repeat(v[x.table.numpy()[b, j // 16], :, j % 16], x.Hq // x.H, axis=1)
+        lo, hi, far = kept.min(0), kept.max(0), np.abs(kept).max(0)
+        tol = (2.0 ** -11 + (len(j) + 64) * 2.0 ** -23 + 2.0 ** -8 * (1 + 2.0 ** -7)) * far
+        assert (got[b] >= lo - tol).all() and (got[b] <= hi + tol).all()
+
+
 @pytest.mark.parametrize("shape", SHAPES)
 @pytest.mark.parametrize("scale,q_scale", [(0.0, 1.0), (-0.07, 1.0), (1.0, 0.1), (1e-3, 300.0), (1e20, 1e-21), (1e-9, 1e8)])
 def test_scales_of_queries(cuda_device, shape, scale, q_scale):
