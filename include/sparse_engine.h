@@ -497,9 +497,14 @@ SE_API se_status_t se_paged_decode(const se_paged_kv_t* kv, const void* q, int64
  *   SE_ROTARY_SCALING_NONE: w_i;   SE_ROTARY_SCALING_LINEAR: w_i / factor;
  *   SE_ROTARY_SCALING_NTK: base replaced by base * factor^(rotary_dim / (rotary_dim - 2)) (rotary_dim > 2);
  *   SE_ROTARY_SCALING_YARN: w_i g + w_i / factor (1 - g), g = clamp((turns - 1) / (32 - 1), 0, 1) with
- *     turns = original_len * w_i / (2 pi), and *amplitude = 0.1 ln(factor) + 1 (1 otherwise).
+ *     turns = original_len * w_i / (2 pi), and *amplitude = 0.1 ln(factor) + 1 (1 otherwise). That is the ramp of the
+ *     method's paper, linear in the turns. Models trained with the method's released program, and what serves them, have
+ *     another one, linear in the pair's index, whose frequencies differ by tens of percent:
+ *   SE_ROTARY_SCALING_YARN_PAIRS: the same with g = 1 - clamp((i - low) / max(high - low, 0.001), 0, 1),
+ *     low = max(floor(pair(32)), 0), high = min(ceil(pair(1)), rotary_dim - 1), where pair(t) =
+ *     rotary_dim ln(original_len / (2 pi t)) / (2 ln base) is the (fractional) pair that makes t turns.
  *   freqs: uint64 [rotary_dim / 2] on the host; amplitude: float on the host.
- * rotary_dim: a positive multiple of 2; base > 1; factor >= 1; original_len > 0 for YARN. Computed in
+ * rotary_dim: a positive multiple of 2; base > 1; factor >= 1; original_len > 0 for both YARN ramps. Computed in
  * 64-bit floating point.
  */
 #define SE_ROTARY_INTERLEAVED 0x1u
@@ -508,6 +513,7 @@ SE_API se_status_t se_paged_decode(const se_paged_kv_t* kv, const void* q, int64
 #define SE_ROTARY_SCALING_LINEAR 1
 #define SE_ROTARY_SCALING_NTK    2
 #define SE_ROTARY_SCALING_YARN   3
+#define SE_ROTARY_SCALING_YARN_PAIRS 19 /* SE_ROTARY_SCALING_YARN, 0x10: by pairs */
 SE_API se_status_t se_rotary_frequencies(int32_t rotary_dim, double base, int32_t scaling, double factor,
                                          int32_t original_len, uint64_t* freqs, float* amplitude);
 SE_API se_status_t se_rotary(const void* q, int64_t q_stride, int32_t num_q_heads, const void* k, int64_t k_stride,

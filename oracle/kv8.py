@@ -127,8 +127,13 @@ def frequencies(dim, base, scaling, factor=1.0, original=0):
             turns = original * x / (2 * math.pi)
             g = min(1.0, max(0.0, (turns - 1) / 31))
             x = g * x + (1 - g) * x / factor
+        if scaling == "yarn_pairs":
+            low, high = (dim * math.log(original / (2 * math.pi * t)) / (2 * math.log(base)) for t in (32, 1))
+            low, high = max(math.floor(low), 0), min(math.ceil(high), dim - 1)
+            g = 1 - min(1.0, max(0.0, (i - low) / max(high - low, 0.001)))
+            x = g * x + (1 - g) * x / factor
         w.append(x)
-    return np.array(w), (0.1 * math.log(factor) + 1 if scaling == "yarn" else 1.0)
+    return np.array(w), (0.1 * math.log(factor) + 1 if scaling.startswith("yarn") else 1.0)
 
 
 def rotary(x, positions, w, offset=0, interleaved=False, inverse=False, amplitude=1.0):

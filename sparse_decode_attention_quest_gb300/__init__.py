@@ -39,7 +39,7 @@ DEVERR_PAGE_RANGE = 0x1
 DEVERR_LENGTH = 0x2
 DEVERR_WAIT_TIMEOUT = 0x4
 DEVERR_NO_PAGES = 0x8
-ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "yarn_pairs": 19}
 APPEND_OVERLAP_PREVIOUS = 0x1  # se_quest_update_summaries_ex: may run alongside the previous kernel
 
 
@@ -572,7 +572,9 @@ def se_rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str =
                           original_len: int = 0):
     """(freqs, amplitude) for se_rotary: turns per position of each pair of dims times 2^64, as the bits of an int64
     CPU tensor [rotary_dim / 2], and what the cosines and sines are multiplied by. ``scaling``: "none", "linear",
-    "ntk" or "yarn" (ROTARY_SCALINGS), for contexts ``factor`` times as long as the ``original_len`` trained for."""
+    "ntk", "yarn" or "yarn_pairs" (ROTARY_SCALINGS), for contexts ``factor`` times as long as the ``original_len`` trained
+    for. "yarn" is the paper's ramp, linear in a pair's turns; "yarn_pairs" the one that models trained with the method's
+    released program need, linear in the pair's index."""
     if scaling not in ROTARY_SCALINGS:
         raise ValueError(f"scaling: expected one of {', '.join(ROTARY_SCALINGS)}, got {scaling!r}")
     freqs = torch.zeros(max(int(rotary_dim) // 2, 1), dtype=torch.int64)

@@ -992,25 +992,31 @@ se_status_t se_rotary_frequencies(int32_t rotary_dim, double base, int32_t scali
   if (rotary_dim < 2 || (rotary_dim % 2)) return fail(SE_ERR_INVALID_ARG, fn, "rotary_dim must be a positive multiple of 2");
   if (!freqs || !amplitude) return fail(SE_ERR_INVALID_ARG, fn, "freqs/amplitude NULL");
   if (!std::isfinite(base) || base <= 1.0) return fail(SE_ERR_INVALID_ARG, fn, "base must be above 1");
-  if (scaling < SE_ROTARY_SCALING_NONE || scaling > SE_ROTARY_SCALING_YARN)
+  const bool by_pairs = scaling == SE_ROTARY_SCALING_YARN_PAIRS, yarn = by_pairs || scaling == SE_ROTARY_SCALING_YARN;
+  if (!yarn && (scaling < SE_ROTARY_SCALING_NONE || scaling > SE_ROTARY_SCALING_NTK))
     return fail(SE_ERR_INVALID_ARG, fn, "unknown scaling");
   if (!std::isfinite(factor) || factor < 1.0) return fail(SE_ERR_INVALID_ARG, fn, "factor must be at least 1");
-  if (scaling == SE_ROTARY_SCALING_YARN && original_len < 1)
+  if (yarn && original_len < 1)
     return fail(SE_ERR_INVALID_ARG, fn, "original_len must be positive");
   constexpr double kTwoPi = 6.283185307179586476925;
   const double r = rotary_dim;
   if (scaling == SE_ROTARY_SCALING_NTK && rotary_dim > 2) base *= std::pow(factor, r / (r - 2.0));
+  // The pair that makes t turns over the original length.
+  auto pair = [&](double t) { return r * std::log(original_len / (kTwoPi * t)) / (2.0 * std::log(base)); };
+  const double low = by_pairs ? std::max(std::floor(pair(32.0)), 0.0) : 0.0;
+  const double high = by_pairs ? std::min(std::ceil(pair(1.0)), r - 1.0) : 0.0;
   for (int i = 0; i < rotary_dim / 2; ++i) {
     double w = std::pow(base, -2.0 * i / r);
     if (scaling == SE_ROTARY_SCALING_LINEAR) w /= factor;
-    if (scaling == SE_ROTARY_SCALING_YARN) {
-      const double g = std::min(1.0, std::max(0.0, (original_len * w / kTwoPi - 1.0) / 31.0));
+    if (yarn) {
+      const double ramp = by_pairs ? 1.0 - (i - low) / std::max(high - low, 0.001) : (original_len * w / kTwoPi - 1.0) / 31.0;
+      const double g = std::min(1.0, std::max(0.0, ramp));
       w = w * g + w / factor * (1.0 - g);
     }
     // Turns per position below 1/6 as a fraction of 2^64, to the nearest (the product is exact).
     freqs[i] = (uint64_t)std::nearbyint(std::ldexp(w / kTwoPi, 64));
   }
-  *amplitude = scaling == SE_ROTARY_SCALING_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+  *amplitude = yarn ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
   return SE_OK;
 }
 

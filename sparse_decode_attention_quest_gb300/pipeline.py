@@ -78,7 +78,8 @@ class DenseAttention:
 class Rotary:
     """The frequencies of rotary positions on a device, and which dims of a head they turn: ``rotary_dim`` of them from
     ``offset`` on, pairs of a half's distance or next to each other (``interleaved``). ``scaling``, ``factor`` and
-    ``original_len``: se_rotary_frequencies."""
+    ``original_len``: se_rotary_frequencies ("yarn" and "yarn_pairs" are two ramps: a model needs the one it was trained
+    with). ``amplitude`` may be set to a model's own."""
 
     def __init__(self, rotary_dim: int, device, base: float = 10000.0, offset: int = 0, interleaved: bool = False,
                  scaling: str = "none", factor: float = 1.0, original_len: int = 0):
