@@ -43,6 +43,7 @@ constexpr int kMaxBatch = 4096;  // requests whose prefix fits beside the ring
 constexpr float kWeightTop = 14.f;    // log2 of the weight at the reference
 constexpr float kWeightMost = 15.9f;  // log2 of the largest weight, within fp16
 constexpr float kLowest = -3.4e38f;   // m and d before any logit
+constexpr int kLaunchRegs = 168;      // a thread's: a kernel that moves registers between warps gets as many as it may have
 constexpr int kDown = 8;              // joins: up to 2^8 partials whose sum may pass fp32's largest
 static_assert(kMaxCtas <= 1 << kDown, "an item has no more partials than CTAs");
 
@@ -62,7 +63,10 @@ struct Cfg {
   static constexpr int kIssuers = 4;
   static constexpr int kProducers = kIssuers * 32;
   static constexpr int kThreads = kConsumers + kProducers;
-  static constexpr int kProducerRegs = 56, kConsumerRegs = 224;  // kMany: a thread's, of 168 at launch
+  static constexpr int kProducerRegs = 56, kConsumerRegs = 224;  // kMany: a thread's, of kLaunchRegs at launch
+  // A consumer waits for registers that the launch does not have forever.
+  static_assert(kProducerRegs * kProducers + kConsumerRegs * kConsumers <= kLaunchRegs * kThreads, "registers of the shares");
+  static_assert(kLaunchRegs * kThreads <= 65536, "registers of a launch");
   static constexpr int kSlots = kD == 256 ? 4 : 5;
   static constexpr int kBlocks = kSlotBytes / (kPageSize * kD);  // (page, head) blocks of a slot
   static constexpr int kStageFloats = kWarps * 8 * kD;           // states handed over at a segment's end
@@ -131,7 +135,7 @@ struct Kv8Args {
 // kSolo: no two warps share a (head, tile) (code of its own: as a branch
 // beside the other it cost that one 0.8 us of 9.9).
 template <int kD, bool kMany, bool kSolo>
-__global__ void __launch_bounds__(Cfg<kD, kMany>::kThreads, 1) kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap,
+__global__ void __maxnreg__(kLaunchRegs) kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                                                                            const __grid_constant__ CUtensorMap vmap,
                                                                            const Kv8Args a) {
   using C = Cfg<kD, kMany>;
@@ -717,7 +721,7 @@ cudaError_t launch_as(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv
   static_assert(C::kMaxSmem <= 227 * 1024, "the largest batch fits");
   static std::atomic<uint64_t> allowed{0};
   if (kMany && !allowed.load(std::memory_order_acquire)) {
-    // The consumers take their registers from the launch's: with fewer they would wait for them forever.
+    // Were it built with fewer registers after all, no launch would end.
     cudaFuncAttributes at;
     const cudaError_t e = cudaFuncGetAttributes(&at, kv8_decode_kernel<kD, kMany, kSolo>);
     if (e != cudaSuccess) return e;
