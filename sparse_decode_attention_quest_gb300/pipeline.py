@@ -144,8 +144,10 @@ class PagedCache:
     def rotate(self, rotary: Rotary, q, k, q_out=None, k_out=None, stream=None):
         """The query and key rows [T][heads][D] of the tokens that extend placed, turned by their positions (in place
         without outputs); the padded rows behind the batch's last token are left."""
-        rows = (k if q is None else q).shape[0]
-        rotary.apply(q, k, self.positions[:rows], q_out, k_out, self.token_start[-1:], stream=stream)
+        given = k if q is None else q
+        if given is None:
+            raise ValueError("q, k: neither is given")
+        rotary.apply(q, k, self.positions[:given.shape[0]], q_out, k_out, self.token_start[-1:], stream=stream)
 
     def load(self, token_start, k_out, v_out, first=None, stream=None):
         """Rows of an 8-bit cache back as bf16 into k_out and v_out [T][Hkv][D]: request b's positions from first[b]

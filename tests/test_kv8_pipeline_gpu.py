@@ -249,6 +249,12 @@ def test_eight_bits_stay_close_to_sixteen(cuda_device):
     assert float((a - b).abs().max()) <= 2 * dz * (1 + dz) * big + 2.0 ** -4 * big + 2.0 ** -10 * sv + 2.0 ** -7 * big
 
 
+def test_rows_of_neither_kind(cuda_device):
+    cache = PagedCache(4, 1, 32, 8, 2, 128, 8, cuda_device, eight_bit=True)
+    with pytest.raises(ValueError, match="neither is given"):
+        cache.rotate(Rotary(128, cuda_device), None, None)
+
+
 def test_refusals(cuda_device):
     dev = cuda_device
     for bad in (dict(latent=True, head_dim_v=512, head_dim=576, num_q_heads=16, num_kv_heads=1),
