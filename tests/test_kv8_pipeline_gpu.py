@@ -249,6 +249,48 @@ def test_eight_bits_stay_close_to_sixteen(cuda_device):
     assert float((a - b).abs().max()) <= 2 * dz * (1 + dz) * big + 2.0 ** -4 * big + 2.0 ** -10 * sv + 2.0 ** -7 * big
 
 
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_eight_bits_against_the_rows_themselves(cuda_device, shape):
+    """Against 64 bits over the bf16 rows that were stored, bounded for each request and head. A value is off by half a
+    step of e4m3: e(x) = max(2^-4 |x|, 2^-10 of its page's scale). Logits are then off by at most
+    dz = s max_j sum_c |q_c| e(k_jc), weights by a factor within exp(+-2 dz), and the output by
+    (exp(2 dz) - 1) sum_j w_j (|v_j| + e(v_j)) + sum_j w_j e(v_j), beside the kernel's own roundings (weights in fp16, sums, bf16).
+    Outputs of zeros, of the other request or of the other sign are farther off than that."""
+    dev, kw = cuda_device, SHAPES[shape]
+    hq, H, D = kw["num_q_heads"], kw["num_kv_heads"], kw["head_dim"]
+    g = torch.Generator().manual_seed(5)
+    lens = [70, 33]
+    cache = PagedCache(10, 2, 160, max_new_tokens=200, device=dev, eight_bit=True, **kw)
+    k, v = (_bf16((103, H, D), g, dev) for _ in range(2))
+    k = k * 0.1
+    q = _bf16((2, hq, D), g, dev)
+    cache.extend(torch.tensor(lens, dtype=torch.int32, device=dev))
+    cache.store(k, v)
+    out = cache.attend(q).double().cpu().numpy()
+    table, s = cache.block_table.cpu().numpy(), cache.attention.sm_scale
+    ref, tol = np.zeros_like(out), np.zeros_like(out)
+    for b, n in enumerate(lens):
+        page = table[b, np.arange(n) // 16]
+        rows = slice(0, 70) if b == 0 else slice(70, 103)
+        # [heads][tokens][dims], a KV head's for each of its query heads
+        kk, vv = (np.repeat(x[rows].double().cpu().numpy().transpose(1, 0, 2), hq // H, 0) for x in (k, v))
+        ks, vs = (np.repeat(x.double().cpu().numpy()[page].T, hq // H, 0)[:, :, None] for x in (cache.k_scale, cache.v_scale))
+        qq = q[b].double().cpu().numpy()
+        ek, ev = np.maximum(2.0 ** -4 * np.abs(kk), 2.0 ** -10 * ks), np.maximum(2.0 ** -4 * np.abs(vv), 2.0 ** -10 * vs)
+        z = s * np.einsum("hd,hnd->hn", qq, kk)
+        w = np.exp(z - z.max(1, keepdims=True))
+        w /= w.sum(1, keepdims=True)
+        dz = s * np.einsum("hd,hnd->hn", np.abs(qq), ek).max(1)[:, None]
+        mag, off = (np.einsum("hn,hnd->hd", w, x) for x in (np.abs(vv), ev))
+        ref[b] = np.einsum("hn,hnd->hd", w, vv)
+        tol[b] = np.expm1(2 * dz) * (mag + off) + off + (2.0 ** -11 + (D + n + 64) * 2.0 ** -22) * (mag + off) * np.exp(2 * dz)
+        tol[b] += 2.0 ** -8 * 1.01 * (np.abs(ref[b]) + tol[b])
+    assert (np.abs(out - ref) <= tol).all()
+    for wrong in (np.zeros_like(out), out[::-1], -out):
+        for b in range(2):
+            assert (np.abs(wrong[b] - ref[b]) > tol[b]).any()
+
+
 def test_rows_of_neither_kind(cuda_device):
     cache = PagedCache(4, 1, 32, 8, 2, 128, 8, cuda_device, eight_bit=True)
     with pytest.raises(ValueError, match="neither is given"):
