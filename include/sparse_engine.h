@@ -586,9 +586,11 @@ SE_API se_status_t se_paged_kv8_load(const se_paged_kv8_t* kv, const int32_t* bl
  * cached tokens, all of them or the first sink_tokens and the last recent_tokens, with k_j = code * scale and
  * v_j alike. Same arguments, windows, errors, splitting and repeatability; half the bytes.
  * Logits, maxima, sums, partial outputs and joins are fp32. A query row is scaled by a power of two and enters the
- * products as fp16, within 2^-32 of its largest magnitude or 2^-125; a weight, times its page's V scale, meets its value row as
- * fp16 (half a step, 2^-11 of it), but not the sum that divides the output nor out_lse. A query row that holds
- * an infinity or a NaN gives NaN. A query row's largest magnitude times |sm_scale|, and that times a kept page's K scale,
+ * products as fp16, within 2^-32 of its largest magnitude or 2^-125. A weight, times its page's V scale, meets its value
+ * row as fp16: within 2^-11 of itself where that product is at least 2^-28 of the row's largest one, within 2^-39 of the
+ * largest below (so that one of less than 2^-39 may be lost); the sum that divides the output, and out_lse, take it
+ * unrounded. Quotients and logarithms at the end are good to 2^-22. A query row that holds an infinity or a NaN gives
+ * NaN. A query row's largest magnitude times |sm_scale|, and that times a kept page's K scale,
  * are within fp32; a logit that is not is -inf (no weight) or makes its row NaN.
  * Shapes: head_dim 64, 128 or 256 with 1..64 query heads per KV head; batch <= 4096. Scales are positive and finite,
  * V's no less than 2^-100, the least that the store writes (those of pages that no kept token lies in are not used).
