@@ -1009,7 +1009,8 @@ se_status_t se_rotary_frequencies(int32_t rotary_dim, double base, int32_t scali
     double w = std::pow(base, -2.0 * i / r);
     if (scaling == SE_ROTARY_SCALING_LINEAR) w /= factor;
     if (yarn) {
-      const double ramp = by_pairs ? 1.0 - (i - low) / std::max(high - low, 0.001) : (original_len * w / kTwoPi - 1.0) / 31.0;
+      const double ramp =
+          by_pairs ? 1.0 - (i - low) / std::max(high - low, 0.001) : (original_len * w / kTwoPi - 1.0) / 31.0;
       const double g = std::min(1.0, std::max(0.0, ramp));
       w = w * g + w / factor * (1.0 - g);
     }

@@ -15,7 +15,7 @@
 //    P^T has them in that order, which the rows of K and V are read in such orders for (and without bank
 //    conflicts): no bytes are moved in registers. (m16n8k32 e4m3 MMAs on K's codes as they lie, the query split into
 //    two e4m3 numbers a dim, were slower: 454 instructions a block of 16 tokens and one head, 691 us for 3.2 GB.)
-//  * A query row is scaled by a power of two to at most 448 and held as fp16: exact for dims down to 2^-25 of the
+//  * A query row is scaled by a power of two to at most 448 and held as fp16: exact for dims down to 2^-24 of the
 //    row's largest magnitude, within 2^-32 of it below (2^-125 where the power of two is the least, 2^-100).
 //  * V's scales go into the weights before they are rounded to fp16: a weight enters as
 //    w_j = exp2(z_j - m + log2 s_v - d + 14), with m + d a reference of their product's maximum, so that it is rounded
@@ -48,14 +48,15 @@ constexpr int kDown = 8;              // joins: up to 2^8 partials whose sum may
 static_assert(kMaxCtas <= 1 << kDown, "an item has no more partials than CTAs");
 
 // Four warps issue the boxes, every fourth page each: a warp takes some 65 clocks to issue one and 35 more per KB, so
-// that one warp alone kept boxes of 1 KB to 48% of the copy rate and of 2 KB to 72% (0.3 GB in 32K tokens a request: one
-// head of 64 dims 49 us, of 128 dims 61; so 31 and 51; 5 heads of 128 dims, 0.7 GB: 133 and 108).
+// that one warp alone kept boxes of 1 KB to 48% of the copy rate and of 2 KB to 72% (32 x 32K tokens of one head: 64 dims,
+// 0.13 GB, 49 us, so 31; 128 dims, 0.27 GB, 61 and 51; 32 x 16K tokens of 5 heads of 128 dims, 0.67 GB: 133 and 108).
 //
 // kMany: the kernel for many query heads per KV head. The twelve warps have 168 registers a thread at launch; here those of
-// the issuers go to the consumers, for tiles of sixteen heads and two pages at once without spills (0.3 GB in 16K tokens a
-// request, 32 heads of 128 dims over one: 118 us before, 98 so; 64: 201 and 164; 16 over each of 4 of 64 dims: 80 and
-// 71; 12 over each of 2 of 256 dims, 0.5 GB: 124 and 106). What bounds it is the time of the MMAs (8 clocks each) with
-// the conversions, which hardly overlap.
+// the issuers go to the consumers, for tiles of sixteen heads (256 dims: eight) and two pages at once, which 128 dims still
+// spill 44 bytes a thread for and 256 dims 8 (64 x 16K tokens, 0.27 GB, 32 heads of 128 dims over one: 118 us before, 99
+// so; 64: 201 and 166; 32 x 16K tokens, 0.27 GB, 16 over each of 4 of 64 dims: 80 and 72; 0.54 GB, 12 over each of 2 of
+// 256 dims: 124 and 105). What bounds it is the time of the MMAs (8 clocks each) with the conversions, which hardly
+// overlap.
 template <int kD, bool kMany>
 struct Cfg {
   static constexpr int kWarps = 8;  // consumers
@@ -65,7 +66,7 @@ struct Cfg {
   static constexpr int kThreads = kConsumers + kProducers;
   static constexpr int kProducerRegs = 56, kConsumerRegs = 224;  // kMany: a thread's, of kLaunchRegs at launch
   // A consumer waits for registers that the launch does not have forever.
-  static_assert(kProducerRegs * kProducers + kConsumerRegs * kConsumers <= kLaunchRegs * kThreads, "registers of the shares");
+  static_assert(kProducerRegs * kProducers + kConsumerRegs * kConsumers <= kLaunchRegs * kThreads, "the shares");
   static_assert(kLaunchRegs * kThreads <= 65536, "registers of a launch");
   static constexpr int kSlots = kD == 256 ? 4 : 5;
   static constexpr int kBlocks = kSlotBytes / (kPageSize * kD);  // (page, head) blocks of a slot
@@ -389,8 +390,8 @@ __global__ void __maxnreg__(kLaunchRegs) kv8_decode_kernel(const __grid_constant
           }
 #pragma unroll
           for (int u = 0; u < kPp; ++u) {
-            // Both factors at once: the products times the query's alone pass fp32 where K's scale brings logits back. Rounded
-            // here, not in a fused subtraction of a maximum: equal logits stay equal, however large.
+            // Both factors at once: the products times the query's alone pass fp32 where K's scale brings logits back.
+            // Rounded here, not in a fused subtraction of a maximum: equal logits stay equal, however large.
             const float ks = scales[sk * C::kBlocks + blk[u]];
 #pragma unroll
             for (int nt = 0; nt < kNt; ++nt)
@@ -658,13 +659,13 @@ struct HeadPlan {
   bool deferred;
 };
 
-// Query heads per KV head from which the kernel for many is taken: 64 and 256 dims 9, 128 dims 17 (16 over each of 4, 0.3 GB in
-// 16K tokens a request: 65 us against 68; but 32 requests of 2K tokens 30 against 28).
+// Query heads per KV head from which the kernel for many is taken: 64 and 256 dims 9, 128 dims 17 (16 over each of 4, 16 x
+// 16K tokens, 0.27 GB: 65 us against 68; but 32 requests of 2K tokens 30 against 28).
 bool takes_many(int head_dim, int group) { return group > (head_dim == 128 ? 16 : 8); }
 
-// The KV heads of a box, up to `most_heads`: the count for which most warps have pages, the larger of two alike (0.6
-// GB, 16K tokens a request: 5 heads of 64 dims one to a box 61 us, five 86; 3 heads of 128 dims 70, 75). A warp's pages are
-// whole sets of those it takes at once.
+// The KV heads of a box, up to `most_heads`: the count for which most warps have pages, the larger of two alike (32 x
+// 16K tokens: 5 heads of 64 dims, 0.34 GB, one to a box 61 us, five 86; 3 heads of 128 dims, 0.40 GB, 71 and 75). A
+// warp's pages are whole sets of those it takes at once.
 HeadPlan head_plan(int num_kv_heads, int group, int head_dim, int most_heads) {
   const int warps = Cfg<128, false>::kWarps, blocks = kSlotBytes / (kPageSize * head_dim);
   const bool many = takes_many(head_dim, group);
@@ -691,7 +692,7 @@ HeadPlan head_plan(int num_kv_heads, int group, int head_dim, int most_heads) {
 // Largest boxes of which an item's partials, counted in slices of the least length over the table's (or the windows')
 // width, have no more than 32 KB, so that the decode kernel joins them itself without delay; otherwise no more than 48
 // KB; otherwise the largest of all and a second kernel (48 windows of 1,064 tokens, 32/4 heads: 21.6 us, 22.6 with 48 KB
-// alone; 8 requests of 4K tokens, 64/8 heads of 64 dims: 15.5, 19.1, with 192 KB 34.3; but 1 request of 8K tokens, 32/8
+// alone; 8 requests of 4K tokens, 64/8 heads of 64 dims: 15.6, 19.1, with 192 KB 34.3; but 1 request of 8K tokens, 32/8
 // heads: 12.0, 14.8 with 32 KB alone). More items than two to a CTA are not made for that: 300 requests of up to 1,000
 // tokens, 32/4 heads: 45 us, 63 in boxes of one head.
 HeadPlan call_plan(int num_kv_heads, int group, int head_dim, int32_t bt_stride, int32_t sink_tokens,

@@ -10,9 +10,12 @@
 //
 // Store: bound by reading 2 bytes and writing 1 of every value. A warp takes the runs
 // (tokens next to each other whose slots lie in one page) that begin in its window of
-// tokens, for one KV head of K or V: it holds a run's rows in registers (16 rows of
-// 128 dims: eight 16-byte loads in flight per lane), folds their magnitudes, exchanges
-// them in five shuffles, and writes the codes, 8 bytes a lane. Windows as in the bf16
+// tokens, for one KV head of K or V or for several next to each other, 256 dims in all
+// where the number of heads allows: it holds a run's rows in registers (256 dims wide,
+// a row a load: sixteen 16-byte loads in flight per lane; 128 wide, two rows a load: eight),
+// folds their magnitudes, exchanges them between the lanes of a head and of its other
+// rows (three shuffles for four heads of 64 dims, four for two of 128, otherwise five or,
+// for two of 64, four), and writes the codes, 8 bytes a lane. Windows as in the bf16
 // store: 16 tokens for long batches, shorter ones down to one token where there are
 // fewer windows than warps.
 //
