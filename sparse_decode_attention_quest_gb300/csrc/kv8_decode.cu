@@ -137,8 +137,8 @@ struct Kv8Args {
 // beside the other it cost that one 0.8 us of 9.9).
 template <int kD, bool kMany, bool kSolo>
 __global__ void __maxnreg__(kLaunchRegs) kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap,
-                                                                           const __grid_constant__ CUtensorMap vmap,
-                                                                           const Kv8Args a) {
+                                                           const __grid_constant__ CUtensorMap vmap,
+                                                           const Kv8Args a) {
   using C = Cfg<kD, kMany>;
   constexpr int kSlots = C::kSlots, kNt = tiles_at_once(kD, kMany), kPp = pages_at_once(kD, kMany);
   extern __shared__ uint8_t smem_raw[];
@@ -549,8 +549,8 @@ __global__ void __maxnreg__(kLaunchRegs) kv8_decode_kernel(const __grid_constant
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
         const int hd = 2 * t + e;
-        // The average over the warp's own tokens (values near fp32's largest have no sum), 2^3 lower where it meets those of
-        // up to 2^3 warps.
+        // The average over the warp's own tokens (values near fp32's largest have no sum), 2^3 lower where it meets those
+        // of up to 2^3 warps.
         const bool none = l[nt][e] == 0.f;
         const float inv = none ? 0.f : fast_rcp(l[nt][e]);
         const float f = fast_exp2(d[nt][e] - (kSolo ? kWeightTop : kWeightTop + 3.f));
